@@ -59,6 +59,10 @@ typedef enum {
 #define ENTMAXKV_DEV_TIMEOUT         0x40u /* a bounded wait on an asynchronous copy ran out (about
                                               4M polls); the block waited for its copies in flight,
                                               stopped early, and its results are incomplete             */
+#define ENTMAXKV_DEV_BAD_BATCH       0x80u /* a batch slot whose rows leave [0, total), exceed max_count or
+                                              the sequence's length, or have a negative count: skipped */
+#define ENTMAXKV_DEV_NONFINITE       0x100u /* append_q8 met an infinity (stored as the largest code of
+                                              its sign) or a NaN (stored as 0)                         */
 
 /* KV storage types. */
 #define ENTMAXKV_F32  0
@@ -364,6 +368,190 @@ size_t entmaxkv_noalloc_scratch_bytes(void);
 int32_t entmaxkv_decode_softmax_noalloc(const entmaxkv_config* cfg, const entmaxkv_cache* cache,
                                         const void* q, const int32_t* seq_ids, int32_t n_seqs,
                                         float* out, float* lse, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit paged cache: page planning, a quantising append, its read-back
+ * and attention over the cache. A serving step is plan, append, attend.
+ *
+ * A stored value is code * scale with one float32 scale for the K and one for
+ * the V rows of each (physical page, KV head). The calls take an
+ * entmaxkv_config whose kv_dtype is one of the code types below; the other
+ * fields and their limits are those of the 16- and 32-bit cache.
+ */
+#define ENTMAXKV_I8   2   /* signed whole numbers -127..127          */
+#define ENTMAXKV_E4M3 3   /* 4 exponent, 3 mantissa bits, finite, <= 448 */
+
+/*
+ * Caller-owned device buffers, row-major:
+ *   k_pool, v_pool    [num_phys_pages][num_kv_heads][page_size][head_dim] codes,
+ *                     from a 16-byte boundary
+ *   k_scale, v_scale  [num_phys_pages][num_kv_heads] float32
+ *   block_table       [max_seqs][max_pages_per_seq] int32
+ *   seq_lens          [max_seqs] int32: tokens of each sequence, those of the
+ *                     step under way included (entmaxkv_plan_pages counts
+ *                     them in before append and attend run)
+ *   status            one uint32 of ENTMAXKV_DEV_* bits (may be NULL)
+ */
+typedef struct {
+  void* k_pool;
+  void* v_pool;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  uint32_t* status;
+} entmaxkv_q8_cache;
+
+/*
+ * bfloat16 rows of the new tokens: element (token, head, i) is at
+ * data[token * token_stride + head * head_stride + i]. data starts on a
+ * 16-byte boundary; both strides are multiples of 8 elements, and positive
+ * where the call writes the rows. Slices of one projection's output fit.
+ */
+typedef struct {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} entmaxkv_rows;
+
+/*
+ * A batch of ragged rows (device arrays): slot b is sequence row seq_ids[b]
+ * (b itself when seq_ids is NULL) and owns rows start[b] .. start[b] + count[b]
+ * - 1 of `total`: its last count[b] tokens. count[b] = 0 is an idle slot (its
+ * seq_ids entry is not looked at). Slots are distinct sequences and their rows
+ * do not overlap. max_count bounds count[b]. Rows that belong to no slot are
+ * neither read nor written.
+ */
+typedef struct {
+  const int32_t* seq_ids;
+  const int32_t* start;
+  const int32_t* count;
+  int32_t n_seqs;
+  int32_t total;
+  int32_t max_count;
+} entmaxkv_batch;
+
+/*
+ * Pages for n_new[b] >= 0 more tokens of each slot's sequence, from a free list
+ * on the device. Works for any cache of this library: it reads and writes the
+ * block table and the lengths only. Of cfg it uses page_size, max_seqs,
+ * max_pages_per_seq and num_phys_pages.
+ * Slot b needs ceil((L+n)/P) - ceil(L/P) pages (L = seq_lens of its row). Slots
+ * are taken in order, and a slot is admitted while the sum of the needs up to
+ * and including its own is at most *free_count: the first that does not fit
+ * stops those behind it. A slot with a bad row, a negative n_new or more tokens
+ * than its block-table row holds is refused alone. Refusals raise
+ * ENTMAXKV_DEV_CAPACITY, _BAD_SEQ_ID or _BAD_BATCH. The i-th page handed out is
+ * free_pages[*free_count - 1 - i].
+ *   block_table   (in/out) the admitted slots' new entries are written
+ *   seq_lens      lengths before the step
+ *   free_pages    [num_phys_pages] a stack of free physical pages (read only)
+ *   free_count    its height; free_count_out its height afterwards
+ *   lens_out      [max_seqs] the admitted slots' rows get L + n (NULL: not
+ *                 written, for caches whose append counts the tokens itself)
+ *   start, count  [n_seqs] the batch's rows: start is the running sum of
+ *                 n_new, count is n_new, or 0 for a refused slot
+ *   positions     [total] each new token's position in its sequence
+ *   slots         [total] int64: physical page * page_size + offset;
+ *                 positions and slots of a refused slot's tokens are -1, and
+ *                 entries past the last token are left as they were
+ * free_count_out may be free_count and lens_out may be seq_lens. positions and
+ * slots may be NULL. n_seqs = 0 queues nothing and leaves every output alone.
+ */
+int32_t entmaxkv_plan_pages(const entmaxkv_config* cfg, int32_t* block_table, const int32_t* seq_lens,
+                            uint32_t* status, const int32_t* seq_ids, const int32_t* n_new,
+                            int32_t n_seqs, int32_t total, const int32_t* free_pages,
+                            const int32_t* free_count, int32_t* free_count_out, int32_t* lens_out,
+                            int32_t* start, int32_t* count, int32_t* positions, int64_t* slots,
+                            void* stream);
+
+/*
+ * Give the pages of n_seqs sequences back: each row's pages go on the free
+ * list, last page first (so that planning the same length again hands out the
+ * same pages in the same order), and its length becomes 0. Entries outside
+ * [0, num_phys_pages) are flagged and dropped; a list that would pass
+ * num_phys_pages raises ENTMAXKV_DEV_CAPACITY and takes no more.
+ */
+int32_t entmaxkv_release_pages(const entmaxkv_config* cfg, const int32_t* block_table, int32_t* seq_lens,
+                               uint32_t* status, const int32_t* seq_ids, int32_t n_seqs,
+                               int32_t* free_pages, int32_t* free_count, void* stream);
+
+/*
+ * Write the batch's new tokens (the last count[b] of each sequence) into their
+ * pages as codes. For each touched (page, KV head), K and V apart:
+ *   s' = max(amax / c, 2^-96, s), amax over the page's new values, c = 127 or
+ *        448, s the present scale if the page held tokens before (else 0);
+ *   a new value x becomes the code nearest to the exact x / s', ties to even;
+ *   a code v held before becomes the code nearest to the exact v * r, where
+ *        r = s / s' rounded to float32 (nothing changes while s' = s).
+ * Infinities are stored as the largest code of their sign and NaN as 0, both
+ * outside amax, and raise ENTMAXKV_DEV_NONFINITE. seq_lens is not changed.
+ *   k, v  bfloat16 rows, num_kv_heads heads
+ */
+int32_t entmaxkv_append_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache,
+                           const entmaxkv_batch* batch, const entmaxkv_rows* k, const entmaxkv_rows* v,
+                           void* stream);
+
+/*
+ * Copy tokens out of the cache as bfloat16 (code * scale, rounded to nearest):
+ * slot b's rows are tokens first[b] .. first[b] + count[b] - 1 of its sequence.
+ * A slot that asks for tokens outside [0, seq_lens) is flagged BAD_BATCH and
+ * skipped. With head_stride = T*d and token_stride = d the rows are laid out
+ * as entmaxkv_append takes them, for a move into a 16-bit cache.
+ */
+int32_t entmaxkv_read_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache,
+                         const entmaxkv_batch* batch, const int32_t* first, const entmaxkv_rows* k,
+                         const entmaxkv_rows* v, void* stream);
+
+/*
+ * How attend_q8 scores and masks. Row i of a slot (0 <= i < count) is the token
+ * at position x = seq_lens - count + i, and key j is seen by it when
+ *   max(x - window + 1 (window > 0), first_key[row]) <= j <= x,  or  j < prefix[slot].
+ * Its score for query head h is s = scale * q.k; with softcap > 0, s becomes
+ * softcap * tanh(s / softcap); with slopes, slopes[h] * |x - j| is taken off.
+ *   scale      0: 1/sqrt(head_dim)
+ *   softcap    0: none
+ *   window     0: none
+ *   slopes     (device) [Hq] float32, or NULL
+ *   prefix     (device) [n_seqs] int32 tokens of a prefix that every row sees
+ *              (at most the sequence's length counts), or NULL
+ *   first_key  (device) [total] int32 first key of each row (the start of its
+ *              document), or NULL
+ */
+typedef struct {
+  float scale;
+  float softcap;
+  int32_t window;
+  const float* slopes;
+  const int32_t* prefix;
+  const int32_t* first_key;
+} entmaxkv_score;
+
+/* Bytes of device workspace entmaxkv_attend_q8 needs; 0 for invalid arguments. */
+size_t entmaxkv_attend_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, int32_t total,
+                                    int32_t max_count, float alpha);
+
+/*
+ * Attention of the batch's rows over their sequences in the cache.
+ *   alpha = 1  softmax, any count: o = sum_j softmax(s)_j v_j; tau gets log sum exp(s)
+ *   alpha > 1  alpha-entmax, max_count = 1: z = (alpha-1) s,
+ *              p_j = [z_j - tau]_+^{1/(alpha-1)}, sum p = 1
+ *   q     bfloat16 rows, Hq heads (head h reads KV head h / group)
+ *   out   bfloat16 rows, Hq heads; a row that sees no key gets 0
+ *   tau   [total][Hq] float32, or NULL; NaN for a row that sees no key
+ *   score may be NULL (all defaults)
+ *   workspace  (device) at least entmaxkv_attend_q8_workspace(...) bytes,
+ *              256-byte aligned, contents are scratch; not to be shared by
+ *              calls that may run at the same time
+ * Products and sums are float32; before they meet V, weights are rounded to
+ * 11 bits, or to 2^-24 of the largest weight of their page where that is more. The order of every sum is
+ * fixed by the arguments and the device, so equal calls give equal bits.
+ * Rows of a slot with a bad row or batch entry are left as they were.
+ */
+int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache,
+                           const entmaxkv_batch* batch, const entmaxkv_rows* q,
+                           const entmaxkv_score* score, float alpha, void* workspace,
+                           size_t workspace_bytes, const entmaxkv_rows* out, float* tau, void* stream);
 
 #ifdef __cplusplus
 }

@@ -17,6 +17,8 @@ Modules:
              the normalisation solve for τ̂, top-k and Gaussian selection.
   decode  -- one decode step per (sequence, KV head): selection, sparse
              entmax attention, τ, dropped mass δ, support recall.
+  q8      -- the 8-bit paged cache: page planning, quantising append,
+             attention with its score forms and masks.
 
 Pins: the pages print no worked example and no numeric value for τ, τ̂, δ,
 recall or outputs on any input, so no function here is checked against a
@@ -25,4 +27,4 @@ special cases, brute force on small inputs and the invariants the pages
 state; ``tests/test_oracle_*.py`` hold those pins.
 """
 
-from . import entmax, pages, decode  # noqa: F401
+from . import entmax, pages, decode, q8  # noqa: F401

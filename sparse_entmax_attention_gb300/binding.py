@@ -19,7 +19,7 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libentmaxkv.so")
 
-F32, BF16 = 0, 1
+F32, BF16, I8, E4M3 = 0, 1, 2, 3
 POLICY_FULL, POLICY_TOPK, POLICY_GAUSSIAN, POLICY_SOFTMAX, POLICY_SOFTMAX_TOPK = 0, 1, 2, 3, 4
 POLICIES = {"full": POLICY_FULL, "topk": POLICY_TOPK, "gaussian": POLICY_GAUSSIAN,
             "softmax": POLICY_SOFTMAX, "softmax_topk": POLICY_SOFTMAX_TOPK}
@@ -27,6 +27,7 @@ FLAG_DENSE_V, FLAG_EXACT_DELTA, FLAG_EXPIRE_WAITS = 0x1, 0x2, 0x100
 DELTA_ZERO, DELTA_CERTIFIED, DELTA_MODEL, DELTA_EXACT = 0, 1, 2, 3
 DEV_BAD_PAGE_TABLE, DEV_CAPACITY, DEV_TAUHAT_NOCONV = 0x1, 0x2, 0x4
 DEV_CAND_OVERFLOW, DEV_TAU_NOCONV, DEV_BAD_SEQ_ID, DEV_TIMEOUT = 0x8, 0x10, 0x20, 0x40
+DEV_BAD_BATCH, DEV_NONFINITE = 0x80, 0x100
 
 # Symbols the header declares (kept in step with include/entmaxkv.h by a test).
 EXPORTS = ("entmaxkv_version", "entmaxkv_status_string", "entmaxkv_append",
@@ -34,7 +35,9 @@ EXPORTS = ("entmaxkv_version", "entmaxkv_status_string", "entmaxkv_append",
            "entmaxkv_workspace_layout", "entmaxkv_noalloc_scratch_bytes",
            "entmaxkv_decode_softmax_noalloc", "entmaxkv_workspace_bytes_flags",
            "entmaxkv_delta_kind", "entmaxkv_read_status", "entmaxkv_gaussian_alpha_supported",
-           "entmaxkv_moment_fit_eval")
+           "entmaxkv_moment_fit_eval", "entmaxkv_plan_pages", "entmaxkv_release_pages",
+           "entmaxkv_append_q8", "entmaxkv_read_q8", "entmaxkv_attend_q8_workspace",
+           "entmaxkv_attend_q8")
 STAGE_EVENTS = 6
 STAGES = ("clear", "score", "select", "pass_a", "pass_b")
 
@@ -62,6 +65,28 @@ class WorkspaceView(ctypes.Structure):
                 ("page_zmax", ctypes.c_size_t),
                 ("cap_pages", ctypes.c_int32), ("splits", ctypes.c_int32),
                 ("total", ctypes.c_size_t), ("z_scores", ctypes.c_size_t)]
+
+
+class Q8CacheView(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
+class RowsView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class BatchView(ctypes.Structure):
+    _fields_ = [("seq_ids", ctypes.c_void_p), ("start", ctypes.c_void_p), ("count", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("total", ctypes.c_int32), ("max_count", ctypes.c_int32)]
+
+
+class ScoreView(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p), ("first_key", ctypes.c_void_p)]
 
 
 _lib = None
@@ -107,6 +132,21 @@ def lib() -> ctypes.CDLL:
     L.entmaxkv_workspace_layout.restype = i32
     L.entmaxkv_workspace_layout.argtypes = [ctypes.POINTER(Config), i32, i32, i32,
                                             ctypes.POINTER(WorkspaceView)]
+    cfg_p, q8_p = ctypes.POINTER(Config), ctypes.POINTER(Q8CacheView)
+    bat_p, row_p = ctypes.POINTER(BatchView), ctypes.POINTER(RowsView)
+    L.entmaxkv_plan_pages.restype = i32
+    L.entmaxkv_plan_pages.argtypes = [cfg_p, vp, vp, vp, vp, vp, i32, i32] + [vp] * 9
+    L.entmaxkv_release_pages.restype = i32
+    L.entmaxkv_release_pages.argtypes = [cfg_p, vp, vp, vp, vp, i32, vp, vp, vp]
+    L.entmaxkv_append_q8.restype = i32
+    L.entmaxkv_append_q8.argtypes = [cfg_p, q8_p, bat_p, row_p, row_p, vp]
+    L.entmaxkv_read_q8.restype = i32
+    L.entmaxkv_read_q8.argtypes = [cfg_p, q8_p, bat_p, vp, row_p, row_p, vp]
+    L.entmaxkv_attend_q8_workspace.restype = sz
+    L.entmaxkv_attend_q8_workspace.argtypes = [cfg_p, i32, i32, i32, f32]
+    L.entmaxkv_attend_q8.restype = i32
+    L.entmaxkv_attend_q8.argtypes = [cfg_p, q8_p, bat_p, row_p, ctypes.POINTER(ScoreView), f32, vp, sz,
+                                     row_p, vp, vp]
     _lib = L
     return L
 
@@ -400,3 +440,344 @@ def moment_fit_eval(alpha: float, order: int, t):
     _check(lib().entmaxkv_moment_fit_eval(float(alpha), int(order), ta.ctypes.data_as(ctypes.c_void_p),
                                           int(ta.size), out.ctypes.data_as(ctypes.c_void_p)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# The 8-bit paged cache: plan, append, attend.
+
+_CODES = {torch.int8: I8, torch.float8_e4m3fn: E4M3}
+
+
+def _need(ok, what):
+    if not ok:
+        raise EntmaxKVError(what)
+
+
+def _dev_i32(t, shape, device, name):
+    _need(t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape and t.device == device,
+          f"{name}: a contiguous int32 tensor of shape {shape} on {device} is wanted")
+
+
+def _q8_call(device, stream, fn, *args):
+    """fn(*args, stream) on the tensors' device, whichever device is current."""
+    if torch.cuda.current_device() == device.index:
+        s = stream if stream is not None else torch.cuda.current_stream(device)
+        code = fn(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            s = stream if stream is not None else torch.cuda.current_stream(device)
+            code = fn(*args, s.cuda_stream)
+    if code:
+        _check(code)
+
+
+def _rows(t, shape, device, name):
+    """entmaxkv_rows of a [tokens, heads, d] bf16 tensor (its first two strides are free)."""
+    _need(t.dtype == torch.bfloat16 and tuple(t.shape) == shape and t.device == device,
+          f"{name}: a bfloat16 tensor of shape {shape} on {device} is wanted")
+    st = t.stride()
+    _need(st[2] == 1 or shape[2] == 1, f"{name}: the head dimension must be contiguous")
+    ts, hs = st[0], st[1]
+    if shape[0] == 1:
+        ts = max(8, shape[1] * shape[2])
+    if shape[1] == 1:
+        hs = max(8, shape[2])
+    return RowsView(t.data_ptr(), ts, hs)
+
+
+class PageTable:
+    """A block table and lengths alone, for planning pages of caches kept elsewhere."""
+
+    def __init__(self, block_table, seq_lens, page_size, num_phys_pages, status=None):
+        self.device = block_table.device
+        max_seqs, max_pages = block_table.shape
+        _dev_i32(block_table, (max_seqs, max_pages), self.device, "block_table")
+        _dev_i32(seq_lens, (max_seqs,), self.device, "seq_lens")
+        self.cfg = Config(1, 1, 64, page_size, max_seqs, max_pages, num_phys_pages, I8)
+        self.block_table, self.seq_lens = block_table, seq_lens
+        self.status = status if status is not None else torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def device_status(self) -> int:
+        return int(self.status.item()) & 0xffffffff
+
+
+class PagePool:
+    """A stack of free physical pages on the device: free_pages[0 .. free_count - 1].
+    PagePool.full(n, device) starts with all n pages, page 0 handed out first."""
+
+    def __init__(self, free_pages, free_count):
+        self.free_pages, self.free_count = free_pages, free_count
+        _dev_i32(free_pages, (free_pages.numel(),), free_pages.device, "free_pages")
+        _dev_i32(free_count, (1,), free_pages.device, "free_count")
+
+    @classmethod
+    def full(cls, num_phys_pages, device="cuda"):
+        return cls(torch.arange(num_phys_pages - 1, -1, -1, dtype=torch.int32, device=device),
+                   torch.full((1,), num_phys_pages, dtype=torch.int32, device=device))
+
+
+class Batch:
+    """Rows of a ragged batch (entmaxkv_batch): slot b owns rows start[b] .. start[b] + count[b] - 1
+    of `total`, the last count[b] tokens of sequence seq_ids[b] (b without seq_ids)."""
+
+    def __init__(self, start, count, total, max_count, seq_ids=None):
+        n = start.shape[0]
+        _dev_i32(start, (n,), start.device, "start")
+        _dev_i32(count, (n,), start.device, "count")
+        if seq_ids is not None:
+            _dev_i32(seq_ids, (n,), start.device, "seq_ids")
+        self.start, self.count, self.seq_ids = start, count, seq_ids
+        self.total, self.max_count, self.device = int(total), int(max_count), start.device
+        self.view = BatchView(None if seq_ids is None else seq_ids.data_ptr(), start.data_ptr(), count.data_ptr(),
+                              n, self.total, self.max_count)
+
+    @classmethod
+    def uniform(cls, n_seqs, count=1, seq_ids=None, device="cuda"):
+        """count rows of every sequence, one sequence behind the other."""
+        start = torch.arange(0, n_seqs * count, count, dtype=torch.int32, device=device)
+        return cls(start, torch.full_like(start, count), n_seqs * count, count, seq_ids)
+
+
+@dataclass
+class PagePlan:
+    """What plan_pages writes: the batch's rows, positions and slots of its tokens."""
+    start: torch.Tensor
+    count: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+
+    def batch(self, max_count, seq_ids=None) -> Batch:
+        return Batch(self.start, self.count, self.positions.shape[0], max_count, seq_ids)
+
+
+def alloc_plan(n_seqs, total, device="cuda") -> PagePlan:
+    i32 = dict(dtype=torch.int32, device=device)
+    return PagePlan(torch.zeros(n_seqs, **i32), torch.zeros(n_seqs, **i32), torch.full((total,), -1, **i32),
+                    torch.full((total,), -1, dtype=torch.int64, device=device))
+
+
+def plan_pages(cache, pool: PagePool, n_new, plan: PagePlan, seq_ids=None, advance=True, lens_out=None,
+               count_out=None, stream=None) -> PagePlan:
+    """entmaxkv_plan_pages: pages, positions and slots for n_new[b] more tokens of each sequence.
+
+    cache: a QuantCache, a PagedCache or a PageTable. With advance the lengths count the new
+    tokens in (into lens_out when given, else in place); a PagedCache, whose append counts them
+    itself, is planned with advance=False. The free list's new height goes to count_out, or in place.
+    """
+    n, dev = n_new.shape[0], cache.block_table.device
+    _dev_i32(n_new, (n,), dev, "n_new")
+    _need(plan.start.shape[0] == n and plan.start.device == dev, "plan: allocated for another batch")
+    _need(pool.free_pages.numel() >= cache.cfg.num_phys_pages and pool.free_pages.device == dev,
+          "pool: a free list of num_phys_pages entries is wanted")
+    if seq_ids is not None:
+        _dev_i32(seq_ids, (n,), dev, "seq_ids")
+    if lens_out is not None:
+        _dev_i32(lens_out, (cache.cfg.max_seqs,), dev, "lens_out")
+    if count_out is not None:
+        _dev_i32(count_out, (1,), dev, "count_out")
+    lens = None
+    if advance:
+        lens = (cache.seq_lens if lens_out is None else lens_out).data_ptr()
+    _q8_call(dev, stream, lib().entmaxkv_plan_pages, cache.cfg, cache.block_table.data_ptr(),
+             cache.seq_lens.data_ptr(), cache.status.data_ptr(), None if seq_ids is None else seq_ids.data_ptr(),
+             n_new.data_ptr(), n, plan.positions.shape[0], pool.free_pages.data_ptr(), pool.free_count.data_ptr(),
+             (pool.free_count if count_out is None else count_out).data_ptr(), lens, plan.start.data_ptr(),
+             plan.count.data_ptr(), plan.positions.data_ptr(), plan.slots.data_ptr())
+    return plan
+
+
+def release_pages(cache, pool: PagePool, seq_ids, stream=None):
+    """entmaxkv_release_pages: the sequences' pages go back to the pool, their lengths become 0."""
+    dev = cache.block_table.device
+    _dev_i32(seq_ids, (seq_ids.shape[0],), dev, "seq_ids")
+    _need(pool.free_pages.numel() >= cache.cfg.num_phys_pages and pool.free_pages.device == dev,
+          "pool: a free list of num_phys_pages entries is wanted")
+    _q8_call(dev, stream, lib().entmaxkv_release_pages, cache.cfg, cache.block_table.data_ptr(),
+             cache.seq_lens.data_ptr(), cache.status.data_ptr(), seq_ids.data_ptr(), seq_ids.shape[0],
+             pool.free_pages.data_ptr(), pool.free_count.data_ptr())
+
+
+class QuantCache:
+    """Caller-owned paged KV cache in 8 bits (torch memory): codes in int8 or float8_e4m3fn and a
+    float32 scale for the K and one for the V rows of each (physical page, KV head). seq_lens
+    counts the tokens of the step under way (plan_pages advances it)."""
+
+    def __init__(self, num_kv_heads, group, head_dim, page_size, max_seqs, max_pages_per_seq, num_phys_pages,
+                 code_dtype=torch.int8, device="cuda"):
+        shape = (num_phys_pages, num_kv_heads, page_size, head_dim)
+        pools = [torch.zeros(shape, dtype=torch.int8, device=device).view(code_dtype) for _ in range(2)]
+        scales = [torch.zeros(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
+        self._init(*pools, *scales, torch.zeros(max_seqs, max_pages_per_seq, dtype=torch.int32, device=device),
+                   torch.zeros(max_seqs, dtype=torch.int32, device=device), group, None)
+
+    @classmethod
+    def of(cls, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, group, status=None):
+        """The cache over tensors the caller already has."""
+        c = cls.__new__(cls)
+        c._init(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, group, status)
+        return c
+
+    def _init(self, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, group, status):
+        dev, shape = k_pool.device, tuple(k_pool.shape)
+        _need(k_pool.dtype in _CODES, "k_pool: int8 or float8_e4m3fn codes are wanted")
+        _need(v_pool.dtype == k_pool.dtype and tuple(v_pool.shape) == shape and len(shape) == 4
+              and v_pool.device == dev and k_pool.is_contiguous() and v_pool.is_contiguous(),
+              "k_pool, v_pool: contiguous [pages, KV heads, page size, head dim] of one type are wanted")
+        for t in (k_scale, v_scale):
+            _need(t.dtype == torch.float32 and tuple(t.shape) == shape[:2] and t.is_contiguous() and t.device == dev,
+                  "k_scale, v_scale: contiguous float32 [pages, KV heads] are wanted")
+        max_seqs, max_pages = block_table.shape
+        _dev_i32(block_table, (max_seqs, max_pages), dev, "block_table")
+        _dev_i32(seq_lens, (max_seqs,), dev, "seq_lens")
+        self.device, self.code_dtype = dev, k_pool.dtype
+        self.k_pool, self.v_pool, self.k_scale, self.v_scale = k_pool, v_pool, k_scale, v_scale
+        self.block_table, self.seq_lens = block_table, seq_lens
+        self.status = status if status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
+        self.cfg = Config(shape[1], group, shape[3], shape[2], max_seqs, max_pages, shape[0], _CODES[k_pool.dtype])
+        self.view = Q8CacheView(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                block_table.data_ptr(), seq_lens.data_ptr(), self.status.data_ptr())
+
+    @property
+    def num_q_heads(self):
+        return self.cfg.num_kv_heads * self.cfg.group
+
+    def device_status(self) -> int:
+        return int(self.status.item()) & 0xffffffff
+
+
+def append_q8(cache: QuantCache, k, v, batch: Batch, stream=None):
+    """entmaxkv_append_q8: k, v [total, Hkv, d] bf16 (any token and head strides that are multiples
+    of 8): the last count[b] tokens of each sequence become codes."""
+    shape = (batch.total, cache.cfg.num_kv_heads, cache.cfg.head_dim)
+    _need(batch.device == cache.device, "batch: on another device than the cache")
+    kr, vr = _rows(k, shape, cache.device, "k"), _rows(v, shape, cache.device, "v")
+    _q8_call(cache.device, stream, lib().entmaxkv_append_q8, cache.cfg, cache.view, batch.view, kr, vr)
+
+
+def read_q8(cache: QuantCache, first, batch: Batch, k=None, v=None, stream=None):
+    """entmaxkv_read_q8: tokens first[b] .. first[b] + count[b] - 1 of each sequence as bf16 rows
+    [total, Hkv, d] in k and v (allocated when not given). Returns (k, v)."""
+    shape = (batch.total, cache.cfg.num_kv_heads, cache.cfg.head_dim)
+    _need(batch.device == cache.device, "batch: on another device than the cache")
+    _dev_i32(first, (batch.view.n_seqs,), cache.device, "first")
+    k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
+    kr, vr = _rows(k, shape, cache.device, "k"), _rows(v, shape, cache.device, "v")
+    _q8_call(cache.device, stream, lib().entmaxkv_read_q8, cache.cfg, cache.view, batch.view, first.data_ptr(), kr, vr)
+    return k, v
+
+
+@dataclass
+class AttendOutputs:
+    out: torch.Tensor  # [total, Hq, d] bf16
+    tau: torch.Tensor  # [total, Hq] float32: log-sum-exp (softmax) or the entmax threshold
+
+
+def alloc_attend_outputs(cache: QuantCache, batch: Batch) -> AttendOutputs:
+    Hq = cache.num_q_heads
+    return AttendOutputs(torch.zeros(batch.total, Hq, cache.cfg.head_dim, dtype=torch.bfloat16, device=cache.device),
+                         torch.zeros(batch.total, Hq, dtype=torch.float32, device=cache.device))
+
+
+def attend_workspace_bytes(cache: QuantCache, batch: Batch, alpha=1.0) -> int:
+    b = batch.view
+    return int(lib().entmaxkv_attend_q8_workspace(cache.cfg, b.n_seqs, b.total, b.max_count, float(alpha)))
+
+
+def alloc_attend_workspace(cache: QuantCache, batch: Batch, alpha=1.0):
+    n = attend_workspace_bytes(cache, batch, alpha)
+    if n == 0:
+        raise EntmaxKVError("invalid attention arguments for workspace sizing")
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)  # caching allocator: 256-B aligned
+
+
+def attend_q8(cache: QuantCache, q, batch: Batch, alpha=1.0, scale=0.0, softcap=0.0, slopes=None, window=0,
+              prefix=None, first_key=None, workspace=None, outputs: AttendOutputs | None = None,
+              stream=None) -> AttendOutputs:
+    """entmaxkv_attend_q8: q [total, Hq, d] bf16 against each row's sequence. alpha = 1 is softmax;
+    alpha > 1 is alpha-entmax, for one new token a sequence.
+
+    softcap: s becomes softcap * tanh(s / softcap). slopes: float32 [Hq], slopes[h] * distance is
+    taken off. window: keys seen back from the row's own. prefix: int32 [n_seqs], keys in front
+    that every row sees. first_key: int32 [total], where each row's document begins.
+    """
+    c, dev = cache.cfg, cache.device
+    Hq = c.num_kv_heads * c.group
+    shape = (batch.total, Hq, c.head_dim)
+    _need(batch.device == dev, "batch: on another device than the cache")
+    if outputs is None:
+        outputs = alloc_attend_outputs(cache, batch)
+    if workspace is None:
+        workspace = alloc_attend_workspace(cache, batch, alpha)
+    _need(workspace.device == dev, "workspace: on another device than the cache")
+    score = ScoreView(scale, softcap, window, None, None, None)
+    if slopes is not None:
+        _need(slopes.dtype == torch.float32 and tuple(slopes.shape) == (Hq,) and slopes.is_contiguous()
+              and slopes.device == dev, "slopes: contiguous float32 [Hq] is wanted")
+        score.slopes = slopes.data_ptr()
+    if prefix is not None:
+        _dev_i32(prefix, (batch.view.n_seqs,), dev, "prefix")
+        score.prefix = prefix.data_ptr()
+    if first_key is not None:
+        _dev_i32(first_key, (batch.total,), dev, "first_key")
+        score.first_key = first_key.data_ptr()
+    t = outputs.tau
+    if t is not None:
+        _need(t.dtype == torch.float32 and tuple(t.shape) == shape[:2] and t.is_contiguous() and t.device == dev,
+              "tau: contiguous float32 [total, Hq] is wanted")
+    _q8_call(dev, stream, lib().entmaxkv_attend_q8, cache.cfg, cache.view, batch.view,
+             _rows(q, shape, dev, "q"), score, float(alpha), workspace.data_ptr(),
+             workspace.numel() * workspace.element_size(), _rows(outputs.out, shape, dev, "out"),
+             None if t is None else t.data_ptr())
+    return outputs
+
+
+class QuantStep:
+    """One serving step over an 8-bit cache for n_seqs slots of up to max_count new tokens each:
+    plan pages, append, attend, captured once as a CUDA graph of the library's launches over fixed
+    buffers. Arguments as for attend_q8; prefix and first_key are fixed buffers too.
+
+    run(n_new, seq_ids, q, k, v): n_new and seq_ids int32 [n_seqs] (a slot with n_new 0 is idle),
+    q, k, v the new tokens' rows one slot behind the other, in the first sum(n_new) rows of at most
+    n_seqs * max_count. Rows past the last token, and those of refused slots, are left as they were.
+    Capturing launches nothing: the cache changes only on replay."""
+
+    def __init__(self, cache: QuantCache, pool: PagePool, n_seqs, max_count=1, alpha=1.0, **score):
+        dev, c = cache.device, cache.cfg
+        total, Hq = n_seqs * max_count, cache.num_q_heads
+        bf = dict(dtype=torch.bfloat16, device=dev)
+        self.cache, self.pool = cache, pool
+        self.n_new = torch.zeros(n_seqs, dtype=torch.int32, device=dev)
+        self.seq_ids = torch.zeros(n_seqs, dtype=torch.int32, device=dev)
+        self.q = torch.zeros(total, Hq, c.head_dim, **bf)
+        self.k = torch.zeros(total, c.num_kv_heads, c.head_dim, **bf)
+        self.v = torch.zeros_like(self.k)
+        self.plan = alloc_plan(n_seqs, total, dev)
+        self.batch = self.plan.batch(max_count, self.seq_ids)
+        self.outputs = alloc_attend_outputs(cache, self.batch)
+        self.workspace = alloc_attend_workspace(cache, self.batch, alpha)
+        self._score = dict(score, alpha=alpha)
+
+        def launches():
+            plan_pages(cache, pool, self.n_new, self.plan, seq_ids=self.seq_ids)
+            append_q8(cache, self.k, self.v, self.batch)
+            attend_q8(cache, self.q, self.batch, workspace=self.workspace, outputs=self.outputs, **self._score)
+
+        with torch.cuda.device(dev):
+            launches()  # every slot idle: first-launch set-up outside the capture
+            torch.cuda.synchronize(dev)
+            self.graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(self.graph):
+                launches()
+
+    def run(self, n_new, seq_ids, q, k, v) -> AttendOutputs:
+        """Device tensors in; the outputs (and plan) stay on the device."""
+        rows = q.shape[0]
+        _need(rows <= self.q.shape[0], "more rows than the step was made for")
+        self.n_new.copy_(n_new, non_blocking=True)
+        self.seq_ids.copy_(seq_ids, non_blocking=True)
+        self.q[:rows].copy_(q, non_blocking=True)
+        self.k[:rows].copy_(k, non_blocking=True)
+        self.v[:rows].copy_(v, non_blocking=True)
+        self.graph.replay()
+        return self.outputs

@@ -21,7 +21,7 @@ constexpr int kLayoutBlocks = 2048;
 constexpr int kMaxDevices = 64;
 static std::atomic<int> g_sms[kMaxDevices];
 
-static int device_sms() {
+int device_sms() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
   int n = g_sms[dev].load(std::memory_order_relaxed);
@@ -32,7 +32,7 @@ static int device_sms() {
 }
 
 // The driver's tensor-map encoder, looked up once through the runtime.
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static std::atomic<void*> fn{nullptr};
   void* f = fn.load(std::memory_order_acquire);
   if (f) return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);

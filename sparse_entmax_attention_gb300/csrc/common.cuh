@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -662,6 +663,11 @@ __device__ __forceinline__ void block_page_range(const DecodeArgs& a, int s, int
 
 // Host: the fits for order β (cached); 0 when they pass their accuracy check.
 int moment_fit_for(float beta, MomentFit* out);
+
+// Host: SMs of the current device (0 when the query fails) and the driver's
+// tensor-map encoder (null when it cannot be found).
+int device_sms();
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Launchers (one translation unit each).
 cudaError_t launch_append(const AppendArgs& a, int kv_dtype, cudaStream_t st);

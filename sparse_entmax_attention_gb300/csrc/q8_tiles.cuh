@@ -1,0 +1,127 @@
+// q8_tiles.cuh -- pieces of the kernels that stream 8-bit pages through shared
+// memory: the slab layout, K and V fragments, query fragments. Internal.
+#pragma once
+
+#include "q8.cuh"
+
+namespace ekv {
+
+// A slab of P rows of D codes arrives by a swizzled tensor copy (128- or
+// 64-byte swizzle for D = 128 or 64): byte offset of 16-byte chunk ch of row t.
+// The copies below and ldmatrix then touch eight different 16-byte banks a
+// phase.
+template <int D>
+__device__ __forceinline__ uint32_t slab_off(int t, int ch) {
+  if constexpr (D == 128) return (uint32_t)(t * 128 + ((ch ^ (t & 7)) << 4));
+  return (uint32_t)(t * 64 + ((ch ^ ((t >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr));
+  return r;
+}
+
+// A query row as mma B fragments in halves: lane (n = lane/4, c = lane%4) holds
+// dims (D/4)·c + 4ks .. +3 of row n, the order in which a lane's K bytes lie.
+// A power of two brings the row's largest value into [2^13, 2^14), so bf16
+// values down to 2^-27 of it are exact as halves; inv is that power's inverse.
+// p = null: a row of zeros.
+template <int D>
+__device__ __forceinline__ void q_half_frag(const __nv_bfloat16* p, int lane, uint32_t (&b)[D / 16][2], float& inv) {
+  const int c = lane & 3;
+  uint2 w[D / 16];
+  uint32_t m = 0u;
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    w[ks] = p ? *reinterpret_cast<const uint2*>(p + (D / 4) * c + 4 * ks) : make_uint2(0u, 0u);
+    m = max(m, max((w[ks].x & 0x7fffu), (w[ks].x >> 16) & 0x7fffu));
+    m = max(m, max((w[ks].y & 0x7fffu), (w[ks].y >> 16) & 0x7fffu));
+  }
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  int e = (int)(m >> 7) - 127;
+  if (m >= 0x7f80u) e = 13;  // infinities and NaN stay what they are
+  e = max(e, -100);
+  const float f = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+  inv = __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const __half2 x = __floats2half2_rn(bf_lo(w[ks].x) * f, bf_hi(w[ks].x) * f);
+    const __half2 y = __floats2half2_rn(bf_lo(w[ks].y) * f, bf_hi(w[ks].y) * f);
+    b[ks][0] = *reinterpret_cast<const uint32_t*>(&x);
+    b[ks][1] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+// acc[nt] = codes of 16 tokens (rows from token t16) · query rows 8nt..8nt+7:
+// lane l holds tokens l/4 and l/4 + 8 of rows 2(l%4), 2(l%4) + 1.
+template <bool I8, int D, int NT>
+__device__ __forceinline__ void k_dot(uint32_t slab, int t16, int lane, const uint32_t (&bq)[NT][D / 16][2],
+                                      float (&acc)[NT][4]) {
+  const int r = lane >> 2, c = lane & 3;
+  constexpr int CH = D / 64;  // 16-byte chunks a lane holds of a row
+  uint4 x[2][CH];
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    x[0][j] = lds128(slab + slab_off<D>(t16 + r, CH * c + j));
+    x[1][j] = lds128(slab + slab_off<D>(t16 + r + 8, CH * c + j));
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const int j = ks >> 2, w = ks & 3;
+    const uint32_t w0 = w == 0 ? x[0][j].x : w == 1 ? x[0][j].y : w == 2 ? x[0][j].z : x[0][j].w;
+    const uint32_t w1 = w == 0 ? x[1][j].x : w == 1 ? x[1][j].y : w == 2 ? x[1][j].z : x[1][j].w;
+    uint32_t a0, a1, a2, a3;
+    codes_half<I8, false>(w0, a0, a2);
+    codes_half<I8, false>(w1, a1, a3);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], a0, a1, a2, a3, bq[nt][ks][0], bq[nt][ks][1]);
+  }
+}
+
+// tmp[mt][nt] += V^T of 16 tokens (from t16) · p: b[nt] are p's B fragments.
+// Lane l's sums are of dims 16mt + 2(l/4) (elements 0, 1) and the next one
+// (elements 2, 3), for rows 2(l%4) and 2(l%4) + 1.
+template <bool I8, int D, int NT>
+__device__ __forceinline__ void v_dot(uint32_t slab, int t16, int lane, const uint32_t (&b)[NT][2],
+                                      float (&tmp)[D / 16][NT][4]) {
+  const int t = t16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+  for (int mt = 0; mt < D / 16; mt += 2) {
+    uint32_t w0, w1, w2, w3;
+    ldsm_x4_trans(w0, w1, w2, w3, slab + slab_off<D>(t, mt + (lane >> 4)));
+    uint32_t a0, a1, a2, a3;
+    codes_half<I8, true>(w0, a0, a1);
+    codes_half<I8, true>(w1, a2, a3);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mma_f16(tmp[mt][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+    codes_half<I8, true>(w2, a0, a1);
+    codes_half<I8, true>(w3, a2, a3);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) mma_f16(tmp[mt + 1][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+  }
+}
+
+// What a lane knows of the two rows of an mma column pair. Scores come in
+// units of 1/unit: unit = log2(e) for a softmax in base 2, α − 1 for entmax.
+struct Q8Row {
+  float cs;     // score per unit of the fp32 dot product (times the page's K scale); without the cap's unit
+  float slope;  // times unit
+  int pos, lo;  // position, first key seen
+};
+
+// Score of key j for a row; NaN-free for finite codes.
+__device__ __forceinline__ float q8_score(float dot, const Q8Row& r, float ks, int j, const Q8Score& sc, bool general,
+                                          float unit) {
+  float s = dot * (r.cs * ks);
+  if (general) {
+    if (sc.cap > 0.0f) s = soft_cap(s, sc.cap, sc.inv_cap) * unit;
+    s -= r.slope * (float)abs(r.pos - j);
+  }
+  return s;
+}
+__device__ __forceinline__ bool q8_sees(const Q8Row& r, int j, int pre) { return (j >= r.lo && j <= r.pos) || j < pre; }
+
+}  // namespace ekv
