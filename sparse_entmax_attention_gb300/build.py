@@ -21,7 +21,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libentmaxkv.so")
 
 SOURCES = ["api.cu", "append.cu", "score.cu", "select.cu", "decode.cu", "softmax.cu", "noalloc.cu",
-           "moment_fit.cu", "q8_api.cu", "pages.cu", "q8_append.cu", "q8_attend.cu", "q8_entmax.cu"]
+           "moment_fit.cu", "q8_api.cu", "pages.cu", "q8_append.cu", "q8_attend.cu", "q8_chunk.cu",
+           "q8_entmax.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

@@ -135,13 +135,13 @@ struct Q8Span {
   int pre, npre, wfirst, npages, T;
   __device__ __forceinline__ int page(int t) const { return t < npre ? t : t - npre + wfirst; }
 };
-// The span of rows [r0, r0 + n) of slot b (first_key looked at for up to 64 rows).
+// The span of rows [r0, r0 + n) of slot b.
 __device__ __forceinline__ Q8Span q8_span(const Q8Cache& c, const Q8Score& sc, const Q8Slot& s, int b, int r0, int n) {
   Q8Span v;
   const int x0 = s.L - s.count + r0, end = x0 + n;  // positions [x0, end)
   v.pre = sc.prefix ? min(max(sc.prefix[b], 0), s.L) : 0;
   int lo = sc.window > 0 ? max(0, x0 - sc.window + 1) : 0;
-  if (sc.first_key && n <= 64) {
+  if (sc.first_key) {
     int fk = 0x7fffffff;
     for (int i = 0; i < n; ++i) fk = min(fk, sc.first_key[s.start + r0 + i]);
     lo = max(lo, fk);
@@ -180,6 +180,11 @@ cudaError_t launch_read_q8(const Q8Cache& c, const Q8Batch& b, const int32_t* fi
                            bool i8, cudaStream_t st);
 size_t attend_softmax_bytes(const entmaxkv_config& cfg, int n_seqs, int max_count);
 cudaError_t launch_attend_softmax(Q8AttendArgs a, bool i8, void* ws, int sms, cudaStream_t st);
+// Rows of a sequence up to which the streaming kernel answers a batch; with
+// more, a 128-row product tile is the better fit for every slot.
+constexpr int kStreamRows = 16;
+size_t attend_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total);
+cudaError_t launch_attend_chunk(const Q8AttendArgs& a, bool i8, void* ws, int sms, cudaStream_t st);
 size_t attend_entmax_bytes(const entmaxkv_config& cfg, int n_seqs);
 cudaError_t launch_attend_entmax(Q8AttendArgs a, bool i8, float alpha, void* ws, int sms, cudaStream_t st);
 // A pool as (dim, KV head · token, page) of bytes, in boxes of one slab.

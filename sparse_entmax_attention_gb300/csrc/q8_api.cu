@@ -51,6 +51,9 @@ static Q8Batch batch_of(const entmaxkv_batch* b) {
 static Q8Rows rows_of(const entmaxkv_rows* r) {
   return Q8Rows{static_cast<__nv_bfloat16*>(r->data), r->token_stride, r->head_stride};
 }
+static bool streams(const entmaxkv_config* c, int max_count) {
+  return (long long)max_count * c->group <= kStreamRows;
+}
 static int32_t code_of(cudaError_t e) { return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_ERR_CUDA; }
 
 }  // namespace ekv
@@ -126,7 +129,8 @@ static int check_attend(const entmaxkv_config* cfg, int n_seqs, int total, int m
 size_t entmaxkv_attend_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, int32_t total, int32_t max_count,
                                     float alpha) {
   if (check_attend(cfg, n_seqs, total, max_count, alpha)) return 0;
-  return alpha > 1.0f ? attend_entmax_bytes(*cfg, n_seqs) : attend_softmax_bytes(*cfg, n_seqs, max_count);
+  if (alpha > 1.0f) return attend_entmax_bytes(*cfg, n_seqs);
+  return streams(cfg, max_count) ? attend_softmax_bytes(*cfg, n_seqs, max_count) : attend_chunk_bytes(*cfg, n_seqs, total);
 }
 
 int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache, const entmaxkv_batch* batch,
@@ -160,8 +164,10 @@ int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* 
   a.out = rows_of(out);
   a.tau = tau;
   const bool i8 = cfg->kv_dtype == ENTMAXKV_I8;
-  return code_of(alpha > 1.0f ? launch_attend_entmax(a, i8, alpha, workspace, sms, (cudaStream_t)stream)
-                              : launch_attend_softmax(a, i8, workspace, sms, (cudaStream_t)stream));
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (alpha > 1.0f) return code_of(launch_attend_entmax(a, i8, alpha, workspace, sms, s));
+  return code_of(streams(cfg, batch->max_count) ? launch_attend_softmax(a, i8, workspace, sms, s)
+                                                : launch_attend_chunk(a, i8, workspace, sms, s));
 }
 
 }  // extern "C"

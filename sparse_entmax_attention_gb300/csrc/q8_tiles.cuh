@@ -124,4 +124,22 @@ __device__ __forceinline__ float q8_score(float dot, const Q8Row& r, float ks, i
 }
 __device__ __forceinline__ bool q8_sees(const Q8Row& r, int j, int pre) { return (j >= r.lo && j <= r.pos) || j < pre; }
 
+// Wait for a phase of an mbarrier for at most a second.
+__device__ __forceinline__ bool mbar_wait_second(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0, t;
+  asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t0));
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+    asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
+  } while (t - t0 < 1000000000ull);
+  return false;
+}
+
+// One row's answer from its sums.
+__device__ __forceinline__ float att_inv(float l) { return l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : CUDART_NAN_F); }
+__device__ __forceinline__ float att_lse(float m, float l) {
+  return l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : CUDART_NAN_F;
+}
+
 }  // namespace ekv
