@@ -22,6 +22,7 @@ LIB = os.path.join(HERE, "libentmaxkv.so")
 
 SOURCES = ["api.cu", "append.cu", "score.cu", "select.cu", "decode.cu", "softmax.cu", "noalloc.cu",
            "moment_fit.cu", "q8_api.cu", "pages.cu", "q8_append.cu", "q8_attend.cu", "q8_chunk.cu",
+           "q8_chunk_i8_d128.cu", "q8_chunk_i8_d64.cu", "q8_chunk_e4m3_d128.cu", "q8_chunk_e4m3_d64.cu",
            "q8_entmax.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]

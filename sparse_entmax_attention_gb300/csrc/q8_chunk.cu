@@ -1,56 +1,17 @@
-// q8_chunk.cu -- softmax attention of many new tokens a sequence over the 8-bit
-// paged cache (prompt chunks, mixed batches) on the fifth-generation tensor
-// cores.
-//
-// An item is 256 rows of one (slot, KV head): rows are (token, head of the
-// group), so a K/V tile serves the whole group. Per tile of 128 keys (the
-// pages of the item's span in order):
-//   S = Q·K^T          two 128×128 products (one per 128 rows), Q and the codes
-//                      as halves (both exact: a power of two per query row),
-//                      fp32 sums in tensor memory;
-//   t = S·ks·scale·log2 e (capped, biased, masked) + log2 vs, one row a thread;
-//   w = 2^{t − M + 8}  as halves into tensor memory over S, M a running bound of
-//                      the row's maximum that is moved when the maximum passes it
-//                      by 6: w ≤ 2^14, and weights down to 2^-32 of the largest
-//                      survive the rounding;
-//   O += w·codes       accumulated in tensor memory, rescaled when M moves.
-// The V scale rides in w, so Σp is Σ over pages of (Σ w)/vs, of unrounded w.
-//
-// Warps: 4 + 4 softmax (a thread a row), 4 converters (codes from L2 through
-// registers into swizzled half tiles, two stages), 1 that issues the products.
-// The two row halves take turns: while one is in its softmax the products of
-// the other run. All items' tiles form one line (KV head outermost) cut into
-// equal pieces for one block a multiprocessor; an item cut in two leaves
-// (M, Σp, O) pieces that a second kernel joins in the order of the line.
-#include "q8_tiles.cuh"
+// q8_chunk.cu -- the item list, the joining kernel and the launches of the
+// chunk attention (q8_chunk.cuh).
+#include "q8_chunk.cuh"
 
 namespace ekv {
 
-constexpr int kChunkThreads = 512;
-constexpr int kChunkRows = 256;
-constexpr int kChunkKeys = 128;
-constexpr int kChunkMaxBlocks = 256;
-constexpr float kLift = 8.0f;   // w = 2^{t − M + kLift}
-constexpr float kSlack = 6.0f;  // M moves when the row's maximum passes it by more
-
-struct ChunkItem {
-  int slot, rt;
-};
-struct ChunkArgs {
-  Q8AttendArgs a;
-  ChunkItem* items;
-  int* cum;        // [n_items + 1] tiles of one KV head before each item
-  int* n_items;
-  float* part_o;   // [blocks][2][256][D]
-  float2* part_ml; // [blocks][2][256]
-  int max_items, blocks;
-};
-
-// The span of item (slot, rt): its tokens' pages.
-__device__ __forceinline__ Q8Span chunk_span(const Q8AttendArgs& a, const Q8Slot& s, int b, int rt) {
-  const int t0 = rt * kChunkRows / a.c.G, t1 = min(s.count, (rt * kChunkRows + kChunkRows - 1) / a.c.G + 1);
-  return q8_span(a.c, a.sc, s, b, t0, t1 - t0);
-}
+template <>
+cudaError_t chunk_run<true, 128>(const ChunkArgs& g, cudaStream_t st);
+template <>
+cudaError_t chunk_run<true, 64>(const ChunkArgs& g, cudaStream_t st);
+template <>
+cudaError_t chunk_run<false, 128>(const ChunkArgs& g, cudaStream_t st);
+template <>
+cudaError_t chunk_run<false, 64>(const ChunkArgs& g, cudaStream_t st);
 
 // One block lists the items and the line: slots 1024 at a time, then the
 // round's items, a thread each.
@@ -100,495 +61,6 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(ChunkArgs g) {
     *g.n_items = items;
     g.cum[items] = tiles;
   }
-}
-
-// ---------------------------------------------------------------------------
-// tensor memory and products
-
-__device__ __forceinline__ void tm_alloc(uint32_t* out) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(out)) : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
-}
-__device__ __forceinline__ void tm_free(uint32_t base) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(base) : "memory");
-}
-__device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
-__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void tm_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
-}
-// 32 columns of the thread's lane.
-__device__ __forceinline__ void tm_ld32(uint32_t addr, float* v) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
-      : "memory");
-}
-
-// Shared-memory descriptors of a half tile with 128-byte swizzle. Rows of 64
-// halves (128 bytes) lie in groups of 8 (1024 bytes); a 128-wide tile is two
-// such halves, `half` bytes apart. Bits: address/16, leading and stride byte
-// offsets/16, version 1, swizzle 2 (128 bytes).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-  return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(stride >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
-}
-// D fp32, A and B halves; M = 128; B rows along K (mn = 0) or along N (mn = 1).
-__device__ __forceinline__ constexpr uint32_t instr_desc(int n, int mn) {
-  return (1u << 4) | ((uint32_t)mn << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
-
-// Byte offset of 16-byte chunk ch (8 halves) of row t in a tile of 128 rows.
-__device__ __forceinline__ uint32_t tile_off(int t, int ch) {
-  return (uint32_t)((ch >> 3) * 16384 + t * 128 + (((ch & 7) ^ (t & 7)) << 4));
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
-// A block's part of one item: `n` tiles from tile t0 of T.
-struct ChunkSeg {
-  int kvh, slot, rt, t0, n, T;
-  Q8Slot s;
-  Q8Span sp;
-};
-__device__ __forceinline__ ChunkSeg chunk_seg(const ChunkArgs& g, long long w, long long w_end, int S, int n_items) {
-  ChunkSeg x;
-  x.kvh = (int)(w / S);
-  const int off = (int)(w - (long long)x.kvh * S);
-  int lo = 0, hi = n_items - 1;  // the last item that begins at or before `off`
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (g.cum[m] <= off) lo = m;
-    else hi = m - 1;
-  }
-  const ChunkItem it = g.items[lo];
-  x.slot = it.slot;
-  x.rt = it.rt;
-  x.t0 = off - g.cum[lo];
-  x.T = g.cum[lo + 1] - g.cum[lo];
-  x.n = (int)min((long long)(x.T - x.t0), w_end - w);
-  x.s = q8_slot(g.a.c, g.a.b, x.slot, nullptr);
-  x.sp = chunk_span(g.a, x.s, x.slot, x.rt);
-  return x;
-}
-
-struct PageMeta {
-  float ks, lv, ivs;  // K scale, log2 of the V scale, its inverse
-  int key0;           // first key; beyond every key where there is no page
-};
-constexpr int kNoKey = 0x40000000;
-
-template <bool I8, int D, int P>
-__global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
-  pdl_enter();
-  constexpr int KP = kChunkKeys / P;           // pages a tile
-  constexpr int TILE = kChunkKeys * D * 2;     // bytes of a half tile
-  extern __shared__ __align__(128) unsigned char dyn_sm[];
-  __shared__ uint64_t q_full, o_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
-  __shared__ uint32_t tm_base;
-  __shared__ PageMeta meta[4][KP];
-  __shared__ volatile int gave_up;
-  const Q8AttendArgs& a = g.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
-  const uint32_t sm0 = (smem_u32(dyn_sm) + 1023u) & ~1023u;
-  const uint32_t q_sm = sm0, k_sm = sm0 + 2 * TILE, v_sm = sm0 + 4 * TILE;
-  if (tid == 0) {
-    mbar_init(&q_full, 256);
-    mbar_init(&o_full, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 128);
-      mbar_init(&v_full[i], 128);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
-    }
-    gave_up = 0;
-    mbar_fence_init();
-  }
-  if (warp == 12) tm_alloc(&tm_base);
-  tm_fence_before();
-  __syncthreads();
-  tm_fence_after();
-  const uint32_t tm = tm_base;  // S of the two halves at columns 0 and 128, O at 256 and 256 + D
-  const int n_items = *g.n_items;
-  const int S = n_items ? g.cum[n_items] : 0;
-  const long long W = (long long)S * a.c.Hkv, nb = max(1LL, min(W, (long long)gridDim.x));
-  const long long w_begin = blockIdx.x < nb ? W * blockIdx.x / nb : 0;
-  const long long w_end = blockIdx.x < nb ? W * (blockIdx.x + 1) / nb : 0;
-  const int G = a.c.G, Hkv = a.c.Hkv;
-  // a wait that runs out of its bound stops every role
-  auto wait = [&](uint64_t* bar, int phase) -> bool {
-    if (mbar_wait_second(bar, (uint32_t)(phase & 1))) return true;
-    gave_up = 1;
-    return false;
-  };
-  auto wait_warp = [&](uint64_t* bar, int phase) -> bool { return __all_sync(0xffffffffu, wait(bar, phase)); };
-  // registers after the splits below: 256 x 184 + 128 x 96 + 128 x 48 = 512 x 128, what the block was launched with
-
-  if (wg < 2) {  // ------------------------------------------------ softmax: a thread a row
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n");
-    const int row = tid & 127;
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t s_tm = tm + lanes + 128 * wg, o_tm = tm + lanes + 256 + D * wg;
-    const bool capped = a.sc.cap > 0.0f, biased = a.sc.slopes != nullptr;
-    int it = 0, seg = 0, tile = 0;  // tiles of this half, items and all tiles so far
-    bool ok = true;
-    for (long long w = w_begin; w < w_end && ok; ++seg) {
-      const ChunkSeg x = chunk_seg(g, w, w_end, S, n_items);
-      const int rho = x.rt * kChunkRows + 128 * wg + row, rows = x.s.count * G;
-      const bool mine = rho < rows, half = x.rt * kChunkRows + 128 * wg < rows;
-      const int tok = mine ? rho / G : 0, head = x.kvh * G + (mine ? rho % G : 0);
-      float cs = 0.0f, slope = 0.0f;
-      int pos = -1, lo = 0;
-      if (half) {
-        // the query row as halves, brought near 2^13 by a power of two
-        uint4 v[D / 8];
-        const __nv_bfloat16* qp = a.q.p + (long long)(x.s.start + tok) * a.q.ts + (long long)head * a.q.hs;
-        uint32_t m = 0u;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          v[i] = mine ? *reinterpret_cast<const uint4*>(qp + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) m = __vmaxu2(m, u[j] & 0x7fff7fffu);
-        }
-        m = max(m & 0xffffu, m >> 16);
-        int e = (int)(m >> 7) - 127;
-        if (m >= 0x7f80u) e = 13;
-        e = max(e, -100);
-        const float f = __uint_as_float((uint32_t)(13 - e + 127) << 23);
-        cs = __uint_as_float((uint32_t)(e - 13 + 127) << 23) * a.sc.scale * (capped ? 1.0f : kLog2e);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __half2 h = __floats2half2_rn(bf_lo(u[j]) * f, bf_hi(u[j]) * f);
-            u[j] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          sts128(q_sm + wg * TILE + tile_off(row, i), make_uint4(u[0], u[1], u[2], u[3]));
-        }
-        if (mine) {
-          pos = x.s.L - x.s.count + tok;
-          if (a.sc.window > 0) lo = max(0, pos - a.sc.window + 1);
-          if (a.sc.first_key) lo = max(lo, a.sc.first_key[x.s.start + tok]);
-          if (biased) slope = a.sc.slopes[head] * kLog2e;
-        }
-      }
-      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      mbar_arrive(&q_full);
-      const int pos_min = __reduce_min_sync(0xffffffffu, mine ? pos : 0x7fffffff);
-      const int lo_max = __reduce_max_sync(0xffffffffu, lo);
-      float M = -CUDART_INF_F, l = 0.0f;
-      if (half) {
-        for (int j = 0; j < x.n; ++j, ++it) {
-          if (!wait_warp(&s_full[wg], it)) {
-            ok = false;
-            break;
-          }
-          tm_fence_after();
-          float t[128];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tm_ld32(s_tm + 32 * i, t + 32 * i);
-          tm_wait_ld();
-          const PageMeta* pg = meta[(tile + j) & 3];
-          float mx = -CUDART_INF_F;
-#pragma unroll
-          for (int p = 0; p < KP; ++p) {
-            const PageMeta pm = pg[p];
-            const float ksc = pm.ks * cs;
-            if (capped) {
-#pragma unroll
-              for (int i = 0; i < P; ++i)
-                t[p * P + i] = fmaf(soft_cap(t[p * P + i] * ksc, a.sc.cap, a.sc.inv_cap), kLog2e, pm.lv);
-            } else {
-#pragma unroll
-              for (int i = 0; i < P; ++i) t[p * P + i] = fmaf(t[p * P + i], ksc, pm.lv);
-            }
-            if (biased) {
-#pragma unroll
-              for (int i = 0; i < P; ++i) t[p * P + i] -= slope * (float)abs(pos - pm.key0 - i);
-            }
-            if (!((pm.key0 + P - 1 <= pos_min && pm.key0 >= lo_max) || pm.key0 + P <= x.sp.pre)) {
-#pragma unroll
-              for (int i = 0; i < P; ++i) {
-                const int key = pm.key0 + i;
-                if (!((key >= lo && key <= pos) || key < x.sp.pre)) t[p * P + i] = -CUDART_INF_F;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < P; ++i) mx = fmaxf(mx, t[p * P + i]);
-          }
-          // the bound moves when the maximum passes it by more than the slack
-          const bool move = mx > M + kSlack || (M == -CUDART_INF_F && mx > M);
-          if (__any_sync(0xffffffffu, move)) {
-            const float f = move ? ex2f(M - mx) : 1.0f;  // 0 from -inf
-            if (move) M = mx;
-            l *= f;
-            if (j > 0) {
-#pragma unroll
-              for (int i = 0; i < D / 32; ++i) {
-                float o[32];
-                uint32_t u[32];
-                tm_ld32(o_tm + 32 * i, o);
-                tm_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(o[k] * f);
-                tm_st32(o_tm + 32 * i, u);
-              }
-            }
-          }
-          const float base = M > -CUDART_INF_F ? M - kLift : 0.0f;
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t u[32];
-#pragma unroll
-            for (int q = 0; q < KP / 2; ++q) {
-              const int p = hf * (KP / 2) + q;
-              float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-              for (int i = 0; i < P; i += 2) {
-                const float e0 = ex2f(t[p * P + i] - base), e1 = ex2f(t[p * P + i + 1] - base);
-                s0 += e0;
-                s1 += e1;
-                const __half2 h = __floats2half2_rn(e0, e1);
-                u[(q * P + i) / 2] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              l = fmaf(s0 + s1, pg[p].ivs, l);
-            }
-            tm_st32(s_tm + 32 * hf, u);
-          }
-          tm_wait_st();
-          tm_fence_before();
-          mbar_arrive(&p_full[wg]);
-        }
-      }
-      if (!ok || !wait_warp(&o_full, seg)) {
-        ok = false;
-        break;
-      }
-      tm_fence_after();
-      const bool whole = x.n == x.T;
-      const int piece = 2 * blockIdx.x + (w == w_begin ? 0 : 1);
-      const float inv = whole ? att_inv(l) : 1.0f;
-      if (half) {
-        __nv_bfloat16* op = a.out.p + (long long)(x.s.start + tok) * a.out.ts + (long long)head * a.out.hs;
-        float* pp = g.part_o + ((size_t)piece * kChunkRows + 128 * wg + row) * D;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          float o[32];
-          __syncwarp();
-          tm_ld32(o_tm + 32 * i, o);
-          tm_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            if (!mine) {
-            } else if (whole) {
-              uint4 v;
-              v.x = bf2_rn(o[k] * inv, o[k + 1] * inv);
-              v.y = bf2_rn(o[k + 2] * inv, o[k + 3] * inv);
-              v.z = bf2_rn(o[k + 4] * inv, o[k + 5] * inv);
-              v.w = bf2_rn(o[k + 6] * inv, o[k + 7] * inv);
-              *reinterpret_cast<uint4*>(op + 32 * i + k) = v;
-            } else {
-              *reinterpret_cast<float4*>(pp + 32 * i + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-              *reinterpret_cast<float4*>(pp + 32 * i + k + 4) = make_float4(o[k + 4], o[k + 5], o[k + 6], o[k + 7]);
-            }
-          }
-        }
-        if (mine) {
-          if (!whole) g.part_ml[(size_t)piece * kChunkRows + 128 * wg + row] = make_float2(M - kLift, l);
-          else if (a.tau) a.tau[(size_t)(x.s.start + tok) * Hkv * G + head] = att_lse(M - kLift, l);
-        }
-      }
-      tm_fence_before();
-      tile += x.n;
-      w += x.n;
-    }
-  } else if (wg == 2) {  // ------------------------------------------ converters
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
-    const int cw = warp - 8;                      // rows 32·cw .. 32·cw + 31 of a tile
-    constexpr int CPR = D / 16;                   // 16-code chunks of a row
-    constexpr int RPI = 32 / CPR, NI = 32 / RPI;  // rows a load, loads of a warp's rows
-    constexpr int PW = 32 / P;                    // pages of a warp's rows: 1 or 2
-    const int cch = lane % CPR, crow = lane / CPR;
-    int it = 0;
-    bool ok = true;
-    for (long long w = w_begin; w < w_end && ok;) {
-      const ChunkSeg x = chunk_seg(g, w, w_end, S, n_items);
-      // 32 tiles' pages at once, a tile a lane
-      int ph[PW], key[PW];
-      float ks[PW], vs[PW];
-      auto load = [&](const uint8_t* pool, int j, uint4 (&codes)[NI]) {
-        int f[PW], k0[PW];
-#pragma unroll
-        for (int q = 0; q < PW; ++q) {
-          f[q] = __shfl_sync(0xffffffffu, ph[q], j & 31);
-          k0[q] = __shfl_sync(0xffffffffu, key[q], j & 31);
-        }
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int rr = i * RPI + crow, tk = rr % P;
-          const int fq = rr < P ? f[0] : f[PW - 1], kq = rr < P ? k0[0] : k0[PW - 1];
-          codes[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (kq + tk < x.s.L)  // (false where there is no page)
-            codes[i] = __ldg(reinterpret_cast<const uint4*>(pool + (((size_t)fq * Hkv + x.kvh) * P + tk) * D + cch * 16));
-        }
-      };
-      auto store = [&](uint32_t dst, const uint4 (&codes)[NI]) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int rr = 32 * cw + i * RPI + crow;
-          uint4 h0, h1;
-          codes_half<I8, false>(codes[i].x, h0.x, h0.y);
-          codes_half<I8, false>(codes[i].y, h0.z, h0.w);
-          codes_half<I8, false>(codes[i].z, h1.x, h1.y);
-          codes_half<I8, false>(codes[i].w, h1.z, h1.w);
-          // chunks of the two 64-wide halves would meet in the same banks: those of the second go odd first
-          const bool flip = cch & 4;
-          sts128(dst + tile_off(rr, 2 * cch + (flip ? 1 : 0)), flip ? h1 : h0);
-          sts128(dst + tile_off(rr, 2 * cch + (flip ? 0 : 1)), flip ? h0 : h1);
-        }
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      };
-      uint4 kc[NI], vc[NI];
-      for (int j = 0; j < x.n; ++j, ++it) {
-        if ((j & 31) == 0) {
-#pragma unroll
-          for (int q = 0; q < PW; ++q) {
-            const int t = (x.t0 + j + lane) * KP + cw * PW + q;
-            ph[q] = -1;
-            key[q] = kNoKey;
-            ks[q] = 0.0f;
-            vs[q] = 1.0f;
-            if (j + lane < x.n && t < x.sp.T) {
-              const int page = x.sp.page(t);
-              ph[q] = phys_page(a.c.block_table, x.s.seq, page, a.c.maxp, a.c.nphys, a.c.status);
-              if (ph[q] >= 0) {
-                key[q] = page * P;
-                ks[q] = a.c.k_scale[(size_t)ph[q] * Hkv + x.kvh];
-                vs[q] = a.c.v_scale[(size_t)ph[q] * Hkv + x.kvh];
-              }
-            }
-          }
-          load(a.c.k_pool, j, kc);
-        }
-        load(a.c.v_pool, j, vc);
-#pragma unroll
-        for (int q = 0; q < PW; ++q) {
-          const float kk = __shfl_sync(0xffffffffu, ks[q], j & 31);
-          const float vv = fmaxf(__shfl_sync(0xffffffffu, vs[q], j & 31), 0x1p-100f);
-          const int k0 = __shfl_sync(0xffffffffu, key[q], j & 31);
-          if (lane == 0) meta[it & 3][cw * PW + q] = PageMeta{kk, log2f(vv), 1.0f / vv, k0};
-        }
-        const int sg = it & 1;
-        if (it >= 2 && !wait_warp(&k_empty[sg], it / 2 - 1)) {
-          ok = false;
-          break;
-        }
-        store(k_sm + sg * TILE, kc);
-        mbar_arrive(&k_full[sg]);
-        if (j + 1 < x.n && ((j + 1) & 31)) load(a.c.k_pool, j + 1, kc);
-        if (it >= 2 && !wait_warp(&v_empty[sg], it / 2 - 1)) {
-          ok = false;
-          break;
-        }
-        store(v_sm + sg * TILE, vc);
-        mbar_arrive(&v_full[sg]);
-      }
-      w += x.n;
-    }
-  } else {  // ------------------------------------------------------- products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
-    if (warp == 12 && lane == 0) {
-      constexpr uint32_t id_qk = instr_desc(kChunkKeys, 0), id_pv = instr_desc(D, 1);
-      int it = 0, seg = 0;  // tiles and items so far
-      int p_it[2] = {0, 0};
-      bool ok = true;
-      auto scores = [&](int hf, int sg) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t o = (k >> 2) * 16384 + (k & 3) * 32;
-          mma_ss(tm + 128 * hf, smem_desc(q_sm + hf * TILE + o, 16, 1024), smem_desc(k_sm + sg * TILE + o, 16, 1024), id_qk,
-                 k > 0);
-        }
-        tm_commit(&s_full[hf]);
-      };
-      for (long long w = w_begin; w < w_end && ok; ++seg) {
-        const ChunkSeg x = chunk_seg(g, w, w_end, S, n_items);
-        const int halves = x.s.count * G - x.rt * kChunkRows > 128 ? 2 : 1;
-        ok = wait(&q_full, seg) && wait(&k_full[it & 1], it / 2);
-        if (!ok) break;
-        tm_fence_after();
-        for (int hf = 0; hf < halves; ++hf) scores(hf, it & 1);
-        tm_commit(&k_empty[it & 1]);
-        for (int j = 0; j < x.n && ok; ++j, ++it) {
-          const int sg = it & 1;
-          ok = wait(&v_full[sg], it / 2) && (j + 1 == x.n || wait(&k_full[sg ^ 1], (it + 1) / 2));
-          for (int hf = 0; hf < halves && ok; ++hf) {
-            ok = wait(&p_full[hf], p_it[hf]);
-            if (!ok) break;
-            ++p_it[hf];
-            tm_fence_after();
-#pragma unroll
-            for (int k = 0; k < kChunkKeys / 16; ++k)
-              mma_ts(tm + 256 + D * hf, tm + 128 * hf + 8 * k, smem_desc(v_sm + sg * TILE + k * 2048, 16384, 1024), id_pv,
-                     j > 0 || k > 0);
-            if (j + 1 < x.n) scores(hf, sg ^ 1);
-          }
-          if (!ok) break;
-          tm_commit(&v_empty[sg]);
-          if (j + 1 < x.n) tm_commit(&k_empty[sg ^ 1]);
-        }
-        if (ok) tm_commit(&o_full);
-        w += x.n;
-      }
-    }
-    __syncwarp();
-  }
-  tm_fence_before();
-  __syncthreads();
-  tm_fence_after();
-  if (warp == 12) tm_free(tm);
-  if (tid == 0 && gave_up) raise_flag(a.c.status, ENTMAXKV_DEV_TIMEOUT);
 }
 
 // Joins items that several blocks hold and answers rows that see no key.
@@ -652,22 +124,9 @@ size_t attend_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total) {
          up256c((size_t)kChunkMaxBlocks * 2 * kChunkRows * 8);
 }
 
-template <bool I8, int D, int P>
-static cudaError_t chunk_t(ChunkArgs& g, cudaStream_t st) {
-  const int smem = 6 * kChunkKeys * D * 2 + 1024;
-  cudaError_t e = ensure_smem((const void*)chunk_kernel<I8, D, P>, smem);
-  if (e == cudaSuccess) e = launch_k(false, chunk_plan_kernel, dim3(1), dim3(1024), 0, st, g);
-  if (e == cudaSuccess)
-    e = launch_k(false, chunk_kernel<I8, D, P>, dim3(g.blocks), dim3(kChunkThreads), (size_t)smem, st, g);
-  if (e == cudaSuccess)
-    e = launch_k(false, chunk_join_kernel<D>, dim3((unsigned)(g.max_items * g.a.c.Hkv), kChunkRows / 8), dim3(256), 0, st,
-                 g);
-  return e;
-}
 template <bool I8>
 static cudaError_t chunk_d(ChunkArgs& g, cudaStream_t st) {
-  if (g.a.c.D == 128) return g.a.c.P == 32 ? chunk_t<I8, 128, 32>(g, st) : chunk_t<I8, 128, 16>(g, st);
-  return g.a.c.P == 32 ? chunk_t<I8, 64, 32>(g, st) : chunk_t<I8, 64, 16>(g, st);
+  return g.a.c.D == 128 ? chunk_run<I8, 128>(g, st) : chunk_run<I8, 64>(g, st);
 }
 
 cudaError_t launch_attend_chunk(const Q8AttendArgs& a, bool i8, void* ws, int sms, cudaStream_t st) {
@@ -686,7 +145,12 @@ cudaError_t launch_attend_chunk(const Q8AttendArgs& a, bool i8, void* ws, int sm
   g.part_o = reinterpret_cast<float*>(p);
   p += up256c((size_t)kChunkMaxBlocks * 2 * kChunkRows * a.c.D * 4);
   g.part_ml = reinterpret_cast<float2*>(p);
-  return i8 ? chunk_d<true>(g, st) : chunk_d<false>(g, st);
+  cudaError_t e = launch_k(false, chunk_plan_kernel, dim3(1), dim3(1024), 0, st, g);
+  if (e == cudaSuccess) e = i8 ? chunk_d<true>(g, st) : chunk_d<false>(g, st);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)(g.max_items * a.c.Hkv), kChunkRows / 8);
+  return a.c.D == 128 ? launch_k(false, chunk_join_kernel<128>, grid, dim3(256), 0, st, g)
+                      : launch_k(false, chunk_join_kernel<64>, grid, dim3(256), 0, st, g);
 }
 
 }  // namespace ekv
