@@ -143,6 +143,7 @@ __device__ __forceinline__ Q8Span q8_span(const Q8Cache& c, const Q8Score& sc, c
   int lo = sc.window > 0 ? max(0, x0 - sc.window + 1) : 0;
   if (sc.first_key) {
     int fk = 0x7fffffff;
+#pragma unroll 8
     for (int i = 0; i < n; ++i) fk = min(fk, sc.first_key[s.start + r0 + i]);
     lo = max(lo, fk);
   }

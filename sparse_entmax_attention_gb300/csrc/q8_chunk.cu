@@ -21,6 +21,8 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(ChunkArgs g) {
   __shared__ int end_sh[1024];
   const Q8AttendArgs& a = g.a;
   const int tid = threadIdx.x, per = kChunkKeys / a.c.P;
+  __shared__ int none_sh;
+  if (tid == 0) none_sh = 0;
   int items = 0, tiles = 0;
   for (int b0 = 0; b0 < a.b.n_seqs; b0 += 1024) {
     const int b = b0 + tid;
@@ -45,8 +47,11 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(ChunkArgs g) {
         }
         const int rt = j - (lo ? end_sh[lo - 1] : 0);
         const Q8Slot s = q8_slot(a.c, a.b, b0 + lo, nullptr);
-        T = (chunk_span(a, s, b0 + lo, rt).T + per - 1) / per;
-        if (items + j < g.max_items) g.items[items + j] = ChunkItem{b0 + lo, rt};
+        const Q8Span v = chunk_span(a, s, b0 + lo, rt);
+        T = (v.T + per - 1) / per;
+        if (items + j < g.max_items)
+          g.items[items + j] = ChunkItem{b0 + lo, rt, T, v.T, s.seq, s.L, s.start, s.count, v.pre, v.npre, v.wfirst, v.npages};
+        if (T == 0 && items + j < g.max_items) g.empty[atomicAdd(&none_sh, 1)] = items + j;  // (any order will do)
       }
       int all;
       const int before = block_exclusive_scan(T, sh_scan, all);
@@ -58,58 +63,81 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(ChunkArgs g) {
   }
   if (tid == 0) {
     items = min(items, g.max_items);  // (slots whose rows overlap can claim more: those are not answered)
-    *g.n_items = items;
+    g.n_items[0] = items;
+    g.n_items[1] = none_sh;
     g.cum[items] = tiles;
   }
 }
 
-// Joins items that several blocks hold and answers rows that see no key.
-// Block (item · KV head, 8 rows): a warp a row.
+// Joins items that several blocks hold: at each block that begins inside an
+// item it shares with the block before it alone or first. Eight blocks a cut,
+// 32 rows each, a warp a row; the first eight answer rows that see no key.
 template <int D>
 __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs g) {
   pdl_enter();
   const Q8AttendArgs& a = g.a;
-  const int item = blockIdx.x / a.c.Hkv, kvh = blockIdx.x % a.c.Hkv, n_items = *g.n_items;
-  if (item >= n_items) return;
-  const ChunkItem it = g.items[item];
-  const Q8Slot s = q8_slot(a.c, a.b, it.slot, nullptr);
-  const int S = g.cum[n_items], G = a.c.G;
-  const long long W = (long long)S * a.c.Hkv, nb = max(1LL, min(W, (long long)g.blocks));
-  const int T = g.cum[item + 1] - g.cum[item];
-  const long long A = (long long)kvh * S + g.cum[item];
-  long long c0 = 0, c1 = -1;
-  if (T > 0) {
-    c0 = ((A + 1) * nb - 1) / W;
-    c1 = ((A + T) * nb - 1) / W;
-    if (c0 == c1) return;  // finished by that block
-  }
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 8 + (threadIdx.x >> 5), rho = it.rt * kChunkRows + row;
-  if (rho >= s.count * G) return;
-  auto piece = [&](long long c) -> size_t {
-    return ((size_t)(2 * c + (W * c / nb >= A ? 0 : 1))) * kChunkRows + row;
-  };
-  float M = -CUDART_INF_F, l = 0.0f;
+  const int c = blockIdx.x >> 3, part = blockIdx.x & 7, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = a.c.G, Hkv = a.c.Hkv;
   constexpr int V = D / 32;
-  float o[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) o[i] = 0.0f;
-  for (long long c = c0; c <= c1; ++c) M = fmaxf(M, g.part_ml[piece(c)].x);
-#pragma unroll 2
-  for (long long c = c0; c <= c1; ++c) {
-    const float2 ml = g.part_ml[piece(c)];
-    const float f = ml.x > -CUDART_INF_F ? ex2f(ml.x - M) : 0.0f;
-    l = fmaf(f, ml.y, l);
-#pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = fmaf(f, g.part_o[piece(c) * D + 32 * i + lane], o[i]);
+  if (c == 0) {
+    const long long n = (long long)g.n_items[1] * Hkv;
+    for (long long i = part; i < n; i += 8) {
+      const ChunkItem it = g.items[g.empty[i / Hkv]];
+      for (int row = warp; row < kChunkRows; row += 8) {
+        const int rho = it.rt * kChunkRows + row;
+        if (rho >= it.count * G) break;
+        const int head = (int)(i % Hkv) * G + rho % G;
+        const long long tok = it.start + rho / G;
+        for (int k = lane; k < D; k += 32) a.out.p[tok * a.out.ts + (long long)head * a.out.hs + k] = __float2bfloat16_rn(0.0f);
+        if (a.tau && lane == 0) a.tau[tok * Hkv * G + head] = CUDART_NAN_F;
+      }
+    }
+    return;
   }
-  const int head = kvh * G + rho % G;
-  const long long tok = s.start + rho / G;
-  const float inv = att_inv(l);
+  const int2 cut = g.cuts[c];
+  if (cut.x < 0) return;
+  const ChunkItem it = g.items[cut.x];
+  const int cum = g.cum[cut.x], S = g.cum[g.n_items[0]];
+  const long long W = (long long)S * Hkv, nb = max(1LL, min(W, (long long)g.blocks));
+  const long long A = (long long)cut.y * S + cum;
+  const int c0 = (int)(((A + 1) * nb - 1) / W), n = (int)(((A + it.T) * nb - 1) / W) - c0 + 1;
+  if (c0 != c - 1) return;  // joined at an earlier cut
+  const int last0 = W * c0 / nb >= A ? 0 : 1;  // the first block's piece: its first or its last
+#pragma unroll 2
+  for (int row = 32 * part + warp; row < 32 * part + 32; row += 8) {
+    const int rho = it.rt * kChunkRows + row;
+    if (rho >= it.count * G) break;
+    auto piece = [&](int i) -> size_t { return (size_t)(2 * (c0 + i) + (i ? 0 : last0)) * kChunkRows + row; };
+    float M = -CUDART_INF_F, l = 0.0f;
+    float o[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    a.out.p[tok * a.out.ts + (long long)head * a.out.hs + 32 * i + lane] = __float2bfloat16_rn(o[i] * inv);
-  if (a.tau && lane == 0) a.tau[tok * a.c.Hkv * G + head] = att_lse(M, l);
+    for (int i = 0; i < V; ++i) o[i] = 0.0f;
+    for (int i0 = 0; i0 < n; i0 += 32) {  // 32 pieces' maxima and sums at once, one a lane
+      float2 ml = make_float2(-CUDART_INF_F, 0.0f);
+      if (i0 + lane < n) ml = g.part_ml[piece(i0 + lane)];
+      const float m = fmaxf(M, warp_max(ml.x));
+      const float old = M > -CUDART_INF_F ? ex2f(M - m) : 0.0f, f = ml.x > -CUDART_INF_F ? ex2f(ml.x - m) : 0.0f;
+      l = l * old + warp_sum(f * ml.y);
+#pragma unroll
+      for (int k = 0; k < V; ++k) o[k] *= old;
+      M = m;
+      const int m32 = min(32, n - i0);
+#pragma unroll 4
+      for (int i = 0; i < m32; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float* p = g.part_o + piece(i0 + i) * D + lane;
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[k] = fmaf(fi, p[32 * k], o[k]);
+      }
+    }
+    const int head = cut.y * G + rho % G;
+    const long long tok = it.start + rho / G;
+    const float inv = att_inv(l);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      a.out.p[tok * a.out.ts + (long long)head * a.out.hs + 32 * i + lane] = __float2bfloat16_rn(o[i] * inv);
+    if (a.tau && lane == 0) a.tau[tok * Hkv * G + head] = att_lse(M, l);
+  }
 }
 
 static size_t up256c(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -119,7 +147,8 @@ static long long chunk_items(int n_seqs, int total, int G) {
 
 size_t attend_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total) {
   const size_t items = (size_t)chunk_items(n_seqs, total, cfg.group);
-  return up256c(items * sizeof(ChunkItem)) + up256c((items + 1) * 4) + 256 +
+  return up256c(items * sizeof(ChunkItem)) + up256c((items + 1) * 4) + 256 + up256c(items * 4) +
+         up256c((size_t)kChunkMaxBlocks * 8) +
          up256c((size_t)kChunkMaxBlocks * 2 * kChunkRows * cfg.head_dim * 4) +
          up256c((size_t)kChunkMaxBlocks * 2 * kChunkRows * 8);
 }
@@ -142,15 +171,18 @@ cudaError_t launch_attend_chunk(const Q8AttendArgs& a, bool i8, void* ws, int sm
   p += up256c((items + 1) * 4);
   g.n_items = reinterpret_cast<int*>(p);
   p += 256;
+  g.empty = reinterpret_cast<int*>(p);
+  p += up256c(items * 4);
+  g.cuts = reinterpret_cast<int2*>(p);
+  p += up256c((size_t)kChunkMaxBlocks * 8);
   g.part_o = reinterpret_cast<float*>(p);
   p += up256c((size_t)kChunkMaxBlocks * 2 * kChunkRows * a.c.D * 4);
   g.part_ml = reinterpret_cast<float2*>(p);
   cudaError_t e = launch_k(false, chunk_plan_kernel, dim3(1), dim3(1024), 0, st, g);
   if (e == cudaSuccess) e = i8 ? chunk_d<true>(g, st) : chunk_d<false>(g, st);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(g.max_items * a.c.Hkv), kChunkRows / 8);
-  return a.c.D == 128 ? launch_k(false, chunk_join_kernel<128>, grid, dim3(256), 0, st, g)
-                      : launch_k(false, chunk_join_kernel<64>, grid, dim3(256), 0, st, g);
+  return a.c.D == 128 ? launch_k(true, chunk_join_kernel<128>, dim3(8 * g.blocks), dim3(256), 0, st, g)
+                      : launch_k(true, chunk_join_kernel<64>, dim3(8 * g.blocks), dim3(256), 0, st, g);
 }
 
 }  // namespace ekv

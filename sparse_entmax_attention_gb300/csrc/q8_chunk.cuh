@@ -35,14 +35,19 @@ constexpr int kChunkMaxBlocks = 256;
 constexpr float kLift = 8.0f;   // w = 2^{t − M + kLift}
 constexpr float kSlack = 6.0f;  // M moves when the row's maximum passes it by more
 
-struct ChunkItem {
-  int slot, rt;
+// What the roles know of an item, filled in once by the listing kernel.
+struct __align__(16) ChunkItem {
+  int slot, rt, T, Tp;                // its tiles and pages
+  int seq, L, start, count;           // Q8Slot
+  int pre, npre, wfirst, npages;      // Q8Span
 };
 struct ChunkArgs {
   Q8AttendArgs a;
   ChunkItem* items;
   int* cum;        // [n_items + 1] tiles of one KV head before each item
-  int* n_items;
+  int* n_items;    // [2] items, and those of them without a tile
+  int* empty;      // the latter
+  int2* cuts;      // [blocks] (item, KV head) that a block begins inside of; item −1: at one's start
   float* part_o;   // [blocks][2][256][D]
   float2* part_ml; // [blocks][2][256]
   int max_items, blocks;
@@ -98,14 +103,22 @@ __device__ __forceinline__ void tm_tie32(float* v) {
                  "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
                  "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
 }
-__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* r) {
+// 16 columns, read behind their own wait, and written.
+__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::"r"(r[0]),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n" ::"r"(
+          r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
 
@@ -142,37 +155,50 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// A block's part of one item: `n` tiles from tile t0 of T.
+// A block's part of one item: `n` tiles, tile t0 + n − 1 first. (Nearest keys
+// come first, so that with a distance bias the first maximum is the last one.)
 struct ChunkSeg {
-  int kvh, slot, rt, t0, n, T;
+  int kvh, item, slot, rt, t0, n, T;
   Q8Slot s;
   Q8Span sp;
 };
-__device__ __forceinline__ ChunkSeg chunk_seg(const ChunkArgs& g, long long w, long long w_end, int S, int n_items) {
+// The part that begins at w; `item` is looked for from the start of the list
+// (item < 0) or is the one behind the part before.
+__device__ __forceinline__ ChunkSeg chunk_seg(const ChunkArgs& g, long long w, long long w_end, int S, int n_items,
+                                              int item) {
   ChunkSeg x;
   x.kvh = (int)(w / S);
   const int off = (int)(w - (long long)x.kvh * S);
-  int lo = 0, hi = n_items - 1;  // the last item that begins at or before `off`
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (g.cum[m] <= off) lo = m;
-    else hi = m - 1;
+  if (item < 0) {
+    int lo = 0, hi = n_items - 1;  // the last item that begins at or before `off`
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (g.cum[m] <= off) lo = m;
+      else hi = m - 1;
+    }
+    item = lo;
+  } else if (item == n_items) {
+    item = 0;
   }
-  const ChunkItem it = g.items[lo];
+  ChunkItem it;
+  for (;; ++item) {  // (items without a tile are passed over)
+    const int4* p = reinterpret_cast<const int4*>(g.items + item);
+    *reinterpret_cast<int4*>(&it) = __ldcg(p);
+    *(reinterpret_cast<int4*>(&it) + 1) = __ldcg(p + 1);
+    *(reinterpret_cast<int4*>(&it) + 2) = __ldcg(p + 2);
+    if (it.T > 0 || item + 1 >= n_items) break;
+  }
+  x.item = item;
   x.slot = it.slot;
   x.rt = it.rt;
-  x.t0 = off - g.cum[lo];
-  x.T = g.cum[lo + 1] - g.cum[lo];
+  x.t0 = off - __ldcg(g.cum + item);
+  x.T = it.T;
   x.n = (int)min((long long)(x.T - x.t0), w_end - w);
-  x.s = q8_slot(g.a.c, g.a.b, x.slot, nullptr);
-  x.sp = chunk_span(g.a, x.s, x.slot, x.rt);
+  x.s = Q8Slot{it.seq, it.L, it.start, it.count};
+  x.sp = Q8Span{it.pre, it.npre, it.wfirst, it.npages, it.Tp};
   return x;
 }
 
-template <bool B>
-struct Flag {
-  static constexpr bool value = B;
-};
 struct PageMeta {
   float ks, lv, ivs;  // K scale, log2 of the V scale, its inverse
   int key0;           // first key; beyond every key where there is no page
@@ -234,40 +260,56 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
     const uint32_t s_tm = tm + lanes + 128 * wg, o_tm = tm + lanes + 256 + D * wg;
     int it = 0, seg = 0, tile = 0;  // tiles of this half, items and all tiles so far
     bool ok = true;
+    int item = -1;
     for (long long w = w_begin; w < w_end && ok; ++seg) {
-      const ChunkSeg x = chunk_seg(g, w, w_end, S, n_items);
+      const ChunkSeg x = chunk_seg(g, w, w_end, S, n_items, item);
+      item = x.item + 1;
       const int rho = x.rt * kChunkRows + 128 * wg + row, rows = x.s.count * G;
       const bool mine = rho < rows, half = x.rt * kChunkRows + 128 * wg < rows;
       const int tok = mine ? rho / G : 0, head = x.kvh * G + (mine ? rho % G : 0);
       float kc = 0.0f, slope = 0.0f;  // the raw sums' factor (times the page's K scale): log2 units, or of the cap
       int pos = -1, lo = 0;
+      const long long q_at = (long long)(x.s.start + tok) * a.q.ts + (long long)head * a.q.hs;
+      const long long o_at = (long long)(x.s.start + tok) * a.out.ts + (long long)head * a.out.hs;
+      const uint32_t rows_sm = q_sm + wg * TILE;  // this half's query tile, and its answers on their way out
       if (half) {
-        // the query row as halves, brought near 2^13 by a power of two
-        uint4 v[D / 8];
-        const __nv_bfloat16* qp = a.q.p + (long long)(x.s.start + tok) * a.q.ts + (long long)head * a.q.hs;
-        uint32_t m = 0u;
+        // the warp's query rows as halves, CPR lanes a row, each row brought near 2^13 by a power of two
+        constexpr int CPR = D / 8, RPI = 32 / CPR;
+        const int ch = lane % CPR, sub = lane / CPR;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          v[i] = mine ? *reinterpret_cast<const uint4*>(qp + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        for (int i0 = 0; i0 < CPR; i0 += 8) {
+          uint4 v[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) m = __vmaxu2(m, u[j] & 0x7fff7fffu);
-        }
-        m = max(m & 0xffffu, m >> 16);
-        int e = (int)(m >> 7) - 127;
-        if (m >= 0x7f80u) e = 13;
-        e = max(e, -100);
-        const float f = __uint_as_float((uint32_t)(13 - e + 127) << 23);
-        kc = __uint_as_float((uint32_t)(e - 13 + 127) << 23) * a.sc.scale * (capped ? a.sc.inv_cap : kLog2e);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __half2 h = __floats2half2_rn(bf_lo(u[j]) * f, bf_hi(u[j]) * f);
-            u[j] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int i = 0; i < 8; ++i) {
+            const int rl = (i0 + i) * RPI + sub;
+            const long long at = __shfl_sync(0xffffffffu, q_at, rl);
+            const bool there = __shfl_sync(0xffffffffu, (int)mine, rl);
+            v[i] = there ? *reinterpret_cast<const uint4*>(a.q.p + at + ch * 8) : make_uint4(0u, 0u, 0u, 0u);
           }
-          sts128(q_sm + wg * TILE + tile_off(row, i), make_uint4(u[0], u[1], u[2], u[3]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rl = (i0 + i) * RPI + sub;
+            uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t m = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m = __vmaxu2(m, u[j] & 0x7fff7fffu);
+            m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+            for (int o = 1; o < CPR; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            int e = (int)(m >> 7) - 127;
+            if (m >= 0x7f80u) e = 13;
+            e = max(e, -100);
+            const float f = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __half2 h = __floats2half2_rn(bf_lo(u[j]) * f, bf_hi(u[j]) * f);
+              u[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            sts128(rows_sm + tile_off(32 * (warp & 3) + rl, ch), make_uint4(u[0], u[1], u[2], u[3]));
+            const int back = __shfl_sync(0xffffffffu, e, (lane % RPI) * CPR);  // rows 8·RPI of the warp in turn
+            if (lane / RPI == i0 + i)
+              kc = __uint_as_float((uint32_t)(back - 13 + 127) << 23) * a.sc.scale * (capped ? a.sc.inv_cap : kLog2e);
+          }
         }
         if (mine) {
           pos = x.s.L - x.s.count + tok;
@@ -289,43 +331,54 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
           }
           tm_fence_after();
           const PageMeta* pg = meta[(tile + j) & 3];
-          bool whole = true, past = true;  // every key seen by every row of the warp; none behind a row
-#pragma unroll
-          for (int p = 0; p < KP; ++p) {
-            const int k0 = pg[p].key0;
-            past &= k0 + P - 1 <= pos_min;
-            whole &= (k0 + P - 1 <= pos_min && k0 >= lo_max) || k0 + P <= x.sp.pre;
-          }
-          // t + base of 32 columns from their raw sums, in pairs
-          auto eval = [&](auto masked, int col0, const float (&raw)[32], unsigned long long (&t2)[16], float base) {
+          // 32 columns (keys 32c ..) from their raw sums to halves at columns 64 + 16c: behind the sums that
+          // are still to be read, which come last to first
+          auto weigh = [&](int c, const float (&raw)[32]) {
+            unsigned long long t2[16];
+            float mx = -CUDART_INF_F;
 #pragma unroll
             for (int q = 0; q < 32 / P; ++q) {
-              const PageMeta pm = pg[col0 / P + q];
-              float add = pm.lv + base;
-              if (biased && past) add = fmaf(-slope, (float)(pos - pm.key0), add);
-              const unsigned long long k2 = f2_splat(pm.ks * kc), a2 = f2_splat(add);
+              const PageMeta pm = pg[c * (32 / P) + q];
               unsigned long long* u = t2 + q * (P / 2);
               const float* v = raw + q * P;
-              if (capped) {
+              const bool past = pm.key0 + P - 1 <= pos_min;
+              float add = pm.lv;
+              if (biased && past) add = fmaf(-slope, (float)(pos - pm.key0), add);
+              const unsigned long long k2 = f2_splat(pm.ks * kc), a2 = f2_splat(add);
+              if (capped) {  // y = raw·k, then cap·log2 e·y·T(y²)
+                unsigned long long z2[P / 2];
                 float big = 0.0f;
 #pragma unroll
                 for (int i = 0; i < P / 2; ++i) {
                   u[i] = f2_mul(f2_pack(v[2 * i], v[2 * i + 1]), k2);
+                  z2[i] = f2_mul(u[i], u[i]);
                   float y0, y1;
-                  f2_unpack(f2_mul(u[i], u[i]), y0, y1);
+                  f2_unpack(z2[i], y0, y1);
                   big = max3(big, y0, y1);
                 }
-                const unsigned long long c2 = f2_splat(a.sc.cap * kLog2e);
-                if (__any_sync(0xffffffffu, !(big <= 1.0f))) {
+                constexpr TanhPoly poly = tanh_poly();
+                const float out = a.sc.cap * kLog2e;
+                if (__all_sync(0xffffffffu, big <= 0.25f)) {
+                  const unsigned long long c0 = f2_splat(poly.near[0] * out), c1 = f2_splat(poly.near[1] * out),
+                                           c2 = f2_splat(poly.near[2] * out), c3 = f2_splat(poly.near[3] * out);
+#pragma unroll
+                  for (int i = 0; i < P / 2; ++i)
+                    u[i] = f2_fma(f2_fma(f2_fma(f2_fma(c3, z2[i], c2), z2[i], c1), z2[i], c0), u[i], a2);
+                } else if (__all_sync(0xffffffffu, big <= 1.0f)) {
+#pragma unroll
+                  for (int i = 0; i < P / 2; ++i) {
+                    unsigned long long r = f2_fma(z2[i], f2_splat(poly.far[6]), f2_splat(poly.far[5]));
+#pragma unroll
+                    for (int n = 4; n >= 0; --n) r = f2_fma(r, z2[i], f2_splat(poly.far[n]));
+                    u[i] = f2_fma(f2_mul(r, f2_splat(out)), u[i], a2);
+                  }
+                } else {
 #pragma unroll
                   for (int i = 0; i < P / 2; ++i) {
                     float y0, y1;
                     f2_unpack(u[i], y0, y1);
-                    u[i] = f2_fma(f2_pack(soft_cap(y0, 1.0f, 1.0f), soft_cap(y1, 1.0f, 1.0f)), c2, a2);
+                    u[i] = f2_fma(f2_pack(soft_cap(y0, 1.0f, 1.0f), soft_cap(y1, 1.0f, 1.0f)), f2_splat(out), a2);
                   }
-                } else {
-#pragma unroll
-                  for (int i = 0; i < P / 2; ++i) u[i] = f2_fma(tanh2_small(u[i], f2_mul(u[i], u[i])), c2, a2);
                 }
               } else {
 #pragma unroll
@@ -341,8 +394,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
                     at = f2_add(at, two);
                   }
                 } else {
-                  const float d = (float)(pos - pm.key0);
-                  float y = d;
+                  float y = (float)(pos - pm.key0);
 #pragma unroll
                   for (int i = 0; i < P / 2; ++i) {
                     u[i] = f2_fma(f2_pack(-fabsf(y), -fabsf(y - 1.0f)), sl, u[i]);
@@ -350,7 +402,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
                   }
                 }
               }
-              if (decltype(masked)::value) {
+              if (!((past && pm.key0 >= lo_max) || pm.key0 + P <= x.sp.pre)) {
                 // one bit a key: those from lo to pos, and the prefix
                 const int from = min(max(lo - pm.key0, 0), P), to = min(max(pos - pm.key0 + 1, 0), P);
                 const int pre = min(max(x.sp.pre - pm.key0, 0), P);
@@ -365,73 +417,81 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
                   u[i] = f2_pack(y0, y1);
                 }
               }
-            }
-          };
-          uint32_t u[64];  // the weights as halves
-          float mx, lt;
-          auto weigh = [&](auto masked) {
-            const float base = M > -CUDART_INF_F ? kLift - M : 0.0f;
-            mx = -CUDART_INF_F;
-            lt = 0.0f;
-            float raw[2][32];
-            tm_ld32(s_tm, raw[0]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tm_wait_ld();
-              tm_tie32(raw[c & 1]);
-              if (c < 3) tm_ld32(s_tm + 32 * (c + 1), raw[(c + 1) & 1]);
-              unsigned long long t2[16];
-              eval(masked, 32 * c, raw[c & 1], t2, base);
               float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F;
 #pragma unroll
-              for (int q = 0; q < 32 / P; ++q) {
-                unsigned long long s2[2] = {0ull, 0ull};
-#pragma unroll
-                for (int i = 0; i < P / 2; ++i) {
-                  float e0, e1;
-                  f2_unpack(t2[q * (P / 2) + i], e0, e1);
-                  if (i & 1) m1 = max3(m1, e0, e1);
-                  else m0 = max3(m0, e0, e1);
-                  e0 = ex2f(e0);
-                  e1 = ex2f(e1);
-                  s2[i & 1] = f2_add(s2[i & 1], f2_pack(e0, e1));
-                  const __half2 h = __floats2half2_rn(e0, e1);
-                  u[c * 16 + q * (P / 2) + i] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-                lt = fmaf(f2_sum(f2_add(s2[0], s2[1])), pg[c * (32 / P) + q].ivs, lt);
+              for (int i = 0; i < P / 2; i += 2) {
+                float y0, y1;
+                f2_unpack(u[i], y0, y1);
+                m0 = max3(m0, y0, y1);
+                f2_unpack(u[i + 1], y0, y1);
+                m1 = max3(m1, y0, y1);
               }
               mx = max3(mx, m0, m1);
             }
-          };
-          // Weights against the bound that the earlier tiles left. Where the tile's maximum passes it by more than
-          // the slack (the first tile, and rarely after it) the bound moves, and the tile is done again.
-          for (;;) {
-            if (whole) weigh(Flag<false>{});
-            else weigh(Flag<true>{});
-            const bool first = M == -CUDART_INF_F;
-            const bool move = first ? mx > M : mx > kLift + kSlack;
-            if (!__any_sync(0xffffffffu, move)) break;
-            const float to = first ? mx : M + (mx - kLift);
-            const float f = move ? ex2f(M - to) : 1.0f;  // 0 from -inf
-            if (move) M = to;
-            l *= f;
-            if (j > 0) {
+            // the bound moves when the maximum passes it by more than the slack: in an item's first columns, and
+            // seldom behind them
+            const bool move = mx > M + kSlack;
+            if (__any_sync(0xffffffffu, move)) {
+              const float f = move ? ex2f(M - mx) : 1.0f;  // 0 from -inf
+              if (move) M = mx;
+              l *= f;
+              tm_wait_ld();  // (a load under way keeps its registers)
+              tm_wait_st();
+              if (j > 0) {
 #pragma unroll 1
-              for (int i = 0; i < D / 32; ++i) {
-                float o[32];
-                uint32_t v[32];
-                tm_ld32(o_tm + 32 * i, o);
-                tm_wait_ld();
-                tm_tie32(o);
+                for (int i = 0; i < D / 16; ++i) {
+                  uint32_t o[16];
+                  tm_ld16(o_tm + 16 * i, o);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(o[k] * f);
-                tm_st32(o_tm + 32 * i, v);
+                  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                  tm_st16(o_tm + 16 * i, o);
+                }
+              }
+              const __half2 fh = __float2half2_rn(f);
+#pragma unroll 1
+              for (int i = 3; i > c; --i) {
+                uint32_t o[16];
+                tm_ld16(s_tm + 64 + 16 * i, o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&o[k]), fh);
+                  o[k] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                tm_st16(s_tm + 64 + 16 * i, o);
               }
             }
+            const unsigned long long base2 = f2_splat(M > -CUDART_INF_F ? kLift - M : 0.0f);
+            uint32_t w16[16];
+#pragma unroll
+            for (int q = 0; q < 32 / P; ++q) {
+              unsigned long long s2[2] = {0ull, 0ull};
+#pragma unroll
+              for (int i = 0; i < P / 2; ++i) {
+                float e0, e1;
+                f2_unpack(f2_add(t2[q * (P / 2) + i], base2), e0, e1);
+                e0 = ex2f(e0);
+                e1 = ex2f(e1);
+                s2[i & 1] = f2_add(s2[i & 1], f2_pack(e0, e1));
+                const __half2 h = __floats2half2_rn(e0, e1);
+                w16[q * (P / 2) + i] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              l = fmaf(f2_sum(f2_add(s2[0], s2[1])), pg[c * (32 / P) + q].ivs, l);
+            }
+            tm_st16(s_tm + 64 + 16 * c, w16);
+          };
+          float ra[32], rb[32];
+          tm_ld32(s_tm + 96, ra);
+#pragma unroll 1
+          for (int c = 3; c > 0; c -= 2) {
+            tm_wait_ld();
+            tm_tie32(ra);
+            tm_ld32(s_tm + 32 * c - 32, rb);
+            weigh(c, ra);
+            tm_wait_ld();
+            tm_tie32(rb);
+            if (c > 1) tm_ld32(s_tm + 32, ra);
+            weigh(c - 1, rb);
           }
-          l += lt;
-          tm_st32(s_tm, u);
-          tm_st32(s_tm + 32, u + 32);
           tm_wait_st();
           tm_fence_before();
           mbar_arrive(&p_full[wg]);
@@ -446,31 +506,50 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
       const int piece = 2 * blockIdx.x + (w == w_begin ? 0 : 1);
       const float inv = whole ? att_inv(l) : 1.0f;
       if (half) {
-        __nv_bfloat16* op = a.out.p + (long long)(x.s.start + tok) * a.out.ts + (long long)head * a.out.hs;
-        float* pp = g.part_o + ((size_t)piece * kChunkRows + 128 * wg + row) * D;
-#pragma unroll
+        // rows leave through the query tile, so that a warp writes whole rows: bf16 rows at once, fp32 pieces in
+        // column blocks of 256 bytes too
+        constexpr int LPR = D == 128 ? 16 : 8;  // lanes a bf16 row
+        const int wrow = 32 * (warp & 3);
+        float* pp = g.part_o + ((size_t)piece * kChunkRows + 128 * wg + wrow) * D;
+#pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
           float o[32];
           __syncwarp();
           tm_ld32(o_tm + 32 * i, o);
           tm_wait_ld();
           tm_tie32(o);
+          if (whole) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            if (!mine) {
-            } else if (whole) {
-              uint4 v;
-              v.x = bf2_rn(o[k] * inv, o[k + 1] * inv);
-              v.y = bf2_rn(o[k + 2] * inv, o[k + 3] * inv);
-              v.z = bf2_rn(o[k + 4] * inv, o[k + 5] * inv);
-              v.w = bf2_rn(o[k + 6] * inv, o[k + 7] * inv);
-              *reinterpret_cast<uint4*>(op + 32 * i + k) = v;
-            } else {
-              *reinterpret_cast<float4*>(pp + 32 * i + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-              *reinterpret_cast<float4*>(pp + 32 * i + k + 4) = make_float4(o[k + 4], o[k + 5], o[k + 6], o[k + 7]);
+            for (int k = 0; k < 32; k += 8)
+              sts128(rows_sm + tile_off(row, 4 * i + k / 8),
+                     make_uint4(bf2_rn(o[k] * inv, o[k + 1] * inv), bf2_rn(o[k + 2] * inv, o[k + 3] * inv),
+                                bf2_rn(o[k + 4] * inv, o[k + 5] * inv), bf2_rn(o[k + 6] * inv, o[k + 7] * inv)));
+          } else {  // 32 columns are 128 bytes a row: 8 lanes a row
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              sts128(rows_sm + tile_off(row, k / 4), make_uint4(__float_as_uint(o[k]), __float_as_uint(o[k + 1]),
+                                                                __float_as_uint(o[k + 2]), __float_as_uint(o[k + 3])));
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const int rl = 4 * n + lane / 8;
+              if (__shfl_sync(0xffffffffu, (int)mine, rl))
+                *reinterpret_cast<uint4*>(pp + rl * D + 32 * i + 4 * (lane % 8)) =
+                    lds128(rows_sm + tile_off(wrow + rl, lane % 8));
             }
           }
         }
+        if (whole) {
+          __syncwarp();
+#pragma unroll 4
+          for (int n = 0; n < LPR; ++n) {
+            const int rl = n * (32 / LPR) + lane / LPR;
+            const long long at = __shfl_sync(0xffffffffu, o_at, rl);
+            if (__shfl_sync(0xffffffffu, (int)mine, rl))
+              *reinterpret_cast<uint4*>(a.out.p + at + 8 * (lane % LPR)) = lds128(rows_sm + tile_off(wrow + rl, lane % LPR));
+          }
+        }
+        __syncwarp();
         if (mine) {
           if (!whole) g.part_ml[(size_t)piece * kChunkRows + 128 * wg + row] = make_float2(M - kLift, l);
           else if (a.tau) a.tau[(size_t)(x.s.start + tok) * Hkv * G + head] = att_lse(M - kLift, l);
@@ -489,8 +568,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
     const int cch = lane % CPR, crow = lane / CPR;
     int it = 0;
     bool ok = true;
+    int item = -1;
     for (long long w = w_begin; w < w_end && ok;) {
-      const ChunkSeg x = chunk_seg(g, w, w_end, S, n_items);
+      const ChunkSeg x = chunk_seg(g, w, w_end, S, n_items, item);
+      item = x.item + 1;
       // 32 tiles' pages at once, a tile a lane
       int ph[PW], key[PW];
       float ks[PW], vs[PW];
@@ -531,7 +612,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
         if ((j & 31) == 0) {
 #pragma unroll
           for (int q = 0; q < PW; ++q) {
-            const int t = (x.t0 + j + lane) * KP + cw * PW + q;
+            const int t = (x.t0 + x.n - 1 - j - lane) * KP + cw * PW + q;
             ph[q] = -1;
             key[q] = kNoKey;
             ks[q] = 0.0f;
@@ -592,8 +673,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
         }
         tm_commit(&s_full[hf]);
       };
+      int item = -1;
+      if (w_begin >= w_end) g.cuts[blockIdx.x] = make_int2(-1, 0);
       for (long long w = w_begin; w < w_end && ok; ++seg) {
-        const ChunkSeg x = chunk_seg(g, w, w_end, S, n_items);
+        const ChunkSeg x = chunk_seg(g, w, w_end, S, n_items, item);
+        item = x.item + 1;
+        if (seg == 0) g.cuts[blockIdx.x] = make_int2(x.t0 > 0 ? x.item : -1, x.kvh);
         const int halves = x.s.count * G - x.rt * kChunkRows > 128 ? 2 : 1;
         ok = wait(&q_full, seg) && wait(&k_full[it & 1], it / 2);
         if (!ok) break;
@@ -609,7 +694,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
             ++p_it[hf];
             tm_fence_after();
             const uint64_t v = v_desc + (uint32_t)(sg * (TILE >> 4));
-            const uint32_t d = tm + 256 + D * hf, pa = tm + 128 * hf;
+            const uint32_t d = tm + 256 + D * hf, pa = tm + 128 * hf + 64;
 #pragma unroll
             for (int k = 0; k < kChunkKeys / 16; ++k) mma_ts(d, pa + 8 * k, v + 128 * k, id_pv, k > 0 || j > 0);
             if (j + 1 < x.n) scores(hf, sg ^ 1);
@@ -641,7 +726,7 @@ cudaError_t chunk_start(const ChunkArgs& g, cudaStream_t st) {
   const int smem = 6 * kChunkKeys * D * 2 + 1024;
   const cudaError_t e = ensure_smem((const void*)chunk_kernel<I8, D, P, CAP, BIAS>, smem);
   if (e != cudaSuccess) return e;
-  return launch_k(false, chunk_kernel<I8, D, P, CAP, BIAS>, dim3(g.blocks), dim3(kChunkThreads), (size_t)smem, st, g);
+  return launch_k(true, chunk_kernel<I8, D, P, CAP, BIAS>, dim3(g.blocks), dim3(kChunkThreads), (size_t)smem, st, g);
 }
 template <bool I8, int D, int P>
 cudaError_t chunk_form(const ChunkArgs& g, cudaStream_t st) {

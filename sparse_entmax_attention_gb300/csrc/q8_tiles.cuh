@@ -124,16 +124,15 @@ __device__ __forceinline__ float q8_score(float dot, const Q8Row& r, float ks, i
 }
 __device__ __forceinline__ bool q8_sees(const Q8Row& r, int j, int pre) { return (j >= r.lo && j <= r.pos) || j < pre; }
 
-// tanh(y) = y·T(y²) for |y| ≤ 1: T interpolates tanh(√z)/√z at the Chebyshev
-// points of [0, 1] (degree 6; relative error below 1.5e-7 in fp32, against
-// tanh in 64 bits at 20001 points).
-__device__ __forceinline__ unsigned long long tanh2_small(unsigned long long y, unsigned long long z) {
-  constexpr float kTanh[7] = {0.99999994f,  -0.33332828f,   0.13325076f, -0.053451646f,
-                              0.020279707f, -0.0061943247f, 0.0010380251f};
-  unsigned long long r = f2_fma(z, f2_splat(kTanh[6]), f2_splat(kTanh[5]));
-#pragma unroll
-  for (int i = 4; i >= 0; --i) r = f2_fma(r, z, f2_splat(kTanh[i]));
-  return f2_mul(r, y);
+// tanh(y) = y·T(y²): T interpolates tanh(√z)/√z at the Chebyshev points of
+// [0, 1/4] (degree 3, relative error below 7e-7 in fp32 for |y| ≤ 1/2) and of
+// [0, 1] (degree 6, below 1.5e-7), both against tanh in 64 bits at 20001 points.
+struct TanhPoly {
+  float near[4], far[7];
+};
+__device__ __forceinline__ constexpr TanhPoly tanh_poly() {
+  return TanhPoly{{0.99999946f, -0.33326283f, 0.1318994f, -0.04439274f},
+                  {0.99999994f, -0.33332828f, 0.13325076f, -0.053451646f, 0.020279707f, -0.0061943247f, 0.0010380251f}};
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
