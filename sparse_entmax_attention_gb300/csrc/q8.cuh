@@ -37,11 +37,14 @@ struct Q8Slot {
 };
 __device__ __forceinline__ Q8Slot q8_slot(const Q8Cache& c, const Q8Batch& b, int i, uint32_t* st) {
   Q8Slot s{-1, 0, 0, 0};
-  const int n = b.count[i];
+  const int n = b.count[i], start = b.start[i], seq = b.seq_ids ? b.seq_ids[i] : i;  // (one round trip)
   if (n == 0) return s;
-  s.start = b.start[i];
-  s.seq = seq_row(b.seq_ids, i, c.max_seqs, st);
-  if (s.seq < 0) return s;
+  s.start = start;
+  if (seq < 0 || seq >= c.max_seqs) {
+    raise_flag(st, ENTMAXKV_DEV_BAD_SEQ_ID);
+    return s;
+  }
+  s.seq = seq;
   s.L = seq_len_clamped(c.seq_lens, s.seq, c.maxp, c.P, st);
   if (n < 0 || n > b.max_count || n > s.L || s.start < 0 || (long long)s.start + n > b.total) {
     raise_flag(st, ENTMAXKV_DEV_BAD_BATCH);
@@ -51,11 +54,11 @@ __device__ __forceinline__ Q8Slot q8_slot(const Q8Cache& c, const Q8Batch& b, in
   return s;
 }
 
-// e4m3 pair -> two halves (exact), low byte first.
-__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t two) {
-  uint32_t r;
-  asm("{\n .reg .b16 t;\n cvt.u16.u32 t, %1;\n cvt.rn.f16x2.e4m3x2 %0, t;\n}\n" : "=r"(r) : "r"(two));
-  return r;
+// Four e4m3 codes -> halves (exact): bytes 0 and 1 to x, 2 and 3 to y.
+__device__ __forceinline__ void e4m3x4_half(uint32_t w, uint32_t& x, uint32_t& y) {
+  asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
+      : "=r"(x), "=r"(y)
+      : "r"(w));
 }
 
 // Four codes of a word as halves, exact: even holds bytes 0 and 2, odd bytes 1
@@ -74,9 +77,7 @@ __device__ __forceinline__ void codes_half(uint32_t w, uint32_t& x, uint32_t& y)
     x = *reinterpret_cast<const uint32_t*>(&ha);
     y = *reinterpret_cast<const uint32_t*>(&hb);
   } else {
-    const uint32_t p = SPLIT ? __byte_perm(w, 0u, 0x3120) : w;
-    x = e4m3x2_half2(p);
-    y = e4m3x2_half2(p >> 16);
+    e4m3x4_half(SPLIT ? __byte_perm(w, 0u, 0x3120) : w, x, y);
   }
 }
 
@@ -84,8 +85,9 @@ __device__ __forceinline__ void codes_half(uint32_t w, uint32_t& x, uint32_t& y)
 template <bool I8>
 __device__ __forceinline__ float code_f(uint32_t byte) {
   if constexpr (I8) return (float)(int)(int8_t)(byte & 0xffu);
-  const uint32_t h = e4m3x2_half2(byte & 0xffu);
-  return __low2float(*reinterpret_cast<const __half2*>(&h));
+  uint32_t x, y;
+  e4m3x4_half(byte & 0xffu, x, y);
+  return __low2float(*reinterpret_cast<const __half2*>(&x));
 }
 
 // D = A·B + D for one m16n8k16 tile, fp16 inputs, fp32 accumulate.
@@ -162,7 +164,8 @@ struct Q8AttendArgs {
   Q8Rows q, out;
   float* tau;
   // workspace
-  long long* cum;   // [n_seqs + 1] tile-pages before each slot
+  long long* cum;   // [n_seqs + 1] tiles before each slot
+  void* slots;      // [n_seqs] what the streaming kernel made of each slot
   float* part_o;    // [blocks][2][rows][D]
   float* part_ml;   // [blocks][2][rows][2] running max (base 2) and sum
   int blocks;

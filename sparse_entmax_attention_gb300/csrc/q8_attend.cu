@@ -8,34 +8,37 @@
 // for all warps of the device, so sequences of any lengths load it evenly. A
 // warp streams its pages through a ring of tensor copies in shared memory:
 //   S = K·q^T      m16n8k16 in halves (codes are exact as halves; q is scaled
-//                  to exact halves), 16 tokens × 8 rows a tile, fp32 sums;
-//   page max m_p, p = 2^{s − m_p} as halves (2^-12), transposed in registers;
-//   T = V^T·p      16 dims × 8 rows a tile, fp32 sums of the page alone;
-//   acc = acc·2^{m − m'} + T·(vs·2^{m_p − m'}), and the same for Σ p (which
-//                  keeps the unrounded p).
-// Weights are rounded against their own page's maximum, so many small ones
-// behind a large one are not lost. A unit inside one warp's piece is finished
-// there; the others leave (m, Σp, acc) pieces which a second kernel joins in
-// the order of the line.
+//                  to exact halves), 16 tokens × 8 rows a product, fp32 sums;
+//   t = S·ks·scale·log2 e (capped, biased, masked) + log2 vs
+//   w = 2^{t − M + 8} as halves (2^-12), transposed in registers, M a bound of
+//                  the row's maximum that moves when a t passes it by 6 (a vote
+//                  a tile; the maximum itself is only formed then): w ≤ 2^14, and
+//                  weights down to 2^-32 of the largest survive the rounding;
+//   acc += V^T·w   16 dims × 8 rows a product, fp32; Σp is Σ over pages of
+//                  (Σ w)/vs, of unrounded w.
+// A tile is 32 keys: one page, or two of 16. A unit inside one warp's piece is
+// finished there, neighbouring warps of a block join theirs in shared memory,
+// and the rest leaves (M, Σp, acc) pieces which a second kernel joins in the
+// order of the line.
 #include "q8_tiles.cuh"
 
 namespace ekv {
 
-constexpr int kAttWarps = 8;
-constexpr int kAttMaxBlocks = 512;
-// Stages of a warp's ring: 24 KB of pages at d = 128, whatever the page size.
-template <int P>
-constexpr int kAttStages = 96 / P;
+// Warps of a block, and K or V slabs (4 KB each at d = 128) of a warp's ring:
+// 16 warps keep the pipes busier than 12 or 8 do, and fit 128 registers with
+// one tile of 8 rows; with two they need twice as many.
+template <int NT>
+constexpr int kAttWarps = NT == 1 ? 16 : 8;
+template <int NT>
+constexpr int kAttSlabs = NT == 1 ? 3 : 6;
+constexpr int kAttMaxBlocks = 256;
+constexpr int kAttKeys = 32;
 
-static int att_rows(const entmaxkv_config& cfg, int max_count) {
-  return (long long)max_count * cfg.group <= 8 ? 8 : 16;
-}
-
-// Row tiles and span of a slot; W = its pages on the line.
+// Row tiles, tiles of keys and span of a slot; W = its tiles on the line.
 struct AttSlot {
   Q8Slot s;
   Q8Span sp;
-  int nrt;
+  int nrt, T;
   long long W;
 };
 template <int NT>
@@ -44,22 +47,14 @@ __device__ __forceinline__ AttSlot att_slot(const Q8AttendArgs& a, int b, uint32
   x.s = q8_slot(a.c, a.b, b, st);
   x.nrt = (x.s.count * a.c.G + 8 * NT - 1) / (8 * NT);
   x.W = 0;
+  x.T = 0;
   x.sp = Q8Span{0, 0, 0, 0, 0};
   if (x.s.count > 0) {
     x.sp = q8_span(a.c, a.sc, x.s, b, 0, x.s.count);
-    x.W = (long long)x.sp.T * a.c.Hkv * x.nrt;
+    x.T = (x.sp.T * a.c.P + kAttKeys - 1) / kAttKeys;
+    x.W = (long long)x.T * a.c.Hkv * x.nrt;
   }
   return x;
-}
-
-// The line's cut: warp w of nw begins at W·w/nw; nw ≤ W, so no piece is empty.
-struct AttCut {
-  long long W, nw;
-  __device__ __forceinline__ long long begin(long long w) const { return W * w / nw; }
-  __device__ __forceinline__ long long of(long long at) const { return ((at + 1) * nw - 1) / W; }  // warp that holds `at`
-};
-__device__ __forceinline__ AttCut att_cut(long long W, int blocks) {
-  return AttCut{W, max(1LL, min(W, (long long)blocks * kAttWarps))};
 }
 
 // A warp's last piece: the unit that starts at A on the line, T pages long.
@@ -69,95 +64,51 @@ struct AttPiece {
 };
 
 template <bool I8, int D, int P, int NT>
-__global__ void __launch_bounds__(kAttWarps * 32, 1)
+__global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
     attend_kernel(Q8AttendArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   pdl_enter();
-  constexpr int NW = kAttWarps, ST = kAttStages<P>, SLAB = P * D, NTH = NW * 32, R = 8 * NT;
-  static_assert(R * D * 4 <= ST * 2 * SLAB, "a warp's sums fit its ring");
+  constexpr int NW = kAttWarps<NT>, ST = kAttSlabs<NT>, SLAB = kAttKeys * D, NTH = NW * 32, R = 8 * NT;
+  constexpr int PP = kAttKeys / P;  // pages a tile
+  static_assert(R * D * 4 <= ST * SLAB, "a warp's sums fit its ring");
   extern __shared__ __align__(128) unsigned char dyn_sm[];
   __shared__ uint64_t bars[NW][ST];
-  __shared__ long long sh_sum[NW];
-  __shared__ long long sh_cum[NW];
-  __shared__ int sh_slot[NW];
+  __shared__ LineSmem<NW> sh_line;
   __shared__ AttSlot sh_info[NTH];  // the slots, when they are few
   __shared__ AttPiece sh_piece[NW];
   __shared__ float2 sh_ml[NW][R];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring0 = (smem_u32(dyn_sm) + 1023u) & ~1023u;
-  const uint32_t ring = ring0 + (uint32_t)warp * ST * 2 * SLAB;
+  const uint32_t ring = ring0 + (uint32_t)warp * ST * SLAB;
   unsigned char* ring_p = dyn_sm + (ring - smem_u32(dyn_sm));
   if (lane == 0) {
     for (int i = 0; i < ST; ++i) mbar_init(&bars[warp][i], 1);
     mbar_fence_init();
     sh_piece[warp].A = -1;
   }
-  // the line: its length, then where each warp's piece begins
-  uint32_t* st0 = blockIdx.x == 0 ? a.c.status : nullptr;
+  if (tid == 0) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
   const int n_seqs = a.b.n_seqs;
   const bool few = n_seqs <= NTH;
-  long long own = 0;
-  for (int b = tid; b < n_seqs; b += NTH) {
-    const AttSlot x = att_slot<NT>(a, b, st0);
-    own += x.W;
-    if (few) sh_info[b] = x;
-  }
-  long long inc = own;  // inclusive over the block's threads
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += u;
-  }
-  if (lane == 31) sh_sum[warp] = inc;
-  __syncthreads();
-  long long W = 0, before = inc - own;
-  for (int i = 0; i < NW; ++i) {
-    if (i < warp) before += sh_sum[i];
-    W += sh_sum[i];
-  }
-  const AttCut cut = att_cut(W, (int)gridDim.x);
-  auto place = [&](int b, long long at, long long n) {  // slot b lies at [at, at + n) of the line
-    if (blockIdx.x == 0) a.cum[b] = at;
-    for (int i = 0; i < NW; ++i) {
-      const long long w = cut.begin((long long)blockIdx.x * NW + i);
-      if (at <= w && w < at + n) {
-        sh_slot[i] = b;
-        sh_cum[i] = at;
-      }
-    }
-  };
-  if (few) {
-    if (tid < n_seqs) place(tid, before, own);
-  } else {
-    long long base = 0;
-    for (int b0 = 0; b0 < n_seqs; b0 += NTH) {
-      const int b = b0 + tid;
-      const long long mine = b < n_seqs ? att_slot<NT>(a, b, nullptr).W : 0;
-      long long in = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, in, o);
-        if (lane >= o) in += u;
-      }
-      __syncthreads();  // the sums of the round before are read
-      if (lane == 31) sh_sum[warp] = in;
-      __syncthreads();
-      long long at = base + in - mine;
-      for (int i = 0; i < NW; ++i) {
-        if (i < warp) at += sh_sum[i];
-        base += sh_sum[i];
-      }
-      if (b < n_seqs) place(b, at, mine);
-    }
-  }
-  if (blockIdx.x == 0 && tid == 0) a.cum[n_seqs] = W;
-  __syncthreads();
+  const LinePlace at = line_place<NW>(
+      n_seqs, a.c.status, sh_line,
+      [&](int b, uint32_t* st) {
+        const AttSlot x = att_slot<NT>(a, b, st);
+        if (few) sh_info[b] = x;
+        return x.W;
+      },
+      [&](int b, long long where) {
+        a.cum[b] = where;
+        if (b < n_seqs) reinterpret_cast<AttSlot*>(a.slots)[b] = few ? sh_info[b] : att_slot<NT>(a, b, nullptr);
+      });
+  const LineCut cut = at.cut;
   const long long me = (long long)blockIdx.x * NW + warp;
-  const long long w_begin = me < cut.nw ? cut.begin(me) : 0, w_end = me < cut.nw ? cut.begin(me + 1) : 0;
+  const long long w_begin = at.begin, w_end = at.end;
   const int G = a.c.G, Hkv = a.c.Hkv;
   const int r = lane >> 2, c = lane & 3;
-  const bool general = a.sc.cap > 0.0f || a.sc.slopes;
-  int slot = w_begin < w_end ? sh_slot[warp] : 0;
-  long long cum = sh_cum[warp];
+  int slot = at.slot;
+  long long cum = at.cum;
   long long w = w_begin;
   int filled = 0, used = 0;  // ring fills of this warp, in order
   bool stuck = false;
@@ -168,44 +119,56 @@ __global__ void __launch_bounds__(kAttWarps * 32, 1)
       ++slot;
       continue;
     }
-    const int T = x.sp.T;
+    const int T = x.T;
     const long long off = w - cum;
     const int u = (int)(off / T), t0 = (int)(off - (long long)u * T);
     const int n = (int)min((long long)(T - t0), w_end - w);
     const int kvh = u / x.nrt, rt = u - kvh * x.nrt;
     const int rows = min(R, x.s.count * G - rt * R);
-    // 32 pages' places and scales at once, one a lane; those of the next 32 come in meanwhile
-    int ph[2];
-    float ks_l[2], vs_l[2];
-    auto look_up = [&](int p0, int& f, float& ks, float& vs) {
-      f = -1;
-      ks = vs = 0.0f;
-      if (p0 + lane < n) {
-        f = phys_page(a.c.block_table, x.s.seq, x.sp.page(t0 + p0 + lane), a.c.maxp, a.c.nphys, a.c.status);
-        if (f >= 0) {
-          ks = a.c.k_scale[(size_t)f * Hkv + kvh];
-          vs = a.c.v_scale[(size_t)f * Hkv + kvh];
+    // 32 tiles' places and scales at once, a tile a lane
+    int ph[PP];
+    float ks_l[PP], vs_l[PP];
+    auto look_up = [&](int p0) {
+#pragma unroll
+      for (int q = 0; q < PP; ++q) {
+        const int t = (t0 + n - 1 - p0 - lane) * PP + q;  // nearest keys first: a distance bias sets the bound at once
+        ph[q] = -1;
+        ks_l[q] = 0.0f;
+        vs_l[q] = 1.0f;
+        if (p0 + lane < n && t < x.sp.T) {
+          ph[q] = phys_page(a.c.block_table, x.s.seq, x.sp.page(t), a.c.maxp, a.c.nphys, a.c.status);
+          if (ph[q] >= 0) {
+            ks_l[q] = a.c.k_scale[(size_t)ph[q] * Hkv + kvh];
+            vs_l[q] = a.c.v_scale[(size_t)ph[q] * Hkv + kvh];
+          }
         }
       }
     };
-    look_up(0, ph[0], ks_l[0], vs_l[0]);
-    ph[1] = -1;
-    int ask = 0;  // next page to ask for
-    auto refill = [&](int chunk, int end) {
-      while (ask < end && filled - used < ST) {
-        const int f = __shfl_sync(0xffffffffu, (ask >> 5) == chunk ? ph[0] : ph[1], ask & 31);
+    int ask = 0;  // next slab to ask for: K and V of a tile in turn
+    auto refill = [&](int end) {
+      while (ask < 2 * end && filled - used < ST) {
+        int f[PP], there = 0;
+#pragma unroll
+        for (int q = 0; q < PP; ++q) {
+          f[q] = __shfl_sync(0xffffffffu, ph[q], (ask >> 1) & 31);
+          there += f[q] >= 0;
+        }
+        const int side = ask & 1;
         ++ask;
-        if (f < 0) continue;
+        if (!there) continue;
         const int sg = filled % ST;
         if (lane == 0) {
-          mbar_expect_tx(&bars[warp][sg], 2 * SLAB);
-          tma_load_3d(ring_p + sg * 2 * SLAB, &kmap, 0, kvh * P, f, &bars[warp][sg]);
-          tma_load_3d(ring_p + sg * 2 * SLAB + SLAB, &vmap, 0, kvh * P, f, &bars[warp][sg]);
+          mbar_expect_tx(&bars[warp][sg], (uint32_t)(there * P * D));
+#pragma unroll
+          for (int q = 0; q < PP; ++q)
+            if (f[q] >= 0)
+              tma_load_3d(ring_p + sg * SLAB + q * P * D, side ? &vmap : &kmap, 0, kvh * P, f[q], &bars[warp][sg]);
         }
         ++filled;
       }
     };
-    refill(0, min(n, 32));  // before the queries are looked at
+    look_up(0);
+    refill(min(n, 32));  // before the queries are looked at
     // query fragments and row facts
     uint32_t bq[NT][D / 16][2];
     Q8Row row[NT][2];
@@ -223,7 +186,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 1)
         const float f = __shfl_sync(0xffffffffu, inv, (2 * c + j) * 4);
         const int rj = 8 * nt + 2 * c + j, rg = rt * R + rj;
         Q8Row& q = row[nt][j];
-        q.cs = f * a.sc.scale * (a.sc.cap > 0.0f ? 1.0f : kLog2e);
+        q.cs = q8_row_scale(f, a.sc, kLog2e);
         q.slope = 0.0f;
         q.pos = 0;
         q.lo = 0;
@@ -241,7 +204,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 1)
     pos_min = __reduce_min_sync(0xffffffffu, pos_min);
     lo_max = __reduce_max_sync(0xffffffffu, lo_max);
 
-    float m[NT][2], l[NT][2], acc[D / 16][NT][4];
+    float m[NT][2], l[NT][2], acc[D / 16][NT][4];  // M, Σp, Σ w·code
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -CUDART_INF_F;
@@ -250,116 +213,124 @@ __global__ void __launch_bounds__(kAttWarps * 32, 1)
       for (int mt = 0; mt < D / 16; ++mt) acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.0f;
     }
     for (int i = 0; i < n; ++i) {
-      if ((i & 31) == 0) {
-        if (i) {
-          ph[0] = ph[1];
-          ks_l[0] = ks_l[1];
-          vs_l[0] = vs_l[1];
-        }
-        look_up(i + 32, ph[1], ks_l[1], vs_l[1]);
-        refill(i >> 5, min(n, i + 64));
+      if ((i & 31) == 0 && i) {
+        look_up(i);
+        refill(min(n, i + 32));
       }
-      if (__shfl_sync(0xffffffffu, ph[0], i & 31) < 0) continue;
-      const float ks = __shfl_sync(0xffffffffu, ks_l[0], i & 31), vs = __shfl_sync(0xffffffffu, vs_l[0], i & 31);
-      const int sg = used % ST;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[warp][sg], (used / ST) & 1))) {
+      const int end = min(n, (i | 31) + 1);
+      int f[PP], key0[PP];
+      float ks[PP], vs[PP];
+      bool some = false, whole = true;
+#pragma unroll
+      for (int q = 0; q < PP; ++q) {
+        f[q] = __shfl_sync(0xffffffffu, ph[q], i & 31);
+        ks[q] = __shfl_sync(0xffffffffu, ks_l[q], i & 31);
+        vs[q] = fmaxf(__shfl_sync(0xffffffffu, vs_l[q], i & 31), 0x1p-100f);
+        key0[q] = f[q] >= 0 ? x.sp.page((t0 + n - 1 - i) * PP + q) * P : kNoKey;
+        some |= f[q] >= 0;
+        whole &= (key0[q] + P - 1 <= pos_min && key0[q] >= lo_max) || key0[q] + P <= x.sp.pre;
+      }
+      if (!some) continue;
+      auto arrived = [&]() -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(&bars[warp][used % ST], (used / ST) & 1));
+      };
+      if (!arrived()) {
         stuck = true;
         break;
       }
-      const uint32_t slab = ring + sg * 2 * SLAB;
-      const int key0 = x.sp.page(t0 + i) * P;
-      const bool whole = (key0 + P - 1 <= pos_min && key0 >= lo_max) || key0 + P <= x.sp.pre;
-      if (x.s.L - key0 < P) {  // slots past the sequence's end: any bytes, so that p = 0 meets no NaN
-        const int nv = x.s.L - key0;
-        for (int e = lane; e < (P - nv) * (D / 16); e += 32)
-          *reinterpret_cast<uint4*>(ring_p + sg * 2 * SLAB + SLAB + nv * D + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        __syncwarp();
-      }
-      float s[P / 16][NT][4];
-      float pm[NT][2];
+      uint32_t slab = ring + (used % ST) * SLAB;
+      float s[2][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) pm[nt][0] = pm[nt][1] = -CUDART_INF_F;
-#pragma unroll
-      for (int mt = 0; mt < P / 16; ++mt) {
+      for (int mt = 0; mt < 2; ++mt) {
         k_dot<I8, D, NT>(slab, 16 * mt, lane, bq, s[mt]);
+        const int q = 16 * mt / P, j0 = key0[q] + (16 * mt) % P + r;
+        const float lv = __log2f(vs[q]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = key0 + 16 * mt + r + 8 * (e >> 1);
-            float v = q8_score(s[mt][nt][e], row[nt][e & 1], ks, j, a.sc, general, kLog2e);
-            if (!whole && !q8_sees(row[nt][e & 1], j, x.sp.pre)) v = -CUDART_INF_F;
-            s[mt][nt][e] = v;
-            pm[nt][e & 1] = fmaxf(pm[nt][e & 1], v);
+          for (int j = 0; j < 2; ++j) {
+            const float dot[2] = {s[mt][nt][j], s[mt][nt][2 + j]};
+            float v[2];
+            q8_scores(dot, v, row[nt][j], ks[q], j0, a.sc, kLog2e, lv);
+            if (!whole) {
+              if (!q8_sees(row[nt][j], j0, x.sp.pre)) v[0] = -CUDART_INF_F;
+              if (!q8_sees(row[nt][j], j0 + 8, x.sp.pre)) v[1] = -CUDART_INF_F;
+            }
+            s[mt][nt][j] = v[0];
+            s[mt][nt][2 + j] = v[1];
           }
       }
-      float fv[NT][2], cr[NT][2];
-      bool grew = false;
+      __syncwarp();  // every lane has read the K slab
+      ++used;
+      refill(end);
+      bool over = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float v = pm[nt][j];
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          const float mn = fmaxf(m[nt][j], v);
-          cr[nt][j] = mn > m[nt][j] ? ex2f(m[nt][j] - mn) : 1.0f;  // 0 from -inf
-          grew |= mn > m[nt][j];
-          fv[nt][j] = v > -CUDART_INF_F ? ex2f(v - mn) : 0.0f;
-          m[nt][j] = mn;
-          pm[nt][j] = v > -CUDART_INF_F ? v : 0.0f;
+        for (int j = 0; j < 2; ++j)
+          over |= fmaxf(max3(s[0][nt][j], s[0][nt][2 + j], s[1][nt][j]), s[1][nt][2 + j]) > m[nt][j] + kSlack;
+      if (__any_sync(0xffffffffu, over)) {  // some bound moves
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float v = fmaxf(fmaxf(s[0][nt][j], s[0][nt][2 + j]), fmaxf(s[1][nt][j], s[1][nt][2 + j]));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            if (v > m[nt][j] + kSlack) {
+              const float cr = ex2f(m[nt][j] - v);  // 0 from -inf
+              m[nt][j] = v;
+              l[nt][j] *= cr;
+#pragma unroll
+              for (int mt = 0; mt < D / 16; ++mt) {
+                acc[mt][nt][j] *= cr;
+                acc[mt][nt][2 + j] *= cr;
+              }
+            }
+          }
+      }
+      if (!arrived()) {
+        stuck = true;
+        break;
+      }
+      slab = ring + (used % ST) * SLAB;
+      if (!whole) {  // slots past the sequence's end, or of no page: any bytes, so that w = 0 meets no NaN
+        bool wrote = false;
+#pragma unroll
+        for (int q = 0; q < PP; ++q) {
+          const int nv = max(0, min(P, x.s.L - key0[q]));
+          if (nv == P) continue;
+          for (int e = lane; e < (P - nv) * (D / 16); e += 32)
+            *reinterpret_cast<uint4*>(ring_p + (used % ST) * SLAB + (q * P + nv) * D + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+          wrote = true;
         }
-      float tmp[D / 16][NT][4];
+        if (wrote) {
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+          __syncwarp();
+        }
+      }
 #pragma unroll
-      for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) tmp[mt][nt][0] = tmp[mt][nt][1] = tmp[mt][nt][2] = tmp[mt][nt][3] = 0.0f;
-      float ls[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) ls[nt][0] = ls[nt][1] = 0.0f;
-#pragma unroll
-      for (int kt = 0; kt < P / 16; ++kt) {
+      for (int kt = 0; kt < 2; ++kt) {
         uint32_t b[NT][2];
+        const float ivs = __fdividef(1.0f, vs[16 * kt / P]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float p[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = ex2f(s[kt][nt][e] - pm[nt][e & 1]);
-            ls[nt][e & 1] += p[e];
-          }
+          for (int e = 0; e < 4; ++e)
+            p[e] = ex2f(s[kt][nt][e] + (m[nt][e & 1] > -CUDART_INF_F ? kLift - m[nt][e & 1] : 0.0f));
+          l[nt][0] = fmaf(p[0] + p[2], ivs, l[nt][0]);
+          l[nt][1] = fmaf(p[1] + p[3], ivs, l[nt][1]);
           const __half2 h0 = __floats2half2_rn(p[0], p[1]), h1 = __floats2half2_rn(p[2], p[3]);
           b[nt][0] = transpose8(*reinterpret_cast<const uint32_t*>(&h0));
           b[nt][1] = transpose8(*reinterpret_cast<const uint32_t*>(&h1));
         }
-        v_dot<I8, D, NT>(slab + SLAB, 16 * kt, lane, b, tmp);
+        v_dot<I8, D, NT>(slab, 16 * kt, lane, b, acc);
       }
-      if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          l[nt][0] *= cr[nt][0];
-          l[nt][1] *= cr[nt][1];
-#pragma unroll
-          for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[mt][nt][e] *= cr[nt][e & 1];
-        }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        l[nt][0] = fmaf(ls[nt][0], fv[nt][0], l[nt][0]);
-        l[nt][1] = fmaf(ls[nt][1], fv[nt][1], l[nt][1]);
-        const float f0 = fv[nt][0] * vs, f1 = fv[nt][1] * vs;
-#pragma unroll
-        for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[mt][nt][e] = fmaf(tmp[mt][nt][e], e & 1 ? f1 : f0, acc[mt][nt][e]);
-      }
-      __syncwarp();  // every lane has read the stage
+      __syncwarp();  // every lane has read the V slab
       ++used;
-      refill(i >> 5, min(n, ((i >> 5) + 2) * 32));
+      refill(end);
     }
     if (stuck) break;
 #pragma unroll
@@ -369,6 +340,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 1)
         l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
         l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
         l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
+        m[nt][j] -= kLift;
       }
     const bool last = w + n == w_end;
     if (n == T) {  // the whole unit
@@ -435,7 +407,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, 1)
         const float2 ml = sh_ml[i][rj];
         const float f = ml.x > -CUDART_INF_F ? ex2f(ml.x - M) : 0.0f;
         l = fmaf(f, ml.y, l);
-        o = fmaf(f, reinterpret_cast<const float*>(dyn_sm + (ring0 - smem_u32(dyn_sm)) + i * ST * 2 * SLAB)[e], o);
+        o = fmaf(f, reinterpret_cast<const float*>(dyn_sm + (ring0 - smem_u32(dyn_sm)) + i * ST * SLAB)[e], o);
       }
       if (all) {
         const int rg = x.rt * R + rj;
@@ -460,15 +432,15 @@ __global__ void __launch_bounds__(kAttWarps * 32, 1)
 template <int D, int NT>
 __global__ void __launch_bounds__(D) attend_join_kernel(Q8AttendArgs a, int nrt_max) {
   pdl_enter();
-  constexpr int R = 8 * NT, NW = kAttWarps;
+  constexpr int R = 8 * NT, NW = kAttWarps<NT>;
   const int b = blockIdx.y, rj = blockIdx.x % R, rt = blockIdx.x / R % nrt_max, kvh = blockIdx.x / R / nrt_max;
-  const AttSlot x = att_slot<NT>(a, b, nullptr);
+  const AttSlot x = reinterpret_cast<const AttSlot*>(a.slots)[b];
+  const long long W = a.cum[a.b.n_seqs], at = a.cum[b];
   const int G = a.c.G;
   if (rt >= x.nrt || rj >= x.s.count * G - rt * R) return;
-  const long long W = a.cum[a.b.n_seqs];
-  const AttCut cut = att_cut(W, a.blocks);
-  const int T = x.sp.T;
-  const long long A = a.cum[b] + ((long long)kvh * x.nrt + rt) * T, B = A + T;
+  const LineCut cut = line_cut(W, a.blocks, NW);
+  const int T = x.T;
+  const long long A = at + ((long long)kvh * x.nrt + rt) * T, B = A + T;
   float M = -CUDART_INF_F, l = 0.0f, o = 0.0f;
   if (T > 0) {
     const long long w0 = cut.of(A), w1 = cut.of(B - 1);
@@ -481,14 +453,32 @@ __global__ void __launch_bounds__(D) attend_join_kernel(Q8AttendArgs a, int nrt_
       return (size_t)(i ? (c0 + i) * NW : w0) * 2 + 1;
     };
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) M = fmaxf(M, ml[piece(i) * R + rj].x);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float2 v = ml[piece(i) * R + rj];
-      const float f = v.x > -CUDART_INF_F ? ex2f(v.x - M) : 0.0f;
-      l = fmaf(f, v.y, l);
-      o = fmaf(f, a.part_o[(piece(i) * R + rj) * D + threadIdx.x], o);
+    for (int i0 = 0; i0 < n; i0 += 8) {  // eight pieces' loads in flight
+      float2 v[8];
+      float p[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = make_float2(-CUDART_INF_F, 0.0f);
+        p[k] = 0.0f;
+        if (i0 + k < n) {
+          const size_t at8 = piece(i0 + k) * R + rj;
+          v[k] = ml[at8];
+          p[k] = a.part_o[at8 * D + threadIdx.x];
+        }
+      }
+      float m = M;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = fmaxf(m, v[k].x);
+      const float old = M > -CUDART_INF_F ? ex2f(M - m) : 0.0f;
+      l *= old;
+      o *= old;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float f = v[k].x > -CUDART_INF_F ? ex2f(v[k].x - m) : 0.0f;
+        l = fmaf(f, v[k].y, l);
+        o = fmaf(f, p[k], o);
+      }
+      M = m;
     }
   }
   const int rg = rt * R + rj;
@@ -515,13 +505,13 @@ cudaError_t make_q8_map(CUtensorMap* map, const void* pool, int nphys, int Hkv, 
 static size_t up256z(size_t x) { return (x + 255) & ~(size_t)255; }
 
 size_t attend_softmax_bytes(const entmaxkv_config& cfg, int n_seqs, int max_count) {
-  const size_t pieces = (size_t)kAttMaxBlocks * kAttWarps * 2 * att_rows(cfg, max_count);
-  return up256z((size_t)(n_seqs + 1) * 8) + up256z(pieces * cfg.head_dim * 4) + up256z(pieces * 8);
+  const size_t pieces = (size_t)kAttMaxBlocks * 16 * 2 * 8;  // 16 warps of 8 rows, or 8 of 16
+  return up256z((size_t)(n_seqs + 1) * 8) + up256z((size_t)n_seqs * sizeof(AttSlot)) + up256z(pieces * cfg.head_dim * 4) + up256z(pieces * 8);
 }
 
 template <bool I8, int D, int P, int NT>
 static cudaError_t attend_t(Q8AttendArgs& a, void* ws, int sms, cudaStream_t st) {
-  const int smem = kAttWarps * kAttStages<P> * 2 * P * D + 1024;
+  const int smem = kAttWarps<NT> * kAttSlabs<NT> * kAttKeys * D + 1024;
   cudaError_t e = ensure_smem((const void*)attend_kernel<I8, D, P, NT>, smem);
   if (e != cudaSuccess) return e;
   CUtensorMap km, vm;
@@ -529,16 +519,18 @@ static cudaError_t attend_t(Q8AttendArgs& a, void* ws, int sms, cudaStream_t st)
   if ((e = make_q8_map(&vm, a.c.v_pool, a.c.nphys, a.c.Hkv, P, D)) != cudaSuccess) return e;
   a.blocks = min(sms, kAttMaxBlocks);
   char* p = static_cast<char*>(ws);
-  const size_t pieces = (size_t)kAttMaxBlocks * kAttWarps * 2 * 8 * NT;
+  const size_t pieces = (size_t)kAttMaxBlocks * kAttWarps<NT> * 2 * 8 * NT;
   a.cum = reinterpret_cast<long long*>(p);
   p += up256z((size_t)(a.b.n_seqs + 1) * 8);
+  a.slots = p;
+  p += up256z((size_t)a.b.n_seqs * sizeof(AttSlot));
   a.part_o = reinterpret_cast<float*>(p);
   p += up256z(pieces * D * 4);
   a.part_ml = reinterpret_cast<float*>(p);
-  e = launch_k(false, attend_kernel<I8, D, P, NT>, dim3(a.blocks), dim3(kAttWarps * 32), (size_t)smem, st, a, km, vm);
+  e = launch_k(false, attend_kernel<I8, D, P, NT>, dim3(a.blocks), dim3(kAttWarps<NT> * 32), (size_t)smem, st, a, km, vm);
   if (e != cudaSuccess) return e;
   const int nrt = (int)(((long long)a.b.max_count * a.c.G + 8 * NT - 1) / (8 * NT));
-  return launch_k(false, attend_join_kernel<D, NT>, dim3(nrt * 8 * NT * a.c.Hkv, a.b.n_seqs), dim3(D), 0,
+  return launch_k(true, attend_join_kernel<D, NT>, dim3(nrt * 8 * NT * a.c.Hkv, a.b.n_seqs), dim3(D), 0,
                   st, a, nrt);
 }
 

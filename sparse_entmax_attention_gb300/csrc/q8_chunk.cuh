@@ -32,8 +32,6 @@ constexpr int kChunkThreads = 512;
 constexpr int kChunkRows = 256;
 constexpr int kChunkKeys = 128;
 constexpr int kChunkMaxBlocks = 256;
-constexpr float kLift = 8.0f;   // w = 2^{t − M + kLift}
-constexpr float kSlack = 6.0f;  // M moves when the row's maximum passes it by more
 
 // What the roles know of an item, filled in once by the listing kernel.
 struct __align__(16) ChunkItem {
@@ -203,7 +201,6 @@ struct PageMeta {
   float ks, lv, ivs;  // K scale, log2 of the V scale, its inverse
   int key0;           // first key; beyond every key where there is no page
 };
-constexpr int kNoKey = 0x40000000;
 
 template <bool I8, int D, int P, bool capped, bool biased>
 __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {

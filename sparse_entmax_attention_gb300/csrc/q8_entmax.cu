@@ -43,9 +43,7 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
   constexpr int NW = kEntWarps, ST = kEntStages, SLAB = P * D;
   extern __shared__ __align__(128) unsigned char dyn_sm[];
   __shared__ uint64_t bars[NW][ST];
-  __shared__ long long sh_sum[NW];
-  __shared__ long long sh_cum[NW];
-  __shared__ int sh_slot[NW];
+  __shared__ LineSmem<NW> sh_line;
   const Q8AttendArgs& a = e.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = ((smem_u32(dyn_sm) + 1023u) & ~1023u) + (uint32_t)warp * ST * SLAB;
@@ -55,55 +53,19 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
     mbar_fence_init();
   }
   const int Hkv = a.c.Hkv, G = a.c.G;
-  uint32_t* st0 = blockIdx.x == 0 ? a.c.status : nullptr;
-  auto pages_of = [&](int b, uint32_t* st) -> long long {
-    const Q8Slot s = q8_slot(a.c, a.b, b, st);
-    return s.count > 0 ? (long long)ent_span(a, s, b).T * Hkv : 0;
-  };
-  long long own = 0;
-  for (int b = tid; b < a.b.n_seqs; b += NW * 32) own += pages_of(b, st0);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
-  if (lane == 0) sh_sum[warp] = own;
-  __syncthreads();
-  long long W = 0;
-  for (int i = 0; i < NW; ++i) W += sh_sum[i];
-  __syncthreads();
-  const long long nw = (long long)gridDim.x * NW, me = (long long)blockIdx.x * NW + warp;
-  const long long w_begin = W * me / nw, w_end = W * (me + 1) / nw;
-  long long base = 0;
-  for (int b0 = 0; b0 < a.b.n_seqs; b0 += NW * 32) {
-    const int b = b0 + tid;
-    const long long mine = b < a.b.n_seqs ? pages_of(b, nullptr) : 0;
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += u;
-    }
-    if (lane == 31) sh_sum[warp] = inc;
-    __syncthreads();
-    long long before = base + inc - mine, all = 0;
-    for (int i = 0; i < NW; ++i) {
-      if (i < warp) before += sh_sum[i];
-      all += sh_sum[i];
-    }
-    if (blockIdx.x == 0 && b < a.b.n_seqs) a.cum[b] = before;
-    for (int i = 0; i < NW; ++i) {
-      const long long w = W * ((long long)blockIdx.x * NW + i) / nw;
-      if (before <= w && w < before + mine) {
-        sh_slot[i] = b;
-        sh_cum[i] = before;
-      }
-    }
-    base += all;
-    __syncthreads();
-  }
+  if (tid == 0) prefetch_map(&kmap);
+  const LinePlace at = line_place<NW>(
+      a.b.n_seqs, a.c.status, sh_line,
+      [&](int b, uint32_t* st) {
+        const Q8Slot s = q8_slot(a.c, a.b, b, st);
+        return s.count > 0 ? (long long)ent_span(a, s, b).T * Hkv : 0LL;
+      },
+      [&](int b, long long where) { a.cum[b] = where; });
+  const long long w_begin = at.begin, w_end = at.end;
   if (w_begin >= w_end) return;
   const int r = lane >> 2, c = lane & 3;
-  const bool general = a.sc.cap > 0.0f || a.sc.slopes;
-  int slot = sh_slot[warp];
-  long long cum = sh_cum[warp], w = w_begin;
+  int slot = at.slot;
+  long long cum = at.cum, w = w_begin;
   int filled = 0, used = 0;
   bool stuck = false;
   while (w < w_end && !stuck) {
@@ -128,7 +90,7 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
     if (a.sc.first_key) lo = max(lo, a.sc.first_key[s.start]);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      row[j].cs = __shfl_sync(0xffffffffu, inv, (2 * c + j) * 4) * a.sc.scale * (a.sc.cap > 0.0f ? 1.0f : e.a1);
+      row[j].cs = q8_row_scale(__shfl_sync(0xffffffffu, inv, (2 * c + j) * 4), a.sc, e.a1);
       row[j].slope = a.sc.slopes && 2 * c + j < G ? a.sc.slopes[kvh * G + 2 * c + j] * e.a1 : 0.0f;
       row[j].pos = pos;
       row[j].lo = lo;
@@ -174,12 +136,18 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
           float acc[1][4] = {{0.f, 0.f, 0.f, 0.f}};
           if (there) k_dot<I8, D, 1>(ring + sg * SLAB, 16 * mt, lane, bq, acc);
 #pragma unroll
-          for (int el = 0; el < 4; ++el) {
-            const int tk = 16 * mt + r + 8 * (el >> 1), h = 2 * c + (el & 1);
-            float v = q8_score(acc[0][el], row[el & 1], ks, key0 + tk, a.sc, general, e.a1);
-            if (!there || (!whole && !q8_sees(row[el & 1], key0 + tk, sp.pre))) v = -CUDART_INF_F;
-            if (h < G) zo[h * P + tk] = v;
-            pm[el & 1] = fmaxf(pm[el & 1], v);
+          for (int j = 0; j < 2; ++j) {
+            const int tk = 16 * mt + r, h = 2 * c + j;
+            const float dot[2] = {acc[0][j], acc[0][2 + j]};
+            float v[2];
+            q8_scores(dot, v, row[j], ks, key0 + tk, a.sc, e.a1, 0.0f);
+            if (!there || (!whole && !q8_sees(row[j], key0 + tk, sp.pre))) v[0] = -CUDART_INF_F;
+            if (!there || (!whole && !q8_sees(row[j], key0 + tk + 8, sp.pre))) v[1] = -CUDART_INF_F;
+            if (h < G) {
+              zo[h * P + tk] = v[0];
+              zo[h * P + tk + 8] = v[1];
+            }
+            pm[j] = max3(pm[j], v[0], v[1]);
           }
         }
 #pragma unroll

@@ -104,26 +104,6 @@ __device__ __forceinline__ void v_dot(uint32_t slab, int t16, int lane, const ui
   }
 }
 
-// What a lane knows of the two rows of an mma column pair. Scores come in
-// units of 1/unit: unit = log2(e) for a softmax in base 2, α − 1 for entmax.
-struct Q8Row {
-  float cs;     // score per unit of the fp32 dot product (times the page's K scale); without the cap's unit
-  float slope;  // times unit
-  int pos, lo;  // position, first key seen
-};
-
-// Score of key j for a row; NaN-free for finite codes.
-__device__ __forceinline__ float q8_score(float dot, const Q8Row& r, float ks, int j, const Q8Score& sc, bool general,
-                                          float unit) {
-  float s = dot * (r.cs * ks);
-  if (general) {
-    if (sc.cap > 0.0f) s = soft_cap(s, sc.cap, sc.inv_cap) * unit;
-    s -= r.slope * (float)abs(r.pos - j);
-  }
-  return s;
-}
-__device__ __forceinline__ bool q8_sees(const Q8Row& r, int j, int pre) { return (j >= r.lo && j <= r.pos) || j < pre; }
-
 // tanh(y) = y·T(y²): T interpolates tanh(√z)/√z at the Chebyshev points of
 // [0, 1/4] (degree 3, relative error below 7e-7 in fp32 for |y| ≤ 1/2) and of
 // [0, 1] (degree 6, below 1.5e-7), both against tanh in 64 bits at 20001 points.
@@ -139,6 +119,59 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+
+// Weights are 2^{t − M + kLift}; M moves when a t passes it by more than kSlack.
+constexpr float kLift = 8.0f, kSlack = 6.0f;
+constexpr int kNoKey = 0x40000000;  // first key of a place without a page: beyond every key
+
+// What a lane knows of the two rows of an mma column pair. Scores come in
+// units of 1/unit: unit = log2(e) for a softmax in base 2, α − 1 for entmax.
+struct Q8Row {
+  float cs;     // of the fp32 dot product (times the page's K scale): the score's, or with a cap score/cap's, units
+  float slope;  // times unit
+  int pos, lo;  // position, first key seen
+};
+__device__ __forceinline__ float q8_row_scale(float q_inv, const Q8Score& sc, float unit) {
+  return q_inv * sc.scale * (sc.cap > 0.0f ? sc.inv_cap : unit);
+}
+
+// Scores of N keys for one row: dot[i] is of key j0 + 8·i; add is added to
+// each. NaN-free for finite codes.
+template <int N>
+__device__ __forceinline__ void q8_scores(const float (&dot)[N], float (&out)[N], const Q8Row& r, float ks, int j0,
+                                          const Q8Score& sc, float unit, float add) {
+  const float k = r.cs * ks;
+  if (sc.cap > 0.0f) {
+    float big = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      out[i] = dot[i] * k;
+      big = fmaxf(big, fabsf(out[i]));
+    }
+    constexpr TanhPoly poly = tanh_poly();
+    const float c = sc.cap * unit;
+    if (__all_sync(0xffffffffu, big <= 0.5f)) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float z = out[i] * out[i];
+        const float t = fmaf(fmaf(fmaf(poly.near[3], z, poly.near[2]), z, poly.near[1]), z, poly.near[0]);
+        out[i] = fmaf(t * out[i], c, add);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) out[i] = fmaf(soft_cap(out[i], 1.0f, 1.0f), c, add);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = fmaf(dot[i], k, add);
+  }
+  if (sc.slopes) {
+    const float d = (float)(r.pos - j0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = fmaf(fabsf(d - 8.0f * i), -r.slope, out[i]);
+  }
+}
+__device__ __forceinline__ bool q8_sees(const Q8Row& r, int j, int pre) { return (j >= r.lo && j <= r.pos) || j < pre; }
 
 // Wait for a phase of an mbarrier for at most a second.
 __device__ __forceinline__ bool mbar_wait_second(uint64_t* bar, uint32_t parity) {
@@ -156,6 +189,93 @@ __device__ __forceinline__ bool mbar_wait_second(uint64_t* bar, uint32_t parity)
 __device__ __forceinline__ float att_inv(float l) { return l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : CUDART_NAN_F); }
 __device__ __forceinline__ float att_lse(float m, float l) {
   return l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : CUDART_NAN_F;
+}
+
+// The line: every slot's tiles one behind the other, cut into one piece a warp
+// of the grid. Warp w of nw begins at W·w/nw; nw ≤ W, so no piece is empty.
+struct LineCut {
+  long long W, nw;
+  __device__ __forceinline__ long long begin(long long w) const { return W * w / nw; }
+  __device__ __forceinline__ long long of(long long at) const { return ((at + 1) * nw - 1) / W; }  // warp that holds `at`
+};
+__device__ __forceinline__ LineCut line_cut(long long W, int blocks, int warps) {
+  return LineCut{W, max(1LL, min(W, (long long)blocks * warps))};
+}
+
+// Where a warp's piece begins: the slot and its place on the line.
+struct LinePlace {
+  LineCut cut;
+  long long begin, end, cum;
+  int slot;
+};
+template <int NW>
+struct LineSmem {
+  long long sum[NW], cum[NW * 32];
+};
+// tiles(b, st) gives slot b's tiles (flagging it on st); put(b, at) is called
+// once a slot, by a thread of block 0, with its place.
+template <int NW, class Tiles, class Put>
+__device__ __forceinline__ LinePlace line_place(int n_seqs, uint32_t* status, LineSmem<NW>& sh, Tiles&& tiles, Put&& put) {
+  constexpr int NTH = NW * 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t* st = blockIdx.x == 0 ? status : nullptr;
+  LinePlace p{};
+  long long total = 0;
+  if (n_seqs > NTH) {  // several rounds: the sum first
+    for (int b = tid; b < n_seqs; b += NTH) total += tiles(b, nullptr);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) sh.sum[warp] = total;
+    __syncthreads();
+    total = 0;
+    for (int i = 0; i < NW; ++i) total += sh.sum[i];
+    __syncthreads();
+  }
+  long long base = 0;
+  for (int b0 = 0; b0 < n_seqs; b0 += NTH) {
+    const int b = b0 + tid;
+    const long long mine = b < n_seqs ? tiles(b, st) : 0;
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) sh.sum[warp] = inc;
+    __syncthreads();
+    long long at = base + inc - mine, all = 0;
+    for (int i = 0; i < NW; ++i) {
+      if (i < warp) at += sh.sum[i];
+      all += sh.sum[i];
+    }
+    sh.cum[tid] = at;
+    if (n_seqs <= NTH) total = all;
+    if (b0 == 0) {
+      p.cut = line_cut(total, (int)gridDim.x, NW);
+      const long long me = (long long)blockIdx.x * NW + warp;
+      if (me < p.cut.nw) {
+        p.begin = p.cut.begin(me);
+        p.end = p.cut.begin(me + 1);
+      }
+    }
+    if (blockIdx.x == 0 && b < n_seqs) put(b, at);
+    __syncthreads();
+    if (p.begin >= base && p.begin < base + all) {  // the last slot that begins at or before the piece
+      int n = 0;
+      for (int i = 0; i < NTH && b0 + i < n_seqs; i += 32)
+        n += __popc(__ballot_sync(0xffffffffu, b0 + i + lane < n_seqs && sh.cum[i + lane] <= p.begin));
+      p.slot = b0 + n - 1;
+      p.cum = sh.cum[n - 1];
+    }
+    base += all;
+    if (b0 + NTH < n_seqs) __syncthreads();
+  }
+  if (blockIdx.x == 0 && tid == 0) put(n_seqs, total);
+  return p;
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
 }  // namespace ekv
