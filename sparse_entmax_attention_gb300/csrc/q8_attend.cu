@@ -34,25 +34,24 @@ constexpr int kAttSlabs = NT == 1 ? 3 : 6;
 constexpr int kAttMaxBlocks = 256;
 constexpr int kAttKeys = 32;
 
-// Row tiles, tiles of keys and span of a slot; W = its tiles on the line.
+// Tiles of keys and span of a slot (its rows are at most 8·NT); W = its tiles
+// on the line.
 struct AttSlot {
   Q8Slot s;
   Q8Span sp;
-  int nrt, T;
+  int T;
   long long W;
 };
-template <int NT>
 __device__ __forceinline__ AttSlot att_slot(const Q8AttendArgs& a, int b, uint32_t* st) {
   AttSlot x;
   x.s = q8_slot(a.c, a.b, b, st);
-  x.nrt = (x.s.count * a.c.G + 8 * NT - 1) / (8 * NT);
   x.W = 0;
   x.T = 0;
   x.sp = Q8Span{0, 0, 0, 0, 0};
   if (x.s.count > 0) {
     x.sp = q8_span(a.c, a.sc, x.s, b, 0, x.s.count);
     x.T = (x.sp.T * a.c.P + kAttKeys - 1) / kAttKeys;
-    x.W = (long long)x.T * a.c.Hkv * x.nrt;
+    x.W = (long long)x.T * a.c.Hkv;
   }
   return x;
 }
@@ -60,7 +59,7 @@ __device__ __forceinline__ AttSlot att_slot(const Q8AttendArgs& a, int b, uint32
 // A warp's last piece: the unit that starts at A on the line, T pages long.
 struct AttPiece {
   long long A;
-  int T, start, kvh, rt, rows;
+  int T, start, kvh, rows;
 };
 
 template <bool I8, int D, int P, int NT>
@@ -76,6 +75,7 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
   __shared__ AttSlot sh_info[NTH];  // the slots, when they are few
   __shared__ AttPiece sh_piece[NW];
   __shared__ float2 sh_ml[NW][R];
+  __shared__ float sh_f[NW][R];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring0 = (smem_u32(dyn_sm) + 1023u) & ~1023u;
   const uint32_t ring = ring0 + (uint32_t)warp * ST * SLAB;
@@ -94,13 +94,13 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
   const LinePlace at = line_place<NW>(
       n_seqs, a.c.status, sh_line,
       [&](int b, uint32_t* st) {
-        const AttSlot x = att_slot<NT>(a, b, st);
+        const AttSlot x = att_slot(a, b, st);
         if (few) sh_info[b] = x;
         return x.W;
       },
       [&](int b, long long where) {
         a.cum[b] = where;
-        if (b < n_seqs) reinterpret_cast<AttSlot*>(a.slots)[b] = few ? sh_info[b] : att_slot<NT>(a, b, nullptr);
+        if (b < n_seqs) reinterpret_cast<AttSlot*>(a.slots)[b] = few ? sh_info[b] : att_slot(a, b, nullptr);
       });
   const LineCut cut = at.cut;
   const long long me = (long long)blockIdx.x * NW + warp;
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
   int filled = 0, used = 0;  // ring fills of this warp, in order
   bool stuck = false;
   while (w < w_end && !stuck) {
-    const AttSlot x = few ? sh_info[slot] : att_slot<NT>(a, slot, nullptr);
+    const AttSlot x = few ? sh_info[slot] : att_slot(a, slot, nullptr);
     if (w >= cum + x.W) {
       cum += x.W;
       ++slot;
@@ -121,10 +121,9 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
     }
     const int T = x.T;
     const long long off = w - cum;
-    const int u = (int)(off / T), t0 = (int)(off - (long long)u * T);
+    const int kvh = (int)div_line(off, T), t0 = (int)(off - (long long)kvh * T);
     const int n = (int)min((long long)(T - t0), w_end - w);
-    const int kvh = u / x.nrt, rt = u - kvh * x.nrt;
-    const int rows = min(R, x.s.count * G - rt * R);
+    const int rows = x.s.count * G;
     // 32 tiles' places and scales at once, a tile a lane
     int ph[PP];
     float ks_l[PP], vs_l[PP];
@@ -167,39 +166,43 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
         ++filled;
       }
     };
-    look_up(0);
-    refill(min(n, 32));  // before the queries are looked at
-    // query fragments and row facts
+    // the queries come in beside the pages' places; the first pages are asked for before they are looked at
+    uint4 qw[NT][D / 32];
     uint32_t bq[NT][D / 16][2];
     Q8Row row[NT][2];
     int pos_min = 0x7fffffff, lo_max = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int rho = rt * R + 8 * nt + r;
-      const bool ok = 8 * nt + r < rows;
-      const __nv_bfloat16* qp =
-          ok ? a.q.p + (long long)(x.s.start + rho / G) * a.q.ts + (long long)(kvh * G + rho % G) * a.q.hs : nullptr;
-      float inv;
-      q_half_frag<D>(qp, lane, bq[nt], inv);
+      const uint32_t rho = 8 * nt + r, tok = rho / (uint32_t)G;
+      q_load<D>((int)rho < rows ? a.q.p + (long long)(x.s.start + (int)tok) * a.q.ts +
+                                      (long long)(kvh * G + (int)(rho - tok * G)) * a.q.hs
+                                : nullptr,
+                lane, qw[nt]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float f = __shfl_sync(0xffffffffu, inv, (2 * c + j) * 4);
-        const int rj = 8 * nt + 2 * c + j, rg = rt * R + rj;
+        const uint32_t rj = 8 * nt + 2 * c + j, i = rj / (uint32_t)G;
         Q8Row& q = row[nt][j];
-        q.cs = q8_row_scale(f, a.sc, kLog2e);
         q.slope = 0.0f;
         q.pos = 0;
         q.lo = 0;
-        if (rj < rows) {
-          const int i = rg / G;
-          q.pos = x.s.L - x.s.count + i;
+        if ((int)rj < rows) {
+          q.pos = x.s.L - x.s.count + (int)i;
           if (a.sc.window > 0) q.lo = max(0, q.pos - a.sc.window + 1);
-          if (a.sc.first_key) q.lo = max(q.lo, a.sc.first_key[x.s.start + i]);
-          if (a.sc.slopes) q.slope = a.sc.slopes[kvh * G + rg % G] * kLog2e;
+          if (a.sc.first_key) q.lo = max(q.lo, a.sc.first_key[x.s.start + (int)i]);
+          if (a.sc.slopes) q.slope = a.sc.slopes[kvh * G + (int)(rj - i * G)] * kLog2e;
           pos_min = min(pos_min, q.pos);
           lo_max = max(lo_max, q.lo);
         }
       }
+    }
+    look_up(0);
+    refill(min(n, 32));
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float inv;
+      q_half_frag<D>(qw[nt], bq[nt], inv);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) row[nt][j].cs = q8_row_scale(__shfl_sync(0xffffffffu, inv, (2 * c + j) * 4), a.sc, kLog2e);
     }
     pos_min = __reduce_min_sync(0xffffffffu, pos_min);
     lo_max = __reduce_max_sync(0xffffffffu, lo_max);
@@ -350,9 +353,8 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
         for (int j = 0; j < 2; ++j) {
           const int rj = 8 * nt + 2 * c + j;
           if (rj >= rows) continue;
-          const int rg = rt * R + rj;
-          const long long tok = x.s.start + rg / G;
-          const int h = kvh * G + rg % G;
+          const int i = (int)((uint32_t)rj / (uint32_t)G), h = kvh * G + rj - i * G;
+          const long long tok = x.s.start + i;
           const float inv = att_inv(l[nt][j]);
           __nv_bfloat16* o = a.out.p + tok * a.out.ts + (long long)h * a.out.hs;
 #pragma unroll
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
             else reinterpret_cast<float2*>(a.part_ml)[(size_t)me * 2 * R + rj] = make_float2(m[nt][j], l[nt][j]);
           }
         }
-      if (last && lane == 0) sh_piece[warp] = AttPiece{w - t0, T, x.s.start, kvh, rt, rows};
+      if (last && lane == 0) sh_piece[warp] = AttPiece{w - t0, T, x.s.start, kvh, rows};
     }
     w += n;
   }
@@ -390,7 +392,34 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
     __syncwarp();
   }
   __syncthreads();
-  // the warps' last pieces: neighbours of one unit are joined here
+  // the warps' last pieces: neighbours of one unit are joined here. First each row's maximum and the pieces' factors
+  // (a lane a piece, its row's other pieces by shuffles)
+  static_assert(NW == 16 ? R == 8 : NW == 8 && R == 16, "NW lanes a row, 32/NW rows a warp");
+  if (tid < NW * R) {
+    const int i = tid % NW, rj = tid / NW;
+    const AttPiece& x = sh_piece[i];
+    const bool in = x.A >= 0 && rj < x.rows;
+    const int unit = in ? (int)x.A : -1;
+    const float2 v = in ? sh_ml[i][rj] : make_float2(-CUDART_INF_F, 0.0f);
+    float M = v.x;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const int u = __shfl_sync(0xffffffffu, unit, k, NW);
+      const float y = __shfl_sync(0xffffffffu, v.x, k, NW);
+      if (u == unit) M = fmaxf(M, y);
+    }
+    const float f = v.x > -CUDART_INF_F ? ex2f(v.x - M) : 0.0f;
+    float l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const int u = __shfl_sync(0xffffffffu, unit, k, NW);
+      const float y = __shfl_sync(0xffffffffu, f * v.y, k, NW);
+      if (u == unit) l += y;
+    }
+    sh_f[i][rj] = f;
+    sh_ml[i][rj] = make_float2(M, l);
+  }
+  __syncthreads();
   for (int i0 = 0, i1; i0 < NW; i0 = i1) {
     i1 = i0 + 1;
     const AttPiece x = sh_piece[i0];
@@ -398,21 +427,16 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
     while (i1 < NW && sh_piece[i1].A == x.A) ++i1;
     const long long first = (long long)blockIdx.x * NW + i0;
     const bool all = cut.begin(first) <= x.A && cut.begin((long long)blockIdx.x * NW + i1) == x.A + x.T;
+    const float* ring_f = reinterpret_cast<const float*>(dyn_sm + (ring0 - smem_u32(dyn_sm)));
     for (int e = tid; e < x.rows * D; e += NTH) {
       const int rj = e / D;
-      float M = -CUDART_INF_F;
-      for (int i = i0; i < i1; ++i) M = fmaxf(M, sh_ml[i][rj].x);
-      float l = 0.0f, o = 0.0f;
-      for (int i = i0; i < i1; ++i) {
-        const float2 ml = sh_ml[i][rj];
-        const float f = ml.x > -CUDART_INF_F ? ex2f(ml.x - M) : 0.0f;
-        l = fmaf(f, ml.y, l);
-        o = fmaf(f, reinterpret_cast<const float*>(dyn_sm + (ring0 - smem_u32(dyn_sm)) + i * ST * SLAB)[e], o);
-      }
+      float o = 0.0f;
+#pragma unroll 4
+      for (int i = i0; i < i1; ++i) o = fmaf(sh_f[i][rj], ring_f[i * (ST * SLAB / 4) + e], o);
+      const float M = sh_ml[i0][rj].x, l = sh_ml[i0][rj].y;
       if (all) {
-        const int rg = x.rt * R + rj;
-        const long long tok = x.start + rg / G;
-        const int h = x.kvh * G + rg % G;
+        const int i = (int)((uint32_t)rj / (uint32_t)G), h = x.kvh * G + rj - i * G;
+        const long long tok = x.start + i;
         a.out.p[tok * a.out.ts + (long long)h * a.out.hs + e % D] = __float2bfloat16_rn(o * att_inv(l));
         if (a.tau && e % D == 0) a.tau[tok * Hkv * G + h] = att_lse(M, l);
       } else {
@@ -427,20 +451,20 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
 // Joins the pieces of units that several blocks hold, and answers rows that see
 // no page at all. A unit's pieces, in the order of the line: one a block from
 // its first warp on (left by the block's first warp of the unit), and where its
-// last warp goes on behind it, that warp's own. Block (KV head · row tile ·
-// row, slot), a thread a dimension.
+// last warp goes on behind it, that warp's own. Block (KV head · row, slot), a
+// thread a dimension.
 template <int D, int NT>
-__global__ void __launch_bounds__(D) attend_join_kernel(Q8AttendArgs a, int nrt_max) {
+__global__ void __launch_bounds__(D) attend_join_kernel(Q8AttendArgs a) {
   pdl_enter();
   constexpr int R = 8 * NT, NW = kAttWarps<NT>;
-  const int b = blockIdx.y, rj = blockIdx.x % R, rt = blockIdx.x / R % nrt_max, kvh = blockIdx.x / R / nrt_max;
+  const int b = blockIdx.y, rj = blockIdx.x % R, kvh = blockIdx.x / R;
   const AttSlot x = reinterpret_cast<const AttSlot*>(a.slots)[b];
   const long long W = a.cum[a.b.n_seqs], at = a.cum[b];
   const int G = a.c.G;
-  if (rt >= x.nrt || rj >= x.s.count * G - rt * R) return;
+  if (rj >= x.s.count * G) return;
   const LineCut cut = line_cut(W, a.blocks, NW);
   const int T = x.T;
-  const long long A = at + ((long long)kvh * x.nrt + rt) * T, B = A + T;
+  const long long A = at + (long long)kvh * T, B = A + T;
   float M = -CUDART_INF_F, l = 0.0f, o = 0.0f;
   if (T > 0) {
     const long long w0 = cut.of(A), w1 = cut.of(B - 1);
@@ -481,9 +505,8 @@ __global__ void __launch_bounds__(D) attend_join_kernel(Q8AttendArgs a, int nrt_
       M = m;
     }
   }
-  const int rg = rt * R + rj;
-  const long long tok = x.s.start + rg / G;
-  const int h = kvh * G + rg % G;
+  const int i = (int)((uint32_t)rj / (uint32_t)G), h = kvh * G + rj - i * G;
+  const long long tok = x.s.start + i;
   a.out.p[tok * a.out.ts + (long long)h * a.out.hs + threadIdx.x] = __float2bfloat16_rn(o * att_inv(l));
   if (a.tau && threadIdx.x == 0) a.tau[tok * a.c.Hkv * G + h] = att_lse(M, l);
 }
@@ -529,9 +552,7 @@ static cudaError_t attend_t(Q8AttendArgs& a, void* ws, int sms, cudaStream_t st)
   a.part_ml = reinterpret_cast<float*>(p);
   e = launch_k(false, attend_kernel<I8, D, P, NT>, dim3(a.blocks), dim3(kAttWarps<NT> * 32), (size_t)smem, st, a, km, vm);
   if (e != cudaSuccess) return e;
-  const int nrt = (int)(((long long)a.b.max_count * a.c.G + 8 * NT - 1) / (8 * NT));
-  return launch_k(true, attend_join_kernel<D, NT>, dim3(nrt * 8 * NT * a.c.Hkv, a.b.n_seqs), dim3(D), 0,
-                  st, a, nrt);
+  return launch_k(true, attend_join_kernel<D, NT>, dim3(8 * NT * a.c.Hkv, a.b.n_seqs), dim3(D), 0, st, a);
 }
 
 template <bool I8, int D, int P>

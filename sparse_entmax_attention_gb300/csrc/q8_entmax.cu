@@ -78,13 +78,14 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
       continue;
     }
     const long long off = w - cum;
-    const int kvh = (int)(off / T), t0 = (int)(off - (long long)kvh * T);
+    const int kvh = (int)div_line(off, T), t0 = (int)(off - (long long)kvh * T);
     const int n = (int)min((long long)(T - t0), w_end - w);
     uint32_t bq[1][D / 16][2];
     Q8Row row[2];
     float inv;
-    q_half_frag<D>(r < G ? a.q.p + (long long)s.start * a.q.ts + (long long)(kvh * G + r) * a.q.hs : nullptr, lane,
-                   bq[0], inv);
+    uint4 qw[D / 32];
+    q_load<D>(r < G ? a.q.p + (long long)s.start * a.q.ts + (long long)(kvh * G + r) * a.q.hs : nullptr, lane, qw);
+    q_half_frag<D>(qw, bq[0], inv);
     const int pos = s.L - 1;
     int lo = a.sc.window > 0 ? max(0, pos - a.sc.window + 1) : 0;
     if (a.sc.first_key) lo = max(lo, a.sc.first_key[s.start]);

@@ -27,16 +27,20 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 // values down to 2^-27 of it are exact as halves; inv is that power's inverse.
 // p = null: a row of zeros.
 template <int D>
-__device__ __forceinline__ void q_half_frag(const __nv_bfloat16* p, int lane, uint32_t (&b)[D / 16][2], float& inv) {
-  const int c = lane & 3;
-  uint2 w[D / 16];
+__device__ __forceinline__ void q_load(const __nv_bfloat16* p, int lane, uint4 (&w)[D / 32]) {
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+    w[i] = p ? *reinterpret_cast<const uint4*>(p + (D / 4) * (lane & 3) + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+}
+template <int D>
+__device__ __forceinline__ void q_half_frag(const uint4 (&w)[D / 32], uint32_t (&b)[D / 16][2], float& inv) {
   uint32_t m = 0u;
 #pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks) {
-    w[ks] = p ? *reinterpret_cast<const uint2*>(p + (D / 4) * c + 4 * ks) : make_uint2(0u, 0u);
-    m = max(m, max((w[ks].x & 0x7fffu), (w[ks].x >> 16) & 0x7fffu));
-    m = max(m, max((w[ks].y & 0x7fffu), (w[ks].y >> 16) & 0x7fffu));
+  for (int i = 0; i < D / 32; ++i) {
+    m = __vmaxu2(__vmaxu2(m, w[i].x & 0x7fff7fffu), w[i].y & 0x7fff7fffu);
+    m = __vmaxu2(__vmaxu2(m, w[i].z & 0x7fff7fffu), w[i].w & 0x7fff7fffu);
   }
+  m = max(m & 0xffffu, m >> 16);
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   int e = (int)(m >> 7) - 127;
@@ -45,11 +49,13 @@ __device__ __forceinline__ void q_half_frag(const __nv_bfloat16* p, int lane, ui
   const float f = __uint_as_float((uint32_t)(13 - e + 127) << 23);
   inv = __uint_as_float((uint32_t)(e - 13 + 127) << 23);
 #pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks) {
-    const __half2 x = __floats2half2_rn(bf_lo(w[ks].x) * f, bf_hi(w[ks].x) * f);
-    const __half2 y = __floats2half2_rn(bf_lo(w[ks].y) * f, bf_hi(w[ks].y) * f);
-    b[ks][0] = *reinterpret_cast<const uint32_t*>(&x);
-    b[ks][1] = *reinterpret_cast<const uint32_t*>(&y);
+  for (int i = 0; i < D / 32; ++i) {
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2 x = __floats2half2_rn(bf_lo(u[j]) * f, bf_hi(u[j]) * f);
+      b[2 * i + (j >> 1)][j & 1] = *reinterpret_cast<const uint32_t*>(&x);
+    }
   }
 }
 
@@ -191,15 +197,26 @@ __device__ __forceinline__ float att_lse(float m, float l) {
   return l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : CUDART_NAN_F;
 }
 
+// n / d for n ≥ 0, d > 0: in 32 bits where both fit (the 64-bit division is a
+// long subroutine, and code that runs once costs its instructions' fetch).
+__device__ __forceinline__ long long div_line(long long n, long long d) {
+  if (((unsigned long long)(n | d) >> 32) == 0) return (long long)((uint32_t)n / (uint32_t)d);
+  return n / d;
+}
+
 // The line: every slot's tiles one behind the other, cut into one piece a warp
-// of the grid. Warp w of nw begins at W·w/nw; nw ≤ W, so no piece is empty.
+// of the grid: warp w of nw begins at ⌊W·w/nw⌋ (so units of equal length that
+// divide the grid begin with a warp); nw ≤ W, so no piece is empty.
 struct LineCut {
-  long long W, nw;
-  __device__ __forceinline__ long long begin(long long w) const { return W * w / nw; }
-  __device__ __forceinline__ long long of(long long at) const { return ((at + 1) * nw - 1) / W; }  // warp that holds `at`
+  long long W, nw, each, more;  // each = ⌊W/nw⌋, more = W mod nw
+  __device__ __forceinline__ long long begin(long long w) const {
+    return w * each + (long long)((uint32_t)more * (uint32_t)w / (uint32_t)nw);  // (both below nw < 2^16)
+  }
+  __device__ __forceinline__ long long of(long long at) const { return div_line((at + 1) * nw - 1, W); }  // holds `at`
 };
 __device__ __forceinline__ LineCut line_cut(long long W, int blocks, int warps) {
-  return LineCut{W, max(1LL, min(W, (long long)blocks * warps))};
+  const long long nw = max(1LL, min(W, (long long)blocks * warps)), each = div_line(W, nw);
+  return LineCut{W, nw, each, W - each * nw};
 }
 
 // Where a warp's piece begins: the slot and its place on the line.
