@@ -446,6 +446,7 @@ def moment_fit_eval(alpha: float, order: int, t):
 # The 8-bit paged cache: plan, append, attend.
 
 _CODES = {torch.int8: I8, torch.float8_e4m3fn: E4M3}
+_I32, _F32, _BF16 = torch.int32, torch.float32, torch.bfloat16
 
 
 def _need(ok, what):
@@ -453,31 +454,31 @@ def _need(ok, what):
         raise EntmaxKVError(what)
 
 
-def _dev_i32(t, shape, device, name):
-    _need(t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape and t.device == device,
-          f"{name}: a contiguous int32 tensor of shape {shape} on {device} is wanted")
+def _i32(t, shape, dev, name):
+    """The pointer of a contiguous int32 tensor of this shape on device number `dev`."""
+    if t.dtype is not _I32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise EntmaxKVError(f"{name}: a contiguous int32 tensor of shape {tuple(shape)} on device {dev} is wanted")
+    return t.data_ptr()
 
 
-def _q8_call(device, stream, fn, *args):
+def _q8_call(dev, stream, fn, *args):
     """fn(*args, stream) on the tensors' device, whichever device is current."""
-    if torch.cuda.current_device() == device.index:
-        s = stream if stream is not None else torch.cuda.current_stream(device)
-        code = fn(*args, s.cuda_stream)
+    if torch._C._cuda_getDevice() == dev:
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            s = stream if stream is not None else torch.cuda.current_stream(device)
-            code = fn(*args, s.cuda_stream)
+        with torch.cuda.device(dev):
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if code:
         _check(code)
 
 
-def _rows(t, shape, device, name):
+def _rows(t, shape, dev, name):
     """entmaxkv_rows of a [tokens, heads, d] bf16 tensor (its first two strides are free)."""
-    _need(t.dtype == torch.bfloat16 and tuple(t.shape) == shape and t.device == device,
-          f"{name}: a bfloat16 tensor of shape {shape} on {device} is wanted")
-    st = t.stride()
-    _need(st[2] == 1 or shape[2] == 1, f"{name}: the head dimension must be contiguous")
-    ts, hs = st[0], st[1]
+    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev:
+        raise EntmaxKVError(f"{name}: a bfloat16 tensor of shape {shape} on device {dev} is wanted")
+    ts, hs, es = t.stride()
+    if es != 1:
+        raise EntmaxKVError(f"{name}: the head dimension must be contiguous")
     if shape[0] == 1:
         ts = max(8, shape[1] * shape[2])
     if shape[1] == 1:
@@ -489,10 +490,10 @@ class PageTable:
     """A block table and lengths alone, for planning pages of caches kept elsewhere."""
 
     def __init__(self, block_table, seq_lens, page_size, num_phys_pages, status=None):
-        self.device = block_table.device
+        self.device, self._dev = block_table.device, block_table.get_device()
         max_seqs, max_pages = block_table.shape
-        _dev_i32(block_table, (max_seqs, max_pages), self.device, "block_table")
-        _dev_i32(seq_lens, (max_seqs,), self.device, "seq_lens")
+        _i32(block_table, (max_seqs, max_pages), self._dev, "block_table")
+        _i32(seq_lens, (max_seqs,), self._dev, "seq_lens")
         self.cfg = Config(1, 1, 64, page_size, max_seqs, max_pages, num_phys_pages, I8)
         self.block_table, self.seq_lens = block_table, seq_lens
         self.status = status if status is not None else torch.zeros(1, dtype=torch.int32, device=self.device)
@@ -507,8 +508,9 @@ class PagePool:
 
     def __init__(self, free_pages, free_count):
         self.free_pages, self.free_count = free_pages, free_count
-        _dev_i32(free_pages, (free_pages.numel(),), free_pages.device, "free_pages")
-        _dev_i32(free_count, (1,), free_pages.device, "free_count")
+        self._dev, self._n = free_pages.get_device(), free_pages.numel()
+        self._pages = _i32(free_pages, (self._n,), self._dev, "free_pages")
+        self._count = _i32(free_count, (1,), self._dev, "free_count")
 
     @classmethod
     def full(cls, num_phys_pages, device="cuda"):
@@ -521,33 +523,35 @@ class Batch:
     of `total`, the last count[b] tokens of sequence seq_ids[b] (b without seq_ids)."""
 
     def __init__(self, start, count, total, max_count, seq_ids=None):
-        n = start.shape[0]
-        _dev_i32(start, (n,), start.device, "start")
-        _dev_i32(count, (n,), start.device, "count")
-        if seq_ids is not None:
-            _dev_i32(seq_ids, (n,), start.device, "seq_ids")
+        self._n, self._dev = start.shape[0], start.get_device()
+        shape = (self._n,)
         self.start, self.count, self.seq_ids = start, count, seq_ids
         self.total, self.max_count, self.device = int(total), int(max_count), start.device
-        self.view = BatchView(None if seq_ids is None else seq_ids.data_ptr(), start.data_ptr(), count.data_ptr(),
-                              n, self.total, self.max_count)
+        self.view = BatchView(None if seq_ids is None else _i32(seq_ids, shape, self._dev, "seq_ids"),
+                              _i32(start, shape, self._dev, "start"), _i32(count, shape, self._dev, "count"),
+                              self._n, self.total, self.max_count)
 
     @classmethod
     def uniform(cls, n_seqs, count=1, seq_ids=None, device="cuda"):
         """count rows of every sequence, one sequence behind the other."""
-        start = torch.arange(0, n_seqs * count, count, dtype=torch.int32, device=device)
+        start = torch.arange(0, n_seqs * count, max(count, 1), dtype=torch.int32, device=device)
         return cls(start, torch.full_like(start, count), n_seqs * count, count, seq_ids)
 
 
-@dataclass
 class PagePlan:
-    """What plan_pages writes: the batch's rows, positions and slots of its tokens."""
-    start: torch.Tensor
-    count: torch.Tensor
-    positions: torch.Tensor
-    slots: torch.Tensor
+    """What plan_pages writes: the batch's rows (start, count [n_seqs]), positions and slots [total]
+    of its tokens (int32, int64)."""
+
+    def __init__(self, start, count, positions, slots):
+        self.start, self.count, self.positions, self.slots = start, count, positions, slots
+        self._n, self._total, self._dev = start.shape[0], positions.shape[0], start.get_device()
+        _need(slots.dtype == torch.int64 and slots.shape == positions.shape and slots.is_contiguous()
+              and slots.get_device() == self._dev, "slots: a contiguous int64 tensor beside positions is wanted")
+        self._ptrs = (_i32(start, (self._n,), self._dev, "start"), _i32(count, (self._n,), self._dev, "count"),
+                      _i32(positions, (self._total,), self._dev, "positions"), slots.data_ptr())
 
     def batch(self, max_count, seq_ids=None) -> Batch:
-        return Batch(self.start, self.count, self.positions.shape[0], max_count, seq_ids)
+        return Batch(self.start, self.count, self._total, max_count, seq_ids)
 
 
 def alloc_plan(n_seqs, total, device="cuda") -> PagePlan:
@@ -564,37 +568,36 @@ def plan_pages(cache, pool: PagePool, n_new, plan: PagePlan, seq_ids=None, advan
     tokens in (into lens_out when given, else in place); a PagedCache, whose append counts them
     itself, is planned with advance=False. The free list's new height goes to count_out, or in place.
     """
-    n, dev = n_new.shape[0], cache.block_table.device
-    _dev_i32(n_new, (n,), dev, "n_new")
-    _need(plan.start.shape[0] == n and plan.start.device == dev, "plan: allocated for another batch")
-    _need(pool.free_pages.numel() >= cache.cfg.num_phys_pages and pool.free_pages.device == dev,
-          "pool: a free list of num_phys_pages entries is wanted")
-    if seq_ids is not None:
-        _dev_i32(seq_ids, (n,), dev, "seq_ids")
-    if lens_out is not None:
-        _dev_i32(lens_out, (cache.cfg.max_seqs,), dev, "lens_out")
-    if count_out is not None:
-        _dev_i32(count_out, (1,), dev, "count_out")
-    lens = None
-    if advance:
-        lens = (cache.seq_lens if lens_out is None else lens_out).data_ptr()
-    _q8_call(dev, stream, lib().entmaxkv_plan_pages, cache.cfg, cache.block_table.data_ptr(),
-             cache.seq_lens.data_ptr(), cache.status.data_ptr(), None if seq_ids is None else seq_ids.data_ptr(),
-             n_new.data_ptr(), n, plan.positions.shape[0], pool.free_pages.data_ptr(), pool.free_count.data_ptr(),
-             (pool.free_count if count_out is None else count_out).data_ptr(), lens, plan.start.data_ptr(),
-             plan.count.data_ptr(), plan.positions.data_ptr(), plan.slots.data_ptr())
+    n, dev, cfg = plan._n, plan._dev, cache.cfg
+    table, lens = cache.block_table, cache.seq_lens
+    if table.get_device() != dev or pool._dev != dev:
+        raise EntmaxKVError("cache, pool and plan: on one device are wanted")
+    if pool._n < cfg.num_phys_pages:
+        raise EntmaxKVError("pool: a free list of num_phys_pages entries is wanted")
+    start, count, positions, slots = plan._ptrs
+    lens_p = lens.data_ptr()
+    if not advance:
+        to = None
+    elif lens_out is None:
+        to = lens_p
+    else:
+        to = _i32(lens_out, lens.shape, dev, "lens_out")
+    _q8_call(dev, stream, lib().entmaxkv_plan_pages, cfg, table.data_ptr(), lens_p, cache.status.data_ptr(),
+             None if seq_ids is None else _i32(seq_ids, (n,), dev, "seq_ids"), _i32(n_new, (n,), dev, "n_new"), n,
+             plan._total, pool._pages, pool._count,
+             pool._count if count_out is None else _i32(count_out, (1,), dev, "count_out"), to, start, count,
+             positions, slots)
     return plan
 
 
 def release_pages(cache, pool: PagePool, seq_ids, stream=None):
     """entmaxkv_release_pages: the sequences' pages go back to the pool, their lengths become 0."""
-    dev = cache.block_table.device
-    _dev_i32(seq_ids, (seq_ids.shape[0],), dev, "seq_ids")
-    _need(pool.free_pages.numel() >= cache.cfg.num_phys_pages and pool.free_pages.device == dev,
-          "pool: a free list of num_phys_pages entries is wanted")
+    dev, n = pool._dev, seq_ids.shape[0]
+    _need(cache.block_table.get_device() == dev, "cache and pool: on one device are wanted")
+    _need(pool._n >= cache.cfg.num_phys_pages, "pool: a free list of num_phys_pages entries is wanted")
     _q8_call(dev, stream, lib().entmaxkv_release_pages, cache.cfg, cache.block_table.data_ptr(),
-             cache.seq_lens.data_ptr(), cache.status.data_ptr(), seq_ids.data_ptr(), seq_ids.shape[0],
-             pool.free_pages.data_ptr(), pool.free_count.data_ptr())
+             cache.seq_lens.data_ptr(), cache.status.data_ptr(), _i32(seq_ids, (n,), dev, "seq_ids"), n,
+             pool._pages, pool._count)
 
 
 class QuantCache:
@@ -612,65 +615,67 @@ class QuantCache:
 
     @classmethod
     def of(cls, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, group, status=None):
-        """The cache over tensors the caller already has."""
+        """The cache over tensors the caller already has (scales of pages in use are positive)."""
         c = cls.__new__(cls)
         c._init(k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, group, status)
         return c
 
     def _init(self, k_pool, v_pool, k_scale, v_scale, block_table, seq_lens, group, status):
-        dev, shape = k_pool.device, tuple(k_pool.shape)
+        dev, shape = k_pool.get_device(), k_pool.shape
         _need(k_pool.dtype in _CODES, "k_pool: int8 or float8_e4m3fn codes are wanted")
-        _need(v_pool.dtype == k_pool.dtype and tuple(v_pool.shape) == shape and len(shape) == 4
-              and v_pool.device == dev and k_pool.is_contiguous() and v_pool.is_contiguous(),
+        _need(v_pool.dtype == k_pool.dtype and v_pool.shape == shape and len(shape) == 4
+              and v_pool.get_device() == dev and k_pool.is_contiguous() and v_pool.is_contiguous(),
               "k_pool, v_pool: contiguous [pages, KV heads, page size, head dim] of one type are wanted")
         for t in (k_scale, v_scale):
-            _need(t.dtype == torch.float32 and tuple(t.shape) == shape[:2] and t.is_contiguous() and t.device == dev,
+            _need(t.dtype is _F32 and t.shape == shape[:2] and t.is_contiguous() and t.get_device() == dev,
                   "k_scale, v_scale: contiguous float32 [pages, KV heads] are wanted")
         max_seqs, max_pages = block_table.shape
-        _dev_i32(block_table, (max_seqs, max_pages), dev, "block_table")
-        _dev_i32(seq_lens, (max_seqs,), dev, "seq_lens")
-        self.device, self.code_dtype = dev, k_pool.dtype
+        _i32(block_table, (max_seqs, max_pages), dev, "block_table")
+        _i32(seq_lens, (max_seqs,), dev, "seq_lens")
+        self.device, self._dev, self.code_dtype = k_pool.device, dev, k_pool.dtype
         self.k_pool, self.v_pool, self.k_scale, self.v_scale = k_pool, v_pool, k_scale, v_scale
         self.block_table, self.seq_lens = block_table, seq_lens
-        self.status = status if status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
+        self.status = status if status is not None else torch.zeros(1, dtype=torch.int32, device=self.device)
         self.cfg = Config(shape[1], group, shape[3], shape[2], max_seqs, max_pages, shape[0], _CODES[k_pool.dtype])
+        self.num_q_heads = shape[1] * group
         self.view = Q8CacheView(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                 block_table.data_ptr(), seq_lens.data_ptr(), self.status.data_ptr())
-
-    @property
-    def num_q_heads(self):
-        return self.cfg.num_kv_heads * self.cfg.group
 
     def device_status(self) -> int:
         return int(self.status.item()) & 0xffffffff
 
 
+def _on_cache(cache, batch):
+    if batch._dev != cache._dev:
+        raise EntmaxKVError("batch: on another device than the cache")
+    return cache._dev
+
+
 def append_q8(cache: QuantCache, k, v, batch: Batch, stream=None):
     """entmaxkv_append_q8: k, v [total, Hkv, d] bf16 (any token and head strides that are multiples
     of 8): the last count[b] tokens of each sequence become codes."""
-    shape = (batch.total, cache.cfg.num_kv_heads, cache.cfg.head_dim)
-    _need(batch.device == cache.device, "batch: on another device than the cache")
-    kr, vr = _rows(k, shape, cache.device, "k"), _rows(v, shape, cache.device, "v")
-    _q8_call(cache.device, stream, lib().entmaxkv_append_q8, cache.cfg, cache.view, batch.view, kr, vr)
+    dev, shape = _on_cache(cache, batch), (batch.total, cache.cfg.num_kv_heads, cache.cfg.head_dim)
+    _q8_call(dev, stream, lib().entmaxkv_append_q8, cache.cfg, cache.view, batch.view, _rows(k, shape, dev, "k"),
+             _rows(v, shape, dev, "v"))
 
 
 def read_q8(cache: QuantCache, first, batch: Batch, k=None, v=None, stream=None):
     """entmaxkv_read_q8: tokens first[b] .. first[b] + count[b] - 1 of each sequence as bf16 rows
     [total, Hkv, d] in k and v (allocated when not given). Returns (k, v)."""
-    shape = (batch.total, cache.cfg.num_kv_heads, cache.cfg.head_dim)
-    _need(batch.device == cache.device, "batch: on another device than the cache")
-    _dev_i32(first, (batch.view.n_seqs,), cache.device, "first")
+    dev, shape = _on_cache(cache, batch), (batch.total, cache.cfg.num_kv_heads, cache.cfg.head_dim)
     k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
     v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
-    kr, vr = _rows(k, shape, cache.device, "k"), _rows(v, shape, cache.device, "v")
-    _q8_call(cache.device, stream, lib().entmaxkv_read_q8, cache.cfg, cache.view, batch.view, first.data_ptr(), kr, vr)
+    _q8_call(dev, stream, lib().entmaxkv_read_q8, cache.cfg, cache.view, batch.view,
+             _i32(first, (batch._n,), dev, "first"), _rows(k, shape, dev, "k"), _rows(v, shape, dev, "v"))
     return k, v
 
 
-@dataclass
 class AttendOutputs:
-    out: torch.Tensor  # [total, Hq, d] bf16
-    tau: torch.Tensor  # [total, Hq] float32: log-sum-exp (softmax) or the entmax threshold
+    """out [total, Hq, d] bf16 and tau [total, Hq] float32 (log-sum-exp of a softmax, the entmax
+    threshold), or tau None."""
+
+    def __init__(self, out, tau):
+        self.out, self.tau = out, tau
 
 
 def alloc_attend_outputs(cache: QuantCache, batch: Batch) -> AttendOutputs:
@@ -701,33 +706,28 @@ def attend_q8(cache: QuantCache, q, batch: Batch, alpha=1.0, scale=0.0, softcap=
     taken off. window: keys seen back from the row's own. prefix: int32 [n_seqs], keys in front
     that every row sees. first_key: int32 [total], where each row's document begins.
     """
-    c, dev = cache.cfg, cache.device
-    Hq = c.num_kv_heads * c.group
-    shape = (batch.total, Hq, c.head_dim)
-    _need(batch.device == dev, "batch: on another device than the cache")
+    dev, Hq = _on_cache(cache, batch), cache.num_q_heads
+    shape = (batch.total, Hq, cache.cfg.head_dim)
     if outputs is None:
         outputs = alloc_attend_outputs(cache, batch)
     if workspace is None:
         workspace = alloc_attend_workspace(cache, batch, alpha)
-    _need(workspace.device == dev, "workspace: on another device than the cache")
+    elif workspace.get_device() != dev:
+        raise EntmaxKVError("workspace: on another device than the cache")
     score = ScoreView(scale, softcap, window, None, None, None)
     if slopes is not None:
-        _need(slopes.dtype == torch.float32 and tuple(slopes.shape) == (Hq,) and slopes.is_contiguous()
-              and slopes.device == dev, "slopes: contiguous float32 [Hq] is wanted")
+        if slopes.dtype is not _F32 or slopes.shape != (Hq,) or not slopes.is_contiguous() or slopes.get_device() != dev:
+            raise EntmaxKVError("slopes: contiguous float32 [Hq] is wanted")
         score.slopes = slopes.data_ptr()
     if prefix is not None:
-        _dev_i32(prefix, (batch.view.n_seqs,), dev, "prefix")
-        score.prefix = prefix.data_ptr()
+        score.prefix = _i32(prefix, (batch._n,), dev, "prefix")
     if first_key is not None:
-        _dev_i32(first_key, (batch.total,), dev, "first_key")
-        score.first_key = first_key.data_ptr()
+        score.first_key = _i32(first_key, (batch.total,), dev, "first_key")
     t = outputs.tau
-    if t is not None:
-        _need(t.dtype == torch.float32 and tuple(t.shape) == shape[:2] and t.is_contiguous() and t.device == dev,
-              "tau: contiguous float32 [total, Hq] is wanted")
-    _q8_call(dev, stream, lib().entmaxkv_attend_q8, cache.cfg, cache.view, batch.view,
-             _rows(q, shape, dev, "q"), score, float(alpha), workspace.data_ptr(),
-             workspace.numel() * workspace.element_size(), _rows(outputs.out, shape, dev, "out"),
+    if t is not None and (t.dtype is not _F32 or t.shape != shape[:2] or not t.is_contiguous() or t.get_device() != dev):
+        raise EntmaxKVError("tau: contiguous float32 [total, Hq] is wanted")
+    _q8_call(dev, stream, lib().entmaxkv_attend_q8, cache.cfg, cache.view, batch.view, _rows(q, shape, dev, "q"),
+             score, alpha, workspace.data_ptr(), workspace.nbytes, _rows(outputs.out, shape, dev, "out"),
              None if t is None else t.data_ptr())
     return outputs
 
