@@ -70,15 +70,20 @@ __device__ __forceinline__ void scan2(long long& a, long long& b, long long (*sh
   __syncthreads();
 }
 
-// One block takes the slots 1024 at a time: a thread per slot for the sums,
-// then all threads over the round's new pages and tokens, each finding its
-// slot by bisection in the round's sums.
+// Every block of a cluster takes the slots 1024 at a time, a thread per slot
+// for the sums (all blocks the same), then its share of the round's new pages
+// and tokens, each thread finding its slot by bisection in the round's sums.
+// Lengths and the list's height are written last, by the first block, once the
+// whole cluster has read the old ones (they may be the same arrays).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
   pdl_enter();
   __shared__ long long sh[32][2];
   __shared__ int t_end[kPlanThreads], n_end[kPlanThreads];  // running sums of the round, inclusive, from its base
   __shared__ int seq_sh[kPlanThreads], len_sh[kPlanThreads], take_sh[kPlanThreads];
   const int tid = threadIdx.x, P = a.P;
+  const int all = gridDim.x * kPlanThreads, me = blockIdx.x * kPlanThreads + tid;  // the grid is one cluster
+  const bool head = blockIdx.x == 0;
+  uint32_t* status = head ? a.status : nullptr;
   const int fc = min(max(*a.free_count, 0), a.nphys);
   long long t_base = 0, n_base = 0;  // rows and needs of the earlier rounds
   long long used = 0;                // pages handed out
@@ -90,16 +95,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     if (i < a.n_seqs) {
       n = a.n_new[i];
       if (n < 0) {
-        raise_flag(a.status, ENTMAXKV_DEV_BAD_BATCH);
+        raise_flag(status, ENTMAXKV_DEV_BAD_BATCH);
         n = 0;
         bad = true;
       }
       if (n > 0) {
-        seq = seq_row(a.seq_ids, i, a.max_seqs, a.status);
+        seq = seq_row(a.seq_ids, i, a.max_seqs, status);
         if (seq >= 0) {
           L = a.seq_lens[seq];
           if (L < 0 || (long long)L + n > (long long)a.maxp * P) {
-            raise_flag(a.status, ENTMAXKV_DEV_CAPACITY);
+            raise_flag(status, ENTMAXKV_DEV_CAPACITY);
             bad = true;
           } else {
             need = ((long long)L + n + P - 1) / P - (L + P - 1) / P;
@@ -113,14 +118,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     scan2(ts, ns, sh, tt, nt);
     bool ok = !bad;
     if (ok && n > 0 && n_base + ns + need > fc) {
-      raise_flag(a.status, ENTMAXKV_DEV_CAPACITY);
+      raise_flag(status, ENTMAXKV_DEV_CAPACITY);
       ok = false;
     }
     if (ok && t_base + ts + n > a.total) {
-      raise_flag(a.status, ENTMAXKV_DEV_BAD_BATCH);
+      raise_flag(status, ENTMAXKV_DEV_BAD_BATCH);
       ok = false;
     }
-    if (i < a.n_seqs) {
+    if (head && i < a.n_seqs) {
       a.start[i] = (int)min(t_base + ts, 0x7fffffffLL);
       a.count[i] = ok ? n : 0;
     }
@@ -133,7 +138,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     __syncthreads();
     // pages: those of the round that the list still holds
     const long long n_fit = max(0LL, min(nt, (long long)fc - n_base));
-    for (int j = tid; j < n_fit; j += kPlanThreads) {
+    for (int j = me; j < n_fit; j += all) {
       int lo = 0, hi = kPlanThreads - 1;
       while (lo < hi) {
         const int m = (lo + hi) >> 1;
@@ -147,7 +152,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     // tokens
     const int t_fit = (int)max(0LL, min(tt, t_left));
     if (a.positions || a.slots)
-      for (int j = tid; j < t_fit; j += kPlanThreads) {
+      for (int j = me; j < t_fit; j += all) {
         int lo = 0, hi = kPlanThreads - 1;
         while (lo < hi) {
           const int m = (lo + hi) >> 1;
@@ -177,7 +182,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
     n_base += nt;
     __syncthreads();
   }
-  // every read of the old lengths and of the list's height is done
+  // every read of the old lengths and of the list's height is done, in all blocks
+  if (gridDim.x > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  }
+  if (!head) return;
   if (a.lens_out)
     for (int i = tid; i < a.n_seqs; i += kPlanThreads) {
       const int n = a.count[i];
@@ -227,7 +237,21 @@ cudaError_t launch_plan(const entmaxkv_config& cfg, int32_t* block_table, const 
   PlanArgs a{cfg.page_size, cfg.max_pages_per_seq, cfg.num_phys_pages, cfg.max_seqs, n_seqs, total, block_table,
              seq_lens, status, seq_ids, n_new, free_pages, free_count, free_count_out, lens_out, start, count,
              positions, slots};
-  return launch_k(false, plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, a);
+  // four tokens a thread, up to the eight blocks of a portable cluster (a queue of 333 prompts, 38000 tokens: 39 us
+  // with one block)
+  const int blocks = total > 4 * kPlanThreads ? 8 : total > kPlanThreads ? 2 : 1;
+  cudaLaunchConfig_t cfg_l = {};
+  cfg_l.gridDim = dim3(blocks);
+  cfg_l.blockDim = dim3(kPlanThreads);
+  cfg_l.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = blocks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg_l.attrs = attr;
+  cfg_l.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg_l, plan_kernel, a);
 }
 
 cudaError_t launch_release(const entmaxkv_config& cfg, const int32_t* block_table, int32_t* seq_lens, uint32_t* status,

@@ -178,10 +178,10 @@ cudaError_t launch_plan(const entmaxkv_config& cfg, int32_t* block_table, const 
 cudaError_t launch_release(const entmaxkv_config& cfg, const int32_t* block_table, int32_t* seq_lens, uint32_t* status,
                            const int32_t* seq_ids, int n_seqs, int32_t* free_pages, int32_t* free_count,
                            cudaStream_t st);
-cudaError_t launch_append_q8(const Q8Cache& c, const Q8Batch& b, const Q8Rows& k, const Q8Rows& v, bool i8,
+cudaError_t launch_append_q8(const Q8Cache& c, const Q8Batch& b, const Q8Rows& k, const Q8Rows& v, bool i8, int sms,
                              cudaStream_t st);
 cudaError_t launch_read_q8(const Q8Cache& c, const Q8Batch& b, const int32_t* first, const Q8Rows& k, const Q8Rows& v,
-                           bool i8, cudaStream_t st);
+                           bool i8, int sms, cudaStream_t st);
 size_t attend_softmax_bytes(const entmaxkv_config& cfg, int n_seqs, int max_count);
 cudaError_t launch_attend_softmax(Q8AttendArgs a, bool i8, void* ws, int sms, cudaStream_t st);
 // Rows of a sequence up to which the streaming kernel answers a batch; with

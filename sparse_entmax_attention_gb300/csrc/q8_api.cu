@@ -102,8 +102,10 @@ int32_t entmaxkv_append_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* 
   if ((st = check_q8_config(cfg)) || (st = check_q8_cache(cache)) || (st = check_batch(batch))) return st;
   if (idle(batch)) return ENTMAXKV_OK;
   if ((st = check_rows(k, false)) || (st = check_rows(v, false))) return st;
+  const int sms = device_sms();
+  if (sms < 1) return ENTMAXKV_ERR_CUDA;
   return code_of(launch_append_q8(cache_of(cfg, cache), batch_of(batch), rows_of(k), rows_of(v),
-                                  cfg->kv_dtype == ENTMAXKV_I8, (cudaStream_t)stream));
+                                  cfg->kv_dtype == ENTMAXKV_I8, sms, (cudaStream_t)stream));
 }
 
 int32_t entmaxkv_read_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache, const entmaxkv_batch* batch,
@@ -113,8 +115,10 @@ int32_t entmaxkv_read_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* ca
   if (idle(batch)) return ENTMAXKV_OK;
   if (!first) return ENTMAXKV_ERR_INVALID_ARG;
   if ((st = check_rows(k, true)) || (st = check_rows(v, true))) return st;
+  const int sms = device_sms();
+  if (sms < 1) return ENTMAXKV_ERR_CUDA;
   return code_of(launch_read_q8(cache_of(cfg, cache), batch_of(batch), first, rows_of(k), rows_of(v),
-                                cfg->kv_dtype == ENTMAXKV_I8, (cudaStream_t)stream));
+                                cfg->kv_dtype == ENTMAXKV_I8, sms, (cudaStream_t)stream));
 }
 
 static int check_attend(const entmaxkv_config* cfg, int n_seqs, int total, int max_count, float alpha) {
