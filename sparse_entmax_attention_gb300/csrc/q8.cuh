@@ -190,7 +190,8 @@ constexpr int kStreamRows = 16;
 size_t attend_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total);
 cudaError_t launch_attend_chunk(const Q8AttendArgs& a, bool i8, void* ws, int sms, cudaStream_t st);
 size_t attend_entmax_bytes(const entmaxkv_config& cfg, int n_seqs);
-cudaError_t launch_attend_entmax(Q8AttendArgs a, bool i8, float alpha, void* ws, int sms, cudaStream_t st);
+cudaError_t launch_attend_entmax(const entmaxkv_config& cfg, Q8AttendArgs a, bool i8, float alpha, void* ws, int sms,
+                                 cudaStream_t st);
 // A pool as (dim, KV head · token, page) of bytes, in boxes of one slab.
 cudaError_t make_q8_map(CUtensorMap* map, const void* pool, int nphys, int Hkv, int P, int D);
 

@@ -169,7 +169,7 @@ int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* 
   a.tau = tau;
   const bool i8 = cfg->kv_dtype == ENTMAXKV_I8;
   const cudaStream_t s = (cudaStream_t)stream;
-  if (alpha > 1.0f) return code_of(launch_attend_entmax(a, i8, alpha, workspace, sms, s));
+  if (alpha > 1.0f) return code_of(launch_attend_entmax(*cfg, a, i8, alpha, workspace, sms, s));
   return code_of(streams(cfg, batch->max_count) ? launch_attend_softmax(a, i8, workspace, sms, s)
                                                 : launch_attend_chunk(a, i8, workspace, sms, s));
 }
