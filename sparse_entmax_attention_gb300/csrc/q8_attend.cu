@@ -34,24 +34,26 @@ constexpr int kAttSlabs = NT == 1 ? 3 : 6;
 constexpr int kAttMaxBlocks = 256;
 constexpr int kAttKeys = 32;
 
-// Tiles of keys and span of a slot (its rows are at most 8·NT); W = its tiles
-// on the line.
+// Row tiles (8·NT rows each), tiles of keys and span of a slot; W = its tiles on
+// the line, the row tiles of a KV head one behind the other.
 struct AttSlot {
   Q8Slot s;
   Q8Span sp;
-  int T;
+  int nrt, T;
   long long W;
 };
+template <int NT>
 __device__ __forceinline__ AttSlot att_slot(const Q8AttendArgs& a, int b, uint32_t* st) {
   AttSlot x;
   x.s = q8_slot(a.c, a.b, b, st);
+  x.nrt = (int)((uint32_t)(x.s.count * a.c.G + 8 * NT - 1) / (uint32_t)(8 * NT));
   x.W = 0;
   x.T = 0;
   x.sp = Q8Span{0, 0, 0, 0, 0};
   if (x.s.count > 0) {
     x.sp = q8_span(a.c, a.sc, x.s, b, 0, x.s.count);
     x.T = (x.sp.T * a.c.P + kAttKeys - 1) / kAttKeys;
-    x.W = (long long)x.T * a.c.Hkv;
+    x.W = (long long)x.T * a.c.Hkv * x.nrt;
   }
   return x;
 }
@@ -59,7 +61,7 @@ __device__ __forceinline__ AttSlot att_slot(const Q8AttendArgs& a, int b, uint32
 // A warp's last piece: the unit that starts at A on the line, T pages long.
 struct AttPiece {
   long long A;
-  int T, start, kvh, rows;
+  int T, start, kvh, row0, rows;
 };
 
 template <bool I8, int D, int P, int NT>
@@ -72,7 +74,8 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
   extern __shared__ __align__(128) unsigned char dyn_sm[];
   __shared__ uint64_t bars[NW][ST];
   __shared__ LineSmem<NW> sh_line;
-  __shared__ AttSlot sh_info[NTH];  // the slots, when they are few
+  constexpr int kFew = 256;
+  __shared__ AttSlot sh_info[kFew];  // the slots, when they are few
   __shared__ AttPiece sh_piece[NW];
   __shared__ float2 sh_ml[NW][R];
   __shared__ float sh_f[NW][R];
@@ -90,17 +93,17 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
     prefetch_map(&vmap);
   }
   const int n_seqs = a.b.n_seqs;
-  const bool few = n_seqs <= NTH;
+  const bool few = n_seqs <= kFew;
   const LinePlace at = line_place<NW>(
       n_seqs, a.c.status, sh_line,
       [&](int b, uint32_t* st) {
-        const AttSlot x = att_slot(a, b, st);
+        const AttSlot x = att_slot<NT>(a, b, st);
         if (few) sh_info[b] = x;
         return x.W;
       },
       [&](int b, long long where) {
         a.cum[b] = where;
-        if (b < n_seqs) reinterpret_cast<AttSlot*>(a.slots)[b] = few ? sh_info[b] : att_slot(a, b, nullptr);
+        if (b < n_seqs) reinterpret_cast<AttSlot*>(a.slots)[b] = few ? sh_info[b] : att_slot<NT>(a, b, nullptr);
       });
   const LineCut cut = at.cut;
   const long long me = (long long)blockIdx.x * NW + warp;
@@ -113,7 +116,7 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
   int filled = 0, used = 0;  // ring fills of this warp, in order
   bool stuck = false;
   while (w < w_end && !stuck) {
-    const AttSlot x = few ? sh_info[slot] : att_slot(a, slot, nullptr);
+    const AttSlot x = few ? sh_info[slot] : att_slot<NT>(a, slot, nullptr);
     if (w >= cum + x.W) {
       cum += x.W;
       ++slot;
@@ -121,9 +124,10 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
     }
     const int T = x.T;
     const long long off = w - cum;
-    const int kvh = (int)div_line(off, T), t0 = (int)(off - (long long)kvh * T);
+    const int unit = (int)div_line(off, T), t0 = (int)(off - (long long)unit * T);
     const int n = (int)min((long long)(T - t0), w_end - w);
-    const int rows = x.s.count * G;
+    const int kvh = (int)((uint32_t)unit / (uint32_t)x.nrt), row0 = (unit - kvh * x.nrt) * R;
+    const int rows = min(R, x.s.count * G - row0);
     // 32 tiles' places and scales at once, a tile a lane
     int ph[PP];
     float ks_l[PP], vs_l[PP];
@@ -173,19 +177,19 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
     int pos_min = 0x7fffffff, lo_max = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const uint32_t rho = 8 * nt + r, tok = rho / (uint32_t)G;
-      q_load<D>((int)rho < rows ? a.q.p + (long long)(x.s.start + (int)tok) * a.q.ts +
+      const uint32_t rho = row0 + 8 * nt + r, tok = rho / (uint32_t)G;
+      q_load<D>(8 * nt + r < rows ? a.q.p + (long long)(x.s.start + (int)tok) * a.q.ts +
                                       (long long)(kvh * G + (int)(rho - tok * G)) * a.q.hs
                                 : nullptr,
                 lane, qw[nt]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint32_t rj = 8 * nt + 2 * c + j, i = rj / (uint32_t)G;
+        const uint32_t rj = row0 + 8 * nt + 2 * c + j, i = rj / (uint32_t)G;
         Q8Row& q = row[nt][j];
         q.slope = 0.0f;
         q.pos = 0;
         q.lo = 0;
-        if ((int)rj < rows) {
+        if (8 * nt + 2 * c + j < rows) {
           q.pos = x.s.L - x.s.count + (int)i;
           if (a.sc.window > 0) q.lo = max(0, q.pos - a.sc.window + 1);
           if (a.sc.first_key) q.lo = max(q.lo, a.sc.first_key[x.s.start + (int)i]);
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
         for (int j = 0; j < 2; ++j) {
           const int rj = 8 * nt + 2 * c + j;
           if (rj >= rows) continue;
-          const int i = (int)((uint32_t)rj / (uint32_t)G), h = kvh * G + rj - i * G;
+          const int i = (int)((uint32_t)(row0 + rj) / (uint32_t)G), h = kvh * G + row0 + rj - i * G;
           const long long tok = x.s.start + i;
           const float inv = att_inv(l[nt][j]);
           __nv_bfloat16* o = a.out.p + tok * a.out.ts + (long long)h * a.out.hs;
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
             else reinterpret_cast<float2*>(a.part_ml)[(size_t)me * 2 * R + rj] = make_float2(m[nt][j], l[nt][j]);
           }
         }
-      if (last && lane == 0) sh_piece[warp] = AttPiece{w - t0, T, x.s.start, kvh, rows};
+      if (last && lane == 0) sh_piece[warp] = AttPiece{w - t0, T, x.s.start, kvh, row0, rows};
     }
     w += n;
   }
@@ -435,7 +439,7 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
       for (int i = i0; i < i1; ++i) o = fmaf(sh_f[i][rj], ring_f[i * (ST * SLAB / 4) + e], o);
       const float M = sh_ml[i0][rj].x, l = sh_ml[i0][rj].y;
       if (all) {
-        const int i = (int)((uint32_t)rj / (uint32_t)G), h = x.kvh * G + rj - i * G;
+        const int i = (int)((uint32_t)(x.row0 + rj) / (uint32_t)G), h = x.kvh * G + x.row0 + rj - i * G;
         const long long tok = x.start + i;
         a.out.p[tok * a.out.ts + (long long)h * a.out.hs + e % D] = __float2bfloat16_rn(o * att_inv(l));
         if (a.tau && e % D == 0) a.tau[tok * Hkv * G + h] = att_lse(M, l);
@@ -451,20 +455,20 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
 // Joins the pieces of units that several blocks hold, and answers rows that see
 // no page at all. A unit's pieces, in the order of the line: one a block from
 // its first warp on (left by the block's first warp of the unit), and where its
-// last warp goes on behind it, that warp's own. Block (KV head · row, slot), a
-// thread a dimension.
+// last warp goes on behind it, that warp's own. Block (KV head · row tile · row,
+// slot), a thread a dimension.
 template <int D, int NT>
-__global__ void __launch_bounds__(D) attend_join_kernel(Q8AttendArgs a) {
+__global__ void __launch_bounds__(D) attend_join_kernel(Q8AttendArgs a, int nrt_max) {
   pdl_enter();
   constexpr int R = 8 * NT, NW = kAttWarps<NT>;
-  const int b = blockIdx.y, rj = blockIdx.x % R, kvh = blockIdx.x / R;
+  const int b = blockIdx.y, rj = blockIdx.x % R, unit = blockIdx.x / R, kvh = unit / nrt_max, rt = unit - kvh * nrt_max;
   const AttSlot x = reinterpret_cast<const AttSlot*>(a.slots)[b];
   const long long W = a.cum[a.b.n_seqs], at = a.cum[b];
   const int G = a.c.G;
-  if (rj >= x.s.count * G) return;
+  if (rt >= x.nrt || rt * R + rj >= x.s.count * G) return;
   const LineCut cut = line_cut(W, a.blocks, NW);
   const int T = x.T;
-  const long long A = at + (long long)kvh * T, B = A + T;
+  const long long A = at + ((long long)kvh * x.nrt + rt) * T, B = A + T;
   float M = -CUDART_INF_F, l = 0.0f, o = 0.0f;
   if (T > 0) {
     const long long w0 = cut.of(A), w1 = cut.of(B - 1);
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(D) attend_join_kernel(Q8AttendArgs a) {
       M = m;
     }
   }
-  const int i = (int)((uint32_t)rj / (uint32_t)G), h = kvh * G + rj - i * G;
+  const int i = (int)((uint32_t)(rt * R + rj) / (uint32_t)G), h = kvh * G + rt * R + rj - i * G;
   const long long tok = x.s.start + i;
   a.out.p[tok * a.out.ts + (long long)h * a.out.hs + threadIdx.x] = __float2bfloat16_rn(o * att_inv(l));
   if (a.tau && threadIdx.x == 0) a.tau[tok * a.c.Hkv * G + h] = att_lse(M, l);
@@ -552,7 +556,8 @@ static cudaError_t attend_t(Q8AttendArgs& a, void* ws, int sms, cudaStream_t st)
   a.part_ml = reinterpret_cast<float*>(p);
   e = launch_k(false, attend_kernel<I8, D, P, NT>, dim3(a.blocks), dim3(kAttWarps<NT> * 32), (size_t)smem, st, a, km, vm);
   if (e != cudaSuccess) return e;
-  return launch_k(true, attend_join_kernel<D, NT>, dim3(8 * NT * a.c.Hkv, a.b.n_seqs), dim3(D), 0, st, a);
+  const int nrt = (int)(((long long)a.b.max_count * a.c.G + 8 * NT - 1) / (8 * NT));
+  return launch_k(true, attend_join_kernel<D, NT>, dim3(8 * NT * nrt * a.c.Hkv, a.b.n_seqs), dim3(D), 0, st, a, nrt);
 }
 
 template <bool I8, int D, int P>

@@ -84,40 +84,55 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1)
     const int n = (int)min((long long)(T - t0), w_end - w);
     uint4 qw[D / 32];
     q_load<D>(r < G ? a.q.p + (long long)s.start * a.q.ts + (long long)(kvh * G + r) * a.q.hs : nullptr, lane, qw);
-    // 32 tiles' places and scales at once, a tile a lane
-    int ph[PP];
+    const int pos = s.L - 1;
+    int lo = a.sc.window > 0 ? max(0, pos - a.sc.window + 1) : 0;
+    if (a.sc.first_key) lo = max(lo, a.sc.first_key[s.start]);
+    // 32 tiles' places and scales at once, a tile a lane; bits of those with a page, and of those seen whole
+    int ph[PP], key_l[PP];
     float ks_l[PP];
+    uint32_t some_bits = 0u, whole_bits = 0u;
     auto look_up = [&](int p0) {
+      bool some = false, whole = true;
 #pragma unroll
       for (int q = 0; q < PP; ++q) {
         const int t = (t0 + p0 + lane) * PP + q;
         ph[q] = -1;
         ks_l[q] = 0.0f;
+        key_l[q] = kNoKey;
         if (p0 + lane < n && t < sp.T) {
-          ph[q] = phys_page(a.c.block_table, s.seq, sp.page(t), a.c.maxp, a.c.nphys, a.c.status);
-          if (ph[q] >= 0) ks_l[q] = a.c.k_scale[(size_t)ph[q] * Hkv + kvh];
+          const int page = sp.page(t);
+          ph[q] = phys_page(a.c.block_table, s.seq, page, a.c.maxp, a.c.nphys, a.c.status);
+          if (ph[q] >= 0) {
+            ks_l[q] = a.c.k_scale[(size_t)ph[q] * Hkv + kvh];
+            key_l[q] = page * P;
+            some = true;
+          }
         }
+        whole &= (key_l[q] + P - 1 <= pos && key_l[q] >= lo) || key_l[q] + P <= sp.pre;
       }
+      some_bits = __ballot_sync(0xffffffffu, some);
+      whole_bits = __ballot_sync(0xffffffffu, whole);
     };
     int ask = 0;
     auto refill = [&](int end) {
       while (ask < end && filled - used < ST) {
-        int f[PP], there = 0;
+        if (some_bits >> (ask & 31) & 1u) {
+          int f[PP], there = 0;
 #pragma unroll
-        for (int q = 0; q < PP; ++q) {
-          f[q] = __shfl_sync(0xffffffffu, ph[q], ask & 31);
-          there += f[q] >= 0;
+          for (int q = 0; q < PP; ++q) {
+            f[q] = __shfl_sync(0xffffffffu, ph[q], ask & 31);
+            there += f[q] >= 0;
+          }
+          const int sg = filled % ST;
+          if (lane == 0) {
+            mbar_expect_tx(&bars[warp][sg], (uint32_t)(there * P * D));
+#pragma unroll
+            for (int q = 0; q < PP; ++q)
+              if (f[q] >= 0) tma_load_3d(ring_p + sg * SLAB + q * P * D, &kmap, 0, kvh * P, f[q], &bars[warp][sg]);
+          }
+          ++filled;
         }
         ++ask;
-        if (!there) continue;
-        const int sg = filled % ST;
-        if (lane == 0) {
-          mbar_expect_tx(&bars[warp][sg], (uint32_t)(there * P * D));
-#pragma unroll
-          for (int q = 0; q < PP; ++q)
-            if (f[q] >= 0) tma_load_3d(ring_p + sg * SLAB + q * P * D, &kmap, 0, kvh * P, f[q], &bars[warp][sg]);
-        }
-        ++filled;
       }
     };
     look_up(0);
@@ -126,9 +141,9 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1)
     Q8Row row[2];
     float inv;
     q_half_frag<D>(qw, bq[0], inv);
-    const int pos = s.L - 1;
-    int lo = a.sc.window > 0 ? max(0, pos - a.sc.window + 1) : 0;
-    if (a.sc.first_key) lo = max(lo, a.sc.first_key[s.start]);
+    const bool mine[2] = {2 * c < G, 2 * c + 1 < G};
+    float* zo = e.z + ((size_t)w * G + 2 * c) * kEntKeys + r;  // this lane's scores of the tile
+    float* po = e.pmax + (size_t)w * G + 2 * c;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       row[j].cs = q8_row_scale(__shfl_sync(0xffffffffu, inv, (2 * c + j) * 4), a.sc, e.a1);
@@ -141,53 +156,46 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1)
         look_up(i);
         refill(min(n, i + 32));
       }
-      int key0[PP];
-      float ks[PP];
-      bool some = false, whole = true;
-#pragma unroll
-      for (int q = 0; q < PP; ++q) {
-        const int f = __shfl_sync(0xffffffffu, ph[q], i & 31);
-        ks[q] = __shfl_sync(0xffffffffu, ks_l[q], i & 31);
-        key0[q] = f >= 0 ? sp.page((t0 + i) * PP + q) * P : kNoKey;
-        some |= f >= 0;
-        whole &= (key0[q] + P - 1 <= pos && key0[q] >= lo) || key0[q] + P <= sp.pre;
-      }
+      const bool some = some_bits >> (i & 31) & 1u, whole = whole_bits >> (i & 31) & 1u;
       if (some && !__all_sync(0xffffffffu, mbar_wait_bounded(&bars[warp][used % ST], (used / ST) & 1))) {
         stuck = true;
         break;
       }
       const uint32_t slab = ring + (used % ST) * SLAB;
-      const size_t tile = (size_t)(w + i);
-      float* zo = e.z + tile * G * kEntKeys;
       float pm[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
+        constexpr int kHalf = 16;
+        const int q = kHalf * mt / P;
+        const float ks = __shfl_sync(0xffffffffu, ks_l[q], i & 31);
+        const int j0 = __shfl_sync(0xffffffffu, key_l[q], i & 31) + (kHalf * mt) % P + r;
         float acc[1][4] = {{0.f, 0.f, 0.f, 0.f}};
-        if (some) k_dot<I8, D, 1>(slab, 16 * mt, lane, bq, acc);
-        const int q = 16 * mt / P, j0 = key0[q] + (16 * mt) % P + r, tk = 16 * mt + r;
+        if (some) k_dot<I8, D, 1>(slab, kHalf * mt, lane, bq, acc);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float dot[2] = {acc[0][j], acc[0][2 + j]};
           float v[2];
-          q8_scores(dot, v, row[j], ks[q], j0, a.sc, e.a1, 0.0f);
+          q8_scores(dot, v, row[j], ks, j0, a.sc, e.a1, 0.0f);
           if (!whole) {
             if (!q8_sees(row[j], j0, sp.pre)) v[0] = -CUDART_INF_F;
             if (!q8_sees(row[j], j0 + 8, sp.pre)) v[1] = -CUDART_INF_F;
           }
-          if (2 * c + j < G) {
-            zo[(2 * c + j) * kEntKeys + tk] = v[0];
-            zo[(2 * c + j) * kEntKeys + tk + 8] = v[1];
+          if (mine[j]) {
+            zo[j * kEntKeys + kHalf * mt] = v[0];
+            zo[j * kEntKeys + kHalf * mt + 8] = v[1];
           }
           pm[j] = max3(pm[j], v[0], v[1]);
         }
       }
+      zo += G * kEntKeys;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         pm[j] = fmaxf(pm[j], __shfl_xor_sync(0xffffffffu, pm[j], 4));
         pm[j] = fmaxf(pm[j], __shfl_xor_sync(0xffffffffu, pm[j], 8));
         pm[j] = fmaxf(pm[j], __shfl_xor_sync(0xffffffffu, pm[j], 16));
-        if (r == 0 && 2 * c + j < G) e.pmax[tile * G + 2 * c + j] = pm[j];
+        if (r == 0 && mine[j]) po[j] = pm[j];
       }
+      po += G;
       if (some) {
         __syncwarp();
         ++used;
