@@ -8,10 +8,11 @@
 // 2. finish: a cluster of eight blocks per (slot, KV head), each with an eighth
 //    of the tiles. No token at or below z_max − 1 can carry weight (τ ≥ z_max − 1,
 //    where the sum is at least 1), so only tiles whose largest z clears that are
-//    looked at again: their scores stay in shared memory, and Newton steps from
-//    z_max − 1, which stay below the root of the convex, falling sum, take one
-//    exchange of partial sums and one cluster barrier each. After each step the
-//    closed-form root on the support so far is taken once it lies within it.
+//    looked at again: their scores go to every block of the cluster, and each
+//    solves alone with Newton steps from z_max − 1, which stay below the root of
+//    the convex, falling sum; after each step the closed-form root on the support
+//    so far is taken once it lies within it. (Where there are too many scores to
+//    hand round, a step's partial sums are instead, with a cluster barrier each.)
 //    Then V is read for tiles with some z above its head's τ only, weights
 //    rounded to halves against their tile's largest, and the blocks' sums are
 //    added through the cluster. Every sum has a fixed order.
@@ -24,13 +25,22 @@ constexpr int kScoreSlabs = 2;
 constexpr int kEntWarps = 16;
 constexpr int kEntKeys = 32;
 constexpr int kEntCluster = 8;  // blocks of a cluster, at most
-constexpr int kEntHeld = 32;  // tiles whose scores a warp holds while it solves
+constexpr int kEntSent = 64;  // scores a warp hands round the cluster, at most
+constexpr int kEntList = kEntWarps * 32;  // tiles listed at once
 
 struct EntArgs {
   Q8AttendArgs a;
   float a1, beta;
   float* z;     // [tile of the line][G][32]
   float* pmax;  // [tile of the line][G]
+  struct EntUnit* slots;  // [n_seqs]
+};
+// What the scoring kernel leaves of a slot for the finishing one.
+struct __align__(16) EntUnit {
+  Q8Slot s;
+  Q8Span sp;
+  int T, pad[2];
+  long long cum;
 };
 
 __device__ __forceinline__ Q8Span ent_span(const Q8AttendArgs& a, const Q8Slot& s, int b) {
@@ -62,7 +72,16 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1)
         const Q8Slot s = q8_slot(a.c, a.b, b, st);
         return s.count > 0 ? (long long)ent_tiles(ent_span(a, s, b), P) * Hkv : 0LL;
       },
-      [&](int b, long long where) { a.cum[b] = where; });
+      [&](int b, long long where) {
+        if (b >= a.b.n_seqs) return;
+        EntUnit u;
+        u.s = q8_slot(a.c, a.b, b, nullptr);
+        u.sp = u.s.count > 0 ? ent_span(a, u.s, b) : Q8Span{0, 0, 0, 0, 0};
+        u.T = ent_tiles(u.sp, P);
+        u.pad[0] = u.pad[1] = 0;
+        u.cum = where;
+        e.slots[b] = u;
+      });
   const long long w_end = at.end;
   if (at.begin >= w_end) return;
   const int r = lane >> 2, c = lane & 3;
@@ -233,10 +252,86 @@ __device__ __forceinline__ float peer_load(uint32_t addr) {
   return v;
 }
 
+// x^b at an order without a short form, out of line: the code around it runs
+// once a call, and its instructions come from far.
+__device__ __noinline__ float ent_pow(float x, float b) { return powf(x, b); }
+__device__ __forceinline__ float ent_weight(float y, float beta) {  // [y]_+^β
+  y = fmaxf(y, 0.0f);
+  if (beta == 2.0f) return y * y;
+  if (beta == 1.0f) return y;
+  return y > 0.0f ? ent_pow(y, beta) : 0.0f;
+}
+
 // What one step of the solve learns of the scores y = z − τ > 0: their number,
 // Σy and Σy² (Σy^{β−1} and Σy^β for other orders), and the least of them.
 struct EntSums {
   float k, s1, s2, mn;
+  __device__ __forceinline__ void add(float y, float beta, bool low) {
+    if (y > 0.0f) {
+      k += 1.0f;
+      mn = fminf(mn, y);
+      s1 += low ? y : ent_pow(y, beta - 1.0f);
+      s2 += low ? y * y : ent_pow(y, beta);
+    }
+  }
+  __device__ __forceinline__ void warp_total() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      k += __shfl_xor_sync(0xffffffffu, k, o);
+      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+      s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    }
+  }
+};
+
+// The threshold of one head: τ as an offset from the largest score (exact to a
+// float's resolution of the offset, which is at most 1), moved by the sums of a
+// step. Newton runs on the norm Σy^β to the 1/β, convex and falling like the
+// sum and nearly straight far from the root, so its steps stay below the root.
+struct EntSolve {
+  float t, lo, hi;  // τ − z_max; other orders: the bracket
+  bool done, fine;
+  __device__ __forceinline__ void step(const EntSums& v, float beta) {
+    const float tol = 1e-7f;
+    if (beta == 2.0f || beta == 1.0f) {
+      float d, st;
+      if (beta == 2.0f) {  // Σ(y − δ)² = 1 with δ ≤ min y, written without cancellation
+        const float disc = v.s1 * v.s1 - v.k * (v.s2 - 1.0f);
+        d = disc >= 0.0f ? __fdividef(v.s2 - 1.0f, v.s1 + sqrtf(disc)) : CUDART_INF_F;
+        st = __fdividef(v.s2 - sqrtf(v.s2), v.s1);
+      } else {
+        d = st = __fdividef(v.s1 - 1.0f, v.k);
+      }
+      if (!(v.k > 0.0f)) {
+        done = true;
+        fine = false;
+      } else if (d >= -tol && d <= v.mn * (1.0f + 1e-6f) + tol) {
+        t += d;
+        done = true;
+      } else if (!(st > tol)) {
+        t += fmaxf(st, 0.0f);
+        done = true;
+      } else {
+        t += st;
+      }
+    } else {  // any order: Newton inside a bracket kept by the sign of the sum − 1
+      if (v.k == 0.0f || v.s2 < 1.0f) hi = t;
+      else lo = t;
+      float nt = 0.5f * (lo + hi);
+      if (v.k > 0.0f) {
+        const float st = (v.s2 - 1.0f) / (beta * v.s1);
+        if (fabsf(st) <= tol) {
+          nt = t + st;
+          done = true;
+        } else if (t + st > lo && t + st < hi) {
+          nt = t + st;
+        }
+      }
+      t = nt;
+      if (hi - lo <= tol) done = true;
+    }
+  }
 };
 
 template <bool I8, int D, int P>
@@ -245,11 +340,13 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
   pdl_enter();
   constexpr int NW = kEntWarps, SLAB = kEntKeys * D, PP = kEntKeys / P, NTH = NW * 32;
   extern __shared__ __align__(128) unsigned char dyn_sm[];
-  __shared__ uint64_t bars[NW];
+  __shared__ uint64_t bars[NW][2];
   __shared__ float4 sums[2][kEntCluster][NW];  // every warp of the cluster's partial sums, two steps in turn
+  __shared__ int counts[kEntCluster][NW];      // scores a warp has handed round; over kEntSent: too many
   __shared__ float top_sh[kEntCluster][8];
   __shared__ float wtop[NW][8];
   __shared__ float2 tau_sh[8];
+  __shared__ int found[NW + 1];
   __shared__ __align__(16) float part[8 * D];
   const Q8AttendArgs& a = e.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -258,15 +355,17 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
   const uint32_t base = (smem_u32(dyn_sm) + 1023u) & ~1023u;
   unsigned char* base_p = dyn_sm + (base - smem_u32(dyn_sm));
   if (lane == 0) {
-    mbar_init(&bars[warp], 1);
+    mbar_init(&bars[warp][0], 1);
+    mbar_init(&bars[warp][1], 1);
     mbar_fence_init();
   }
   if (tid == 0) prefetch_map(&vmap);
-  const Q8Slot s = q8_slot(a.c, a.b, b, nullptr);
+  const EntUnit unit = e.slots[b];
+  const Q8Slot s = unit.s;
   if (s.count == 0) return;  // (the whole cluster)
-  const Q8Span sp = ent_span(a, s, b);
-  const int T = ent_tiles(sp, P);
-  const size_t tile0 = (size_t)(a.cum[b] + (long long)kvh * T);
+  const Q8Span sp = unit.sp;
+  const int T = unit.T;
+  const size_t tile0 = (size_t)(unit.cum + (long long)kvh * T);
   const int lo = (int)((long long)T * rank / C), hi = (int)((long long)T * (rank + 1) / C);
   const float* pmax = e.pmax + tile0 * G;
 
@@ -285,28 +384,31 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
       if (lane == 0) wtop[warp][h] = m[h];
     }
     __syncthreads();
-    if (tid < 8) {
+    if (tid < 8 * C) {
+      const int h = tid & 7;
       float v = -CUDART_INF_F;
-      for (int i = 0; i < NW; ++i) v = fmaxf(v, wtop[i][tid]);
-      for (int i = 0; i < C; ++i)
-        asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(peer(smem_u32(&top_sh[rank][tid]), i)), "f"(v) : "memory");
+#pragma unroll
+      for (int i = 0; i < NW; ++i) v = fmaxf(v, wtop[i][h]);
+      asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(peer(smem_u32(&top_sh[rank][h]), tid >> 3)), "f"(v)
+                   : "memory");
     }
     cluster_sync();
   }
-  // the block's warps share out the heads, a head's warps its eighth of the tiles
+  // The block's warps share out the heads, a head's warps its part of the tiles. Scores above z_max − 1 go to every
+  // block of the cluster, kEntSent a warp at most, so that each can solve alone.
   const int wph = NW / G, hd = warp / wph, wi = warp % wph;
   const bool works = hd < G;
   float top = -CUDART_INF_F;
   if (works)
     for (int i = 0; i < C; ++i) top = fmaxf(top, top_sh[i][hd]);
+  const bool none = !(top > -CUDART_INF_F);
   const float T0 = top - 1.0f;
   const int wlo = lo + (int)((long long)(hi - lo) * wi / wph), whi = lo + (int)((long long)(hi - lo) * (wi + 1) / wph);
-  float* held = reinterpret_cast<float*>(base_p) + warp * kEntHeld * 32;  // [tile][32] scores
-  const float* zh = e.z + (tile0 * G + (works ? hd : 0)) * kEntKeys;      // tile t's scores at zh + t·G·32
-  int n_held = 0;
-  bool walk = false;  // too many tiles to hold: go through them all each time
-  if (works && top > -CUDART_INF_F) {
-    for (int t1 = wlo; t1 < whi && !walk; t1 += 128) {
+  float* sent = reinterpret_cast<float*>(base_p);                     // [cluster][warps][kEntSent] scores above T0
+  const float* zh = e.z + (tile0 * G + (works ? hd : 0)) * kEntKeys;  // tile t's scores at zh + t·G·32
+  int n_sent = 0;
+  if (works && !none) {
+    for (int t1 = wlo; t1 < whi && n_sent <= kEntSent; t1 += 128) {
       float m[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -314,186 +416,180 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         uint32_t in = __ballot_sync(0xffffffffu, m[k] > T0);
-        if (n_held + __popc(in) > kEntHeld) {
-          walk = true;
-          break;
-        }
-        while (in) {  // four tiles' scores in flight
-          int u[4];
+        while (in && n_sent <= kEntSent) {  // four tiles' scores in flight
           float z[4];
           const int n4 = min(4, __popc(in));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            u[i] = t1 + 32 * k + __ffs(in) - 1;
-            z[i] = i < n4 ? zh[(size_t)u[i] * G * kEntKeys + lane] : 0.0f;
+            z[i] = i < n4 ? zh[(size_t)(t1 + 32 * k + __ffs(in) - 1) * G * kEntKeys + lane] : -CUDART_INF_F;
             in &= in - 1u;
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < n4) held[(n_held + i) * 32 + lane] = z[i];
-          n_held += n4;
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t up = __ballot_sync(0xffffffffu, z[i] > T0);
+            const int at = n_sent + __popc(up & ((1u << lane) - 1u));
+            if (z[i] > T0 && at < kEntSent)
+              for (int k2 = 0; k2 < C; ++k2)
+                asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(
+                                 peer(smem_u32(&sent[(rank * NW + warp) * kEntSent + at]), k2)),
+                             "f"(z[i] - top)
+                             : "memory");
+            n_sent += __popc(up);
+          }
         }
       }
     }
   }
-  const bool b2 = e.beta == 2.0f, b1 = e.beta == 1.0f;
-  double tau = (double)T0, blo = (double)T0, bhi = (double)top;
-  bool done = !works || !(top > -CUDART_INF_F), fine = true;
-  for (int it = 0; it < 100; ++it) {
-    const float th = (float)tau, tl = (float)(tau - (double)th);
-    EntSums v{0.0f, 0.0f, 0.0f, CUDART_INF_F};
-    auto add = [&](float z) {
-      const float y = (z - th) - tl;
-      if (y > 0.0f) {
-        v.k += 1.0f;
-        v.mn = fminf(v.mn, y);
-        if (b2 || b1) {
-          v.s1 += y;
-          v.s2 = fmaf(y, y, v.s2);
-        } else {
-          v.s1 += powf(y, e.beta - 1.0f);
-          v.s2 += powf(y, e.beta);
+  if (lane < C)
+    asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(peer(smem_u32(&counts[rank][warp]), lane)), "r"(n_sent)
+                 : "memory");
+  cluster_sync();
+  bool many = false;  // some warp had more: the sums of a step are exchanged instead
+  for (int i = lane; i < C * NW; i += 32) many |= counts[i / NW][i % NW] > kEntSent;
+  many = __any_sync(0xffffffffu, many);
+  const bool low = e.beta == 2.0f || e.beta == 1.0f;
+  EntSolve sv{-1.0f, -1.0f, 0.0f, !works || none, true};
+  if (!many) {
+    if (wi == 0) {  // a head's first warp, a lane or more a segment
+      for (int it = 0; it < 100 && !sv.done; ++it) {
+        EntSums v{0.0f, 0.0f, 0.0f, CUDART_INF_F};
+        for (int i = lane; i < C * wph; i += 32) {
+          const int g = (i / wph) * NW + hd * wph + i % wph;
+          const int n = counts[g / NW][g % NW];
+          for (int k = 0; k < n; ++k) v.add(sent[g * kEntSent + k] - sv.t, e.beta, low);
         }
+        v.warp_total();
+        sv.step(v, e.beta);
       }
-    };
-    if (!done) {
-      if (walk) {
+    }
+  } else {
+    for (int it = 0; it < 100; ++it) {
+      EntSums v{0.0f, 0.0f, 0.0f, CUDART_INF_F};
+      if (!sv.done) {
         for (int t1 = wlo; t1 < whi; t1 += 32) {
-          uint32_t in = __ballot_sync(0xffffffffu, t1 + lane < whi && pmax[(size_t)(t1 + lane) * G + hd] > th);
+          uint32_t in = __ballot_sync(0xffffffffu, t1 + lane < whi && pmax[(size_t)(t1 + lane) * G + hd] - top > sv.t);
           while (in) {
-            const int u = t1 + __ffs(in) - 1;
+            const float z = zh[(size_t)(t1 + __ffs(in) - 1) * G * kEntKeys + lane];
             in &= in - 1u;
-            add(zh[(size_t)u * G * kEntKeys + lane]);
+            v.add((z - top) - sv.t, e.beta, low);
           }
         }
-      } else {
-        for (int i = 0; i < n_held; ++i) add(held[i * 32 + lane]);
+        v.warp_total();
       }
-      v.k = warp_sum(v.k);
-      v.s1 = warp_sum(v.s1);
-      v.s2 = warp_sum(v.s2);
-      v.mn = warp_min_f(v.mn);
-    }
-    if (lane < C)
-      peer_store4(peer(smem_u32(&sums[it & 1][rank][warp]), lane), make_float4(done ? -1.0f : v.k, v.s1, v.s2, v.mn));
-    cluster_sync();
-    // every head done? (its first warp in the first block says so)
-    const bool hd_done = lane >= G || sums[it & 1][0][lane * wph].x < 0.0f;
-    if (__all_sync(0xffffffffu, hd_done)) break;
-    if (done) continue;
-    v = EntSums{0.0f, 0.0f, 0.0f, CUDART_INF_F};
-    for (int i = lane; i < C * wph; i += 32) {
-      const float4 p = sums[it & 1][i / wph][hd * wph + i % wph];
-      v.k += p.x;
-      v.s1 += p.y;
-      v.s2 += p.z;
-      v.mn = fminf(v.mn, p.w);
-    }
-    v.k = warp_sum(v.k);
-    v.s1 = warp_sum(v.s1);
-    v.s2 = warp_sum(v.s2);
-    v.mn = warp_min_f(v.mn);
-    const float tol = 1e-7f * fmaxf(1.0f, fabsf((float)tau));
-    if (b2 || b1) {
-      float d, step;
-      if (b2) {  // Σ(y − δ)² = 1 with δ ≤ min y, written without cancellation
-        const float disc = v.s1 * v.s1 - v.k * (v.s2 - 1.0f);
-        d = disc >= 0.0f ? (v.s2 - 1.0f) / (v.s1 + sqrtf(disc)) : CUDART_INF_F;
-        // Newton on the norm √Σy² = 1, convex and falling too, and nearly straight far from the root
-        step = (v.s2 - sqrtf(v.s2)) / v.s1;
-      } else {
-        d = step = (v.s1 - 1.0f) / v.k;
+      if (lane < C)
+        peer_store4(peer(smem_u32(&sums[it & 1][rank][warp]), lane),
+                    make_float4(sv.done ? -1.0f : v.k, v.s1, v.s2, v.mn));
+      cluster_sync();
+      // every head done? (its first warp in the first block says so)
+      const bool hd_done = lane >= G || sums[it & 1][0][lane * wph].x < 0.0f;
+      if (__all_sync(0xffffffffu, hd_done)) break;
+      if (sv.done) continue;
+      v = EntSums{0.0f, 0.0f, 0.0f, CUDART_INF_F};
+      for (int i = lane; i < C * wph; i += 32) {
+        const float4 p = sums[it & 1][i / wph][hd * wph + i % wph];
+        v.k += p.x;
+        v.s1 += p.y;
+        v.s2 += p.z;
+        v.mn = fminf(v.mn, p.w);
       }
-      if (!(v.k > 0.0f)) {
-        done = true;
-        fine = false;
-      } else if (d >= -1e-7f && d <= v.mn * (1.0f + 1e-6f) + 1e-7f) {
-        tau += (double)d;
-        done = true;
-      } else if (!(step > tol)) {
-        if (step > 0.0f) tau += (double)step;
-        done = true;
-      } else {
-        tau += (double)step;
-      }
-    } else {  // any order: Newton inside a bracket kept by the sign of the sum − 1
-      if (v.k == 0.0f || v.s2 < 1.0f) bhi = tau;
-      else blo = tau;
-      double nt = 0.5 * (blo + bhi);
-      if (v.k > 0.0f) {
-        const float step = (v.s2 - 1.0f) / (e.beta * v.s1);
-        if (fabsf(step) <= tol) {
-          nt = tau + (double)step;
-          done = true;
-        } else if (tau + (double)step > blo && tau + (double)step < bhi) {
-          nt = tau + (double)step;
-        }
-      }
-      tau = nt;
-      if (bhi - blo <= (double)tol) done = true;
+      v.warp_total();
+      sv.step(v, e.beta);
     }
   }
   if (works && wi == 0 && lane == 0) {
-    const bool none = !(top > -CUDART_INF_F);
-    const float th = (float)tau;
-    tau_sh[hd] = none ? make_float2(CUDART_NAN_F, 0.0f) : make_float2(th, (float)(tau - (double)th));
+    tau_sh[hd] = none ? make_float2(CUDART_NAN_F, 0.0f) : make_float2(top, sv.t);
     if (rank == 0) {
-      if (!(done && fine)) raise_flag(a.c.status, ENTMAXKV_DEV_TAU_NOCONV);
-      if (a.tau) a.tau[(size_t)s.start * Hkv * G + kvh * G + hd] = none ? CUDART_NAN_F : th;
+      if (!(sv.done && sv.fine)) raise_flag(a.c.status, ENTMAXKV_DEV_TAU_NOCONV);
+      if (a.tau) a.tau[(size_t)s.start * Hkv * G + kvh * G + hd] = none ? CUDART_NAN_F : top + sv.t;
     }
   }
-  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // the copies below write where scores were held
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // the copies below write where scores were kept
   __syncthreads();
 
-  // weights and V: tiles with some score above its head's τ, a warp a tile
+  // Weights and V. The block's tiles with some score above its head's τ are listed in order, and its warps take them
+  // in turns, the next one's V on its way.
+  int* list = reinterpret_cast<int*>(base_p + 2 * NW * SLAB);  // [kEntList] tiles
   const int r = lane >> 2, c = lane & 3;
-  const uint32_t slab = base + warp * SLAB;
-  unsigned char* slab_p = base_p + warp * SLAB;
   const float2 tau_r = r < G ? tau_sh[r] : make_float2(CUDART_INF_F, 0.0f);
   float acc[D / 16][1][4];
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt) acc[mt][0][0] = acc[mt][0][1] = acc[mt][0][2] = acc[mt][0][3] = 0.0f;
-  uint32_t phase = 0u;
+  int used = 0;
   bool stuck = false;
-  const int vlo = lo + (int)((long long)(hi - lo) * warp / NW), vhi = lo + (int)((long long)(hi - lo) * (warp + 1) / NW);
-  for (int t1 = vlo; t1 < vhi && !stuck; t1 += 32) {
+  for (int l0 = lo; l0 < hi; l0 += kEntList) {
+    const int t = l0 + tid;
     bool in = false;
-    if (t1 + lane < vhi)
-      for (int h = 0; h < G; ++h) in |= (pmax[(size_t)(t1 + lane) * G + h] - tau_sh[h].x) - tau_sh[h].y > 0.0f;
-    uint32_t bits = __ballot_sync(0xffffffffu, in);
-    // the places of the tiles found, a tile a lane
-    int ph[PP];
+    if (t < hi && t < l0 + kEntList)
+      for (int h = 0; h < G; ++h) in |= (pmax[(size_t)t * G + h] - tau_sh[h].x) - tau_sh[h].y > 0.0f;
+    const uint32_t bits = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) found[warp] = __popc(bits);
+    __syncthreads();
+    int at = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      if (i < warp) at += found[i];
+      all += found[i];
+    }
+    if (in) list[at + __popc(bits & ((1u << lane) - 1u))] = t;
+    __syncthreads();
+    // this warp's tiles: list[warp], list[warp + NW], ...; their places, a tile a lane
+    const int mine = all > warp ? (all - warp + NW - 1) / NW : 0;
+    int ph[PP], tl = -1;
     float vs_l[PP];
 #pragma unroll
     for (int q = 0; q < PP; ++q) {
-      const int t = (t1 + lane) * PP + q;
-      ph[q] = in && t < sp.T ? phys_page(a.c.block_table, s.seq, sp.page(t), a.c.maxp, a.c.nphys, nullptr) : -1;
-      vs_l[q] = ph[q] >= 0 ? a.c.v_scale[(size_t)ph[q] * Hkv + kvh] : 0.0f;
+      ph[q] = -1;
+      vs_l[q] = 0.0f;
     }
-    while (bits) {
-      const int i = __ffs(bits) - 1, t = t1 + i;
-      bits &= bits - 1u;
+    if (lane < mine) {
+      tl = list[warp + lane * NW];
+#pragma unroll
+      for (int q = 0; q < PP; ++q) {
+        const int p = tl * PP + q;
+        if (p < sp.T) ph[q] = phys_page(a.c.block_table, s.seq, sp.page(p), a.c.maxp, a.c.nphys, nullptr);
+        if (ph[q] >= 0) vs_l[q] = a.c.v_scale[(size_t)ph[q] * Hkv + kvh];
+      }
+    }
+    auto ask = [&](int i) {
       int f[PP], there = 0;
+#pragma unroll
+      for (int q = 0; q < PP; ++q) {
+        f[q] = __shfl_sync(0xffffffffu, ph[q], i);
+        there += f[q] >= 0;
+      }
+      if (lane == 0) {  // (a tile without a page completes at once)
+        uint64_t* bar = &bars[warp][(used + i) & 1];
+        mbar_expect_tx(bar, (uint32_t)(there * P * D));
+#pragma unroll
+        for (int q = 0; q < PP; ++q)
+          if (f[q] >= 0)
+            tma_load_3d(base_p + (warp * 2 + ((used + i) & 1)) * SLAB + q * P * D, &vmap, 0, kvh * P, f[q], bar);
+      }
+    };
+    if (mine > 0) ask(0);
+    for (int i = 0; i < mine; ++i) {
+      if (i + 1 < mine) ask(i + 1);
+      const int tt = __shfl_sync(0xffffffffu, tl, i);
+      int f[PP];
       float vs[PP];
 #pragma unroll
       for (int q = 0; q < PP; ++q) {
         f[q] = __shfl_sync(0xffffffffu, ph[q], i);
         vs[q] = __shfl_sync(0xffffffffu, vs_l[q], i);
-        there += f[q] >= 0;
-      }
-      if (!there) continue;
-      if (lane == 0) {
-        mbar_expect_tx(&bars[warp], (uint32_t)(there * P * D));
-#pragma unroll
-        for (int q = 0; q < PP; ++q)
-          if (f[q] >= 0) tma_load_3d(slab_p + q * P * D, &vmap, 0, kvh * P, f[q], &bars[warp]);
       }
       // row r's weights of this tile against a power of two above its largest; the V scales of a tile's two pages
       // differ: each goes into its own keys' weights, over the larger of them
-      const float ym = r < G ? (pmax[(size_t)t * G + r] - tau_r.x) - tau_r.y : -1.0f;
+      const float ym = r < G ? (pmax[(size_t)tt * G + r] - tau_r.x) - tau_r.y : -1.0f;
+      float2 z[2][2];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          z[kt][j] = r < G ? *reinterpret_cast<const float2*>(e.z + ((tile0 + tt) * G + r) * kEntKeys + 16 * kt + 8 * j + 2 * c)
+                           : make_float2(-CUDART_INF_F, -CUDART_INF_F);
       const float vmax = PP == 1 ? vs[0] : fmaxf(vs[0], vs[PP - 1]);
       const float vinv = vmax > 0.0f ? 1.0f / vmax : 0.0f;
-      const float most = ym > 0.0f ? pos_pow(ym, e.beta) : 0.0f;
+      const float most = ent_weight(ym, e.beta);
       const int ex = min(max((int)(__float_as_uint(most) >> 23) - 126, -100), 100);
       const float up = __uint_as_float((uint32_t)(127 - ex) << 23), down = __uint_as_float((uint32_t)(127 + ex) << 23);
       uint32_t bf[2][1][2];
@@ -502,24 +598,22 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
         const float f0 = PP == 1 ? up : up * (vs[16 * kt / P] * vinv);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float2 z = make_float2(-CUDART_INF_F, -CUDART_INF_F);
-          if (ym > 0.0f)
-            z = *reinterpret_cast<const float2*>(e.z + ((tile0 + t) * G + r) * kEntKeys + 16 * kt + 8 * j + 2 * c);
-          const float y0 = (z.x - tau_r.x) - tau_r.y, y1 = (z.y - tau_r.x) - tau_r.y;
-          const __half2 p = __floats2half2_rn(y0 > 0.0f ? pos_pow(y0, e.beta) * f0 : 0.0f,
-                                              y1 > 0.0f ? pos_pow(y1, e.beta) * f0 : 0.0f);
+          const float y0 = (z[kt][j].x - tau_r.x) - tau_r.y, y1 = (z[kt][j].y - tau_r.x) - tau_r.y;
+          const __half2 p = __floats2half2_rn(ent_weight(y0, e.beta) * f0, ent_weight(y1, e.beta) * f0);
           bf[kt][0][j] = *reinterpret_cast<const uint32_t*>(&p);
         }
       }
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[warp], phase))) {
+      const int n = used + i, sg = n & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[warp][sg], (uint32_t)(n >> 1) & 1u))) {
         stuck = true;
         break;
       }
-      phase ^= 1u;
+      const uint32_t slab = base + (warp * 2 + sg) * SLAB;
+      unsigned char* slab_p = base_p + (warp * 2 + sg) * SLAB;
       bool wrote = false;  // places past the sequence's end, or of no page: any bytes, so that w = 0 meets no NaN
 #pragma unroll
       for (int q = 0; q < PP; ++q) {
-        const int nv = f[q] >= 0 ? min(P, s.L - sp.page(t * PP + q) * P) : 0;
+        const int nv = f[q] >= 0 ? min(P, s.L - sp.page(tt * PP + q) * P) : 0;
         if (nv == P) continue;
         for (int k = lane; k < (P - nv) * (D / 16); k += 32)
           *reinterpret_cast<uint4*>(slab_p + (q * P + nv) * D + k * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -544,10 +638,15 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
       }
       __syncwarp();
     }
-  }
-  if (stuck && lane == 0) {
-    raise_flag(a.c.status, ENTMAXKV_DEV_TIMEOUT);
-    mbar_wait_bounded(&bars[warp], phase);
+    if (stuck) {  // what else was asked for lands before the warp goes on
+      if (lane == 0) {
+        raise_flag(a.c.status, ENTMAXKV_DEV_TIMEOUT);
+        for (int n = used; n < used + mine; ++n) mbar_wait_bounded(&bars[warp][n & 1], (uint32_t)(n >> 1) & 1u);
+      }
+      __syncwarp();
+    }
+    if (__syncthreads_or(stuck)) break;  // (and the list is done with)
+    used += mine;
   }
   __syncthreads();
   // the warps' sums, in order, through the slabs' place (they are done with)
@@ -567,7 +666,7 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
     part[i] = v;
   }
   cluster_sync();
-  // each block adds up its eighth of the outputs
+  // each block adds up its share of the outputs
   const int per = (G * D + C - 1) / C;
   for (int i = rank * per + tid; i < min(G * D, (rank + 1) * per); i += NTH) {
     float v = 0.0f;
@@ -586,16 +685,16 @@ static size_t ent_line(const entmaxkv_config& cfg, int n_seqs) {
 
 size_t attend_entmax_bytes(const entmaxkv_config& cfg, int n_seqs) {
   const size_t line = ent_line(cfg, n_seqs);
-  return up256e((size_t)(n_seqs + 1) * 8) + up256e(line * cfg.group * kEntKeys * 4) + up256e(line * cfg.group * 4);
+  return up256e((size_t)n_seqs * sizeof(EntUnit)) + up256e(line * cfg.group * kEntKeys * 4) + up256e(line * cfg.group * 4);
 }
 
 template <bool I8, int D, int P>
 static cudaError_t entmax_t(EntArgs& e, int sms, cudaStream_t st) {
   const Q8AttendArgs& a = e.a;
   const int smem1 = kScoreWarps * kScoreSlabs * kEntKeys * D + 1024;
-  // held scores, V slabs and the warps' sums take turns
-  const int held = kEntWarps * kEntHeld * 32 * 4, slabs = kEntWarps * kEntKeys * D, red = kEntWarps * 8 * D * 4;
-  const int smem2 = max(held, max(slabs, red)) + 1024;
+  // the scores handed round, V slabs with the list behind them, and the warps' sums take turns
+  const int sent = kEntCluster * kEntWarps * kEntSent * 4, slabs = 2 * kEntWarps * kEntKeys * D + kEntList * 4;
+  const int red = kEntWarps * 8 * D * 4, smem2 = max(sent, max(slabs, red)) + 1024;
   cudaError_t err = ensure_smem((const void*)ent_score_kernel<I8, D, P>, smem1);
   if (err == cudaSuccess) err = ensure_smem((const void*)ent_finish_kernel<I8, D, P>, smem2);
   if (err != cudaSuccess) return err;
@@ -637,8 +736,8 @@ cudaError_t launch_attend_entmax(const entmaxkv_config& cfg, Q8AttendArgs a, boo
   e.beta = (float)(1.0 / ((double)alpha - 1.0));
   const size_t line = ent_line(cfg, a.b.n_seqs);
   char* p = static_cast<char*>(ws);
-  a.cum = reinterpret_cast<long long*>(p);
-  p += up256e((size_t)(a.b.n_seqs + 1) * 8);
+  e.slots = reinterpret_cast<EntUnit*>(p);
+  p += up256e((size_t)a.b.n_seqs * sizeof(EntUnit));
   e.z = reinterpret_cast<float*>(p);
   p += up256e(line * a.c.G * kEntKeys * 4);
   e.pmax = reinterpret_cast<float*>(p);
