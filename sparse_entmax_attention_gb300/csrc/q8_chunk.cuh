@@ -111,6 +111,16 @@ __device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t* r) {
       : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n" ::"r"(
@@ -328,14 +338,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
           }
           tm_fence_after();
           const PageMeta* pg = meta[(tile + j) & 3];
-          // 32 columns (keys 32c ..) from their raw sums to halves at columns 64 + 16c: behind the sums that
+          // 64 columns (keys 64c ..) from their raw sums to halves at columns 64 + 32c: behind the sums that
           // are still to be read, which come last to first
-          auto weigh = [&](int c, const float (&raw)[32]) {
-            unsigned long long t2[16];
+          auto weigh = [&](int c, const float (&raw)[64]) {
+            unsigned long long t2[32];
             float mx = -CUDART_INF_F;
 #pragma unroll
-            for (int q = 0; q < 32 / P; ++q) {
-              const PageMeta pm = pg[c * (32 / P) + q];
+            for (int q = 0; q < 64 / P; ++q) {
+              const PageMeta pm = pg[c * (64 / P) + q];
               unsigned long long* u = t2 + q * (P / 2);
               const float* v = raw + q * P;
               const bool past = pm.key0 + P - 1 <= pos_min;
@@ -444,23 +454,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
                   tm_st16(o_tm + 16 * i, o);
                 }
               }
-              const __half2 fh = __float2half2_rn(f);
+              if (c == 0) {  // the weights of the other 64 keys of this tile too
+                const __half2 fh = __float2half2_rn(f);
 #pragma unroll 1
-              for (int i = 3; i > c; --i) {
-                uint32_t o[16];
-                tm_ld16(s_tm + 64 + 16 * i, o);
+                for (int i = 2; i < 4; ++i) {
+                  uint32_t o[16];
+                  tm_ld16(s_tm + 64 + 16 * i, o);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&o[k]), fh);
-                  o[k] = *reinterpret_cast<const uint32_t*>(&h);
+                  for (int k = 0; k < 16; ++k) {
+                    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&o[k]), fh);
+                    o[k] = *reinterpret_cast<const uint32_t*>(&h);
+                  }
+                  tm_st16(s_tm + 64 + 16 * i, o);
                 }
-                tm_st16(s_tm + 64 + 16 * i, o);
               }
             }
             const unsigned long long base2 = f2_splat(M > -CUDART_INF_F ? kLift - M : 0.0f);
-            uint32_t w16[16];
+            uint32_t w32[32];
 #pragma unroll
-            for (int q = 0; q < 32 / P; ++q) {
+            for (int q = 0; q < 64 / P; ++q) {
               unsigned long long s2[2] = {0ull, 0ull};
 #pragma unroll
               for (int i = 0; i < P / 2; ++i) {
@@ -470,24 +482,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
                 e1 = ex2f(e1);
                 s2[i & 1] = f2_add(s2[i & 1], f2_pack(e0, e1));
                 const __half2 h = __floats2half2_rn(e0, e1);
-                w16[q * (P / 2) + i] = *reinterpret_cast<const uint32_t*>(&h);
+                w32[q * (P / 2) + i] = *reinterpret_cast<const uint32_t*>(&h);
               }
-              l = fmaf(f2_sum(f2_add(s2[0], s2[1])), pg[c * (32 / P) + q].ivs, l);
+              l = fmaf(f2_sum(f2_add(s2[0], s2[1])), pg[c * (64 / P) + q].ivs, l);
             }
-            tm_st16(s_tm + 64 + 16 * c, w16);
+            tm_st32(s_tm + 64 + 32 * c, w32);
           };
-          float ra[32], rb[32];
-          tm_ld32(s_tm + 96, ra);
 #pragma unroll 1
-          for (int c = 3; c > 0; c -= 2) {
+          for (int c = 1; c >= 0; --c) {
+            float raw[64];
+            tm_ld32(s_tm + 64 * c, raw);
+            tm_ld32(s_tm + 64 * c + 32, raw + 32);
             tm_wait_ld();
-            tm_tie32(ra);
-            tm_ld32(s_tm + 32 * c - 32, rb);
-            weigh(c, ra);
-            tm_wait_ld();
-            tm_tie32(rb);
-            if (c > 1) tm_ld32(s_tm + 32, ra);
-            weigh(c - 1, rb);
+            tm_tie32(raw);
+            tm_tie32(raw + 32);
+            weigh(c, raw);
           }
           tm_wait_st();
           tm_fence_before();
