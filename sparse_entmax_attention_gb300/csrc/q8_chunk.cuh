@@ -78,6 +78,12 @@ __device__ __forceinline__ void tm_commit(uint64_t* bar) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 // 32 columns of the thread's lane.
 __device__ __forceinline__ void tm_ld32(uint32_t addr, float* v) {
   uint32_t r[32];
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
   constexpr int KP = kChunkKeys / P;           // pages a tile
   constexpr int TILE = kChunkKeys * D * 2;     // bytes of a half tile
   extern __shared__ __align__(128) unsigned char dyn_sm[];
-  __shared__ uint64_t q_full, o_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
+  __shared__ uint64_t q_full, o_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2][2], p_full[2][2];
   __shared__ uint32_t tm_base;
   __shared__ PageMeta meta[4][KP];
   __shared__ volatile int gave_up;
@@ -228,14 +234,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
   const uint32_t q_sm = sm0, k_sm = sm0 + 2 * TILE, v_sm = sm0 + 4 * TILE;
   if (tid == 0) {
     mbar_init(&q_full, 256);
-    mbar_init(&o_full, 1);
+    mbar_init(&o_full, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&k_full[i], 128);
       mbar_init(&v_full[i], 128);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&k_empty[i], 2);
+      mbar_init(&v_empty[i], 2);
+      for (int c = 0; c < 2; ++c) {
+        mbar_init(&s_full[i][c], 1);
+        mbar_init(&p_full[i][c], 128);
+      }
     }
     gave_up = 0;
     mbar_fence_init();
@@ -265,7 +273,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
     const int row = tid & 127;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_tm = tm + lanes + 128 * wg, o_tm = tm + lanes + 256 + D * wg;
-    int it = 0, seg = 0, tile = 0;  // tiles of this half, items and all tiles so far
+    int it = 0, seg = 0, tile = 0;  // phases of this half's sums, items and all tiles so far
     bool ok = true;
     int item = -1;
     for (long long w = w_begin; w < w_end && ok; ++seg) {
@@ -331,15 +339,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
       const int lo_max = __reduce_max_sync(0xffffffffu, lo);
       float M = -CUDART_INF_F, l = 0.0f;
       if (half) {
-        for (int j = 0; j < x.n; ++j, ++it) {
-          if (!wait_warp(&s_full[wg], it)) {
-            ok = false;
-            break;
-          }
-          tm_fence_after();
+        for (int j = 0; j < x.n && ok; ++j) {
           const PageMeta* pg = meta[(tile + j) & 3];
-          // 64 columns (keys 64c ..) from their raw sums to halves at columns 64 + 32c: behind the sums that
-          // are still to be read, which come last to first
+          // 64 columns (keys 64c ..) from their raw sums to halves over the first of them
           auto weigh = [&](int c, const float (&raw)[64]) {
             unsigned long long t2[32];
             float mx = -CUDART_INF_F;
@@ -442,9 +444,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
               const float f = move ? ex2f(M - mx) : 1.0f;  // 0 from -inf
               if (move) M = mx;
               l *= f;
-              tm_wait_ld();  // (a load under way keeps its registers)
-              tm_wait_st();
-              if (j > 0) {
+              if (j > 0 || c == 0) {
+                // behind the product of the 64 keys before: the next commit to the other columns' barrier
+                ok = wait_warp(&s_full[wg][c ^ 1], it + j + (c ^ 1));
+                tm_fence_after();
 #pragma unroll 1
                 for (int i = 0; i < D / 16; ++i) {
                   uint32_t o[16];
@@ -452,20 +455,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
 #pragma unroll
                   for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
                   tm_st16(o_tm + 16 * i, o);
-                }
-              }
-              if (c == 0) {  // the weights of the other 64 keys of this tile too
-                const __half2 fh = __float2half2_rn(f);
-#pragma unroll 1
-                for (int i = 2; i < 4; ++i) {
-                  uint32_t o[16];
-                  tm_ld16(s_tm + 64 + 16 * i, o);
-#pragma unroll
-                  for (int k = 0; k < 16; ++k) {
-                    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&o[k]), fh);
-                    o[k] = *reinterpret_cast<const uint32_t*>(&h);
-                  }
-                  tm_st16(s_tm + 64 + 16 * i, o);
                 }
               }
             }
@@ -486,10 +475,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
               }
               l = fmaf(f2_sum(f2_add(s2[0], s2[1])), pg[c * (64 / P) + q].ivs, l);
             }
-            tm_st32(s_tm + 64 + 32 * c, w32);
+            tm_st32(s_tm + 64 * c, w32);
           };
 #pragma unroll 1
           for (int c = 1; c >= 0; --c) {
+            if (!ok || !wait_warp(&s_full[wg][c], it + j)) {
+              ok = false;
+              break;
+            }
+            tm_fence_after();
             float raw[64];
             tm_ld32(s_tm + 64 * c, raw);
             tm_ld32(s_tm + 64 * c + 32, raw + 32);
@@ -497,11 +491,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
             tm_tie32(raw);
             tm_tie32(raw + 32);
             weigh(c, raw);
+            tm_wait_st();
+            tm_fence_before();
+            mbar_arrive(&p_full[wg][c]);
           }
-          tm_wait_st();
-          tm_fence_before();
-          mbar_arrive(&p_full[wg]);
         }
+        // (the commits behind the last products, so that no phase is passed over)
+        ok = ok && wait_warp(&s_full[wg][1], it + x.n) && wait_warp(&s_full[wg][0], it + x.n);
+        it += x.n + 1;
       }
       if (!ok || !wait_warp(&o_full, seg)) {
         ok = false;
@@ -662,54 +659,67 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
     }
   } else {  // ------------------------------------------------------- products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
-    if (warp == 12 && lane == 0) {
-      constexpr uint32_t id_qk = instr_desc(kChunkKeys, 0), id_pv = instr_desc(D, 1);
-      const uint64_t q_desc = smem_desc(q_sm, 16, 1024), k_desc = smem_desc(k_sm, 16, 1024);
+    if (warp < 14) {  // a warp a half, one elected thread of it
+      const int hf = warp - 12;
+      constexpr uint32_t id_qk = instr_desc(kChunkKeys / 2, 0), id_pv = instr_desc(D, 1);
+      const uint64_t q_desc = smem_desc(q_sm + hf * TILE, 16, 1024), k_desc = smem_desc(k_sm, 16, 1024);
       const uint64_t v_desc = smem_desc(v_sm, 16384, 1024);
-      int it = 0, seg = 0;  // tiles and items so far
-      int p_it[2] = {0, 0};
+      const uint32_t s_tm = tm + 128 * hf, o_tm = tm + 256 + D * hf;
+      int it = 0, p_it = 0;  // tiles so far, and those of this half
       bool ok = true;
-      auto scores = [&](int hf, int sg) {  // (addresses advance in units of 16 bytes)
-        const uint64_t q = q_desc + (uint32_t)(hf * (TILE >> 4)), k = k_desc + (uint32_t)(sg * (TILE >> 4));
-        const uint32_t d = tm + 128 * hf;
+      auto scores = [&](int c, int sg) {  // (addresses advance in units of 16 bytes)
+        const uint64_t k = k_desc + (uint32_t)(sg * (TILE >> 4) + c * 512);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const uint32_t o = ((i >> 2) * 16384 + (i & 3) * 32) >> 4;
-          mma_ss(d, q + o, k + o, id_qk, i > 0);
+          mma_ss(s_tm + 64 * c, q_desc + o, k + o, id_qk, i > 0);
         }
-        tm_commit(&s_full[hf]);
+        tm_commit(&s_full[hf][c]);
       };
       int item = -1;
-      if (w_begin >= w_end) g.cuts[blockIdx.x] = make_int2(-1, 0);
-      for (long long w = w_begin; w < w_end && ok; ++seg) {
+      if (tid == 384 && w_begin >= w_end) g.cuts[blockIdx.x] = make_int2(-1, 0);
+      for (long long w = w_begin, seg = 0; w < w_end && ok; ++seg) {
         const ChunkSeg x = chunk_seg(g, w, w_end, S, n_items, item);
         item = x.item + 1;
-        if (seg == 0) g.cuts[blockIdx.x] = make_int2(x.t0 > 0 ? x.item : -1, x.kvh);
-        const int halves = x.s.count * G - x.rt * kChunkRows > 128 ? 2 : 1;
-        ok = wait(&q_full, seg) && wait(&k_full[it & 1], it / 2);
+        if (tid == 384 && seg == 0) g.cuts[blockIdx.x] = make_int2(x.t0 > 0 ? x.item : -1, x.kvh);
+        const bool mine = x.s.count * G - x.rt * kChunkRows > 128 * hf;
+        ok = wait_warp(&q_full, (int)seg) && wait_warp(&k_full[it & 1], it / 2);
         if (!ok) break;
         tm_fence_after();
-        for (int hf = 0; hf < halves; ++hf) scores(hf, it & 1);
-        tm_commit(&k_empty[it & 1]);
+        if (elect_one()) {
+          if (mine) {
+            scores(1, it & 1);
+            scores(0, it & 1);
+          }
+          tm_commit(&k_empty[it & 1]);  // (a half without rows commits nothing but its word)
+        }
         for (int j = 0; j < x.n && ok; ++j, ++it) {
           const int sg = it & 1;
-          ok = wait(&v_full[sg], it / 2) && (j + 1 == x.n || wait(&k_full[sg ^ 1], (it + 1) / 2));
-          for (int hf = 0; hf < halves && ok; ++hf) {
-            ok = wait(&p_full[hf], p_it[hf]);
-            if (!ok) break;
-            ++p_it[hf];
-            tm_fence_after();
-            const uint64_t v = v_desc + (uint32_t)(sg * (TILE >> 4));
-            const uint32_t d = tm + 256 + D * hf, pa = tm + 128 * hf + 64;
+          ok = wait_warp(&v_full[sg], it / 2) && (j + 1 == x.n || wait_warp(&k_full[sg ^ 1], (it + 1) / 2));
+          if (mine) {
+#pragma unroll 1
+            for (int c = 1; c >= 0 && ok; --c) {
+              ok = wait_warp(&p_full[hf][c], p_it);
+              if (!ok) break;
+              tm_fence_after();
+              if (elect_one()) {
+                const uint64_t v = v_desc + (uint32_t)(sg * (TILE >> 4) + c * 512);
 #pragma unroll
-            for (int k = 0; k < kChunkKeys / 16; ++k) mma_ts(d, pa + 8 * k, v + 128 * k, id_pv, k > 0 || j > 0);
-            if (j + 1 < x.n) scores(hf, sg ^ 1);
+                for (int k = 0; k < kChunkKeys / 32; ++k)
+                  mma_ts(o_tm, s_tm + 64 * c + 8 * k, v + 128 * k, id_pv, k > 0 || j > 0 || c == 0);
+                if (j + 1 < x.n) scores(c, sg ^ 1);
+                else tm_commit(&s_full[hf][c]);
+              }
+            }
+            ++p_it;
           }
           if (!ok) break;
-          tm_commit(&v_empty[sg]);
-          if (j + 1 < x.n) tm_commit(&k_empty[sg ^ 1]);
+          if (elect_one()) {
+            tm_commit(&v_empty[sg]);
+            if (j + 1 < x.n) tm_commit(&k_empty[sg ^ 1]);
+          }
         }
-        if (ok) tm_commit(&o_full);
+        if (ok && elect_one()) tm_commit(&o_full);
         w += x.n;
       }
     }
