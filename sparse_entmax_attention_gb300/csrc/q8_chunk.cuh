@@ -344,14 +344,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
           // 64 columns (keys 64c ..) from their raw sums to halves over the first of them
           auto weigh = [&](int c, const float (&raw)[64]) {
             unsigned long long t2[32];
-            float mx = -CUDART_INF_F;
+            // exponents against the bound so far, so that they need no other pass
+            float base = M > -CUDART_INF_F ? kLift - M : 0.0f, mx = -CUDART_INF_F;
 #pragma unroll
             for (int q = 0; q < 64 / P; ++q) {
               const PageMeta pm = pg[c * (64 / P) + q];
               unsigned long long* u = t2 + q * (P / 2);
               const float* v = raw + q * P;
               const bool past = pm.key0 + P - 1 <= pos_min;
-              float add = pm.lv;
+              float add = pm.lv + base;
               if (biased && past) add = fmaf(-slope, (float)(pos - pm.key0), add);
               const unsigned long long k2 = f2_splat(pm.ks * kc), a2 = f2_splat(add);
               if (capped) {  // y = raw·k, then cap·log2 e·y·T(y²)
@@ -439,10 +440,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
             }
             // the bound moves when the maximum passes it by more than the slack: in an item's first columns, and
             // seldom behind them
-            const bool move = mx > M + kSlack;
+            const bool move = M > -CUDART_INF_F ? mx > kLift + kSlack : mx > M;
             if (__any_sync(0xffffffffu, move)) {
-              const float f = move ? ex2f(M - mx) : 1.0f;  // 0 from -inf
-              if (move) M = mx;
+              float f = 1.0f;
+              if (move) {
+                const float to = mx - base, less = kLift - mx;  // the new bound, and what it takes off
+                f = ex2f(M - to);                               // 0 from -inf
+                M = to;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) t2[i] = f2_add(t2[i], f2_splat(less));
+              }
               l *= f;
               if (j > 0 || c == 0) {
                 // behind the product of the 64 keys before: the next commit to the other columns' barrier
@@ -458,7 +465,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
                 }
               }
             }
-            const unsigned long long base2 = f2_splat(M > -CUDART_INF_F ? kLift - M : 0.0f);
             uint32_t w32[32];
 #pragma unroll
             for (int q = 0; q < 64 / P; ++q) {
@@ -466,7 +472,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
 #pragma unroll
               for (int i = 0; i < P / 2; ++i) {
                 float e0, e1;
-                f2_unpack(f2_add(t2[q * (P / 2) + i], base2), e0, e1);
+                f2_unpack(t2[q * (P / 2) + i], e0, e1);
                 e0 = ex2f(e0);
                 e1 = ex2f(e1);
                 s2[i & 1] = f2_add(s2[i & 1], f2_pack(e0, e1));
@@ -568,7 +574,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
     constexpr int CPR = D / 16;                   // 16-code chunks of a row
     constexpr int RPI = 32 / CPR, NI = 32 / RPI;  // rows a load, loads of a warp's rows
     constexpr int PW = 32 / P;                    // pages of a warp's rows: 1 or 2
-    const int cch = lane % CPR, crow = lane / CPR;
+    // eight lanes store to eight banks' quads: at D = 128 four chunks of two rows, not eight of one, whose two 64-wide
+    // halves would meet in the same banks
+    const int cch = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane % CPR;
+    const int crow = D == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane / CPR;
     int it = 0;
     bool ok = true;
     int item = -1;
@@ -603,10 +612,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
           codes_half<I8, false>(codes[i].y, h0.z, h0.w);
           codes_half<I8, false>(codes[i].z, h1.x, h1.y);
           codes_half<I8, false>(codes[i].w, h1.z, h1.w);
-          // chunks of the two 64-wide halves would meet in the same banks: those of the second go odd first
-          const bool flip = cch & 4;
-          sts128(dst + tile_off(rr, 2 * cch + (flip ? 1 : 0)), flip ? h1 : h0);
-          sts128(dst + tile_off(rr, 2 * cch + (flip ? 0 : 1)), flip ? h0 : h1);
+          sts128(dst + tile_off(rr, 2 * cch), h0);
+          sts128(dst + tile_off(rr, 2 * cch + 1), h1);
         }
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       };
