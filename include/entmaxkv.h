@@ -510,13 +510,13 @@ int32_t entmaxkv_read_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* ca
  * Its score for query head h is s = scale * q.k; with softcap > 0, s becomes
  * softcap * tanh(s / softcap); with slopes, slopes[h] * |x - j| is taken off.
  *   scale      0: 1/sqrt(head_dim)
- *   softcap    0: none
+ *   softcap    0: none, else from 2^-60 to 2^60
  *   window     0: none
  *   slopes     (device) [Hq] float32, or NULL
  *   prefix     (device) [n_seqs] int32 tokens of a prefix that every row sees
  *              (at most the sequence's length counts), or NULL
  *   first_key  (device) [total] int32 first key of each row (the start of its
- *              document), or NULL
+ *              document), in any order, or NULL
  */
 typedef struct {
   float scale;
@@ -543,10 +543,15 @@ size_t entmaxkv_attend_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, 
  *   workspace  (device) at least entmaxkv_attend_q8_workspace(...) bytes,
  *              256-byte aligned, contents are scratch; not to be shared by
  *              calls that may run at the same time
- * Products and sums are float32; before they meet V, weights are rounded to
- * 11 bits, or to 2^-24 of the largest weight of their page where that is more. The order of every sum is
- * fixed by the arguments and the device, so equal calls give equal bits.
- * Rows of a slot with a bad row or batch entry are left as they were.
+ * Products and sums are float32. Before they meet V's codes, weights (times
+ * their page's V scale) are rounded to halves: to 11 bits, or where that is
+ * more to 2^-33 of the row's largest (softmax) or 2^-24 of the largest of
+ * their 32 keys (entmax). Query rows are exact down to 2^-27 of their head's
+ * largest value; an infinity or NaN in q spoils its own row and head only.
+ * Scales of pages in use are positive and finite, as append leaves them. The
+ * order of every sum is fixed by the arguments and the device, so equal calls
+ * give equal bits. Rows of a slot with a bad row or batch entry are left as
+ * they were.
  */
 int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache,
                            const entmaxkv_batch* batch, const entmaxkv_rows* q,

@@ -182,14 +182,15 @@ cudaError_t launch_append_q8(const Q8Cache& c, const Q8Batch& b, const Q8Rows& k
                              cudaStream_t st);
 cudaError_t launch_read_q8(const Q8Cache& c, const Q8Batch& b, const int32_t* first, const Q8Rows& k, const Q8Rows& v,
                            bool i8, int sms, cudaStream_t st);
-size_t attend_softmax_bytes(const entmaxkv_config& cfg, int n_seqs, int max_count);
+size_t attend_softmax_bytes(const entmaxkv_config& cfg, int n_seqs);
 cudaError_t launch_attend_softmax(Q8AttendArgs a, bool i8, void* ws, int sms, cudaStream_t st);
 // Rows (tokens times the group) a sequence up to which the streaming kernel
 // answers a batch, 16 rows at a time; with more, one 128-row product tile is the
-// better fit for every slot. Measured, streaming against products, 24 sequences
-// of 6000 tokens, 4 KV heads, int8: d = 128 46/120 us at 16 rows, 77/125 at 32,
-// 108/127 at 48, 130/127 at 64; d = 64 36/78, 58/83, 82/83, 84/84.
-constexpr int kStreamRows = 48;
+// better fit for every slot. Measured, streaming against products, int8, 4 KV
+// heads: 24 sequences of 6000 tokens at d = 128 46/99 us at 16 rows, 77/104 at 32,
+// 108/105 at 48, 137/105 at 64; 4 of 30000 (pages of 16) 46/95, 68/103, 94/104,
+// 117/107; 24 of 6000 at d = 64 35/62, 58/67, 82/67, 105/67.
+__host__ __device__ constexpr int stream_rows(int D) { return D == 128 ? 48 : 32; }
 size_t attend_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total);
 cudaError_t launch_attend_chunk(const Q8AttendArgs& a, bool i8, void* ws, int sms, cudaStream_t st);
 size_t attend_entmax_bytes(const entmaxkv_config& cfg, int n_seqs);

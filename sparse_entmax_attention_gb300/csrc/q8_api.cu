@@ -52,7 +52,7 @@ static Q8Rows rows_of(const entmaxkv_rows* r) {
   return Q8Rows{static_cast<__nv_bfloat16*>(r->data), r->token_stride, r->head_stride};
 }
 static bool streams(const entmaxkv_config* c, int max_count) {
-  return (long long)max_count * c->group <= kStreamRows;
+  return (long long)max_count * c->group <= stream_rows(c->head_dim);
 }
 static int32_t code_of(cudaError_t e) { return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_ERR_CUDA; }
 
@@ -134,7 +134,7 @@ size_t entmaxkv_attend_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, 
                                     float alpha) {
   if (check_attend(cfg, n_seqs, total, max_count, alpha)) return 0;
   if (alpha > 1.0f) return attend_entmax_bytes(*cfg, n_seqs);
-  return streams(cfg, max_count) ? attend_softmax_bytes(*cfg, n_seqs, max_count) : attend_chunk_bytes(*cfg, n_seqs, total);
+  return streams(cfg, max_count) ? attend_softmax_bytes(*cfg, n_seqs) : attend_chunk_bytes(*cfg, n_seqs, total);
 }
 
 int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache, const entmaxkv_batch* batch,
@@ -145,12 +145,11 @@ int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* 
   if ((st = check_attend(cfg, batch->n_seqs, batch->total, batch->max_count, alpha))) return st;
   Q8Score sc{0.0f, 0.0f, 0.0f, 0, nullptr, nullptr, nullptr};
   if (score) {
-    if (!isfinite(score->scale) || score->scale < 0.0f || !isfinite(score->softcap) || score->softcap < 0.0f ||
-        score->window < 0)
+    if (!isfinite(score->scale) || score->scale < 0.0f || score->window < 0) return ENTMAXKV_ERR_INVALID_ARG;
+    if (score->softcap != 0.0f && !(score->softcap >= 0x1p-60f && score->softcap <= 0x1p60f))
       return ENTMAXKV_ERR_INVALID_ARG;
     sc = Q8Score{score->scale, score->softcap, score->softcap > 0.0f ? 1.0f / score->softcap : 0.0f, score->window,
                  score->slopes, score->prefix, score->first_key};
-    if (!isfinite(sc.inv_cap)) return ENTMAXKV_ERR_INVALID_ARG;
   }
   if (sc.scale == 0.0f) sc.scale = (float)(1.0 / sqrt((double)cfg->head_dim));
   if (idle(batch)) return ENTMAXKV_OK;

@@ -531,9 +531,10 @@ cudaError_t make_q8_map(CUtensorMap* map, const void* pool, int nphys, int Hkv, 
 
 static size_t up256z(size_t x) { return (x + 255) & ~(size_t)255; }
 
-size_t attend_softmax_bytes(const entmaxkv_config& cfg, int n_seqs, int max_count) {
+size_t attend_softmax_bytes(const entmaxkv_config& cfg, int n_seqs) {
   const size_t pieces = (size_t)kAttMaxBlocks * 16 * 2 * 8;  // 16 warps of 8 rows, or 8 of 16
-  return up256z((size_t)(n_seqs + 1) * 8) + up256z((size_t)n_seqs * sizeof(AttSlot)) + up256z(pieces * cfg.head_dim * 4) + up256z(pieces * 8);
+  return up256z((size_t)(n_seqs + 1) * 8) + up256z((size_t)n_seqs * sizeof(AttSlot)) +
+         up256z(pieces * cfg.head_dim * 4) + up256z(pieces * 8);
 }
 
 template <bool I8, int D, int P, int NT>

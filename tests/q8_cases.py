@@ -57,6 +57,13 @@ def dense(c, b, h, side):
     return x.reshape(-1, c.cfg.head_dim)[:L].cpu().numpy()
 
 
+def v_scales(c, b, h):
+    """[L] float64: the V scale of each token's page."""
+    P, L = c.cfg.page_size, int(c.seq_lens[b])
+    ph = c.block_table[b, :-(-L // P)].long()
+    return np.repeat(c.v_scale[ph, h].double().cpu().numpy(), P)[:L]
+
+
 def filled(code, lens, counts, seed=0, loud=1.0, **kw):
     """A cache whose sequences hold random tokens (through append_q8)."""
     c = empty_cache(code, lens, seed=seed, **kw)
@@ -71,14 +78,17 @@ def filled(code, lens, counts, seed=0, loud=1.0, **kw):
     return c, q
 
 
-def check_attend(c, q, counts, o, seq_ids=None, alpha=1.0, weight_eps=2.0 ** -11, start=None, scale=0.0, softcap=0.0,
+def check_attend(c, q, counts, o, seq_ids=None, alpha=1.0, start=None, scale=0.0, softcap=0.0,
                  slopes=None, window=0, prefix=None, first_key=None):
     """Compare rows with the oracle. Bounds, per element of a row's output o = Σ p v:
       2^-8·|o|           the rounding to bf16 (half a step),
-      weight_eps·Σ p|v|  each weight's rounding before it meets V,
-      2^-24·Σ p_page|v|  and what a half keeps of a small one: weights meet V as halves of at least half their
-                         page's largest weight p_page scaled to 1, whose spacing below 2^-14 is 2^-24, so
-                         rounding moves each by at most 2^-25·(2·p_page),
+      2^-11·Σ p|v|       each weight's rounding to a half before it meets V (half a step),
+      and what a half keeps of a small one: a weight times its page's V scale s meets the codes c (v = s·c) as a
+      half, whose spacing below 2^-14 is 2^-24, so rounding moves it by up to 2^-25.
+        softmax: the row's largest p·s lies at 2^8 or above (2^{t − M + 8} with M at most the largest t), so that
+                 is at most 2^-33·max(p·s) for each key seen: 2^-33·max(p·s)·Σ|c|;
+        entmax:  of 32 keys the largest p is brought to 1/2 or above, and its s/max(s) is at most 1: at most
+                 2^-24·max(p)·max(s) for each key of the support: 2^-24·max(p)·max(s)·Σ|c| over the support,
       δ-terms            a score off by δ = 2^-20·(Σ|q||k|·scale + slope·L + cap) + 2^-20 (fp32 sums of d
                          products, a few further fp32 operations and 2^-22 functions) moves a softmax
                          weight by 2δp; an entmax weight [z−τ]^β by at most β·(y+δz)^{β−1}·δz for β ≥ 1
@@ -112,10 +122,13 @@ def check_attend(c, q, counts, o, seq_ids=None, alpha=1.0, weight_eps=2.0 ** -11
                 dp = np.where(near, dz ** beta if beta < 1 else beta * np.maximum(y + dz, 0.0) ** (beta - 1) * dz, 0.0)
                 dp = np.nan_to_num(dp)
                 t_tol = 2 * (alpha - 1.0) * delta
-            P = c.cfg.page_size
-            pages = np.pad(Pw, ((0, 0), (0, -len(K) % P))).reshape(n, -1, P)
-            page_top = np.repeat(pages.max(2), P, axis=1)[:, :len(K)]
-            tol = 2.0 ** -8 * np.abs(ref) + (weight_eps * Pw + 2.0 ** -24 * page_top + dp) @ np.abs(V) + 1e-30
+            s = v_scales(c, seq, h // G)
+            if alpha == 1.0:
+                small = 2.0 ** -33 * (Pw * s).max(1, initial=0.0)[:, None] * np.isfinite(S)
+            else:
+                on = (Pw > 0) | (dp > 0)
+                small = 2.0 ** -24 * Pw.max(1, initial=0.0)[:, None] * (on * s).max(1, initial=0.0)[:, None] * on
+            tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 * Pw + small / s + dp) @ np.abs(V) + 1e-30
             err = np.abs(out[r0:r0 + n, h] - ref)
             assert np.all(err <= tol), (b, h, float((err / tol).max()))
             some = ~np.isnan(t)

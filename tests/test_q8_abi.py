@@ -70,7 +70,8 @@ def test_bad_attend_arguments(lib):
         assert attend(lib, q=rows) == 1 and attend(lib, out=rows) == 1
     assert attend(lib, out=B.RowsView(P256, 0, 128)) == 1                             # rows that are written
     for score in (B.ScoreView(-1.0, 0.0, 0), B.ScoreView(0.0, -1.0, 0), B.ScoreView(0.0, 0.0, -1),
-                  B.ScoreView(float("nan"), 0.0, 0), B.ScoreView(0.0, float("inf"), 0), B.ScoreView(0.0, 1e-45, 0)):
+                  B.ScoreView(float("nan"), 0.0, 0), B.ScoreView(0.0, float("inf"), 0), B.ScoreView(0.0, 1e-45, 0),
+                  B.ScoreView(0.0, 1e19, 0), B.ScoreView(0.0, float("nan"), 0)):
         assert attend(lib, score=score) == 1
 
 

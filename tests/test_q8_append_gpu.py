@@ -235,3 +235,24 @@ def test_read_back_into_a_16_bit_cache():
     mag = (q[0].float().abs()[:, None] * kk.abs()).sum(-1).max() / d ** 0.5
     assert float((a.tau - b.tau).abs().max()) <= float(2.0 ** -8 * mag * 0.5 * 2)
     torch.testing.assert_close(b.out.float(), a.out, rtol=0.1, atol=0.1)
+
+
+@pytest.mark.parametrize("n", [300, 1100])
+def test_many_slots_write_and_read_what_few_do(n):
+    """One call for all slots and one for every 100 of them leave the same cache and read the same rows."""
+    hkv, d, P = 2, 64, 16
+    lens = [1 + (b * 11) % 70 for b in range(n)]
+    k, v = _rows(sum(lens), hkv, d, 3), _rows(sum(lens), hkv, d, 4)
+    one, many = (empty_cache("int8", lens, hkv=hkv, d=d, P=P) for _ in range(2))
+    B.append_q8(one, k, v, batch_of(lens))
+    ko, vo = B.read_q8(one, i32([0] * n), batch_of(lens))
+    for b in range(0, n, 100):
+        ids = list(range(b, min(b + 100, n)))
+        a, z = sum(lens[:b]), sum(lens[:ids[-1] + 1])
+        part = batch_of(lens[b:ids[-1] + 1], ids)
+        B.append_q8(many, k[a:z], v[a:z], part)
+        kp, vp = B.read_q8(many, i32([0] * len(ids)), part)
+        assert torch.equal(ko[a:z], kp) and torch.equal(vo[a:z], vp)
+    assert one.device_status() == 0 and many.device_status() == 0
+    # quantised once, by half a step at most, and rounded to bf16 (2^-8 of up to 127 steps)
+    assert (ko.float() - k.float()).abs().max() <= (0.5 + 127 / 256) * float(one.k_scale.max())

@@ -44,7 +44,7 @@ def test_captured_step_matches_eager_calls_and_the_oracle(code, most, alpha):
         n = sum(counts)
         assert torch.equal(o.out, os_.out[:n]) and torch.equal(o.tau, os_.tau[:n])
         assert torch.equal(plan.positions, step.plan.positions[:n]) and torch.equal(plan.slots, step.plan.slots[:n])
-        check_attend(c, q, counts, o, seq_ids=seqs, alpha=alpha, weight_eps=2.0 ** -8, **score)
+        check_attend(c, q, counts, o, seq_ids=seqs, alpha=alpha, **score)
     a, b = caches
     assert torch.equal(a.k_pool.view(torch.int8), b.k_pool.view(torch.int8)) and torch.equal(a.v_scale, b.v_scale)
     assert torch.equal(a.seq_lens, b.seq_lens) and torch.equal(pools[0].free_count, pools[1].free_count)
@@ -65,7 +65,7 @@ def test_a_full_pool_refuses_a_slot_and_the_rest_goes_on():
     B.append_q8(c, k, v, batch)
     B.attend_q8(c, q, batch, outputs=o)
     assert bool((o.out[40:] == 5.0).all()) and c.seq_lens.tolist() == [40, 0, 0]
-    check_attend(c, q, [40, 0, 0], o, seq_ids=seqs, start=[0, 40, 70], weight_eps=2.0 ** -8)
+    check_attend(c, q, [40, 0, 0], o, seq_ids=seqs, start=[0, 40, 70])
 
 
 def test_two_captured_steps_do_not_share_a_workspace():
