@@ -252,9 +252,14 @@ __device__ __forceinline__ float peer_load(uint32_t addr) {
   return v;
 }
 
-// x^b at an order without a short form, out of line: the code around it runs
-// once a call, and its instructions come from far.
-__device__ __noinline__ float ent_pow(float x, float b) { return powf(x, b); }
+// x^b for 0 < x ≤ 1 at an order without a short form, as 2^{b·lg x}: the
+// logarithm is good to 2^-22 of itself (or absolutely, near 1), so a power is to
+// b·|lg x|·2^-22 and x^b times that to 2^-22.
+__device__ __forceinline__ float ent_pow(float x, float b) {
+  float l;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(l) : "f"(x));
+  return ex2f(b * l);
+}
 __device__ __forceinline__ float ent_weight(float y, float beta) {  // [y]_+^β
   y = fmaxf(y, 0.0f);
   if (beta == 2.0f) return y * y;
@@ -270,8 +275,9 @@ struct EntSums {
     if (y > 0.0f) {
       k += 1.0f;
       mn = fminf(mn, y);
-      s1 += low ? y : ent_pow(y, beta - 1.0f);
-      s2 += low ? y * y : ent_pow(y, beta);
+      const float w = low ? y : ent_pow(y, beta - 1.0f);
+      s1 += w;
+      s2 = fmaf(w, y, s2);
     }
   }
   __device__ __forceinline__ void warp_total() {
@@ -468,10 +474,16 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
       if (!sv.done) {
         for (int t1 = wlo; t1 < whi; t1 += 32) {
           uint32_t in = __ballot_sync(0xffffffffu, t1 + lane < whi && pmax[(size_t)(t1 + lane) * G + hd] - top > sv.t);
-          while (in) {
-            const float z = zh[(size_t)(t1 + __ffs(in) - 1) * G * kEntKeys + lane];
-            in &= in - 1u;
-            v.add((z - top) - sv.t, e.beta, low);
+          while (in) {  // eight tiles' scores in flight
+            float z[8];
+            const int n8 = min(8, __popc(in));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              z[i] = i < n8 ? zh[(size_t)(t1 + __ffs(in) - 1) * G * kEntKeys + lane] : -CUDART_INF_F;
+              in &= in - 1u;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v.add((z[i] - top) - sv.t, e.beta, low);
           }
         }
         v.warp_total();
