@@ -252,7 +252,7 @@ __device__ __forceinline__ float peer_load(uint32_t addr) {
   return v;
 }
 
-// x^b for 0 < x ≤ 1 at an order without a short form, as 2^{b·lg x}: the
+// x^b for x > 0 at an order without a short form, as 2^{b·lg x}: the
 // logarithm is good to 2^-22 of itself (or absolutely, near 1), so a power is to
 // b·|lg x|·2^-22 and x^b times that to 2^-22.
 __device__ __forceinline__ float ent_pow(float x, float b) {
@@ -326,7 +326,9 @@ struct EntSolve {
       else lo = t;
       float nt = 0.5f * (lo + hi);
       if (v.k > 0.0f) {
-        const float st = (v.s2 - 1.0f) / (beta * v.s1);
+        // of the norm far above the root (β > 1), where the sum's own steps are short
+        const float st = beta > 1.0f && v.s2 > 1.5f ? (v.s2 - ent_pow(v.s2, 1.0f - 1.0f / beta)) / v.s1
+                                                    : (v.s2 - 1.0f) / (beta * v.s1);
         if (fabsf(st) <= tol) {
           nt = t + st;
           done = true;
