@@ -17,11 +17,20 @@
 // The V scale rides in w, so Σp is Σ over pages of (Σ w)/vs, of unrounded w.
 //
 // Warps: 4 + 4 softmax (a thread a row), 4 converters (codes from L2 through
-// registers into swizzled half tiles, two stages), 1 that issues the products.
-// The two row halves take turns: while one is in its softmax the products of
-// the other run. All items' tiles form one line (KV head outermost) cut into
-// equal pieces for one block a multiprocessor; an item cut in two leaves
-// (M, Σp, O) pieces that a second kernel joins in the order of the line.
+// registers into swizzled half tiles, two stages), 2 that issue the products, one
+// for each 128 rows. A row's softmax takes 64 keys at a time, the last ones first,
+// so that while it is at one half of a tile's keys the other half's products run.
+// All items' tiles form one line (KV head outermost) cut into equal pieces for
+// one block a multiprocessor; an item cut in two leaves (M, Σp, O) pieces that a
+// second kernel joins in the order of the line.
+//
+// Bound: the softmax warps, two a scheduler. Of a tile's 2600 cycles of products
+// (measured alone; 2050 in turns of 128 keys) the capped form takes about 5700:
+// fp32 pipe 41-47% busy, tensor pipe 33%, IPC 2.1-2.3. Measured, int8, 8 KV heads
+// of 4 query heads, d = 128: 2048 tokens behind 30001, capped (1.04 TFLOP), 1.25
+// ms, 830 TFLOP/s; behind 8000 without a cap 305 us, 1000 TFLOP/s. One thread that
+// issued all products, and tiles in turns of 128 keys, took 1.54 ms: issuing one
+// costs a thread about 75 cycles, more than the product.
 #pragma once
 
 #include "q8_tiles.cuh"

@@ -16,6 +16,14 @@
 //    Then V is read for tiles with some z above its head's τ only, weights
 //    rounded to halves against their tile's largest, and the blocks' sums are
 //    added through the cluster. Every sum has a fixed order.
+//
+// Measured, 8 KV heads of 4 query heads, d = 128: 131072 tokens, int8, slopes,
+// alpha 1.5: 53 us, of which scoring is 33 (134 MB of K at 4.1 TB/s; the floor is
+// 20): turning codes into halves bounds it (ALU 49%, IPC 2.3, DRAM 53%), 16 and
+// 24 warps alike. The rest is a chain of short phases, most of each the fetch of
+// its instructions. 16 sequences of 1-32k tokens, e4m3, alpha 2: 64 us. Dense
+// supports (random scores of deviation 1, 131072 tokens, every step reads z
+// again): 96 us at alpha 1.5, 151 at 1.25.
 #include "q8_tiles.cuh"
 
 namespace ekv {
