@@ -376,7 +376,8 @@ int32_t entmaxkv_decode_softmax_noalloc(const entmaxkv_config* cfg, const entmax
  * A stored value is code * scale with one float32 scale for the K and one for
  * the V rows of each (physical page, KV head). The calls take an
  * entmaxkv_config whose kv_dtype is one of the code types below; the other
- * fields and their limits are those of the 16- and 32-bit cache.
+ * fields and their limits are those of the 16- and 32-bit cache, but a
+ * sequence has at most 2^30 tokens.
  */
 #define ENTMAXKV_I8   2   /* signed whole numbers -127..127          */
 #define ENTMAXKV_E4M3 3   /* 4 exponent, 3 mantissa bits, finite, <= 448 */
@@ -551,7 +552,9 @@ size_t entmaxkv_attend_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, 
  * Scales of pages in use are positive and finite, as append leaves them. The
  * order of every sum is fixed by the arguments and the device, so equal calls
  * give equal bits. Rows of a slot with a bad row or batch entry are left as
- * they were.
+ * they were. Refused (ENTMAXKV_ERR_UNSUPPORTED): batches of several tokens a
+ * slot for which (total * group / 256 + n_seqs + 1) * max_pages_per_seq *
+ * page_size / 128 passes 2^31.
  */
 int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache,
                            const entmaxkv_batch* batch, const entmaxkv_rows* q,

@@ -191,6 +191,7 @@ cudaError_t launch_attend_softmax(Q8AttendArgs a, bool i8, void* ws, int sms, cu
 // 108/105 at 48, 137/105 at 64; 4 of 30000 (pages of 16) 46/95, 68/103, 94/104,
 // 117/107; 24 of 6000 at d = 64 35/62, 58/67, 82/67, 105/67.
 __host__ __device__ constexpr int stream_rows(int D) { return D == 128 ? 48 : 32; }
+bool chunk_counts_fit(const entmaxkv_config& cfg, int n_seqs, int total);
 size_t attend_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total);
 cudaError_t launch_attend_chunk(const Q8AttendArgs& a, bool i8, void* ws, int sms, cudaStream_t st);
 size_t attend_entmax_bytes(const entmaxkv_config& cfg, int n_seqs);

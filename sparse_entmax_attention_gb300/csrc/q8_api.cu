@@ -14,7 +14,7 @@ static int check_q8_config(const entmaxkv_config* c) {
   if (c->group > 8 || c->num_kv_heads > 4096) return ENTMAXKV_ERR_UNSUPPORTED;
   if (c->head_dim != 64 && c->head_dim != 128) return ENTMAXKV_ERR_UNSUPPORTED;
   if (c->page_size != 16 && c->page_size != 32) return ENTMAXKV_ERR_UNSUPPORTED;
-  if ((long long)c->max_pages_per_seq * c->page_size > 0x7fffffffLL) return ENTMAXKV_ERR_UNSUPPORTED;
+  if ((long long)c->max_pages_per_seq * c->page_size > 1 << 30) return ENTMAXKV_ERR_UNSUPPORTED;  // (kNoKey)
   return ENTMAXKV_OK;
 }
 
@@ -127,6 +127,7 @@ static int check_attend(const entmaxkv_config* cfg, int n_seqs, int total, int m
   if (n_seqs < 0 || n_seqs > 65535 || total < 0 || max_count < 0) return ENTMAXKV_ERR_INVALID_ARG;
   if (!(alpha >= 1.0f) || !isfinite(alpha)) return ENTMAXKV_ERR_INVALID_ARG;
   if (alpha > 1.0f && max_count > 1) return ENTMAXKV_ERR_UNSUPPORTED;
+  if (!streams(cfg, max_count) && !chunk_counts_fit(*cfg, n_seqs, total)) return ENTMAXKV_ERR_UNSUPPORTED;
   return ENTMAXKV_OK;
 }
 

@@ -49,9 +49,13 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(ChunkArgs g) {
         const Q8Slot s = q8_slot(a.c, a.b, b0 + lo, nullptr);
         const Q8Span v = chunk_span(a, s, b0 + lo, rt);
         T = (v.T + per - 1) / per;
-        if (items + j < g.max_items)
+        if (items + j < g.max_items) {
           g.items[items + j] = ChunkItem{b0 + lo, rt, T, v.T, s.seq, s.L, s.start, s.count, v.pre, v.npre, v.wfirst, v.npages};
-        if (T == 0 && items + j < g.max_items) g.empty[atomicAdd(&none_sh, 1)] = items + j;  // (any order will do)
+          if (T == 0) g.empty[atomicAdd(&none_sh, 1)] = items + j;  // (any order will do)
+        } else {  // rows that several slots claim: the items past the list get no place on the line
+          T = 0;
+          raise_flag(a.c.status, ENTMAXKV_DEV_BAD_BATCH);
+        }
       }
       int all;
       const int before = block_exclusive_scan(T, sh_scan, all);
@@ -62,7 +66,7 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(ChunkArgs g) {
     __syncthreads();
   }
   if (tid == 0) {
-    items = min(items, g.max_items);  // (slots whose rows overlap can claim more: those are not answered)
+    items = min(items, g.max_items);
     g.n_items[0] = items;
     g.n_items[1] = none_sh;
     g.cum[items] = tiles;
@@ -140,10 +144,16 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs g) {
   }
 }
 
-static size_t up256c(size_t x) { return (x + 255) & ~(size_t)255; }
 static long long chunk_items(int n_seqs, int total, int G) {
   return (long long)total * G / kChunkRows + n_seqs + 1;
 }
+// Tiles are counted in 32 bits.
+bool chunk_counts_fit(const entmaxkv_config& cfg, int n_seqs, int total) {
+  const long long keys = (long long)cfg.max_pages_per_seq * cfg.page_size;
+  return chunk_items(n_seqs, total, cfg.group) <= 0x7fffffffLL / ((keys + kChunkKeys - 1) / kChunkKeys);
+}
+
+static size_t up256c(size_t x) { return (x + 255) & ~(size_t)255; }
 
 size_t attend_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total) {
   const size_t items = (size_t)chunk_items(n_seqs, total, cfg.group);

@@ -38,7 +38,8 @@ def attend(lib, c=None, view=None, batch=None, q=None, score=None, alpha=1.0, ws
 
 @pytest.mark.parametrize("field,value,code", [
     ("head_dim", 96, 2), ("page_size", 8, 2), ("group", 9, 2), ("kv_dtype", B.BF16, 1), ("kv_dtype", 9, 1),
-    ("num_kv_heads", 0, 1), ("num_kv_heads", 5000, 2), ("max_pages_per_seq", 0, 1), ("max_pages_per_seq", 1 << 30, 2)])
+    ("num_kv_heads", 0, 1), ("num_kv_heads", 5000, 2), ("max_pages_per_seq", 0, 1), ("max_pages_per_seq", 1 << 30, 2),
+    ("max_pages_per_seq", (1 << 25) + 1, 2)])
 def test_bad_configs(lib, field, value, code):
     c = cfg(**{field: value})
     assert attend(lib, c) == code
@@ -73,6 +74,14 @@ def test_bad_attend_arguments(lib):
                   B.ScoreView(float("nan"), 0.0, 0), B.ScoreView(0.0, float("inf"), 0), B.ScoreView(0.0, 1e-45, 0),
                   B.ScoreView(0.0, 1e19, 0), B.ScoreView(0.0, float("nan"), 0)):
         assert attend(lib, score=score) == 1
+
+
+def test_calls_whose_tiles_pass_32_bits(lib):
+    c = cfg(max_pages_per_seq=1 << 25, num_phys_pages=1 << 25)  # 2^30 tokens, 2^23 tiles of 128
+    assert lib.entmaxkv_attend_q8_workspace(c, 1, 15000, 15000, 1.0) > 0          # 234 items and two
+    assert lib.entmaxkv_attend_q8_workspace(c, 1, 17000, 17000, 1.0) == 0         # 265 and two
+    assert attend(lib, c, batch=B.BatchView(None, P256, P256, 1, 17000, 17000)) == 2
+    assert lib.entmaxkv_attend_q8_workspace(c, 1, 17000, 12, 1.0) > 0             # few tokens a slot: counted in 64 bits
 
 
 def test_bad_plan_arguments(lib):

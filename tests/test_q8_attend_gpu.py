@@ -270,3 +270,12 @@ def test_pages_beyond_32_bit_offsets(counts, alpha):
     a, b = (B.attend_q8(c, q, batch_of(counts), alpha=alpha) for c in (small, big))
     assert big.device_status() == 0
     assert torch.equal(a.out, b.out) and torch.equal(a.tau, b.tau)
+
+
+def test_rows_claimed_by_several_slots_are_flagged():
+    """More items than the rows allow: the call ends, and says so."""
+    c, _ = filled("int8", [600, 600, 600, 600], [1], hkv=1, g=8)
+    start, count = i32([0] * 4), i32([600] * 4)
+    q = torch.randn(600, 8, 128, device="cuda").bfloat16()
+    B.attend_q8(c, q, B.Batch(start, count, 600, 600))
+    assert c.device_status() == B.DEV_BAD_BATCH
