@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
           auto weigh = [&](int c, const float (&raw)[64]) {
             unsigned long long t2[32];
             // exponents against the bound so far, so that they need no other pass
-            float base = M > -CUDART_INF_F ? kLift - M : 0.0f, mx = -CUDART_INF_F;
+            const float base = M > -CUDART_INF_F ? kLift - M : 0.0f;
+            float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
             for (int q = 0; q < 64 / P; ++q) {
               const PageMeta pm = pg[c * (64 / P) + q];
@@ -366,15 +367,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
               const unsigned long long k2 = f2_splat(pm.ks * kc), a2 = f2_splat(add);
               if (capped) {  // y = raw·k, then cap·log2 e·y·T(y²)
                 unsigned long long z2[P / 2];
-                float big = 0.0f;
+                float b4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int i = 0; i < P / 2; ++i) {
                   u[i] = f2_mul(f2_pack(v[2 * i], v[2 * i + 1]), k2);
                   z2[i] = f2_mul(u[i], u[i]);
                   float y0, y1;
                   f2_unpack(z2[i], y0, y1);
-                  big = max3(big, y0, y1);
+                  b4[i & 3] = max3(b4[i & 3], y0, y1);
                 }
+                const float big = max3(max3(b4[0], b4[1], b4[2]), b4[3], 0.0f);
                 constexpr TanhPoly poly = tanh_poly();
                 const float out = a.sc.cap * kLog2e;
                 if (__all_sync(0xffffffffu, big <= 0.25f)) {
@@ -436,17 +438,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
                   u[i] = f2_pack(y0, y1);
                 }
               }
-              float m0 = -CUDART_INF_F, m1 = -CUDART_INF_F;
 #pragma unroll
-              for (int i = 0; i < P / 2; i += 2) {
+              for (int i = 0; i < P / 2; ++i) {
                 float y0, y1;
                 f2_unpack(u[i], y0, y1);
-                m0 = max3(m0, y0, y1);
-                f2_unpack(u[i + 1], y0, y1);
-                m1 = max3(m1, y0, y1);
+                m4[i & 3] = max3(m4[i & 3], y0, y1);
               }
-              mx = max3(mx, m0, m1);
             }
+            const float mx = max3(max3(m4[0], m4[1], m4[2]), m4[3], -CUDART_INF_F);
             // the bound moves when the maximum passes it by more than the slack: in an item's first columns, and
             // seldom behind them
             const bool move = M > -CUDART_INF_F ? mx > kLift + kSlack : mx > M;
