@@ -25,12 +25,13 @@
 // second kernel joins in the order of the line.
 //
 // Bound: the softmax warps, two a scheduler. Of a tile's 2600 cycles of products
-// (measured alone; 2050 in turns of 128 keys) the capped form takes about 5700:
-// fp32 pipe 41-47% busy, tensor pipe 33%, IPC 2.1-2.3. Measured, int8, 8 KV heads
-// of 4 query heads, d = 128: 2048 tokens behind 30001, capped (1.04 TFLOP), 1.25
-// ms, 830 TFLOP/s; behind 8000 without a cap 305 us, 1000 TFLOP/s. One thread that
-// issued all products, and tiles in turns of 128 keys, took 1.54 ms: issuing one
-// costs a thread about 75 cycles, more than the product.
+// (measured alone; 2050 in turns of 128 keys) the capped form takes about 5400:
+// fp32 pipe 41-47% busy, tensor pipe 33%, IPC 2.1-2.3, the rest the latency of each
+// row's chain (maxima in one chain instead of four: 8% slower). Measured, int8, 8
+// KV heads of 4 query heads, d = 128: 2048 tokens behind 30001, capped (1.04
+// TFLOP), 1.18 ms, 880 TFLOP/s; behind 8000 without a cap 310 us, 990 TFLOP/s. One
+// thread that issued all products, and tiles in turns of 128 keys, took 1.54 ms:
+// issuing one costs a thread about 75 cycles, more than the product.
 #pragma once
 
 #include "q8_tiles.cuh"
