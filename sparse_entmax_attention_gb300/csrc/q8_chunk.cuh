@@ -297,6 +297,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
       const long long q_at = (long long)(x.s.start + tok) * a.q.ts + (long long)head * a.q.hs;
       const long long o_at = (long long)(x.s.start + tok) * a.out.ts + (long long)head * a.out.hs;
       const uint32_t rows_sm = q_sm + wg * TILE;  // this half's query tile, and its answers on their way out
+      if (mine) {  // (asked for before the queries)
+        pos = x.s.L - x.s.count + tok;
+        if (a.sc.window > 0) lo = max(0, pos - a.sc.window + 1);
+        if (a.sc.first_key) lo = max(lo, a.sc.first_key[x.s.start + tok]);
+        if (biased) slope = a.sc.slopes[head] * kLog2e;
+      }
       if (half) {
         // the warp's query rows as halves, CPR lanes a row, each row brought near 2^13 by a power of two
         constexpr int CPR = D / 8, RPI = 32 / CPR;
@@ -335,12 +341,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
             if (lane / RPI == i0 + i)
               kc = __uint_as_float((uint32_t)(back - 13 + 127) << 23) * a.sc.scale * (capped ? a.sc.inv_cap : kLog2e);
           }
-        }
-        if (mine) {
-          pos = x.s.L - x.s.count + tok;
-          if (a.sc.window > 0) lo = max(0, pos - a.sc.window + 1);
-          if (a.sc.first_key) lo = max(lo, a.sc.first_key[x.s.start + tok]);
-          if (biased) slope = a.sc.slopes[head] * kLog2e;
         }
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
