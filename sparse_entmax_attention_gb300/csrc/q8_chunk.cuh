@@ -205,12 +205,12 @@ __device__ __forceinline__ ChunkSeg chunk_seg(const ChunkArgs& g, long long w, l
     item = 0;
   }
   ChunkItem it;
-  for (;; ++item) {  // (items without a tile are passed over)
+  for (;; item = item + 1 < n_items ? item + 1 : 0) {  // (items without a tile are passed over; some item has one)
     const int4* p = reinterpret_cast<const int4*>(g.items + item);
     *reinterpret_cast<int4*>(&it) = __ldcg(p);
     *(reinterpret_cast<int4*>(&it) + 1) = __ldcg(p + 1);
     *(reinterpret_cast<int4*>(&it) + 2) = __ldcg(p + 2);
-    if (it.T > 0 || item + 1 >= n_items) break;
+    if (it.T > 0) break;
   }
   x.item = item;
   x.slot = it.slot;

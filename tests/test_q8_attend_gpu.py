@@ -279,3 +279,14 @@ def test_rows_claimed_by_several_slots_are_flagged():
     q = torch.randn(600, 8, 128, device="cuda").bfloat16()
     B.attend_q8(c, q, B.Batch(start, count, 600, 600))
     assert c.device_status() == B.DEV_BAD_BATCH
+
+
+@pytest.mark.parametrize("blind", [[2], [0, 2], [1], [0, 1, 2]])
+def test_chunks_whose_rows_see_nothing(blind):
+    """Slots without a visible key, last ones among them, beside others, over several KV heads."""
+    lens, counts = [700, 2100, 300], [100, 310, 90]
+    fk = [10 ** 6 if b in blind else 0 for b in range(3) for _ in range(counts[b])]
+    _, _, o = run("int8", lens, counts, cache_kw=dict(hkv=8, g=4, d=64, P=16), first_key=fk)
+    for b in blind:
+        at = sum(counts[:b])
+        assert torch.isnan(o.tau[at:at + counts[b]]).all() and not o.out[at:at + counts[b]].any()
