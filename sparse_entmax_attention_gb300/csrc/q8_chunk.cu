@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(ChunkArgs g) {
         }
       }
       int all;
-      const int before = block_exclusive_scan(T, sh_scan, all);
+      const int before = block_exclusive_scan(T ? T + kChunkItem : 0, sh_scan, all);
       if (j < total && items + j < g.max_items) g.cum[items + j] = tiles + before;
       tiles += all;
     }
@@ -103,10 +103,10 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs g) {
   const ChunkItem it = g.items[cut.x];
   const int cum = g.cum[cut.x], S = g.cum[g.n_items[0]];
   const long long W = (long long)S * Hkv, nb = max(1LL, min(W, (long long)g.blocks));
-  const long long A = (long long)cut.y * S + cum;
+  const long long A = (long long)cut.y * S + cum + kChunkItem;
   const int c0 = (int)(((A + 1) * nb - 1) / W), n = (int)(((A + it.T) * nb - 1) / W) - c0 + 1;
   if (c0 != c - 1) return;  // joined at an earlier cut
-  const int last0 = W * c0 / nb >= A ? 0 : 1;  // the first block's piece: its first or its last
+  const int last0 = W * c0 / nb >= A - kChunkItem ? 0 : 1;  // the first block's piece: its first or its last
 #pragma unroll 2
   for (int row = 32 * part + warp; row < 32 * part + 32; row += 8) {
     const int rho = it.rt * kChunkRows + row;
@@ -147,10 +147,10 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs g) {
 static long long chunk_items(int n_seqs, int total, int G) {
   return (long long)total * G / kChunkRows + n_seqs + 1;
 }
-// Tiles are counted in 32 bits.
+// A KV head's line is counted in 32 bits.
 bool chunk_counts_fit(const entmaxkv_config& cfg, int n_seqs, int total) {
   const long long keys = (long long)cfg.max_pages_per_seq * cfg.page_size;
-  return chunk_items(n_seqs, total, cfg.group) <= 0x7fffffffLL / ((keys + kChunkKeys - 1) / kChunkKeys);
+  return chunk_items(n_seqs, total, cfg.group) <= 0x7fffffffLL / ((keys + kChunkKeys - 1) / kChunkKeys + kChunkItem);
 }
 
 static size_t up256c(size_t x) { return (x + 255) & ~(size_t)255; }

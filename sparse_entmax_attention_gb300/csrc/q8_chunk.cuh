@@ -20,7 +20,7 @@
 // registers into swizzled half tiles, two stages), 2 that issue the products, one
 // for each 128 rows. A row's softmax takes 64 keys at a time, the last ones first,
 // so that while it is at one half of a tile's keys the other half's products run.
-// All items' tiles form one line (KV head outermost) cut into equal pieces for
+// All items form one line (KV head outermost) cut into equal pieces for
 // one block a multiprocessor; an item cut in two leaves (M, Σp, O) pieces that a
 // second kernel joins in the order of the line.
 //
@@ -29,7 +29,7 @@
 // fp32 pipe 41-47% busy, tensor pipe 33%, IPC 2.1-2.3, the rest the latency of each
 // row's chain (maxima in one chain instead of four: 8% slower). Measured, int8, 8
 // KV heads of 4 query heads, d = 128: 2048 tokens behind 30001, capped (1.04
-// TFLOP), 1.18 ms, 880 TFLOP/s; behind 8000 without a cap 310 us, 990 TFLOP/s. One
+// TFLOP), 1.16 ms, 890 TFLOP/s; behind 8000 without a cap 302 us, 1010 TFLOP/s. One
 // thread that issued all products, and tiles in turns of 128 keys, took 1.54 ms:
 // issuing one costs a thread about 75 cycles, more than the product.
 #pragma once
@@ -42,6 +42,12 @@ constexpr int kChunkThreads = 512;
 constexpr int kChunkRows = 256;
 constexpr int kChunkKeys = 128;
 constexpr int kChunkMaxBlocks = 256;
+// What an item costs beside its tiles, in tiles: its place, queries and answers
+// (14 to 16 thousand cycles against 4500 to 5400 a tile). Items have that many
+// places on the line in front of their tiles', so that blocks of many short items
+// get fewer tiles (six prompts' chunks of 97-token documents, e4m3, slopes: 134 us
+// without them, 109 with).
+constexpr int kChunkItem = 3;
 
 // What the roles know of an item, filled in once by the listing kernel.
 struct __align__(16) ChunkItem {
@@ -52,7 +58,7 @@ struct __align__(16) ChunkItem {
 struct ChunkArgs {
   Q8AttendArgs a;
   ChunkItem* items;
-  int* cum;        // [n_items + 1] tiles of one KV head before each item
+  int* cum;        // [n_items + 1] places of one KV head's line before each item
   int* n_items;    // [2] items, and those of them without a tile
   int* empty;      // the latter
   int2* cuts;      // [blocks] (item, KV head) that a block begins inside of; item −1: at one's start
@@ -179,10 +185,11 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// A block's part of one item: `n` tiles, tile t0 + n − 1 first. (Nearest keys
-// come first, so that with a distance bias the first maximum is the last one.)
+// A block's part of one item: `n` tiles, tile t0 + n − 1 first, `skip` places on.
+// (Nearest keys come first, so that with a distance bias the first maximum is the
+// last one.) n = 0: the block's line ends before the item's tiles.
 struct ChunkSeg {
-  int kvh, item, slot, rt, t0, n, T;
+  int kvh, item, slot, rt, t0, n, T, skip;
   Q8Slot s;
   Q8Span sp;
 };
@@ -215,9 +222,11 @@ __device__ __forceinline__ ChunkSeg chunk_seg(const ChunkArgs& g, long long w, l
   x.item = item;
   x.slot = it.slot;
   x.rt = it.rt;
-  x.t0 = off - __ldcg(g.cum + item);
+  const int at = off - __ldcg(g.cum + item) - kChunkItem;
+  x.t0 = max(at, 0);
+  x.skip = max(-at, 0);
   x.T = it.T;
-  x.n = (int)min((long long)(x.T - x.t0), w_end - w);
+  x.n = (int)max(0LL, min((long long)(x.T - x.t0), w_end - w - x.skip));
   x.s = Q8Slot{it.seq, it.L, it.start, it.count};
   x.sp = Q8Span{it.pre, it.npre, it.wfirst, it.npages, it.Tp};
   return x;
@@ -288,6 +297,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
     int item = -1;
     for (long long w = w_begin; w < w_end && ok; ++seg) {
       const ChunkSeg x = chunk_seg(g, w, w_end, S, n_items, item);
+      if (x.n == 0) break;
       item = x.item + 1;
       const int rho = x.rt * kChunkRows + 128 * wg + row, rows = x.s.count * G;
       const bool mine = rho < rows, half = x.rt * kChunkRows + 128 * wg < rows;
@@ -521,7 +531,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
       }
       tm_fence_after();
       const bool whole = x.n == x.T;
-      const int piece = 2 * blockIdx.x + (w == w_begin ? 0 : 1);
+      const int piece = 2 * blockIdx.x + (seg ? 1 : 0);
       const float inv = whole ? att_inv(l) : 1.0f;
       if (half) {
         // rows leave through the query tile, so that a warp writes whole rows: bf16 rows at once, fp32 pieces in
@@ -575,7 +585,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
       }
       tm_fence_before();
       tile += x.n;
-      w += x.n;
+      w += x.skip + x.n;
     }
   } else if (wg == 2) {  // ------------------------------------------ converters
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;\n");
@@ -592,6 +602,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
     int item = -1;
     for (long long w = w_begin; w < w_end && ok;) {
       const ChunkSeg x = chunk_seg(g, w, w_end, S, n_items, item);
+      if (x.n == 0) break;
       item = x.item + 1;
       // 32 tiles' pages at once, a tile a lane
       int ph[PW], key[PW];
@@ -671,7 +682,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
         store(v_sm + sg * TILE, vc);
         mbar_arrive(&v_full[sg]);
       }
-      w += x.n;
+      w += x.skip + x.n;
     }
   } else {  // ------------------------------------------------------- products
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
@@ -697,7 +708,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
       for (long long w = w_begin, seg = 0; w < w_end && ok; ++seg) {
         const ChunkSeg x = chunk_seg(g, w, w_end, S, n_items, item);
         item = x.item + 1;
-        if (tid == 384 && seg == 0) g.cuts[blockIdx.x] = make_int2(x.t0 > 0 ? x.item : -1, x.kvh);
+        if (tid == 384 && seg == 0) g.cuts[blockIdx.x] = make_int2(x.n > 0 && x.t0 > 0 ? x.item : -1, x.kvh);
+        if (x.n == 0) break;
         const bool mine = x.s.count * G - x.rt * kChunkRows > 128 * hf;
         ok = wait_warp(&q_full, (int)seg) && wait_warp(&k_full[it & 1], it / 2);
         if (!ok) break;
@@ -736,7 +748,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
           }
         }
         if (ok && elect_one()) tm_commit(&o_full);
-        w += x.n;
+        w += x.skip + x.n;
       }
     }
     __syncwarp();
