@@ -188,12 +188,9 @@ cudaError_t launch_attend_softmax(Q8AttendArgs a, bool i8, void* ws, int sms, cu
 // answers a batch, 16 rows at a time; with more, one 128-row product tile is the
 // better fit for every slot. Measured, streaming against products, int8, 4 KV
 // heads: 24 sequences of 6000 tokens at d = 128 46/99 us at 16 rows, 77/104 at 32,
-// 108/105 at 48, 137/105 at 64; 4 of 30000 (pages of 16) 46/95, 68/103, 94/104,
-// 117/107; 24 of 6000 at d = 64 35/62, 58/67, 82/67, 105/67. Streaming takes a slot
-// as many times as its own rows need, so the mean over the slots counts beside the
-// most: 24 sequences of 2-5 tokens of 8 heads, window 4096, d = 64: 36/49.
+// 108/105 at 48, 137/105 at 64; 4 of 30000 (pages of 16) 46/95, 67/103, 94/104,
+// 117/107; 24 of 6000 at d = 64 36/62, 50/67, 68/66, 86/66.
 constexpr int kStreamRows = 48;
-__host__ __device__ constexpr int stream_mean_rows(int D) { return D == 128 ? 48 : 32; }
 bool chunk_counts_fit(const entmaxkv_config& cfg, int n_seqs, int total);
 size_t attend_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total);
 cudaError_t launch_attend_chunk(const Q8AttendArgs& a, bool i8, void* ws, int sms, cudaStream_t st);

@@ -51,10 +51,8 @@ static Q8Batch batch_of(const entmaxkv_batch* b) {
 static Q8Rows rows_of(const entmaxkv_rows* r) {
   return Q8Rows{static_cast<__nv_bfloat16*>(r->data), r->token_stride, r->head_stride};
 }
-static bool streams(const entmaxkv_config* c, int n_seqs, int total, int max_count) {
-  return (long long)max_count * c->group <= kStreamRows &&
-         ((long long)max_count * c->group <= stream_mean_rows(c->head_dim) ||
-          (long long)total * c->group <= (long long)n_seqs * stream_mean_rows(c->head_dim));
+static bool streams(const entmaxkv_config* c, int max_count) {
+  return (long long)max_count * c->group <= kStreamRows;
 }
 static int32_t code_of(cudaError_t e) { return e == cudaSuccess ? ENTMAXKV_OK : ENTMAXKV_ERR_CUDA; }
 
@@ -129,7 +127,7 @@ static int check_attend(const entmaxkv_config* cfg, int n_seqs, int total, int m
   if (n_seqs < 0 || n_seqs > 65535 || total < 0 || max_count < 0) return ENTMAXKV_ERR_INVALID_ARG;
   if (!(alpha >= 1.0f) || !isfinite(alpha)) return ENTMAXKV_ERR_INVALID_ARG;
   if (alpha > 1.0f && max_count > 1) return ENTMAXKV_ERR_UNSUPPORTED;
-  if (!streams(cfg, n_seqs, total, max_count) && !chunk_counts_fit(*cfg, n_seqs, total)) return ENTMAXKV_ERR_UNSUPPORTED;
+  if (!streams(cfg, max_count) && !chunk_counts_fit(*cfg, n_seqs, total)) return ENTMAXKV_ERR_UNSUPPORTED;
   return ENTMAXKV_OK;
 }
 
@@ -137,7 +135,7 @@ size_t entmaxkv_attend_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, 
                                     float alpha) {
   if (check_attend(cfg, n_seqs, total, max_count, alpha)) return 0;
   if (alpha > 1.0f) return attend_entmax_bytes(*cfg, n_seqs);
-  return streams(cfg, n_seqs, total, max_count) ? attend_softmax_bytes(*cfg, n_seqs) : attend_chunk_bytes(*cfg, n_seqs, total);
+  return streams(cfg, max_count) ? attend_softmax_bytes(*cfg, n_seqs) : attend_chunk_bytes(*cfg, n_seqs, total);
 }
 
 int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache, const entmaxkv_batch* batch,
@@ -172,7 +170,7 @@ int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* 
   const bool i8 = cfg->kv_dtype == ENTMAXKV_I8;
   const cudaStream_t s = (cudaStream_t)stream;
   if (alpha > 1.0f) return code_of(launch_attend_entmax(*cfg, a, i8, alpha, workspace, sms, s));
-  if (streams(cfg, batch->n_seqs, batch->total, batch->max_count))
+  if (streams(cfg, batch->max_count))
     return code_of(launch_attend_softmax(a, i8, workspace, sms, s));
   return code_of(launch_attend_chunk(a, i8, workspace, sms, s));
 }

@@ -31,13 +31,14 @@
 
 namespace ekv {
 
-// Warps of a block, and K or V slabs (4 KB each at d = 128) of a warp's ring:
+// Warps of a block, and K or V slabs (32·D bytes) of a warp's ring, 196 KB in all:
 // 16 warps fit 128 registers with one tile of 8 rows (the ragged batch above: 136
-// us, against 199 with 8 of them on whole pages); two tiles need twice as many.
-template <int NT>
-constexpr int kAttWarps = NT == 1 ? 16 : 8;
-template <int NT>
-constexpr int kAttSlabs = NT == 1 ? 3 : 6;
+// us, against 199 with 8 of them on whole pages), or with two at d = 64; at d = 128
+// two tiles need twice as many.
+template <int D, int NT>
+constexpr int kAttWarps = NT == 2 && D == 128 ? 8 : 16;
+template <int D, int NT>
+constexpr int kAttSlabs = 192 * 1024 / (kAttWarps<D, NT> * 32 * D);
 constexpr int kAttMaxBlocks = 256;
 constexpr int kAttKeys = 32;
 
@@ -72,10 +73,10 @@ struct AttPiece {
 };
 
 template <bool I8, int D, int P, int NT>
-__global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
+__global__ void __launch_bounds__(kAttWarps<D, NT> * 32, 1)
     attend_kernel(Q8AttendArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   pdl_enter();
-  constexpr int NW = kAttWarps<NT>, ST = kAttSlabs<NT>, SLAB = kAttKeys * D, NTH = NW * 32, R = 8 * NT;
+  constexpr int NW = kAttWarps<D, NT>, ST = kAttSlabs<D, NT>, SLAB = kAttKeys * D, NTH = NW * 32, R = 8 * NT;
   constexpr int PP = kAttKeys / P;  // pages a tile
   static_assert(R * D * 4 <= ST * SLAB, "a warp's sums fit its ring");
   extern __shared__ __align__(128) unsigned char dyn_sm[];
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
   __syncthreads();
   // the warps' last pieces: neighbours of one unit are joined here. First each row's maximum and the pieces' factors
   // (a lane a piece, its row's other pieces by shuffles)
-  static_assert(NW == 16 ? R == 8 : NW == 8 && R == 16, "NW lanes a row, 32/NW rows a warp");
+  static_assert(NW * R <= NTH && 32 % NW == 0, "NW lanes a row, 32/NW rows a warp");
   if (tid < NW * R) {
     const int i = tid % NW, rj = tid / NW;
     const AttPiece& x = sh_piece[i];
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kAttWarps<NT> * 32, 1)
 template <int D, int NT>
 __global__ void __launch_bounds__(D) attend_join_kernel(Q8AttendArgs a, int nrt_max) {
   pdl_enter();
-  constexpr int R = 8 * NT, NW = kAttWarps<NT>;
+  constexpr int R = 8 * NT, NW = kAttWarps<D, NT>;
   const int b = blockIdx.y, rj = blockIdx.x % R, unit = blockIdx.x / R, kvh = unit / nrt_max, rt = unit - kvh * nrt_max;
   const AttSlot x = reinterpret_cast<const AttSlot*>(a.slots)[b];
   const long long W = a.cum[a.b.n_seqs], at = a.cum[b];
@@ -539,14 +540,14 @@ cudaError_t make_q8_map(CUtensorMap* map, const void* pool, int nphys, int Hkv, 
 static size_t up256z(size_t x) { return (x + 255) & ~(size_t)255; }
 
 size_t attend_softmax_bytes(const entmaxkv_config& cfg, int n_seqs) {
-  const size_t pieces = (size_t)kAttMaxBlocks * 16 * 2 * 8;  // 16 warps of 8 rows, or 8 of 16
+  const size_t pieces = (size_t)kAttMaxBlocks * 16 * 2 * (cfg.head_dim == 64 ? 16 : 8);  // 16 warps of a tile or two
   return up256z((size_t)(n_seqs + 1) * 8) + up256z((size_t)n_seqs * sizeof(AttSlot)) +
          up256z(pieces * cfg.head_dim * 4) + up256z(pieces * 8);
 }
 
 template <bool I8, int D, int P, int NT>
 static cudaError_t attend_t(Q8AttendArgs& a, void* ws, int sms, cudaStream_t st) {
-  const int smem = kAttWarps<NT> * kAttSlabs<NT> * kAttKeys * D + 1024;
+  const int smem = kAttWarps<D, NT> * kAttSlabs<D, NT> * kAttKeys * D + 1024;
   cudaError_t e = ensure_smem((const void*)attend_kernel<I8, D, P, NT>, smem);
   if (e != cudaSuccess) return e;
   CUtensorMap km, vm;
@@ -554,7 +555,7 @@ static cudaError_t attend_t(Q8AttendArgs& a, void* ws, int sms, cudaStream_t st)
   if ((e = make_q8_map(&vm, a.c.v_pool, a.c.nphys, a.c.Hkv, P, D)) != cudaSuccess) return e;
   a.blocks = min(sms, kAttMaxBlocks);
   char* p = static_cast<char*>(ws);
-  const size_t pieces = (size_t)kAttMaxBlocks * kAttWarps<NT> * 2 * 8 * NT;
+  const size_t pieces = (size_t)kAttMaxBlocks * kAttWarps<D, NT> * 2 * 8 * NT;
   a.cum = reinterpret_cast<long long*>(p);
   p += up256z((size_t)(a.b.n_seqs + 1) * 8);
   a.slots = p;
@@ -562,7 +563,7 @@ static cudaError_t attend_t(Q8AttendArgs& a, void* ws, int sms, cudaStream_t st)
   a.part_o = reinterpret_cast<float*>(p);
   p += up256z(pieces * D * 4);
   a.part_ml = reinterpret_cast<float*>(p);
-  e = launch_k(false, attend_kernel<I8, D, P, NT>, dim3(a.blocks), dim3(kAttWarps<NT> * 32), (size_t)smem, st, a, km, vm);
+  e = launch_k(false, attend_kernel<I8, D, P, NT>, dim3(a.blocks), dim3(kAttWarps<D, NT> * 32), (size_t)smem, st, a, km, vm);
   if (e != cudaSuccess) return e;
   const int nrt = (int)(((long long)a.b.max_count * a.c.G + 8 * NT - 1) / (8 * NT));
   return launch_k(true, attend_join_kernel<D, NT>, dim3(8 * NT * nrt * a.c.Hkv, a.b.n_seqs), dim3(D), 0, st, a, nrt);
