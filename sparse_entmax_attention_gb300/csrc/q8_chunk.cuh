@@ -26,7 +26,7 @@
 //
 // Bound: the softmax warps, two a scheduler. Of a tile's 2600 cycles of products
 // (measured alone; 2050 in turns of 128 keys) the capped form takes about 5400:
-// fp32 pipe 41-47% busy, tensor pipe 33%, IPC 2.1-2.3, the rest the latency of each
+// fp32 pipe 44% busy, tensor pipe 37%, IPC 2.3, the rest the latency of each
 // row's chain (maxima in one chain instead of four: 8% slower). Measured, int8, 8
 // KV heads of 4 query heads, d = 128: 2048 tokens behind 30001, capped (1.04
 // TFLOP), 1.16 ms, 890 TFLOP/s; behind 8000 without a cap 302 us, 1010 TFLOP/s. One
