@@ -5,9 +5,9 @@
 // An item is 256 rows of one (slot, KV head): rows are (token, head of the
 // group), so a K/V tile serves the whole group. Per tile of 128 keys (the
 // pages of the item's span in order):
-//   S = Q·K^T          two 128×128 products (one per 128 rows), Q and the codes
-//                      as halves (both exact: a power of two per query row),
-//                      fp32 sums in tensor memory;
+//   S = Q·K^T          128 rows × 64 keys a product, Q and the codes as halves
+//                      (both exact: a power of two per query row), fp32 sums in
+//                      tensor memory;
 //   t = S·ks·scale·log2 e (capped, biased, masked) + log2 vs, one row a thread;
 //   w = 2^{t − M + 8}  as halves into tensor memory over S, M a running bound of
 //                      the row's maximum that is moved when the maximum passes it
