@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
   const EntUnit unit = e.slots[b];
   const Q8Slot s = unit.s;
   if (s.count == 0) return;  // (the whole cluster)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
   const Q8Span sp = unit.sp;
   const int T = unit.T;
   const size_t tile0 = (size_t)(unit.cum + (long long)kvh * T);
@@ -400,6 +401,8 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
       if (lane == 0) wtop[warp][h] = m[h];
     }
     __syncthreads();
+    // every block of the cluster is running before the first store into another's shared memory
+    asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
     if (tid < 8 * C) {
       const int h = tid & 7;
       float v = -CUDART_INF_F;
