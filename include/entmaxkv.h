@@ -536,7 +536,12 @@ size_t entmaxkv_attend_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, 
  * Attention of the batch's rows over their sequences in the cache.
  *   alpha = 1  softmax, any count: o = sum_j softmax(s)_j v_j; tau gets log sum exp(s)
  *   alpha > 1  alpha-entmax, max_count = 1: z = (alpha-1) s,
- *              p_j = [z_j - tau]_+^{1/(alpha-1)}, sum p = 1
+ *              p_j = [z_j - tau]_+^{1/(alpha-1)}, sum p = 1. The sum is brought to 1
+ *              within 2^-14 + 2^-21 / (alpha-1), or DEV_TAU_NOCONV is raised (weights that
+ *              underflow: alpha of 6 and more with many equal scores below the largest).
+ *              Unsupported: alpha - 1 below 2^-10, and orders at which as many equal
+ *              scores as a row of the table holds would underflow:
+ *              (alpha-1) * log2(max_pages_per_seq * page_size) > 120
  *   q     bfloat16 rows, Hq heads (head h reads KV head h / group)
  *   out   bfloat16 rows, Hq heads; a row that sees no key gets 0
  *   tau   [total][Hq] float32, or NULL; NaN for a row that sees no key

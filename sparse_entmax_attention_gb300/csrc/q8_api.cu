@@ -126,6 +126,12 @@ static int check_attend(const entmaxkv_config* cfg, int n_seqs, int total, int m
   if (st) return st;
   if (n_seqs < 0 || n_seqs > 65535 || total < 0 || max_count < 0) return ENTMAXKV_ERR_INVALID_ARG;
   if (!(alpha >= 1.0f) || !isfinite(alpha)) return ENTMAXKV_ERR_INVALID_ARG;
+  if (alpha > 1.0f) {
+    // equal scores of n keys lie n^{1−α} above the threshold, which has to be a normal float with room for the solve's
+    // bracket; a weight's β-th power, β = 1/(α−1), is good to β·2^-22, which has to be less than a half's 2^-11
+    const double a1 = (double)alpha - 1.0, keys = (double)cfg->max_pages_per_seq * cfg->page_size;
+    if (a1 < 0x1p-10 || a1 * log2(keys) > 120.0) return ENTMAXKV_ERR_UNSUPPORTED;
+  }
   if (alpha > 1.0f && max_count > 1) return ENTMAXKV_ERR_UNSUPPORTED;
   if (!streams(cfg, max_count) && !chunk_counts_fit(*cfg, n_seqs, total)) return ENTMAXKV_ERR_UNSUPPORTED;
   return ENTMAXKV_OK;

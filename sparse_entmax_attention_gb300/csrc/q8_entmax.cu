@@ -9,10 +9,9 @@
 //    of the tiles. No token at or below z_max − 1 can carry weight (τ ≥ z_max − 1,
 //    where the sum is at least 1), so only tiles whose largest z clears that are
 //    looked at again: their scores go to every block of the cluster, and each
-//    solves alone with Newton steps from z_max − 1, which stay below the root of
-//    the convex, falling sum; after each step the closed-form root on the support
-//    so far is taken once it lies within it. (Where there are too many scores to
-//    hand round, a step's partial sums are instead, with a cluster barrier each.)
+//    solves alone, from z_max − 1 until the weights' sum is 1 (EntSolve). (Where
+//    there are too many scores to hand round, a step's partial sums are instead,
+//    with a cluster barrier each.)
 //    Then V is read for tiles with some z above its head's τ only, weights
 //    rounded to halves against their tile's largest, and the blocks' sums are
 //    added through the cluster. Every sum has a fixed order.
@@ -23,7 +22,8 @@
 // 24 warps alike. The rest is a chain of short phases, most of each the fetch of
 // its instructions. 16 sequences of 1-32k tokens, e4m3, alpha 2: 64 us. Dense
 // supports (random scores of deviation 1, 131072 tokens, every step reads z
-// again): 96 us at alpha 1.5, 151 at 1.25.
+// again): 103 us at alpha 1.5, 152 at 1.25; equal scores 140 and 132 (110 and 128
+// without the step that shows the sum to be 1).
 #include "q8_tiles.cuh"
 
 namespace ekv {
@@ -260,29 +260,41 @@ __device__ __forceinline__ float peer_load(uint32_t addr) {
   return v;
 }
 
-// x^b for x > 0 at an order without a short form, as 2^{b·lg x}: the
+// x^b for x ≥ 2^-126 at an order without a short form, as 2^{b·lg x}: the
 // logarithm is good to 2^-22 of itself (or absolutely, near 1), so a power is to
 // b·|lg x|·2^-22 and x^b times that to 2^-22.
-__device__ __forceinline__ float ent_pow(float x, float b) {
+__device__ __forceinline__ float lg2f(float x) {
   float l;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(l) : "f"(x));
-  return ex2f(b * l);
+  return l;
 }
+__device__ __forceinline__ float ent_pow(float x, float b) { return ex2f(b * lg2f(x)); }
+constexpr float kLeast = 0x1p-126f;  // a smaller z − τ carries no weight
 __device__ __forceinline__ float ent_weight(float y, float beta) {  // [y]_+^β
   y = fmaxf(y, 0.0f);
   if (beta == 2.0f) return y * y;
   if (beta == 1.0f) return y;
-  return y > 0.0f ? ent_pow(y, beta) : 0.0f;
+  return y >= kLeast ? ent_pow(y, beta) : 0.0f;
 }
 
-// What one step of the solve learns of the scores y = z − τ > 0: their number,
-// Σy and Σy² (Σy^{β−1} and Σy^β for other orders), and the least of them.
+// A head's threshold: τ = top + a + b, top its largest score. The two parts of
+// τ − top keep a difference of any size: b's own 24 bits hold y where a is the
+// score that is left (a y of 1e-10 beside an offset of 0.3 has its weight's share
+// at an order above 2, and equal scores share it).
+struct EntTau {
+  float top, a, b;
+  __device__ __forceinline__ float over(float z) const { return ((z - top) - a) - b; }
+};
+
+// What one step of the solve learns of the scores' offsets d = z − top with
+// y = d − (a + b) > 0: their number, Σy and Σy² (Σy^{β−1} and Σy^β for other
+// orders), and the least of the offsets.
 struct EntSums {
-  float k, s1, s2, mn;
-  __device__ __forceinline__ void add(float y, float beta, bool low) {
-    if (y > 0.0f) {
+  float k, s1, s2, least;
+  __device__ __forceinline__ void add(float d, float y, float beta, bool low) {
+    if (y >= kLeast) {
       k += 1.0f;
-      mn = fminf(mn, y);
+      least = fminf(least, d);
       const float w = low ? y : ent_pow(y, beta - 1.0f);
       s1 += w;
       s2 = fmaf(w, y, s2);
@@ -294,59 +306,102 @@ struct EntSums {
       k += __shfl_xor_sync(0xffffffffu, k, o);
       s1 += __shfl_xor_sync(0xffffffffu, s1, o);
       s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-      mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
     }
   }
 };
+// s += x with what the additions before lost: a lane's sum over a million tiles keeps its 24 bits.
+__device__ __forceinline__ void add_kept(float& s, float& lost, float x) {
+  const float y = x - lost, t = s + y;
+  lost = (t - s) - y;
+  s = t;
+}
 
-// The threshold of one head: τ as an offset from the largest score (exact to a
-// float's resolution of the offset, which is at most 1), moved by the sums of a
-// step. Newton runs on the norm Σy^β to the 1/β, convex and falling like the
-// sum and nearly straight far from the root, so its steps stay below the root.
+// A number of 48 bits, h + l with l within half of h's last bit.
+struct Pair {
+  float h, l;
+  __device__ __forceinline__ Pair plus(float x) const {
+    const float s = h + x, v = s - h, r = ((h - (s - v)) + (x - v)) + l;
+    const float t = s + r;
+    return Pair{t, r - (t - s)};
+  }
+  __device__ __forceinline__ float minus(const Pair& o) const { return (h - o.h) + (l - o.l); }
+};
+
+// The threshold of one head, as the offset t = τ − top in [−1, 0), moved by the
+// sums of a step until the weights' sum S is 1: to kNear + β·2^-21, which is the
+// powers' own error (and to a 64th of that where the steps still gain). Steps:
+//   β = 2, 1  the closed-form root where it keeps the support, which ends the
+//             solve from S ≤ 1.25 (from farther off its rounding shows, and it is
+//             a step like others), else
+//   Newton on the norm S^{1/β} (β = 1: on S), convex and falling for β ≥ 1, so
+//             that steps from S ≥ 1 stay below the root and nearly reach it on
+//             equal scores; close to 1 on S itself.
+// For β < 1 the sum's slope has no bound where a score enters, so every step lies
+// in a bracket, and one that leaves it, or does not halve |S − 1|, becomes the
+// bracket's middle (in the logarithm where its ends are far apart: n equal scores
+// have t = −n^{−1/β}). A bracket that closes on a score is continued in distances
+// from that score.
+constexpr int kEntSteps = 100;
 struct EntSolve {
-  float t, lo, hi;  // τ − z_max; other orders: the bracket
-  bool done, fine;
+  static constexpr float kNear = 0x1p-14f, kFirst = 0x1p127f;
+  Pair t, lo, hi;     // from `org`; S(lo) ≥ 1 > S(hi)
+  float org, a, b;    // a + b = org + t
+  float prev, at_lo;  // |S − 1| of the step before, the least offset of the support at lo
+  bool done;
+  __device__ __forceinline__ explicit EntSolve(bool skip)
+      : t{-1.0f, 0.0f}, lo{-1.0f, 0.0f}, hi{0.0f, 0.0f}, org(0.0f), a(-1.0f), b(0.0f), prev(kFirst), at_lo(0.0f), done(skip) {}
+  __device__ __forceinline__ float over(float d) const { return (d - a) - b; }
   __device__ __forceinline__ void step(const EntSums& v, float beta) {
-    const float tol = 1e-7f;
-    if (beta == 2.0f || beta == 1.0f) {
-      float d, st;
-      if (beta == 2.0f) {  // Σ(y − δ)² = 1 with δ ≤ min y, written without cancellation
-        const float disc = v.s1 * v.s1 - v.k * (v.s2 - 1.0f);
-        d = disc >= 0.0f ? __fdividef(v.s2 - 1.0f, v.s1 + sqrtf(disc)) : CUDART_INF_F;
-        st = __fdividef(v.s2 - sqrtf(v.s2), v.s1);
-      } else {
-        d = st = __fdividef(v.s1 - 1.0f, v.k);
-      }
-      if (!(v.k > 0.0f)) {
-        done = true;
-        fine = false;
-      } else if (d >= -tol && d <= v.mn * (1.0f + 1e-6f) + tol) {
-        t += d;
-        done = true;
-      } else if (!(st > tol)) {
-        t += fmaxf(st, 0.0f);
-        done = true;
-      } else {
-        t += st;
-      }
-    } else {  // any order: Newton inside a bracket kept by the sign of the sum − 1
-      if (v.k == 0.0f || v.s2 < 1.0f) hi = t;
-      else lo = t;
-      float nt = 0.5f * (lo + hi);
-      if (v.k > 0.0f) {
-        // of the norm far above the root (β > 1), where the sum's own steps are short
-        const float st = beta > 1.0f && v.s2 > 1.5f ? (v.s2 - ent_pow(v.s2, 1.0f - 1.0f / beta)) / v.s1
-                                                    : (v.s2 - 1.0f) / (beta * v.s1);
-        if (fabsf(st) <= tol) {
-          nt = t + st;
-          done = true;
-        } else if (t + st > lo && t + st < hi) {
-          nt = t + st;
-        }
-      }
-      t = nt;
-      if (hi - lo <= tol) done = true;
+    const bool two = beta == 2.0f, one = beta == 1.0f;
+    const float S = one ? v.s1 : v.s2, slope = one ? v.k : v.s1;  // slope · β is the sum's
+    const float e = S - 1.0f, ae = fabsf(e), inv = 1.0f / beta;
+    const float near = kNear + beta * 0x1p-21f;
+    if (e < 0.0f) {
+      hi = t;
+    } else {
+      lo = t;
+      at_lo = v.least;
     }
+    // no root above −k^{−1/β}, k scores at −1 (1/64: the powers' error)
+    if (prev == kFirst && beta < 1.0f) hi = Pair{-0.984375f * ent_pow(v.k, -inv), 0.0f};
+    if (ae <= 0x1p-6f * near || (ae <= near && ae > 0.5f * prev)) {
+      done = true;
+      return;
+    }
+    float st = __fdividef(e, beta * slope);
+    bool last = beta >= 1.0f && e > 0.0f && ae <= near;
+    if (two || one) {
+      const float disc = slope * slope - v.k * e;  // Σ(y − δ)² = 1, without cancellation
+      const float d = one ? st : disc >= 0.0f ? __fdividef(e, slope + sqrtf(disc)) : CUDART_INF_F;
+      if (d <= (v.least - a) - b) {
+        st = d;
+        last = e > 0.0f && ae <= 0.25f;
+      } else if (two && e > 0.0f && !last) {
+        st = __fdividef(S - sqrtf(S), slope);
+      }
+    } else if (!last && (beta < 1.0f || S > 1.5f)) {
+      st = __fdividef(S - ent_pow(S, 1.0f - inv), slope);
+    }
+    if (last) {
+      b += st;
+      done = true;
+      return;
+    }
+    Pair to = t.plus(st);
+    if (!(to.minus(lo) > 0.0f && to.minus(hi) < 0.0f) || ae > 0.5f * prev) {
+      if (org == 0.0f && hi.minus(lo) <= -0x1p-40f * lo.h) {
+        org = at_lo;
+        lo = Pair{fminf(lo.minus(Pair{org, 0.0f}), -0x1p-119f), 0.0f};
+        hi = Pair{fminf(hi.minus(Pair{org, 0.0f}), -0x1p-120f), 0.0f};
+      }
+      to = beta < 1.0f && lo.h < 4.0f * hi.h ? Pair{-ex2f(0.5f * (lg2f(-lo.h) + lg2f(-hi.h))), 0.0f}
+                                             : lo.plus(0.5f * hi.minus(lo));
+    }
+    prev = ae;
+    t = to;
+    a = org == 0.0f ? t.h : org;
+    b = org == 0.0f ? t.l : t.h;
   }
 };
 
@@ -361,7 +416,7 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
   __shared__ int counts[kEntCluster][NW];      // scores a warp has handed round; over kEntSent: too many
   __shared__ float top_sh[kEntCluster][8];
   __shared__ float wtop[NW][8];
-  __shared__ float2 tau_sh[8];
+  __shared__ EntTau tau_sh[8];
   __shared__ int found[NW + 1];
   __shared__ __align__(16) float part[8 * D];
   const Q8AttendArgs& a = e.a;
@@ -414,16 +469,15 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
     cluster_sync();
   }
   // The block's warps share out the heads, a head's warps its part of the tiles. Scores above z_max − 1 go to every
-  // block of the cluster, kEntSent a warp at most, so that each can solve alone.
+  // block of the cluster as offsets from z_max, kEntSent a warp at most, so that each can solve alone.
   const int wph = NW / G, hd = warp / wph, wi = warp % wph;
   const bool works = hd < G;
   float top = -CUDART_INF_F;
   if (works)
     for (int i = 0; i < C; ++i) top = fmaxf(top, top_sh[i][hd]);
   const bool none = !(top > -CUDART_INF_F);
-  const float T0 = top - 1.0f;
   const int wlo = lo + (int)((long long)(hi - lo) * wi / wph), whi = lo + (int)((long long)(hi - lo) * (wi + 1) / wph);
-  float* sent = reinterpret_cast<float*>(base_p);                     // [cluster][warps][kEntSent] scores above T0
+  float* sent = reinterpret_cast<float*>(base_p);                     // [cluster][warps][kEntSent] offsets from top
   const float* zh = e.z + (tile0 * G + (works ? hd : 0)) * kEntKeys;  // tile t's scores at zh + t·G·32
   int n_sent = 0;
   if (works && !none) {
@@ -434,7 +488,7 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
         m[k] = t1 + 32 * k + lane < whi ? pmax[(size_t)(t1 + 32 * k + lane) * G + hd] : -CUDART_INF_F;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        uint32_t in = __ballot_sync(0xffffffffu, m[k] > T0);
+        uint32_t in = __ballot_sync(0xffffffffu, m[k] - top > -1.0f);
         while (in && n_sent <= kEntSent) {  // four tiles' scores in flight
           float z[4];
           const int n4 = min(4, __popc(in));
@@ -445,13 +499,14 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t up = __ballot_sync(0xffffffffu, z[i] > T0);
+            const float d = z[i] - top;
+            const uint32_t up = __ballot_sync(0xffffffffu, d > -1.0f);
             const int at = n_sent + __popc(up & ((1u << lane) - 1u));
-            if (z[i] > T0 && at < kEntSent)
+            if (d > -1.0f && at < kEntSent)
               for (int k2 = 0; k2 < C; ++k2)
                 asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(
                                  peer(smem_u32(&sent[(rank * NW + warp) * kEntSent + at]), k2)),
-                             "f"(z[i] - top)
+                             "f"(d)
                              : "memory");
             n_sent += __popc(up);
           }
@@ -467,26 +522,30 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
   for (int i = lane; i < C * NW; i += 32) many |= counts[i / NW][i % NW] > kEntSent;
   many = __any_sync(0xffffffffu, many);
   const bool low = e.beta == 2.0f || e.beta == 1.0f;
-  EntSolve sv{-1.0f, -1.0f, 0.0f, !works || none, true};
+  EntSolve sv(!works || none);
   if (!many) {
     if (wi == 0) {  // a head's first warp, a lane or more a segment
-      for (int it = 0; it < 100 && !sv.done; ++it) {
+      for (int it = 0; it < kEntSteps && !sv.done; ++it) {
         EntSums v{0.0f, 0.0f, 0.0f, CUDART_INF_F};
         for (int i = lane; i < C * wph; i += 32) {
           const int g = (i / wph) * NW + hd * wph + i % wph;
           const int n = counts[g / NW][g % NW];
-          for (int k = 0; k < n; ++k) v.add(sent[g * kEntSent + k] - sv.t, e.beta, low);
+          for (int k = 0; k < n; ++k) {
+            const float d = sent[g * kEntSent + k];
+            v.add(d, sv.over(d), e.beta, low);
+          }
         }
         v.warp_total();
         sv.step(v, e.beta);
       }
     }
   } else {
-    for (int it = 0; it < 100; ++it) {
+    for (int it = 0; it < kEntSteps; ++it) {
       EntSums v{0.0f, 0.0f, 0.0f, CUDART_INF_F};
       if (!sv.done) {
+        float lost1 = 0.0f, lost2 = 0.0f;
         for (int t1 = wlo; t1 < whi; t1 += 32) {
-          uint32_t in = __ballot_sync(0xffffffffu, t1 + lane < whi && pmax[(size_t)(t1 + lane) * G + hd] - top > sv.t);
+          uint32_t in = __ballot_sync(0xffffffffu, t1 + lane < whi && sv.over(pmax[(size_t)(t1 + lane) * G + hd] - top) > 0.0f);
           while (in) {  // eight tiles' scores in flight
             float z[8];
             const int n8 = min(8, __popc(in));
@@ -495,15 +554,20 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
               z[i] = i < n8 ? zh[(size_t)(t1 + __ffs(in) - 1) * G * kEntKeys + lane] : -CUDART_INF_F;
               in &= in - 1u;
             }
+            EntSums u{0.0f, 0.0f, 0.0f, CUDART_INF_F};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v.add((z[i] - top) - sv.t, e.beta, low);
+            for (int i = 0; i < 8; ++i) u.add(z[i] - top, sv.over(z[i] - top), e.beta, low);
+            v.k += u.k;
+            v.least = fminf(v.least, u.least);
+            add_kept(v.s1, lost1, u.s1);
+            add_kept(v.s2, lost2, u.s2);
           }
         }
         v.warp_total();
       }
       if (lane < C)
         peer_store4(peer(smem_u32(&sums[it & 1][rank][warp]), lane),
-                    make_float4(sv.done ? -1.0f : v.k, v.s1, v.s2, v.mn));
+                    make_float4(sv.done ? -1.0f : v.k, v.s1, v.s2, v.least));
       cluster_sync();
       // every head done? (its first warp in the first block says so)
       const bool hd_done = lane >= G || sums[it & 1][0][lane * wph].x < 0.0f;
@@ -515,17 +579,17 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
         v.k += p.x;
         v.s1 += p.y;
         v.s2 += p.z;
-        v.mn = fminf(v.mn, p.w);
+        v.least = fminf(v.least, p.w);
       }
       v.warp_total();
       sv.step(v, e.beta);
     }
   }
   if (works && wi == 0 && lane == 0) {
-    tau_sh[hd] = none ? make_float2(CUDART_NAN_F, 0.0f) : make_float2(top, sv.t);
+    tau_sh[hd] = EntTau{none ? CUDART_NAN_F : top, sv.a, sv.b};
     if (rank == 0) {
-      if (!(sv.done && sv.fine)) raise_flag(a.c.status, ENTMAXKV_DEV_TAU_NOCONV);
-      if (a.tau) a.tau[(size_t)s.start * Hkv * G + kvh * G + hd] = none ? CUDART_NAN_F : top + sv.t;
+      if (!sv.done) raise_flag(a.c.status, ENTMAXKV_DEV_TAU_NOCONV);
+      if (a.tau) a.tau[(size_t)s.start * Hkv * G + kvh * G + hd] = none ? CUDART_NAN_F : top + (sv.a + sv.b);
     }
   }
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // the copies below write where scores were kept
@@ -535,7 +599,7 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
   // in turns, the next one's V on its way.
   int* list = reinterpret_cast<int*>(base_p + 2 * NW * SLAB);  // [kEntList] tiles
   const int r = lane >> 2, c = lane & 3;
-  const float2 tau_r = r < G ? tau_sh[r] : make_float2(CUDART_INF_F, 0.0f);
+  const EntTau tau_r = r < G ? tau_sh[r] : EntTau{CUDART_INF_F, 0.0f, 0.0f};
   float acc[D / 16][1][4];
 #pragma unroll
   for (int mt = 0; mt < D / 16; ++mt) acc[mt][0][0] = acc[mt][0][1] = acc[mt][0][2] = acc[mt][0][3] = 0.0f;
@@ -545,7 +609,7 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
     const int t = l0 + tid;
     bool in = false;
     if (t < hi && t < l0 + kEntList)
-      for (int h = 0; h < G; ++h) in |= (pmax[(size_t)t * G + h] - tau_sh[h].x) - tau_sh[h].y > 0.0f;
+      for (int h = 0; h < G; ++h) in |= tau_sh[h].over(pmax[(size_t)t * G + h]) > 0.0f;
     const uint32_t bits = __ballot_sync(0xffffffffu, in);
     if (lane == 0) found[warp] = __popc(bits);
     __syncthreads();
@@ -604,7 +668,7 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
       }
       // row r's weights of this tile against a power of two above its largest; the V scales of a tile's two pages
       // differ: each goes into its own keys' weights, over the larger of them
-      const float ym = r < G ? (pmax[(size_t)tt * G + r] - tau_r.x) - tau_r.y : -1.0f;
+      const float ym = r < G ? tau_r.over(pmax[(size_t)tt * G + r]) : -1.0f;
       float2 z[2][2];
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt)
@@ -623,7 +687,7 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
         const float f0 = PP == 1 ? up : up * (vs[16 * kt / P] * vinv);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float y0 = (z[kt][j].x - tau_r.x) - tau_r.y, y1 = (z[kt][j].y - tau_r.x) - tau_r.y;
+          const float y0 = tau_r.over(z[kt][j].x), y1 = tau_r.over(z[kt][j].y);
           const __half2 p = __floats2half2_rn(ent_weight(y0, e.beta) * f0, ent_weight(y1, e.beta) * f0);
           bf[kt][0][j] = *reinterpret_cast<const uint32_t*>(&p);
         }

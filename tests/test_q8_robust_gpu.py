@@ -2,12 +2,13 @@
 device do not show: clusters that start one by one, calls on other streams,
 non-finite queries, long and dense supports, steps that ask for too much."""
 
+import numpy as np
 import pytest
 import torch
 
 from sparse_entmax_attention_gb300 import binding as B
 
-from q8_cases import batch_of, filled
+from q8_cases import batch_of, dense, empty_cache, filled
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +32,90 @@ def test_entmax_clusters_that_start_beside_other_work_give_the_same_bits():
         assert torch.equal(o.out, first.out) and torch.equal(o.tau, first.tau)
     torch.cuda.synchronize()
     assert c.device_status() == 0
+
+
+ORDERS = [float(np.float32(a)) for a in (1.002, 1.1, 1.25, 1.5, 1.75, 2.0, 2.2, 2.5, 3.0, 4.0, 6.0)]
+
+
+def _sum_tol(alpha):
+    """Of an output Σ p·v, v 0 or 1: its rounding to bf16 (half a step, 2^-8 of up to 1), each weight's to a half
+    (2^-11), the sum's own bound 2^-14 + β·2^-21, the weights' powers (β·2^-21 again: the solve's and the weights'
+    may differ) and 127 · fl32(1/127) for a 1 (2^-24)."""
+    return 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -14 + 2.0 ** -20 / (alpha - 1.0) + 2.0 ** -24
+
+
+@pytest.mark.parametrize("alpha", ORDERS)
+@pytest.mark.parametrize("n", [1, 33, 1000, 10000, 100001])
+def test_weights_of_equal_keys_add_up_to_one(alpha, n):
+    """Scores that are exactly equal, V all ones: the output is the weights' sum, with and without the scores
+    handed round a cluster (1000 and 10000 keys)."""
+    c = empty_cache("int8", [n, 3], hkv=2, g=4, d=64, P=16)
+    x = torch.ones(n + 3, 2, 64, device="cuda").bfloat16()
+    B.append_q8(c, x, x, batch_of([n, 3]))
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    q = torch.randn(2, 8, 64, generator=gen, device="cuda").bfloat16()
+    o = B.attend_q8(c, q, batch_of([1, 1]), alpha=alpha)
+    assert c.device_status() == 0
+    assert float((o.out.float() - 1.0).abs().max()) <= _sum_tol(alpha)
+    # τ = z − n^{1−α}; a score is good to 2^-20·(Σ|q||k|/√d + 1), and τ is rounded to fp32
+    z = (alpha - 1.0) * q.double().sum(-1) / 8.0
+    want = z - torch.tensor([n, 3], device="cuda").double()[:, None] ** (1.0 - alpha)
+    tol = 2.0 ** -20 * (alpha - 1.0) * (q.double().abs().sum(-1) / 8.0 + 1.0) + 2.0 ** -23 * want.abs()
+    # and by what the sum's bound lets it move: |S − 1|·(z − τ)/β
+    tol += (alpha - 1.0) * (2.0 ** -14 + 2.0 ** -21 / (alpha - 1.0)) * (z - want)
+    assert bool(((o.tau.double() - want).abs() <= tol).all())
+
+
+def _share(D, m, alpha):
+    """Of one key whose z lies D above those of m equal ones: the m keys' share of the weight, in 64 bits:
+    m·ρ^β + (D + ρ)^β = 1 by bisection on log2 ρ."""
+    beta, lo, hi = 1.0 / (alpha - 1.0), -400.0, 0.0
+    for _ in range(200):
+        mid = 0.5 * (lo + hi)
+        lo, hi = (lo, mid) if m * 2.0 ** (mid * beta) + (D + 2.0 ** mid) ** beta >= 1.0 else (mid, hi)
+    return m * 2.0 ** (hi * beta)
+
+
+@pytest.mark.parametrize("alpha", ORDERS[2:-1])
+@pytest.mark.parametrize("m", [40, 1000, 100000])
+@pytest.mark.parametrize("D", [0.9, 0.3, 1e-3])
+def test_one_key_above_many_equal_ones(alpha, m, D):
+    """The threshold lies next to the many keys' score, above order 2 far nearer than a float's step at D."""
+    d, P = 64, 16
+    c = empty_cache("int8", [m + 1], hkv=1, g=2, d=d, P=P)
+    k, v = torch.ones(m + 1, 1, d, device="cuda"), torch.ones(m + 1, 1, d, device="cuda")
+    k[P:] = 0.5   # the strong key's page holds equal keys of its own too: they are masked below
+    v[:P] = 0.0
+    B.append_q8(c, k.bfloat16(), v.bfloat16(), batch_of([m + 1]))
+    K = dense(c, 0, 0, "k")
+    diff = float((K[P - 1] - K[P])[0])
+    q = torch.zeros(1, 2, d, device="cuda")
+    q[0, 0, 0] = q[0, 1, 0] = 1.0
+    scale = D / ((alpha - 1.0) * diff)
+    o = B.attend_q8(c, q.bfloat16(), batch_of([1]), alpha=alpha, scale=scale,
+                    first_key=torch.tensor([P - 1], dtype=torch.int32, device="cuda"))
+    assert c.device_status() == 0
+    many = m + 1 - P
+    share = _share(D, many, alpha)
+    # V is 1 for the many keys and 0 for the strong one. D is good to 2^-20: the scores' common factor has four
+    # roundings of 2^-24, each score (2D and D) two of its own, the difference one. The share at both ends:
+    ends = [_share(D * (1 + s * 2.0 ** -20), many, alpha) for s in (-1, 1)]
+    tol = _sum_tol(alpha) + max(abs(e - share) for e in ends)
+    got = float(o.out[0, 0, 0])
+    assert abs(got - share) <= tol, (got, share, tol)
+    assert torch.equal(o.out[0, 0], o.out[0, 1])
+
+
+@pytest.mark.parametrize("alpha", [1.25, 1.5, 2.0, 3.0])
+def test_dense_supports_add_up_to_one(alpha):
+    """Random scores close together: most of 60000 keys in the support, V all ones."""
+    n = 60000
+    c = empty_cache("e4m3", [n], hkv=2, g=4, d=64, P=32)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    k = torch.randn(n, 2, 64, generator=gen, device="cuda").bfloat16()
+    B.append_q8(c, k, torch.ones_like(k), batch_of([n]))
+    q = torch.randn(1, 8, 64, generator=gen, device="cuda").bfloat16()
+    for scale in (1e-7, 1e-4, 1e-2, 0.1):
+        o = B.attend_q8(c, q, batch_of([1]), alpha=alpha, scale=scale)
+        assert c.device_status() == 0
+        assert float((o.out.float() - 1.0).abs().max()) <= _sum_tol(alpha), scale
