@@ -338,9 +338,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
 #pragma unroll
             for (int o = 1; o < CPR; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             int e = (int)(m >> 7) - 127;
-            if (m >= 0x7f80u) e = 13;
             e = max(e, -100);
-            const float f = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+            // (a row with an infinity or NaN is all NaN, as in q_half_frag)
+            const float f = m >= 0x7f80u ? CUDART_NAN_F : __uint_as_float((uint32_t)(13 - e + 127) << 23);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const __half2 h = __floats2half2_rn(bf_lo(u[j]) * f, bf_hi(u[j]) * f);

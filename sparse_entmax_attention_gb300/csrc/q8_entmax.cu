@@ -211,15 +211,15 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 1)
             zo[j * kEntKeys + kHalf * mt] = v[0];
             zo[j * kEntKeys + kHalf * mt + 8] = v[1];
           }
-          pm[j] = max3(pm[j], v[0], v[1]);
+          pm[j] = max3_nan(pm[j], v[0], v[1]);
         }
       }
       zo += G * kEntKeys;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        pm[j] = fmaxf(pm[j], __shfl_xor_sync(0xffffffffu, pm[j], 4));
-        pm[j] = fmaxf(pm[j], __shfl_xor_sync(0xffffffffu, pm[j], 8));
-        pm[j] = fmaxf(pm[j], __shfl_xor_sync(0xffffffffu, pm[j], 16));
+        pm[j] = max_nan(pm[j], __shfl_xor_sync(0xffffffffu, pm[j], 4));
+        pm[j] = max_nan(pm[j], __shfl_xor_sync(0xffffffffu, pm[j], 8));
+        pm[j] = max_nan(pm[j], __shfl_xor_sync(0xffffffffu, pm[j], 16));
         if (r == 0 && mine[j]) po[j] = pm[j];
       }
       po += G;
@@ -449,10 +449,12 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
     for (int t = lo + tid; t < hi; t += NTH)
 #pragma unroll
       for (int h = 0; h < 8; ++h)
-        if (h < G) m[h] = fmaxf(m[h], pmax[(size_t)t * G + h]);
+        if (h < G) m[h] = max_nan(m[h], pmax[(size_t)t * G + h]);
 #pragma unroll
     for (int h = 0; h < 8; ++h) {
-      if (h < G) m[h] = warp_max(m[h]);
+      if (h < G)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m[h] = max_nan(m[h], __shfl_xor_sync(0xffffffffu, m[h], o));
       if (lane == 0) wtop[warp][h] = m[h];
     }
     __syncthreads();
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
       const int h = tid & 7;
       float v = -CUDART_INF_F;
 #pragma unroll
-      for (int i = 0; i < NW; ++i) v = fmaxf(v, wtop[i][h]);
+      for (int i = 0; i < NW; ++i) v = max_nan(v, wtop[i][h]);
       asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(peer(smem_u32(&top_sh[rank][h]), tid >> 3)), "f"(v)
                    : "memory");
     }
@@ -474,8 +476,9 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
   const bool works = hd < G;
   float top = -CUDART_INF_F;
   if (works)
-    for (int i = 0; i < C; ++i) top = fmaxf(top, top_sh[i][hd]);
-  const bool none = !(top > -CUDART_INF_F);
+    for (int i = 0; i < C; ++i) top = max_nan(top, top_sh[i][hd]);
+  // a head without keys answers 0; one with a score that is NaN or +∞ answers NaN, as its b says
+  const bool odd = !(top < CUDART_INF_F), none = odd || top == -CUDART_INF_F;
   const int wlo = lo + (int)((long long)(hi - lo) * wi / wph), whi = lo + (int)((long long)(hi - lo) * (wi + 1) / wph);
   float* sent = reinterpret_cast<float*>(base_p);                     // [cluster][warps][kEntSent] offsets from top
   const float* zh = e.z + (tile0 * G + (works ? hd : 0)) * kEntKeys;  // tile t's scores at zh + t·G·32
@@ -586,7 +589,7 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
     }
   }
   if (works && wi == 0 && lane == 0) {
-    tau_sh[hd] = EntTau{none ? CUDART_NAN_F : top, sv.a, sv.b};
+    tau_sh[hd] = EntTau{none ? CUDART_NAN_F : top, sv.a, odd ? CUDART_NAN_F : sv.b};
     if (rank == 0) {
       if (!sv.done) raise_flag(a.c.status, ENTMAXKV_DEV_TAU_NOCONV);
       if (a.tau) a.tau[(size_t)s.start * Hkv * G + kvh * G + hd] = none ? CUDART_NAN_F : top + (sv.a + sv.b);
@@ -760,6 +763,7 @@ __global__ void __launch_bounds__(kEntWarps * 32, 1)
   for (int i = rank * per + tid; i < min(G * D, (rank + 1) * per); i += NTH) {
     float v = 0.0f;
     for (int k = 0; k < C; ++k) v += peer_load(peer(smem_u32(&part[i]), k));
+    if (isnan(tau_sh[i / D].b)) v = CUDART_NAN_F;
     a.out.p[(long long)s.start * a.out.ts + (long long)(kvh * G + i / D) * a.out.hs + i % D] = __float2bfloat16_rn(v);
   }
   cluster_sync();  // no block leaves while its sums are read

@@ -24,7 +24,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 // A query row as mma B fragments in halves: lane (n = lane/4, c = lane%4) holds
 // dims (D/4)·c + 4ks .. +3 of row n, the order in which a lane's K bytes lie.
 // A power of two brings the row's largest value into [2^13, 2^14), so bf16
-// values down to 2^-27 of it are exact as halves; inv is that power's inverse.
+// values down to 2^-27 of it are exact as halves; inv is that power's inverse. A
+// row that holds an infinity or a NaN becomes all NaN, and so do its scores (an
+// infinity alone could make all of them −∞, which is a masked key's).
 // p = null: a row of zeros.
 template <int D>
 __device__ __forceinline__ void q_load(const __nv_bfloat16* p, int lane, uint4 (&w)[D / 32]) {
@@ -44,9 +46,8 @@ __device__ __forceinline__ void q_half_frag(const uint4 (&w)[D / 32], uint32_t (
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   int e = (int)(m >> 7) - 127;
-  if (m >= 0x7f80u) e = 13;  // infinities and NaN stay what they are
   e = max(e, -100);
-  const float f = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+  const float f = m >= 0x7f80u ? CUDART_NAN_F : __uint_as_float((uint32_t)(13 - e + 127) << 23);
   inv = __uint_as_float((uint32_t)(e - 13 + 127) << 23);
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
@@ -119,6 +120,17 @@ struct TanhPoly {
 __device__ __forceinline__ constexpr TanhPoly tanh_poly() {
   return TanhPoly{{0.99999946f, -0.33326283f, 0.1318994f, -0.04439274f},
                   {0.99999994f, -0.33332828f, 0.13325076f, -0.053451646f, 0.020279707f, -0.0061943247f, 0.0010380251f}};
+}
+// Maxima in which a NaN stays.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;

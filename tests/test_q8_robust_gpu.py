@@ -119,3 +119,40 @@ def test_dense_supports_add_up_to_one(alpha):
         o = B.attend_q8(c, q, batch_of([1]), alpha=alpha, scale=scale)
         assert c.device_status() == 0
         assert float((o.out.float() - 1.0).abs().max()) <= _sum_tol(alpha), scale
+
+
+@pytest.mark.parametrize("alpha,counts", [(1.0, [1, 1, 1]), (1.25, [1, 1, 1]), (1.5, [1, 1, 1]), (2.0, [1, 1, 1]),
+                                          (3.0, [1, 1, 1]), (1.0, [3, 2, 1]), (1.0, [3, 2, 9]), (1.0, [120, 70, 1])])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+def test_a_non_finite_query_gives_nan_in_its_own_row_and_head(alpha, counts, bad, code):
+    """Sequences of many tokens and of one (where an infinity's score can be -inf, a masked key's), rows that see
+    nothing beside them; every other row and head keeps its bits."""
+    lens = [500, 90, counts[2]]
+    c, q = filled(code, lens, counts, hkv=2, g=3, d=64, P=16)
+    batch = batch_of(counts)
+    fk = torch.zeros(sum(counts), dtype=torch.int32, device="cuda")
+    fk[1 if counts[0] > 1 else 0] = 10 ** 6  # sees no key
+    clean = B.attend_q8(c, q, batch, alpha=alpha, first_key=fk)
+    q2, spoilt = q.clone(), torch.zeros(sum(counts), 6, dtype=torch.bool, device="cuda")
+    blind = fk > 0
+    for row, head, i in ((0, 1, 3), (counts[0], 4, 0), (counts[0], 0, 63), (sum(counts) - 1, 2, 17),
+                         (sum(counts) - 1, 3, 18), (int(blind.nonzero()[0]), 5, 9)):
+        q2[row, head, i] = bad
+        spoilt[row, head] = not blind[row]
+    o = B.attend_q8(c, q2, batch, alpha=alpha, first_key=fk)
+    assert c.device_status() == 0
+    assert bool(torch.isnan(o.out[spoilt]).all()) and bool(torch.isnan(o.tau[spoilt]).all())
+    assert torch.equal(o.out[~spoilt], clean.out[~spoilt])
+    assert torch.equal(o.tau[~spoilt].nan_to_num(7.0), clean.tau[~spoilt].nan_to_num(7.0))
+    assert not o.out[blind].any() and bool(torch.isnan(o.tau[blind]).all())
+
+
+def test_entmax_scores_past_the_largest_float_give_nan():
+    c, q = filled("int8", [200], [1], hkv=1, g=2, d=64, P=16)
+    q2 = q.clone()
+    q2[0, 0] = 2.0 ** 120
+    o = B.attend_q8(c, q2, batch_of([1]), alpha=1.5, scale=2.0 ** 20)
+    base = B.attend_q8(c, q, batch_of([1]), alpha=1.5, scale=2.0 ** 20)
+    assert bool(torch.isnan(o.out[0, 0]).all()) and bool(torch.isnan(o.tau[0, 0]))
+    assert torch.equal(o.out[0, 1], base.out[0, 1]) and c.device_status() == 0
