@@ -9,6 +9,7 @@ raise.
 
 from __future__ import annotations
 
+import contextlib
 import copy
 import ctypes
 import os
@@ -169,6 +170,20 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _allocating(stream):
+    """Where a call given `stream` makes its tensors: on that stream, so that their first fill, the
+    call's launches and the reuse of what the call drops come one behind the other."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _for_caller(stream, *tensors):
+    """Tensors made on `stream` and returned are kept until the caller's current stream is done with
+    them too (it waits for `stream` before it reads them)."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(t.device))
+
+
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
 
@@ -300,16 +315,22 @@ def decode(cache: PagedCache, q, alpha=1.5, policy="gaussian", budget_tokens=0, 
     """entmaxkv_decode: q [n_seqs, Hq, d] in the cache dtype.
 
     With ``events`` (STAGE_EVENTS torch.cuda.Event objects) this calls
-    entmaxkv_decode_profiled, which records them between the stages.
+    entmaxkv_decode_profiled, which records them between the stages. A workspace and
+    outputs that are not given are allocated on ``stream``.
     """
     assert q.is_contiguous() and q.dtype == cache.dtype
     n_seqs = q.shape[0]
     pol = POLICIES.get(policy, policy)
-    if workspace is None:
-        workspace = alloc_workspace(cache, n_seqs, pol, budget_tokens, flags)
-    if outputs is None:
-        outputs = alloc_outputs(cache, n_seqs, pol, budget_tokens)
+    made = outputs is None
+    if made or workspace is None:
+        with _allocating(stream):
+            if workspace is None:
+                workspace = alloc_workspace(cache, n_seqs, pol, budget_tokens, flags)
+            if made:
+                outputs = alloc_outputs(cache, n_seqs, pol, budget_tokens)
     o = outputs
+    if made:
+        _for_caller(stream, o.out, o.page_ids, o.n_sel, o.tau, o.delta)
     args = [ctypes.byref(cache.cfg), ctypes.byref(cache.view), _ptr(q), _ptr(seq_ids), n_seqs,
             float(alpha), pol, int(budget_tokens), float(margin), int(flags), _ptr(workspace),
             workspace.numel(), _ptr(o.out), _ptr(o.page_ids), o.page_ids.shape[-1], _ptr(o.n_sel),
@@ -463,6 +484,8 @@ def _i32(t, shape, dev, name):
 
 def _q8_call(dev, stream, fn, *args):
     """fn(*args, stream) on the tensors' device, whichever device is current."""
+    if stream is not None and stream.device_index != dev:
+        raise EntmaxKVError("stream: on another device than the tensors")
     if torch._C._cuda_getDevice() == dev:
         code = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     else:
@@ -661,10 +684,14 @@ def append_q8(cache: QuantCache, k, v, batch: Batch, stream=None):
 
 def read_q8(cache: QuantCache, first, batch: Batch, k=None, v=None, stream=None):
     """entmaxkv_read_q8: tokens first[b] .. first[b] + count[b] - 1 of each sequence as bf16 rows
-    [total, Hkv, d] in k and v (allocated when not given). Returns (k, v)."""
+    [total, Hkv, d] in k and v (allocated on the call's stream when not given). Returns (k, v)."""
     dev, shape = _on_cache(cache, batch), (batch.total, cache.cfg.num_kv_heads, cache.cfg.head_dim)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
+    if k is None or v is None:
+        with _allocating(stream):
+            made = [torch.empty(shape, dtype=torch.bfloat16, device=cache.device) for t in (k, v) if t is None]
+        _for_caller(stream, *made)
+        v = made.pop() if v is None else v
+        k = made.pop() if k is None else k
     _q8_call(dev, stream, lib().entmaxkv_read_q8, cache.cfg, cache.view, batch.view,
              _i32(first, (batch._n,), dev, "first"), _rows(k, shape, dev, "k"), _rows(v, shape, dev, "v"))
     return k, v
@@ -705,15 +732,21 @@ def attend_q8(cache: QuantCache, q, batch: Batch, alpha=1.0, scale=0.0, softcap=
     softcap: s becomes softcap * tanh(s / softcap). slopes: float32 [Hq], slopes[h] * distance is
     taken off. window: keys seen back from the row's own. prefix: int32 [n_seqs], keys in front
     that every row sees. first_key: int32 [total], where each row's document begins.
+    A workspace and outputs that are not given are allocated on the call's stream.
     """
     dev, Hq = _on_cache(cache, batch), cache.num_q_heads
     shape = (batch.total, Hq, cache.cfg.head_dim)
-    if outputs is None:
-        outputs = alloc_attend_outputs(cache, batch)
-    if workspace is None:
-        workspace = alloc_attend_workspace(cache, batch, alpha)
-    elif workspace.get_device() != dev:
+    if workspace is not None and workspace.get_device() != dev:
         raise EntmaxKVError("workspace: on another device than the cache")
+    made = outputs is None
+    if made or workspace is None:
+        with _allocating(stream):
+            if made:
+                outputs = alloc_attend_outputs(cache, batch)
+            if workspace is None:
+                workspace = alloc_attend_workspace(cache, batch, alpha)
+        if made:
+            _for_caller(stream, outputs.out, outputs.tau)
     score = ScoreView(scale, softcap, window, None, None, None)
     if slopes is not None:
         if slopes.dtype is not _F32 or slopes.shape != (Hq,) or not slopes.is_contiguous() or slopes.get_device() != dev:

@@ -156,3 +156,46 @@ def test_entmax_scores_past_the_largest_float_give_nan():
     base = B.attend_q8(c, q, batch_of([1]), alpha=1.5, scale=2.0 ** 20)
     assert bool(torch.isnan(o.out[0, 0]).all()) and bool(torch.isnan(o.tau[0, 0]))
     assert torch.equal(o.out[0, 1], base.out[0, 1]) and c.device_status() == 0
+
+
+@pytest.mark.parametrize("alpha,counts", [(1.0, [1, 1]), (1.5, [1, 1]), (1.0, [90, 40])])
+def test_calls_on_a_side_stream_make_their_own_buffers_there(alpha, counts):
+    """The current stream is kept busy before each call and takes what the call dropped after it: the outputs
+    neither lose to a late fill nor to another tensor in the workspace's place."""
+    c, q = filled("int8", [4000, 900], counts, hkv=4, g=4)
+    batch = batch_of(counts)
+    want = B.attend_q8(c, q, batch, alpha=alpha)
+    first = torch.tensor([0, 0], dtype=torch.int32, device="cuda")
+    rows = B.read_q8(c, first, batch)
+    size = B.attend_workspace_bytes(c, batch, alpha)
+    x = torch.randn(4096, 4096, device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for _ in range(10):
+            x @ x  # (a few ms)
+        o = B.attend_q8(c, q, batch, alpha=alpha, stream=side)
+        k, v = B.read_q8(c, first, batch, stream=side)
+        torch.empty(size, dtype=torch.uint8, device="cuda").fill_(0xff)
+        torch.cuda.synchronize()
+        assert torch.equal(o.out, want.out) and torch.equal(o.tau, want.tau)
+        assert torch.equal(k, rows[0]) and torch.equal(v, rows[1])
+    assert c.device_status() == 0
+
+
+def test_decode_on_a_side_stream_makes_its_own_buffers_there():
+    cache = B.PagedCache(2, 4, 128, 16, 1, 40, 40, torch.bfloat16)
+    cache.block_table[0] = torch.arange(40, device="cuda")
+    kv = torch.randn(2, 1, 2, 600, 128, device="cuda").bfloat16()
+    B.append(cache, kv[0], kv[1])
+    q = torch.randn(1, 8, 128, device="cuda").bfloat16()
+    want = B.decode(cache, q, 1.5, "full")
+    x = torch.randn(4096, 4096, device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        x @ x
+    o = B.decode(cache, q, 1.5, "full", stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(o.page_ids, want.page_ids) and torch.equal(o.n_sel, want.n_sel)
+    torch.testing.assert_close(o.out, want.out, rtol=1e-5, atol=1e-5)  # (its sums' order is not fixed)
