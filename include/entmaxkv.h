@@ -467,6 +467,20 @@ int32_t entmaxkv_plan_pages(const entmaxkv_config* cfg, int32_t* block_table, co
                             void* stream);
 
 /*
+ * The same with a bound for a slot's new tokens, the max_count of the batch that
+ * append_q8 and attend_q8 take next: a slot with more is refused alone
+ * (DEV_BAD_BATCH), its length, pages and the list as they were. Without it the
+ * slot would be admitted here and skipped there, and its sequence would count
+ * tokens that nobody wrote. max_count = 0: no bound.
+ */
+int32_t entmaxkv_plan_pages_bounded(const entmaxkv_config* cfg, int32_t* block_table, const int32_t* seq_lens,
+                                    uint32_t* status, const int32_t* seq_ids, const int32_t* n_new,
+                                    int32_t n_seqs, int32_t total, int32_t max_count,
+                                    const int32_t* free_pages, const int32_t* free_count,
+                                    int32_t* free_count_out, int32_t* lens_out, int32_t* start,
+                                    int32_t* count, int32_t* positions, int64_t* slots, void* stream);
+
+/*
  * Give the pages of n_seqs sequences back: each row's pages go on the free
  * list, last page first (so that planning the same length again hands out the
  * same pages in the same order), and its length becomes 0. Entries outside

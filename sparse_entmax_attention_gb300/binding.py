@@ -36,7 +36,8 @@ EXPORTS = ("entmaxkv_version", "entmaxkv_status_string", "entmaxkv_append",
            "entmaxkv_workspace_layout", "entmaxkv_noalloc_scratch_bytes",
            "entmaxkv_decode_softmax_noalloc", "entmaxkv_workspace_bytes_flags",
            "entmaxkv_delta_kind", "entmaxkv_read_status", "entmaxkv_gaussian_alpha_supported",
-           "entmaxkv_moment_fit_eval", "entmaxkv_plan_pages", "entmaxkv_release_pages",
+           "entmaxkv_moment_fit_eval", "entmaxkv_plan_pages", "entmaxkv_plan_pages_bounded",
+           "entmaxkv_release_pages",
            "entmaxkv_append_q8", "entmaxkv_read_q8", "entmaxkv_attend_q8_workspace",
            "entmaxkv_attend_q8")
 STAGE_EVENTS = 6
@@ -137,6 +138,8 @@ def lib() -> ctypes.CDLL:
     bat_p, row_p = ctypes.POINTER(BatchView), ctypes.POINTER(RowsView)
     L.entmaxkv_plan_pages.restype = i32
     L.entmaxkv_plan_pages.argtypes = [cfg_p, vp, vp, vp, vp, vp, i32, i32] + [vp] * 9
+    L.entmaxkv_plan_pages_bounded.restype = i32
+    L.entmaxkv_plan_pages_bounded.argtypes = [cfg_p, vp, vp, vp, vp, vp, i32, i32, i32] + [vp] * 9
     L.entmaxkv_release_pages.restype = i32
     L.entmaxkv_release_pages.argtypes = [cfg_p, vp, vp, vp, vp, i32, vp, vp, vp]
     L.entmaxkv_append_q8.restype = i32
@@ -584,9 +587,11 @@ def alloc_plan(n_seqs, total, device="cuda") -> PagePlan:
 
 
 def plan_pages(cache, pool: PagePool, n_new, plan: PagePlan, seq_ids=None, advance=True, lens_out=None,
-               count_out=None, stream=None) -> PagePlan:
-    """entmaxkv_plan_pages: pages, positions and slots for n_new[b] more tokens of each sequence.
+               count_out=None, stream=None, max_count=0) -> PagePlan:
+    """entmaxkv_plan_pages_bounded: pages, positions and slots for n_new[b] more tokens of each sequence.
 
+    max_count: the bound of the batch that comes next (append_q8, attend_q8); a slot with more new
+    tokens is refused here, as it would be there. 0: none.
     cache: a QuantCache, a PagedCache or a PageTable. With advance the lengths count the new
     tokens in (into lens_out when given, else in place); a PagedCache, whose append counts them
     itself, is planned with advance=False. The free list's new height goes to count_out, or in place.
@@ -605,9 +610,9 @@ def plan_pages(cache, pool: PagePool, n_new, plan: PagePlan, seq_ids=None, advan
         to = lens_p
     else:
         to = _i32(lens_out, lens.shape, dev, "lens_out")
-    _q8_call(dev, stream, lib().entmaxkv_plan_pages, cfg, table.data_ptr(), lens_p, cache.status.data_ptr(),
+    _q8_call(dev, stream, lib().entmaxkv_plan_pages_bounded, cfg, table.data_ptr(), lens_p, cache.status.data_ptr(),
              None if seq_ids is None else _i32(seq_ids, (n,), dev, "seq_ids"), _i32(n_new, (n,), dev, "n_new"), n,
-             plan._total, pool._pages, pool._count,
+             plan._total, int(max_count), pool._pages, pool._count,
              pool._count if count_out is None else _i32(count_out, (1,), dev, "count_out"), to, start, count,
              positions, slots)
     return plan
@@ -773,6 +778,8 @@ class QuantStep:
     run(n_new, seq_ids, q, k, v): n_new and seq_ids int32 [n_seqs] (a slot with n_new 0 is idle),
     q, k, v the new tokens' rows one slot behind the other, in the first sum(n_new) rows of at most
     n_seqs * max_count. Rows past the last token, and those of refused slots, are left as they were.
+    A slot with more than max_count tokens is refused (DEV_BAD_BATCH): its sequence, pages and the pool
+    stay as they were.
     Capturing launches nothing: the cache changes only on replay."""
 
     def __init__(self, cache: QuantCache, pool: PagePool, n_seqs, max_count=1, alpha=1.0, **score):
@@ -792,7 +799,7 @@ class QuantStep:
         self._score = dict(score, alpha=alpha)
 
         def launches():
-            plan_pages(cache, pool, self.n_new, self.plan, seq_ids=self.seq_ids)
+            plan_pages(cache, pool, self.n_new, self.plan, seq_ids=self.seq_ids, max_count=max_count)
             append_q8(cache, self.k, self.v, self.batch)
             attend_q8(cache, self.q, self.batch, workspace=self.workspace, outputs=self.outputs, **self._score)
 

@@ -20,7 +20,7 @@ namespace ekv {
 constexpr int kPlanThreads = 1024;
 
 struct PlanArgs {
-  int P, maxp, nphys, max_seqs, n_seqs, total;
+  int P, maxp, nphys, max_seqs, n_seqs, total, max_count;
   int32_t* block_table;
   const int32_t* seq_lens;
   uint32_t* status;
@@ -105,7 +105,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanArgs a) {
         n = 0;
         bad = true;
       }
-      if (n > 0) {
+      if (n > a.max_count) {  // its rows keep their places, as a refused slot's do
+        raise_flag(status, ENTMAXKV_DEV_BAD_BATCH);
+        bad = true;
+      } else if (n > 0) {
         seq = seq_row(a.seq_ids, i, a.max_seqs, status);
         if (seq >= 0) {
           L = a.seq_lens[seq];
@@ -237,12 +240,13 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 cudaError_t launch_plan(const entmaxkv_config& cfg, int32_t* block_table, const int32_t* seq_lens, uint32_t* status,
-                        const int32_t* seq_ids, const int32_t* n_new, int n_seqs, int total, const int32_t* free_pages,
-                        const int32_t* free_count, int32_t* free_count_out, int32_t* lens_out, int32_t* start,
-                        int32_t* count, int32_t* positions, int64_t* slots, cudaStream_t st) {
-  PlanArgs a{cfg.page_size, cfg.max_pages_per_seq, cfg.num_phys_pages, cfg.max_seqs, n_seqs, total, block_table,
-             seq_lens, status, seq_ids, n_new, free_pages, free_count, free_count_out, lens_out, start, count,
-             positions, slots};
+                        const int32_t* seq_ids, const int32_t* n_new, int n_seqs, int total, int max_count,
+                        const int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out,
+                        int32_t* lens_out, int32_t* start, int32_t* count, int32_t* positions, int64_t* slots,
+                        cudaStream_t st) {
+  PlanArgs a{cfg.page_size, cfg.max_pages_per_seq, cfg.num_phys_pages, cfg.max_seqs, n_seqs, total, max_count,
+             block_table, seq_lens, status, seq_ids, n_new, free_pages, free_count, free_count_out, lens_out, start,
+             count, positions, slots};
   // four tokens a thread, up to the eight blocks of a portable cluster (a queue of 333 prompts, 38000 tokens: 10.5 us,
   // 39 with one block; a decode step of 64 sequences has one)
   const int blocks = total > 4 * kPlanThreads ? 8 : total > kPlanThreads ? 2 : 1;

@@ -172,9 +172,10 @@ struct Q8AttendArgs {
 };
 
 cudaError_t launch_plan(const entmaxkv_config& cfg, int32_t* block_table, const int32_t* seq_lens, uint32_t* status,
-                        const int32_t* seq_ids, const int32_t* n_new, int n_seqs, int total, const int32_t* free_pages,
-                        const int32_t* free_count, int32_t* free_count_out, int32_t* lens_out, int32_t* start,
-                        int32_t* count, int32_t* positions, int64_t* slots, cudaStream_t st);
+                        const int32_t* seq_ids, const int32_t* n_new, int n_seqs, int total, int max_count,
+                        const int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out,
+                        int32_t* lens_out, int32_t* start, int32_t* count, int32_t* positions, int64_t* slots,
+                        cudaStream_t st);
 cudaError_t launch_release(const entmaxkv_config& cfg, const int32_t* block_table, int32_t* seq_lens, uint32_t* status,
                            const int32_t* seq_ids, int n_seqs, int32_t* free_pages, int32_t* free_count,
                            cudaStream_t st);

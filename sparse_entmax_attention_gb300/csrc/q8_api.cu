@@ -69,19 +69,30 @@ static int check_table(const entmaxkv_config* c) {
   return ENTMAXKV_OK;
 }
 
+int32_t entmaxkv_plan_pages_bounded(const entmaxkv_config* cfg, int32_t* block_table, const int32_t* seq_lens,
+                                    uint32_t* status, const int32_t* seq_ids, const int32_t* n_new, int32_t n_seqs,
+                                    int32_t total, int32_t max_count, const int32_t* free_pages,
+                                    const int32_t* free_count, int32_t* free_count_out, int32_t* lens_out,
+                                    int32_t* start, int32_t* count, int32_t* positions, int64_t* slots,
+                                    void* stream) {
+  const int st = check_table(cfg);
+  if (st) return st;
+  if (n_seqs < 0 || n_seqs > 65535 || total < 0 || max_count < 0) return ENTMAXKV_ERR_INVALID_ARG;
+  if (n_seqs == 0) return ENTMAXKV_OK;
+  if (!block_table || !seq_lens || !n_new || !free_pages || !free_count || !free_count_out || !start || !count)
+    return ENTMAXKV_ERR_INVALID_ARG;
+  return code_of(launch_plan(*cfg, block_table, seq_lens, status, seq_ids, n_new, n_seqs, total,
+                             max_count ? max_count : 0x7fffffff, free_pages, free_count, free_count_out, lens_out,
+                             start, count, positions, slots, (cudaStream_t)stream));
+}
+
 int32_t entmaxkv_plan_pages(const entmaxkv_config* cfg, int32_t* block_table, const int32_t* seq_lens,
                             uint32_t* status, const int32_t* seq_ids, const int32_t* n_new, int32_t n_seqs,
                             int32_t total, const int32_t* free_pages, const int32_t* free_count,
                             int32_t* free_count_out, int32_t* lens_out, int32_t* start, int32_t* count,
                             int32_t* positions, int64_t* slots, void* stream) {
-  const int st = check_table(cfg);
-  if (st) return st;
-  if (n_seqs < 0 || n_seqs > 65535 || total < 0) return ENTMAXKV_ERR_INVALID_ARG;
-  if (n_seqs == 0) return ENTMAXKV_OK;
-  if (!block_table || !seq_lens || !n_new || !free_pages || !free_count || !free_count_out || !start || !count)
-    return ENTMAXKV_ERR_INVALID_ARG;
-  return code_of(launch_plan(*cfg, block_table, seq_lens, status, seq_ids, n_new, n_seqs, total, free_pages, free_count,
-                             free_count_out, lens_out, start, count, positions, slots, (cudaStream_t)stream));
+  return entmaxkv_plan_pages_bounded(cfg, block_table, seq_lens, status, seq_ids, n_new, n_seqs, total, 0, free_pages,
+                                     free_count, free_count_out, lens_out, start, count, positions, slots, stream);
 }
 
 int32_t entmaxkv_release_pages(const entmaxkv_config* cfg, const int32_t* block_table, int32_t* seq_lens,

@@ -21,6 +21,13 @@ def cfg(pages=100):
     return B.Config(8, 4, 128, 32, 4, pages, 400, B.I8)
 
 
+def test_bounded_planning_checks_its_arguments(lib):
+    def plan(max_count, n=2, table=P256):
+        return lib.entmaxkv_plan_pages_bounded(cfg(), table, P256, None, None, P256, n, 4, max_count, P256, P256, P256,
+                                               None, P256, P256, None, None, None)
+    assert plan(-1) == 1 and plan(3, table=None) == 1 and plan(3, n=-1) == 1 and plan(3, n=0) == 0
+
+
 @pytest.mark.parametrize("alpha,pages,fine", [
     (1.0, 100, True), (1.0 + 2.0 ** -10, 100, True), (1.0 + 2.0 ** -11, 100, False), (1.25, 1 << 25, True),
     (4.0, 1 << 25, True), (5.5, 1 << 25, False),      # 2^30 keys: up to order 5

@@ -8,7 +8,7 @@ import torch
 
 from sparse_entmax_attention_gb300 import binding as B
 
-from q8_cases import batch_of, dense, empty_cache, filled
+from q8_cases import batch_of, check_attend, dense, empty_cache, filled, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -199,3 +199,60 @@ def test_decode_on_a_side_stream_makes_its_own_buffers_there():
     torch.cuda.synchronize()
     assert torch.equal(o.page_ids, want.page_ids) and torch.equal(o.n_sel, want.n_sel)
     torch.testing.assert_close(o.out, want.out, rtol=1e-5, atol=1e-5)  # (its sums' order is not fixed)
+
+
+@pytest.mark.parametrize("most,alpha,news", [(1, 1.5, [2, 0, 0, 0]), (1, 1.0, [0, 0, 3, 1]), (40, 1.0, [41, 0, 7, 0]),
+                                             (3, 1.0, [1, 4, 0, 2])])
+def test_a_step_refuses_a_slot_over_its_bound_and_leaves_its_sequence(most, alpha, news):
+    c = B.QuantCache(2, 4, 64, 16, 6, 20, 60, torch.int8)
+    pool = B.PagePool.full(60)
+    step = B.QuantStep(c, pool, 4, most, alpha=alpha)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    ids = [3, 1, 0, 5]
+
+    def run(counts):
+        n = min(sum(counts), 4 * most)
+        qkv = torch.randn(n, 12, 64, generator=gen, device="cuda").bfloat16()
+        return qkv[:, :8], step.run(i32(counts), i32(ids), qkv[:, :8], qkv[:, 8:10], qkv[:, 10:])
+
+    run([most] * 4)
+    lens, table, free = c.seq_lens.tolist(), c.block_table.clone(), pool.free_count.item()
+    codes = c.k_pool.clone()
+    assert c.device_status() == 0
+    q, o = run(news)
+    assert c.device_status() == B.DEV_BAD_BATCH
+    c.status.zero_()
+    fine = [n if n <= most else 0 for n in news]
+    for b, n in zip(ids, fine):
+        lens[b] += n
+    assert c.seq_lens.tolist() == lens and step.plan.count.tolist() == fine
+    used = sum(-(-x // 16) for x in lens)
+    assert pool.free_count.item() == 60 - used and free >= pool.free_count.item()
+    over = [b for b, n in zip(ids, news) if n > most]
+    assert torch.equal(c.block_table[over], table[over])
+    for b in over:
+        held = table[b, :-(-lens[b] // 16)].long()
+        assert torch.equal(c.k_pool[held], codes[held])
+    check_attend(c, q, fine, o, seq_ids=ids, alpha=alpha, start=step.plan.start.tolist())
+    q, o = run([1, 1, 1, 1])  # and the next step sees what was written alone
+    assert c.device_status() == 0
+    check_attend(c, q, [1] * 4, o, seq_ids=ids, alpha=alpha)
+
+
+def test_planning_with_a_bound_and_without():
+    def state():
+        t = B.PageTable(i32([[-1] * 8] * 3), i32([0, 5, 0]), 16, 20)
+        t.block_table[1, 0] = 19
+        return t, B.PagePool(torch.arange(19, dtype=torch.int32, device="cuda"), i32([19])), B.alloc_plan(3, 60)
+
+    t, pool, plan = state()
+    pool = B.PagePool(torch.cat([pool.free_pages, i32([0])]), pool.free_count)
+    B.plan_pages(t, pool, i32([17, 30, 4]), plan, max_count=17)
+    assert plan.start.tolist() == [0, 17, 47] and plan.count.tolist() == [17, 0, 4]
+    assert t.seq_lens.tolist() == [17, 5, 4] and pool.free_count.item() == 16
+    assert t.block_table[1].tolist() == [19] + [-1] * 7 and t.device_status() == B.DEV_BAD_BATCH
+    assert plan.positions.tolist() == list(range(17)) + [-1] * 30 + [0, 1, 2, 3] + [-1] * 9
+    t, pool, plan = state()
+    pool = B.PagePool(torch.cat([pool.free_pages, i32([0])]), pool.free_count)
+    B.plan_pages(t, pool, i32([17, 30, 4]), plan)
+    assert plan.count.tolist() == [17, 30, 4] and t.device_status() == 0
