@@ -1,4 +1,5 @@
-"""Order of accesses to other blocks' shared memory, read from the kernels' source.
+"""Order of accesses to shared memory that other blocks or warps write, read from the
+kernels' source.
 
 A block may write the shared memory of another block of its cluster only once
 that block is known to run, which a cluster barrier shows; and a block may not
@@ -51,3 +52,14 @@ def test_a_barrier_comes_before_the_first_remote_access(name, body):
 def test_entmax_finish_ends_behind_a_barrier():
     body = next(b for _, n, b in CASES if n == "ent_finish_kernel")
     assert list(BARRIER.finditer(body))[-1].start() > list(REMOTE.finditer(body))[-1].start()
+
+
+def test_page_facts_of_a_tile_are_handed_on_by_threads():
+    """In the chunk kernel the converters' plain stores of page facts reach the softmax warps through the issuing
+    thread: it waits for the converters' arrivals and then arrives itself, once a tile, at the barrier that the
+    softmax warps wait for (a commit's arrival alone says nothing of another thread's stores)."""
+    with open(os.path.join(CSRC, "q8_chunk.cuh")) as fh:
+        body = dict((n, b) for n, b in _kernels(fh.read()))["chunk_kernel"]
+    assert "mbar_init(&s_full[i][c], 1 + c)" in body
+    assert body.count("tm_commit(&s_full") == 1 and "if (c == 1) mbar_arrive(&s_full[hf][1]);" in body
+    assert body.index("meta[it & 3][") < body.index("mbar_arrive(&k_full[sg])") < body.index("wait_warp(&k_full[it & 1]")
