@@ -814,6 +814,10 @@ class QuantStep:
         """Device tensors in; the outputs (and plan) stay on the device."""
         rows = q.shape[0]
         _need(rows <= self.q.shape[0], "more rows than the step was made for")
+        for t, own, name in ((q, self.q, "q"), (k, self.k, "k"), (v, self.v, "v")):
+            _need(t.shape == (rows, *own.shape[1:]), f"{name}: rows of shape {(rows, *own.shape[1:])} are wanted")
+        for t, name in ((n_new, "n_new"), (seq_ids, "seq_ids")):
+            _need(t.shape == self.n_new.shape, f"{name}: a tensor of shape {tuple(self.n_new.shape)} is wanted")
         self.n_new.copy_(n_new, non_blocking=True)
         self.seq_ids.copy_(seq_ids, non_blocking=True)
         self.q[:rows].copy_(q, non_blocking=True)

@@ -239,6 +239,24 @@ def test_a_step_refuses_a_slot_over_its_bound_and_leaves_its_sequence(most, alph
     check_attend(c, q, [1] * 4, o, seq_ids=ids, alpha=alpha)
 
 
+def test_a_step_takes_rows_of_its_own_shapes_only():
+    """copy_ would repeat one row, head or value for all: refused before anything changes."""
+    c = B.QuantCache(2, 4, 64, 16, 3, 8, 20, torch.int8)
+    step = B.QuantStep(c, B.PagePool.full(20), 3, 2)
+    n, ids = i32([2, 1, 0]), i32([0, 1, 2])
+    r = lambda rows, heads, d=64: torch.randn(rows, heads, d, device="cuda").bfloat16()  # noqa: E731
+    q, k, v = r(3, 8), r(3, 2), r(3, 2)
+    for bad in ((n, ids, q, k[:1], v), (n, ids, q, k, v[0]), (n, ids, q[:, :1], k, v),
+                (n, ids, r(7, 8), r(7, 2), r(7, 2)), (n[:1], ids, q, k, v), (n, ids[:1], q, k, v),
+                (n, ids, q, r(3, 2, 1), v)):
+        with pytest.raises(B.EntmaxKVError):
+            step.run(*bad)
+    torch.cuda.synchronize()
+    assert c.seq_lens.tolist() == [0, 0, 0] and not step.k.any()
+    step.run(n, ids, q, k, v)
+    assert c.seq_lens.tolist() == [2, 1, 0] and torch.equal(step.k[:3], k)
+
+
 def test_planning_with_a_bound_and_without():
     def state():
         t = B.PageTable(i32([[-1] * 8] * 3), i32([0, 5, 0]), 16, 20)
