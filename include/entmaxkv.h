@@ -374,7 +374,8 @@ int32_t entmaxkv_decode_softmax_noalloc(const entmaxkv_config* cfg, const entmax
  * and attention over the cache. A serving step is plan, append, attend.
  *
  * A stored value is code * scale with one float32 scale for the K and one for
- * the V rows of each (physical page, KV head). The calls take an
+ * the V rows of each (physical page, KV head). A page belongs to one sequence
+ * (append rescales what it holds, release gives it back). The calls take an
  * entmaxkv_config whose kv_dtype is one of the code types below; the other
  * fields and their limits are those of the 16- and 32-bit cache, but a
  * sequence has at most 2^30 tokens.
@@ -441,7 +442,8 @@ typedef struct {
  * are taken in order, and a slot is admitted while the sum of the needs up to
  * and including its own is at most *free_count: the first that does not fit
  * stops those behind it. A slot with a bad row, a negative n_new or more tokens
- * than its block-table row holds is refused alone. Refusals raise
+ * than its block-table row holds is refused alone. Slots are distinct sequences.
+ * Refusals raise
  * ENTMAXKV_DEV_CAPACITY, _BAD_SEQ_ID or _BAD_BATCH. The i-th page handed out is
  * free_pages[*free_count - 1 - i].
  *   block_table   (in/out) the admitted slots' new entries are written
@@ -508,7 +510,8 @@ int32_t entmaxkv_append_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* 
                            void* stream);
 
 /*
- * Copy tokens out of the cache as bfloat16 (code * scale, rounded to nearest):
+ * Copy tokens out of the cache as bfloat16 (the float32 product code * scale,
+ * rounded to nearest):
  * slot b's rows are tokens first[b] .. first[b] + count[b] - 1 of its sequence.
  * A slot that asks for tokens outside [0, seq_lens) is flagged BAD_BATCH and
  * skipped. With head_stride = T*d and token_stride = d the rows are laid out
@@ -542,13 +545,19 @@ typedef struct {
   const int32_t* first_key;
 } entmaxkv_score;
 
-/* Bytes of device workspace entmaxkv_attend_q8 needs; 0 for invalid arguments. */
+/*
+ * Bytes of device workspace entmaxkv_attend_q8 needs; 0 for invalid arguments.
+ * With alpha > 1 it holds a float32 score for every key that n_seqs rows of the
+ * table have room for and every query head, whatever the sequences' lengths.
+ */
 size_t entmaxkv_attend_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, int32_t total,
                                     int32_t max_count, float alpha);
 
 /*
  * Attention of the batch's rows over their sequences in the cache.
- *   alpha = 1  softmax, any count: o = sum_j softmax(s)_j v_j; tau gets log sum exp(s)
+ *   alpha = 1  softmax, any count: o = sum_j softmax(s)_j v_j; tau gets log sum exp(s).
+ *              max_count chooses the kernel for all slots of a call: single tokens
+ *              beside a chunk of many are faster in a call of their own
  *   alpha > 1  alpha-entmax, max_count = 1: z = (alpha-1) s,
  *              p_j = [z_j - tau]_+^{1/(alpha-1)}, sum p = 1. The sum is brought to 1
  *              within 2^-14 + 2^-21 / (alpha-1), or DEV_TAU_NOCONV is raised (weights that

@@ -185,12 +185,14 @@ cudaError_t launch_read_q8(const Q8Cache& c, const Q8Batch& b, const int32_t* fi
                            bool i8, int sms, cudaStream_t st);
 size_t attend_softmax_bytes(const entmaxkv_config& cfg, int n_seqs);
 cudaError_t launch_attend_softmax(Q8AttendArgs a, bool i8, void* ws, int sms, cudaStream_t st);
-// Rows (tokens times the group) a sequence up to which the streaming kernel
-// answers a batch, 16 rows at a time; with more, one 128-row product tile is the
-// better fit for every slot. Measured, streaming against products, int8, 4 KV
+// Rows (tokens times the group) of a batch's largest slot up to which the
+// streaming kernel answers the batch, 16 rows at a time; with more, 128-row product
+// tiles do. Measured, streaming against products, batches of equal slots, int8, 4 KV
 // heads: 24 sequences of 6000 tokens at d = 128 46/99 us at 16 rows, 77/104 at 32,
 // 108/105 at 48, 137/105 at 64; 4 of 30000 (pages of 16) 46/95, 67/103, 94/104,
-// 117/107; 24 of 6000 at d = 64 36/62, 50/67, 68/66, 86/66.
+// 117/107; 24 of 6000 at d = 64 36/62, 50/67, 68/66, 86/66. A batch of unequal slots
+// is not split: 24 decodes of 4k-29k tokens (8 KV heads, d = 128) take 142 us and a
+// chunk of 1000 behind 8000 151 us, both in one call 576 us.
 constexpr int kStreamRows = 48;
 bool chunk_counts_fit(const entmaxkv_config& cfg, int n_seqs, int total);
 size_t attend_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total);

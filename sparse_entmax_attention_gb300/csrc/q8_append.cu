@@ -12,12 +12,13 @@
 // take that path only where some quotient lies near enough to a tie that the
 // fp32 one could round to another code.
 //
-// Bound: bytes for long prompts, and the instructions beside them (about 1600 a
-// page, KV head and side). A warp has one page at a time, its new rows in
+// Bound: the chain of a page from its load to its codes (about 1600 instructions a
+// page, KV head and side; no pipe is full), then the bytes. A warp has one page at a time, its new rows in
 // registers between the maximum and the codes, so they are read once. 32801
 // tokens, 8 KV heads, d = 128, int8 (134 MB in, 67 MB out): append 47-63 us,
-// read-back 38 us (5.3 TB/s); 64 sequences' single tokens: 13.4 us in all, of
-// which the bytes are 1.2. With the exact path unrolled in the loop the append
+// read-back 38 us (5.3 TB/s); 64 sequences' single tokens: 14 us in all, of
+// which the bytes are 1.2; past kPageSlots slots each warp walks the slots from the
+// first (333 single tokens: append 110 us, read-back 148; 250: 8.3 and 6.2). With the exact path unrolled in the loop the append
 // took 149 us, waiting for instructions.
 #include "q8_tiles.cuh"
 

@@ -10,7 +10,8 @@
 //   S = K·q^T      m16n8k16 in halves (codes are exact as halves; q is scaled
 //                  to exact halves), 16 tokens × 8 rows a product, fp32 sums;
 //   t = S·ks·scale·log2 e (capped, biased, masked) + log2 vs
-//   w = 2^{t − M + 8} as halves (2^-12), transposed in registers, M a bound of
+//   w = 2^{t − M + 8} as halves (off by 2^-11, an eighth of the bf16 output's
+//                  rounding; a second half would double the products), transposed in registers, M a bound of
 //                  the row's maximum that moves when a t passes it by 6 (a vote
 //                  a tile; the maximum itself is only formed then): w ≤ 2^14, and
 //                  weights down to 2^-32 of the largest survive the rounding;
@@ -21,11 +22,11 @@
 // and the rest leaves (M, Σp, acc) pieces which a second kernel joins in the
 // order of the line.
 //
-// Measured (graph replays): 16 sequences of 4-65k tokens, 8 KV heads of 4 query
-// heads, d = 128, e4m3, capped, with slopes (756 MB): 134 us, 5.6 TB/s,
+// Measured (graph replays, inputs in turn): 16 sequences of 4-65k tokens, 8 KV heads of 4 query
+// heads, d = 128, e4m3, capped, with slopes (756 MB): 135 us, 5.6 TB/s,
 // 0.83 of the measured copy rate. Time over bytes is 6.3 TB/s and 8-10 us for
 // start, block join and join kernel, which is what a single sequence of 32k
-// tokens (67 MB) feels: 22.5 us. In a capture (789 MB, 131 us) the pipes wait
+// tokens (67 MB) feels: 27.5 us (23.3 where L2 holds them). In a capture (789 MB, 131 us) the pipes wait
 // for nothing in particular: ALU 48% (codes to halves), IPC 2.2.
 #include "q8_tiles.cuh"
 

@@ -9,7 +9,8 @@
 //                      (both exact: a power of two per query row), fp32 sums in
 //                      tensor memory;
 //   t = S·ks·scale·log2 e (capped, biased, masked) + log2 vs, one row a thread;
-//   w = 2^{t − M + 8}  as halves into tensor memory over S, M a running bound of
+//   w = 2^{t − M + 8}  as halves (off by 2^-11, an eighth of the bf16 output's
+//                      rounding) into tensor memory over S, M a running bound of
 //                      the row's maximum that is moved when the maximum passes it
 //                      by 6: w ≤ 2^14, and weights down to 2^-32 of the largest
 //                      survive the rounding;
@@ -24,12 +25,12 @@
 // one block a multiprocessor; an item cut in two leaves (M, Σp, O) pieces that a
 // second kernel joins in the order of the line.
 //
-// Bound: the softmax warps, two a scheduler. Of a tile's 2600 cycles of products
+// Bound: the latency of the softmax warps, two a scheduler. Of a tile's 2600 cycles of products
 // (measured alone; 2050 in turns of 128 keys) the capped form takes about 5400:
 // fp32 pipe 44% busy, tensor pipe 37%, IPC 2.3, the rest the latency of each
 // row's chain (maxima in one chain instead of four: 8% slower). Measured, int8, 8
 // KV heads of 4 query heads, d = 128: 2048 tokens behind 30001, capped (1.04
-// TFLOP), 1.16 ms, 890 TFLOP/s; behind 8000 without a cap 302 us, 1010 TFLOP/s. One
+// TFLOP), 1.18 ms, 885 TFLOP/s; behind 8000 without a cap 289 us. One
 // thread that issued all products, and tiles in turns of 128 keys, took 1.54 ms:
 // issuing one costs a thread about 75 cycles, more than the product.
 #pragma once

@@ -13,11 +13,12 @@
 //    there are too many scores to hand round, a step's partial sums are instead,
 //    with a cluster barrier each.)
 //    Then V is read for tiles with some z above its head's τ only, weights
-//    rounded to halves against their tile's largest, and the blocks' sums are
+//    rounded to halves against their tile's largest (off by 2^-11, an eighth of the
+//    bf16 output's rounding), and the blocks' sums are
 //    added through the cluster. Every sum has a fixed order.
 //
 // Measured, 8 KV heads of 4 query heads, d = 128: 131072 tokens, int8, slopes,
-// alpha 1.5: 53 us, of which scoring is 33 (134 MB of K at 4.1 TB/s; the floor is
+// alpha 1.5: 56.6 us, of which scoring is 33 (134 MB of K at 4.1 TB/s; the floor is
 // 20): turning codes into halves bounds it (ALU 49%, IPC 2.3, DRAM 53%), 16 and
 // 24 warps alike. The rest is a chain of short phases, most of each the fetch of
 // its instructions. 16 sequences of 1-32k tokens, e4m3, alpha 2: 64 us. Dense
