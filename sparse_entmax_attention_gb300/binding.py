@@ -560,7 +560,7 @@ class Batch:
     @classmethod
     def uniform(cls, n_seqs, count=1, seq_ids=None, device="cuda"):
         """count rows of every sequence, one sequence behind the other."""
-        start = torch.arange(0, n_seqs * count, max(count, 1), dtype=torch.int32, device=device)
+        start = torch.arange(n_seqs, dtype=torch.int32, device=device) * count
         return cls(start, torch.full_like(start, count), n_seqs * count, count, seq_ids)
 
 

@@ -3,6 +3,7 @@
 import os
 
 import pytest
+import torch
 
 from sparse_entmax_attention_gb300 import binding as B
 
@@ -40,3 +41,11 @@ def test_orders_that_cannot_be_solved_are_refused(lib, alpha, pages, fine):
     rows = B.RowsView(P256, 4096, 128)
     code = lib.entmaxkv_attend_q8(c, view, batch, rows, None, alpha, P256, 1 << 50, rows, None, None)
     assert code == (0 if fine else 2)
+
+
+@pytest.mark.parametrize("n,count", [(0, 1), (1, 1), (3, 0), (5, 4)])
+def test_a_uniform_batch_has_every_slot(n, count):
+    b = B.Batch.uniform(n, count, device="cpu")
+    assert b.start.tolist() == [i * count for i in range(n)] and b.count.tolist() == [count] * n
+    assert (b.total, b.max_count, b.view.n_seqs) == (n * count, count, n)
+    assert b.start.dtype == b.count.dtype == torch.int32
