@@ -578,7 +578,9 @@ size_t entmaxkv_attend_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, 
  * their 32 keys (entmax). Query rows are exact down to 2^-27 of their head's
  * largest value; an infinity or NaN in q makes out and tau NaN for its own row
  * and head, if that sees a key, and touches no other. Scales of pages in use are
- * positive and finite and their codes finite, as append leaves them. The
+ * positive and finite and their codes finite, as append leaves them; a softmax
+ * weight is formed times its page's V scale, and vanishes beside a page whose
+ * scale is more than 2^110 times as large. The
  * order of every sum is fixed by the arguments and the device, so equal calls
  * give equal bits. Rows of a slot with a bad row or batch entry are left as
  * they were. Refused (ENTMAXKV_ERR_UNSUPPORTED): batches of several tokens a
