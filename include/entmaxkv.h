@@ -592,6 +592,89 @@ int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* 
                            const entmaxkv_score* score, float alpha, void* workspace,
                            size_t workspace_bytes, const entmaxkv_rows* out, float* tau, void* stream);
 
+/*
+ * Differential attention: query heads 2i and 2i+1 (of one KV head: cfg->group is
+ * even, else ENTMAXKV_ERR_UNSUPPORTED) are a pair, whose answer is the difference
+ * of their two softmax maps times V,
+ *   y = softmax(s_2i) V - lam * softmax(s_2i+1) V,
+ * and with a gain y / sqrt(mean(y^2) + eps) * gain over its head_dim values. Sums,
+ * difference and norm are float32, rounded once, to bfloat16; the rest is as for
+ * attend_q8 with alpha = 1, workspace included.
+ *   lam   (device) float32, pair i of row t takes lam[t * lam_stride + i]; a
+ *         stride of 0 gives all rows the same Hq/2 factors. Finite
+ *   gain  (device) [head_dim] float32, or NULL for no norm. eps: at least 2^-100
+ *   out   bfloat16 rows, Hq/2 heads; a row that sees no key gets 0
+ *   tau   [total][Hq] float32 of both maps, or NULL; NaN for a row that sees no key
+ * A pair whose maps have keys of their own (and V rows twice as wide as these)
+ * keeps both keys one behind the other as one K row: q_2i with zeros behind it,
+ * q_2i+1 with zeros in front, and `scale` of the single key's width.
+ */
+int32_t entmaxkv_attend_diff_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache,
+                                const entmaxkv_batch* batch, const entmaxkv_rows* q, const entmaxkv_score* score,
+                                const float* lam, int64_t lam_stride, const float* gain, float eps, void* workspace,
+                                size_t workspace_bytes, const entmaxkv_rows* out, float* tau, void* stream);
+
+/*
+ * What the batch's rows give to the keys, added to what those gathered before:
+ *   w_j = decay * w_j + sum over the slot's rows and a KV head's query heads of coef * p_j,
+ *   p_j = e^(s_j - tau)                              (alpha = 1)
+ *   p_j = [(alpha-1) s_j - tau]_+^(1/(alpha-1))      (alpha > 1, max_count = 1)
+ * with the scores s_j and masks of attend_q8 (same score, alpha and limits). The
+ * rows are a slot's last count[b] tokens; those of a long prompt's last piece
+ * alone will do (`fresh` then is the whole prompt).
+ *   tau      (device) [total][Hq] float32, as attend_q8 or attend_diff_q8 wrote it;
+ *            a row and head whose tau is not finite (it saw no key) adds nothing
+ *   coef     (device) [total][Hq] float32 factors, or NULL: 1. Those that are not
+ *            above 0 count as 0. (1 and lam for the two maps of a pair weigh keys
+ *            by a bound of the difference's.)
+ *   decay    at least 0; with 0 what was gathered is not read
+ *   fresh    (device) [n_seqs] int32: a sequence's last fresh[b] keys gathered
+ *            nothing before, whatever lies in `weights`; NULL: its count[b] rows
+ *   weights  (device, in/out) [num_phys_pages][num_kv_heads][page_size] float32: a key's
+ *            weight lies as its codes do. Places behind a sequence's last key, and
+ *            with decay = 1 keys that no row may see, are left as they were
+ *   workspace  (device) at least entmaxkv_weigh_q8_workspace(...) bytes, 256-byte
+ *            aligned, contents are scratch; not to be shared by calls that may run
+ *            at the same time
+ * Sums are float32 in an order that the arguments and the device fix.
+ */
+size_t entmaxkv_weigh_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, int32_t total,
+                                   int32_t max_count, float alpha);
+int32_t entmaxkv_weigh_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache,
+                          const entmaxkv_batch* batch, const entmaxkv_rows* q, const float* tau,
+                          const entmaxkv_score* score, float alpha, const float* coef, float decay,
+                          const int32_t* fresh, float* weights, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
+ * Shorten each sequence of more than `above` tokens to `keep`: in each KV head for
+ * itself its first `sinks` keys stay, its last `recent`, and the heaviest of the
+ * others by `weights` (ties: the lower index; NaN counts as the largest). They move
+ * to the front of the sequence's pages in their order, codes, scales and weights:
+ *   a page's scale becomes the largest of the scales of the pages its keys come
+ *   from, and a code v the code nearest to the exact v * r, r = s / s' rounded to
+ *   float32, ties to even (K and V apart, as append_q8 rescales).
+ * Its pages past the first ceil(keep / page_size) go on the free list, slots in order
+ * and a sequence's last page first; their block-table entries are left. Later
+ * calls take a key's place among the kept ones for its position (windows, slopes).
+ * A slot with a bad row, named a second time or with a page outside the pool is
+ * left as it was (ENTMAXKV_DEV_BAD_SEQ_ID, _BAD_BATCH, _BAD_PAGE_TABLE); a list that
+ * would pass num_phys_pages raises ENTMAXKV_DEV_CAPACITY and takes no more.
+ * Refused (ENTMAXKV_ERR_INVALID_ARG): above < keep, keep < 1 or more than a row of the table
+ * holds, sinks + recent > keep.
+ *   weights      as weigh_q8 writes them; NULL where sinks + recent = keep
+ *   weights_out  may be weights; otherwise only the evicted sequences' kept places are written
+ *   lens_out     [max_seqs] evicted rows get `keep`, others are left; may be cache->seq_lens
+ *   free_pages   [num_phys_pages] the stack; free_count_out may be free_count
+ *   workspace    (device) at least entmaxkv_evict_q8_workspace(...) bytes, as above
+ */
+size_t entmaxkv_evict_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, int32_t keep);
+int32_t entmaxkv_evict_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache, const float* weights,
+                          const int32_t* seq_ids, int32_t n_seqs, int32_t keep, int32_t above, int32_t sinks,
+                          int32_t recent, float* weights_out, int32_t* lens_out, int32_t* free_pages,
+                          const int32_t* free_count, int32_t* free_count_out, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -141,3 +141,44 @@ def attend(K, V, Q, alpha=1.0, scale=0.0, softcap=0.0, slope=0.0, window=0, pref
         if idx.size:
             P[i, idx], tau[i] = em.softmax(s[i, idx]) if alpha == 1.0 else em.entmax(s[i, idx], alpha)
     return P @ V, tau, P, np.where(see, s, -np.inf)
+
+
+def difference(o0, o1, lam, gain=None, eps=0.0):
+    """Of one pair's rows [count, d] and factors lam [count]: the difference, normalised over its head with a gain."""
+    y = np.asarray(o0, np.float64) - np.asarray(lam, np.float64)[:, None] * np.asarray(o1, np.float64)
+    if gain is None:
+        return y
+    return y / np.sqrt((y * y).mean(-1, keepdims=True) + eps) * np.asarray(gain, np.float64)
+
+
+def key_weights(scores, tau, alpha=1.0):
+    """[count, L] the weight that each row gives each key, from scores (minus infinity where a key is not seen) and the
+    rows' statistics; rows whose statistic is not finite give nothing."""
+    scores, tau = np.asarray(scores, np.float64), np.asarray(tau, np.float64)[:, None]
+    fine = np.isfinite(tau) & np.isfinite(scores)
+    x = np.where(fine, scores, 0.0) * (alpha - 1.0 if alpha != 1.0 else 1.0) - np.where(np.isfinite(tau), tau, 0.0)
+    p = np.exp(np.where(fine, x, 0.0)) if alpha == 1.0 else np.maximum(x, 0.0) ** (1.0 / (alpha - 1.0))
+    return np.where(fine, p, 0.0)
+
+
+def kept_keys(w, keep, sinks=0, recent=0):
+    """Of one KV head's weights [L]: the `keep` keys that stay, ascending."""
+    L = len(w)
+    if L <= keep:
+        return list(range(L))
+    rank = [math.inf if math.isnan(x) else float(x) for x in w]
+    inner = sorted(range(sinks, L - recent), key=lambda j: (-rank[j], not math.isnan(w[j]), j))
+    return sorted(list(range(sinks)) + inner[:keep - sinks - recent] + list(range(L - recent, L)))
+
+
+def evict_rows(codes, scales, kept, page, code):
+    """codes [L, d] of one (sequence, KV head, side), the scale of each key's page [L]: the kept keys' codes and the
+    scales of the pages that they fill, in their order."""
+    out, now = [], []
+    for p0 in range(0, len(kept), page):
+        src = kept[p0:p0 + page]
+        s = max(float(scales[j]) for j in src)
+        now.append(s)
+        out += [nearest(np.asarray(codes[j], np.float64) * float(np.float32(np.float32(scales[j]) / np.float32(s))), code)
+                for j in src]
+    return np.array(out), now

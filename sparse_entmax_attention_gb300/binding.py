@@ -39,7 +39,8 @@ EXPORTS = ("entmaxkv_version", "entmaxkv_status_string", "entmaxkv_append",
            "entmaxkv_moment_fit_eval", "entmaxkv_plan_pages", "entmaxkv_plan_pages_bounded",
            "entmaxkv_release_pages",
            "entmaxkv_append_q8", "entmaxkv_read_q8", "entmaxkv_attend_q8_workspace",
-           "entmaxkv_attend_q8")
+           "entmaxkv_attend_q8", "entmaxkv_attend_diff_q8", "entmaxkv_weigh_q8_workspace",
+           "entmaxkv_weigh_q8", "entmaxkv_evict_q8_workspace", "entmaxkv_evict_q8")
 STAGE_EVENTS = 6
 STAGES = ("clear", "score", "select", "pass_a", "pass_b")
 
@@ -151,6 +152,18 @@ def lib() -> ctypes.CDLL:
     L.entmaxkv_attend_q8.restype = i32
     L.entmaxkv_attend_q8.argtypes = [cfg_p, q8_p, bat_p, row_p, ctypes.POINTER(ScoreView), f32, vp, sz,
                                      row_p, vp, vp]
+    L.entmaxkv_attend_diff_q8.restype = i32
+    L.entmaxkv_attend_diff_q8.argtypes = [cfg_p, q8_p, bat_p, row_p, ctypes.POINTER(ScoreView), vp, ctypes.c_int64,
+                                          vp, f32, vp, sz, row_p, vp, vp]
+    L.entmaxkv_weigh_q8_workspace.restype = sz
+    L.entmaxkv_weigh_q8_workspace.argtypes = [cfg_p, i32, i32, i32, f32]
+    L.entmaxkv_weigh_q8.restype = i32
+    L.entmaxkv_weigh_q8.argtypes = [cfg_p, q8_p, bat_p, row_p, vp, ctypes.POINTER(ScoreView), f32, vp, f32, vp, vp, vp,
+                                    sz, vp]
+    L.entmaxkv_evict_q8_workspace.restype = sz
+    L.entmaxkv_evict_q8_workspace.argtypes = [cfg_p, i32, i32]
+    L.entmaxkv_evict_q8.restype = i32
+    L.entmaxkv_evict_q8.argtypes = [cfg_p, q8_p, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -728,6 +741,26 @@ def alloc_attend_workspace(cache: QuantCache, batch: Batch, alpha=1.0):
     return torch.empty(n, dtype=torch.uint8, device=cache.device)  # caching allocator: 256-B aligned
 
 
+def _f32(t, shape, dev, name):
+    """The pointer of a contiguous float32 tensor of this shape on device number `dev`."""
+    if t.dtype is not _F32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise EntmaxKVError(f"{name}: a contiguous float32 tensor of shape {tuple(shape)} on device {dev} is wanted")
+    return t.data_ptr()
+
+
+def _score(batch, dev, Hq, scale, softcap, slopes, window, prefix, first_key):
+    score = ScoreView(scale, softcap, window, None, None, None)
+    if slopes is not None:
+        if slopes.dtype is not _F32 or slopes.shape != (Hq,) or not slopes.is_contiguous() or slopes.get_device() != dev:
+            raise EntmaxKVError("slopes: contiguous float32 [Hq] is wanted")
+        score.slopes = slopes.data_ptr()
+    if prefix is not None:
+        score.prefix = _i32(prefix, (batch._n,), dev, "prefix")
+    if first_key is not None:
+        score.first_key = _i32(first_key, (batch.total,), dev, "first_key")
+    return score
+
+
 def attend_q8(cache: QuantCache, q, batch: Batch, alpha=1.0, scale=0.0, softcap=0.0, slopes=None, window=0,
               prefix=None, first_key=None, workspace=None, outputs: AttendOutputs | None = None,
               stream=None) -> AttendOutputs:
@@ -752,15 +785,7 @@ def attend_q8(cache: QuantCache, q, batch: Batch, alpha=1.0, scale=0.0, softcap=
                 workspace = alloc_attend_workspace(cache, batch, alpha)
         if made:
             _for_caller(stream, outputs.out, outputs.tau)
-    score = ScoreView(scale, softcap, window, None, None, None)
-    if slopes is not None:
-        if slopes.dtype is not _F32 or slopes.shape != (Hq,) or not slopes.is_contiguous() or slopes.get_device() != dev:
-            raise EntmaxKVError("slopes: contiguous float32 [Hq] is wanted")
-        score.slopes = slopes.data_ptr()
-    if prefix is not None:
-        score.prefix = _i32(prefix, (batch._n,), dev, "prefix")
-    if first_key is not None:
-        score.first_key = _i32(first_key, (batch.total,), dev, "first_key")
+    score = _score(batch, dev, Hq, scale, softcap, slopes, window, prefix, first_key)
     t = outputs.tau
     if t is not None and (t.dtype is not _F32 or t.shape != shape[:2] or not t.is_contiguous() or t.get_device() != dev):
         raise EntmaxKVError("tau: contiguous float32 [total, Hq] is wanted")
@@ -768,6 +793,127 @@ def attend_q8(cache: QuantCache, q, batch: Batch, alpha=1.0, scale=0.0, softcap=
              score, alpha, workspace.data_ptr(), workspace.nbytes, _rows(outputs.out, shape, dev, "out"),
              None if t is None else t.data_ptr())
     return outputs
+
+
+def alloc_diff_outputs(cache: QuantCache, batch: Batch) -> AttendOutputs:
+    Hq = cache.num_q_heads
+    return AttendOutputs(torch.zeros(batch.total, Hq // 2, cache.cfg.head_dim, dtype=torch.bfloat16, device=cache.device),
+                         torch.zeros(batch.total, Hq, dtype=torch.float32, device=cache.device))
+
+
+def attend_diff_q8(cache: QuantCache, q, lam, batch: Batch, scale=0.0, softcap=0.0, slopes=None, window=0, prefix=None,
+                   first_key=None, gain=None, eps=1e-5, workspace=None, outputs: AttendOutputs | None = None,
+                   stream=None) -> AttendOutputs:
+    """entmaxkv_attend_diff_q8: differential attention. Query heads 2i and 2i+1 of q [total, Hq, d] bf16 (an even
+    group) give out[:, i] = softmax_2i V - lam * softmax_2i+1 V, [total, Hq/2, d] bf16; tau [total, Hq] holds both
+    maps' log-sum-exp.
+
+    lam: float32 [Hq/2], or [total, Hq/2] for a factor of every row's own. gain: float32 [d], the difference is
+    normalised over its head: y / sqrt(mean(y^2) + eps) * gain. The workspace is alloc_attend_workspace's; masks,
+    scores, workspace and outputs are as for attend_q8.
+    """
+    dev, Hq, d = _on_cache(cache, batch), cache.num_q_heads, cache.cfg.head_dim
+    if cache.cfg.group % 2:
+        raise EntmaxKVError("differential attention pairs the query heads of a KV head: an even group is wanted")
+    if workspace is not None and workspace.get_device() != dev:
+        raise EntmaxKVError("workspace: on another device than the cache")
+    each = lam.dim() == 2
+    lam_p = _f32(lam, (batch.total, Hq // 2) if each else (Hq // 2,), dev, "lam")
+    gain_p = None if gain is None else _f32(gain, (d,), dev, "gain")
+    score = _score(batch, dev, Hq, scale, softcap, slopes, window, prefix, first_key)
+    made = outputs is None
+    if made or workspace is None:
+        with _allocating(stream):
+            if made:
+                outputs = alloc_diff_outputs(cache, batch)
+            if workspace is None:
+                workspace = alloc_attend_workspace(cache, batch)
+        if made:
+            _for_caller(stream, outputs.out, outputs.tau)
+    t = outputs.tau
+    _q8_call(dev, stream, lib().entmaxkv_attend_diff_q8, cache.cfg, cache.view, batch.view,
+             _rows(q, (batch.total, Hq, d), dev, "q"), score, lam_p, Hq // 2 if each else 0, gain_p, eps,
+             workspace.data_ptr(), workspace.nbytes, _rows(outputs.out, (batch.total, Hq // 2, d), dev, "out"),
+             None if t is None else _f32(t, (batch.total, Hq), dev, "tau"))
+    return outputs
+
+
+def alloc_weights(cache: QuantCache):
+    """What keys gather, beside their codes: float32 [num_phys_pages, num_kv_heads, page_size], zeros."""
+    c = cache.cfg
+    return torch.zeros(c.num_phys_pages, c.num_kv_heads, c.page_size, dtype=torch.float32, device=cache.device)
+
+
+def _weights(cache, t, name="weights"):
+    c = cache.cfg
+    return _f32(t, (c.num_phys_pages, c.num_kv_heads, c.page_size), cache._dev, name)
+
+
+def alloc_weigh_workspace(cache: QuantCache, batch: Batch, alpha=1.0):
+    b = batch.view
+    n = int(lib().entmaxkv_weigh_q8_workspace(cache.cfg, b.n_seqs, b.total, b.max_count, float(alpha)))
+    if n == 0:
+        raise EntmaxKVError("invalid arguments for workspace sizing")
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def weigh_q8(cache: QuantCache, weights, q, tau, batch: Batch, alpha=1.0, scale=0.0, softcap=0.0, slopes=None, window=0,
+             prefix=None, first_key=None, coef=None, decay=1.0, fresh=None, workspace=None, stream=None):
+    """entmaxkv_weigh_q8: weights (alloc_weights) become decay * weights + what the batch's rows q [total, Hq, d] bf16
+    give to each key, summed over rows and the group's heads. tau [total, Hq] is what attend_q8 (same alpha, scores
+    and masks) or attend_diff_q8 left for these rows. Returns weights.
+
+    coef: float32 [total, Hq] factors at least 0. fresh: int32 [n_seqs], a sequence's last keys that gathered nothing
+    before (by default its rows in the batch: weigh what was appended). A workspace that is not given is allocated on
+    the call's stream.
+    """
+    dev, Hq = _on_cache(cache, batch), cache.num_q_heads
+    heads = (batch.total, Hq)
+    if workspace is not None and workspace.get_device() != dev:
+        raise EntmaxKVError("workspace: on another device than the cache")
+    score = _score(batch, dev, Hq, scale, softcap, slopes, window, prefix, first_key)
+    args = (_rows(q, (*heads, cache.cfg.head_dim), dev, "q"), _f32(tau, heads, dev, "tau"), score, alpha,
+            None if coef is None else _f32(coef, heads, dev, "coef"), decay,
+            None if fresh is None else _i32(fresh, (batch._n,), dev, "fresh"), _weights(cache, weights))
+    if workspace is None:
+        with _allocating(stream):
+            workspace = alloc_weigh_workspace(cache, batch, alpha)
+    _q8_call(dev, stream, lib().entmaxkv_weigh_q8, cache.cfg, cache.view, batch.view, *args, workspace.data_ptr(),
+             workspace.nbytes)
+    return weights
+
+
+def alloc_evict_workspace(cache: QuantCache, n_seqs, keep):
+    n = int(lib().entmaxkv_evict_q8_workspace(cache.cfg, int(n_seqs), int(keep)))
+    if n == 0:
+        raise EntmaxKVError("invalid arguments for workspace sizing")
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def evict_q8(cache: QuantCache, pool: PagePool, weights, seq_ids, keep, above=0, sinks=0, recent=0, lens_out=None,
+             count_out=None, weights_out=None, workspace=None, stream=None):
+    """entmaxkv_evict_q8: each of the sequences seq_ids (int32) with more than `above` tokens (0: keep) is shortened to
+    `keep`: in every KV head its first `sinks`, its last `recent` and the heaviest of the others by weights stay, in
+    their order, and pages that are left over go back to the pool. weights may be None where sinks + recent = keep.
+
+    Lengths, the free list's height and weights change in place, or go to lens_out, count_out and weights_out. A
+    workspace that is not given is allocated on the call's stream.
+    """
+    dev, n = cache._dev, seq_ids.shape[0]
+    if pool._dev != dev or (workspace is not None and workspace.get_device() != dev):
+        raise EntmaxKVError("cache, pool and workspace: on one device are wanted")
+    _need(pool._n >= cache.cfg.num_phys_pages, "pool: a free list of num_phys_pages entries is wanted")
+    _need(weights is not None or weights_out is None, "weights_out: without weights")
+    lens = cache.seq_lens
+    w_in = None if weights is None else _weights(cache, weights)
+    args = (w_in, _i32(seq_ids, (n,), dev, "seq_ids"), n, int(keep), int(above) or int(keep), int(sinks), int(recent),
+            w_in if weights_out is None else _weights(cache, weights_out, "weights_out"),
+            lens.data_ptr() if lens_out is None else _i32(lens_out, lens.shape, dev, "lens_out"), pool._pages, pool._count,
+            pool._count if count_out is None else _i32(count_out, (1,), dev, "count_out"))
+    if workspace is None:
+        with _allocating(stream):
+            workspace = alloc_evict_workspace(cache, n, keep)
+    _q8_call(dev, stream, lib().entmaxkv_evict_q8, cache.cfg, cache.view, *args, workspace.data_ptr(), workspace.nbytes)
 
 
 class QuantStep:

@@ -163,12 +163,38 @@ struct Q8AttendArgs {
   Q8Score sc;
   Q8Rows q, out;
   float* tau;
+  // differential attention (lam not null): out has a head a pair of query heads, their difference
+  const float* lam;   // factor of pair i in row t: lam[t·lam_ts + i]
+  long long lam_ts;
+  const float* gain;  // [D] of the difference's norm over its head, or null: none
+  float eps;
   // workspace
   long long* cum;   // [n_seqs + 1] tiles before each slot
   void* slots;      // [n_seqs] what the streaming kernel made of each slot
   float* part_o;    // [blocks][2][rows][D]
   float* part_ml;   // [blocks][2][rows][2] running max (base 2) and sum
   int blocks;
+};
+
+// o0·i0 − o1·i1, both products rounded: equal maps with a factor of 1 cancel to 0.
+__device__ __forceinline__ float diff_of(float o0, float i0, float o1, float i1) {
+  return __fsub_rn(__fmul_rn(o0, i0), __fmul_rn(o1, i1));
+}
+// What a pair's difference y is multiplied by, dim by dim gain's: 1/√(mean y² + ε), from Σ y².
+__device__ __forceinline__ float diff_norm(const Q8AttendArgs& a, float sum2) {
+  return rsqrtf(fmaf(sum2, 1.0f / (float)a.c.D, a.eps));
+}
+
+struct Q8WeighArgs {
+  Q8Cache c;
+  Q8Batch b;
+  Q8Score sc;
+  Q8Rows q;
+  const float* tau;      // [total][Hq]
+  const float* coef;     // [total][Hq], or null: 1
+  const int32_t* fresh;  // [n_seqs] last keys whose weight begins at 0, or null: the batch's rows
+  float* w;              // [num_phys_pages][Hkv][page_size]
+  float decay, a1, beta; // a1 = α − 1 (0: softmax), beta = 1/a1
 };
 
 cudaError_t launch_plan(const entmaxkv_config& cfg, int32_t* block_table, const int32_t* seq_lens, uint32_t* status,
@@ -200,6 +226,11 @@ cudaError_t launch_attend_chunk(const Q8AttendArgs& a, bool i8, void* ws, int sm
 size_t attend_entmax_bytes(const entmaxkv_config& cfg, int n_seqs);
 cudaError_t launch_attend_entmax(const entmaxkv_config& cfg, Q8AttendArgs a, bool i8, float alpha, void* ws, int sms,
                                  cudaStream_t st);
+cudaError_t launch_weigh_stream(const Q8WeighArgs& a, bool i8, int sms, cudaStream_t st);
+size_t evict_bytes(const entmaxkv_config& cfg, int n, int keep);
+cudaError_t launch_evict(const Q8Cache& c, const int32_t* seq_ids, int n, int keep, int above, int sinks, int recent,
+                         const float* w, float* w_out, int32_t* lens_out, int32_t* free_pages,
+                         const int32_t* free_count, int32_t* count_out, bool i8, void* ws, int sms, cudaStream_t st);
 // A pool as (dim, KV head · token, page) of bytes, in boxes of one slab.
 cudaError_t make_q8_map(CUtensorMap* map, const void* pool, int nphys, int Hkv, int P, int D);
 

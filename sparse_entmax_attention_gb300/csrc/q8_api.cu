@@ -155,13 +155,8 @@ size_t entmaxkv_attend_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, 
   return streams(cfg, max_count) ? attend_softmax_bytes(*cfg, n_seqs) : attend_chunk_bytes(*cfg, n_seqs, total);
 }
 
-int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache, const entmaxkv_batch* batch,
-                           const entmaxkv_rows* q, const entmaxkv_score* score, float alpha, void* workspace,
-                           size_t workspace_bytes, const entmaxkv_rows* out, float* tau, void* stream) {
-  int st;
-  if ((st = check_q8_config(cfg)) || (st = check_q8_cache(cache)) || (st = check_batch(batch))) return st;
-  if ((st = check_attend(cfg, batch->n_seqs, batch->total, batch->max_count, alpha))) return st;
-  Q8Score sc{0.0f, 0.0f, 0.0f, 0, nullptr, nullptr, nullptr};
+static int score_of(const entmaxkv_config* cfg, const entmaxkv_score* score, Q8Score& sc) {
+  sc = Q8Score{0.0f, 0.0f, 0.0f, 0, nullptr, nullptr, nullptr};
   if (score) {
     if (!isfinite(score->scale) || score->scale < 0.0f || score->window < 0) return ENTMAXKV_ERR_INVALID_ARG;
     if (score->softcap != 0.0f && !(score->softcap >= 0x1p-60f && score->softcap <= 0x1p60f))
@@ -170,6 +165,19 @@ int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* 
                  score->slopes, score->prefix, score->first_key};
   }
   if (sc.scale == 0.0f) sc.scale = (float)(1.0 / sqrt((double)cfg->head_dim));
+  return ENTMAXKV_OK;
+}
+
+// lam null: attention, else the differences of pairs of heads.
+static int32_t attend(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache, const entmaxkv_batch* batch,
+                      const entmaxkv_rows* q, const entmaxkv_score* score, float alpha, const float* lam,
+                      int64_t lam_stride, const float* gain, float eps, void* workspace, size_t workspace_bytes,
+                      const entmaxkv_rows* out, float* tau, void* stream) {
+  int st;
+  if ((st = check_q8_config(cfg)) || (st = check_q8_cache(cache)) || (st = check_batch(batch))) return st;
+  if ((st = check_attend(cfg, batch->n_seqs, batch->total, batch->max_count, alpha))) return st;
+  Q8Score sc;
+  if ((st = score_of(cfg, score, sc))) return st;
   if (idle(batch)) return ENTMAXKV_OK;
   if ((st = check_rows(q, false)) || (st = check_rows(out, true))) return st;
   if (!workspace || ((uintptr_t)workspace & 255u) ||
@@ -184,12 +192,97 @@ int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* 
   a.q = rows_of(q);
   a.out = rows_of(out);
   a.tau = tau;
+  a.lam = lam;
+  a.lam_ts = lam_stride;
+  a.gain = gain;
+  a.eps = eps;
   const bool i8 = cfg->kv_dtype == ENTMAXKV_I8;
   const cudaStream_t s = (cudaStream_t)stream;
   if (alpha > 1.0f) return code_of(launch_attend_entmax(*cfg, a, i8, alpha, workspace, sms, s));
   if (streams(cfg, batch->max_count))
     return code_of(launch_attend_softmax(a, i8, workspace, sms, s));
   return code_of(launch_attend_chunk(a, i8, workspace, sms, s));
+}
+
+int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache, const entmaxkv_batch* batch,
+                           const entmaxkv_rows* q, const entmaxkv_score* score, float alpha, void* workspace,
+                           size_t workspace_bytes, const entmaxkv_rows* out, float* tau, void* stream) {
+  return attend(cfg, cache, batch, q, score, alpha, nullptr, 0, nullptr, 0.0f, workspace, workspace_bytes, out, tau,
+                stream);
+}
+
+int32_t entmaxkv_attend_diff_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache,
+                                const entmaxkv_batch* batch, const entmaxkv_rows* q, const entmaxkv_score* score,
+                                const float* lam, int64_t lam_stride, const float* gain, float eps, void* workspace,
+                                size_t workspace_bytes, const entmaxkv_rows* out, float* tau, void* stream) {
+  const int st = check_q8_config(cfg);
+  if (st) return st;
+  if (cfg->group & 1) return ENTMAXKV_ERR_UNSUPPORTED;
+  if (lam_stride < 0 || (gain && !(eps >= 0x1p-100f && isfinite(eps)))) return ENTMAXKV_ERR_INVALID_ARG;
+  if (!lam && batch && !idle(batch)) return ENTMAXKV_ERR_INVALID_ARG;
+  return attend(cfg, cache, batch, q, score, 1.0f, lam, lam_stride, gain, eps, workspace, workspace_bytes, out, tau,
+                stream);
+}
+
+size_t entmaxkv_weigh_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, int32_t total, int32_t max_count,
+                                   float alpha) {
+  if (check_attend(cfg, n_seqs, total, max_count, alpha)) return 0;
+  return 256;
+}
+
+int32_t entmaxkv_weigh_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache, const entmaxkv_batch* batch,
+                          const entmaxkv_rows* q, const float* tau, const entmaxkv_score* score, float alpha,
+                          const float* coef, float decay, const int32_t* fresh, float* weights, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  int st;
+  if ((st = check_q8_config(cfg)) || (st = check_q8_cache(cache)) || (st = check_batch(batch))) return st;
+  if ((st = check_attend(cfg, batch->n_seqs, batch->total, batch->max_count, alpha))) return st;
+  Q8Score sc;
+  if ((st = score_of(cfg, score, sc))) return st;
+  if (!(decay >= 0.0f) || !isfinite(decay)) return ENTMAXKV_ERR_INVALID_ARG;
+  if (idle(batch)) return ENTMAXKV_OK;
+  if ((st = check_rows(q, false))) return st;
+  if (!tau || !weights) return ENTMAXKV_ERR_INVALID_ARG;
+  if (!workspace || ((uintptr_t)workspace & 255u) ||
+      workspace_bytes < entmaxkv_weigh_q8_workspace(cfg, batch->n_seqs, batch->total, batch->max_count, alpha))
+    return ENTMAXKV_ERR_WORKSPACE_TOO_SMALL;
+  const int sms = device_sms();
+  if (sms < 1) return ENTMAXKV_ERR_CUDA;
+  const float a1 = (float)((double)alpha - 1.0);
+  const Q8WeighArgs a{cache_of(cfg, cache), batch_of(batch), sc, rows_of(q), tau, coef, fresh, weights, decay, a1,
+                      a1 > 0.0f ? (float)(1.0 / ((double)alpha - 1.0)) : 0.0f};
+  return code_of(launch_weigh_stream(a, cfg->kv_dtype == ENTMAXKV_I8, sms, (cudaStream_t)stream));
+}
+
+static int check_evict(const entmaxkv_config* cfg, int32_t n_seqs, int32_t keep) {
+  const int st = check_q8_config(cfg);
+  if (st) return st;
+  return n_seqs < 0 || n_seqs > 65535 || keep < 1 || (long long)keep > (long long)cfg->max_pages_per_seq * cfg->page_size
+             ? ENTMAXKV_ERR_INVALID_ARG : ENTMAXKV_OK;
+}
+
+size_t entmaxkv_evict_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, int32_t keep) {
+  return check_evict(cfg, n_seqs, keep) ? 0 : evict_bytes(*cfg, n_seqs, keep);
+}
+
+int32_t entmaxkv_evict_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache, const float* weights,
+                          const int32_t* seq_ids, int32_t n_seqs, int32_t keep, int32_t above, int32_t sinks,
+                          int32_t recent, float* weights_out, int32_t* lens_out, int32_t* free_pages,
+                          const int32_t* free_count, int32_t* free_count_out, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  int st;
+  if ((st = check_evict(cfg, n_seqs, keep)) || (st = check_q8_cache(cache))) return st;
+  if (above < keep || sinks < 0 || recent < 0 || (long long)sinks + recent > keep) return ENTMAXKV_ERR_INVALID_ARG;
+  if (n_seqs == 0) return ENTMAXKV_OK;
+  if (!seq_ids || !lens_out || !free_pages || !free_count || !free_count_out) return ENTMAXKV_ERR_INVALID_ARG;
+  if (weights ? !weights_out : sinks + recent < keep) return ENTMAXKV_ERR_INVALID_ARG;
+  if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < evict_bytes(*cfg, n_seqs, keep))
+    return ENTMAXKV_ERR_WORKSPACE_TOO_SMALL;
+  const int sms = device_sms();
+  if (sms < 1) return ENTMAXKV_ERR_CUDA;
+  return code_of(launch_evict(cache_of(cfg, cache), seq_ids, n_seqs, keep, above, sinks, recent, weights, weights_out,
+                              lens_out, free_pages, free_count, free_count_out, cfg->kv_dtype == ENTMAXKV_I8, workspace,
+                              sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -359,7 +359,41 @@ __global__ void __launch_bounds__(kAttWarps<D, NT> * 32, 1)
         m[nt][j] -= kLift;
       }
     const bool last = w + n == w_end;
-    if (n == T) {  // the whole unit
+    if (n == T && a.lam) {  // the whole unit; a lane's two rows are a pair
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int rj = 8 * nt + 2 * c;
+        const bool in = rj < rows;
+        const int i = (int)((uint32_t)(row0 + rj) / (uint32_t)G), h = kvh * G + row0 + rj - i * G;
+        const long long tok = x.s.start + i;
+        const float i0 = att_inv(l[nt][0]), i1 = in ? att_inv(l[nt][1]) * a.lam[tok * a.lam_ts + (h >> 1)] : 0.0f;
+        float sum2 = 0.0f;
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            acc[mt][nt][e] = diff_of(acc[mt][nt][e], i0, acc[mt][nt][e + 1], i1);
+            sum2 = fmaf(acc[mt][nt][e], acc[mt][nt][e], sum2);
+          }
+        if (a.gain) {
+          sum2 += __shfl_xor_sync(0xffffffffu, sum2, 4);
+          sum2 += __shfl_xor_sync(0xffffffffu, sum2, 8);
+          sum2 += __shfl_xor_sync(0xffffffffu, sum2, 16);
+          const float f = diff_norm(a, sum2);
+#pragma unroll
+          for (int mt = 0; mt < D / 16; ++mt) {
+            acc[mt][nt][0] *= f * a.gain[16 * mt + 2 * r];
+            acc[mt][nt][2] *= f * a.gain[16 * mt + 2 * r + 1];
+          }
+        }
+        if (!in) continue;
+        __nv_bfloat16* o = a.out.p + tok * a.out.ts + (long long)(h >> 1) * a.out.hs;
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt)
+          *reinterpret_cast<uint32_t*>(o + 16 * mt + 2 * r) = bf2_rn(acc[mt][nt][0], acc[mt][nt][2]);
+        if (a.tau && r < 2) a.tau[tok * Hkv * G + h + r] = att_lse(r ? m[nt][1] : m[nt][0], r ? l[nt][1] : l[nt][0]);
+      }
+    } else if (n == T) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -433,20 +467,50 @@ __global__ void __launch_bounds__(kAttWarps<D, NT> * 32, 1)
     sh_ml[i][rj] = make_float2(M, l);
   }
   __syncthreads();
-  for (int i0 = 0, i1; i0 < NW; i0 = i1) {
-    i1 = i0 + 1;
-    const AttPiece x = sh_piece[i0];
+  for (int j0 = 0, j1; j0 < NW; j0 = j1) {
+    j1 = j0 + 1;
+    const AttPiece x = sh_piece[j0];
     if (x.A < 0) continue;
-    while (i1 < NW && sh_piece[i1].A == x.A) ++i1;
-    const long long first = (long long)blockIdx.x * NW + i0;
-    const bool all = cut.begin(first) <= x.A && cut.begin((long long)blockIdx.x * NW + i1) == x.A + x.T;
+    while (j1 < NW && sh_piece[j1].A == x.A) ++j1;
+    const long long first = (long long)blockIdx.x * NW + j0;
+    const bool all = cut.begin(first) <= x.A && cut.begin((long long)blockIdx.x * NW + j1) == x.A + x.T;
     const float* ring_f = reinterpret_cast<const float*>(dyn_sm + (ring0 - smem_u32(dyn_sm)));
+    if (all && a.lam) {  // a warp a pair
+      for (int rj = 2 * warp; rj < x.rows; rj += 2 * NW) {
+        const int i = (int)((uint32_t)(x.row0 + rj) / (uint32_t)G), h = x.kvh * G + x.row0 + rj - i * G;
+        const long long tok = x.start + i;
+        const float i0 = att_inv(sh_ml[j0][rj].y), i1 = att_inv(sh_ml[j0][rj + 1].y) * a.lam[tok * a.lam_ts + (h >> 1)];
+        float y[D / 32], sum2 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          float o0 = 0.0f, o1 = 0.0f;
+#pragma unroll 4
+          for (int n = j0; n < j1; ++n) {
+            const float* p = ring_f + n * (ST * SLAB / 4) + rj * D + 32 * k + lane;
+            o0 = fmaf(sh_f[n][rj], p[0], o0);
+            o1 = fmaf(sh_f[n][rj + 1], p[D], o1);
+          }
+          y[k] = diff_of(o0, i0, o1, i1);
+          sum2 = fmaf(y[k], y[k], sum2);
+        }
+        if (a.gain) {
+          const float f = diff_norm(a, warp_sum(sum2));
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) y[k] *= f * a.gain[32 * k + lane];
+        }
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+          a.out.p[tok * a.out.ts + (long long)(h >> 1) * a.out.hs + 32 * k + lane] = __float2bfloat16_rn(y[k]);
+        if (a.tau && lane < 2) a.tau[tok * Hkv * G + h + lane] = att_lse(sh_ml[j0][rj + lane].x, sh_ml[j0][rj + lane].y);
+      }
+      continue;
+    }
     for (int e = tid; e < x.rows * D; e += NTH) {
       const int rj = e / D;
       float o = 0.0f;
 #pragma unroll 4
-      for (int i = i0; i < i1; ++i) o = fmaf(sh_f[i][rj], ring_f[i * (ST * SLAB / 4) + e], o);
-      const float M = sh_ml[i0][rj].x, l = sh_ml[i0][rj].y;
+      for (int i = j0; i < j1; ++i) o = fmaf(sh_f[i][rj], ring_f[i * (ST * SLAB / 4) + e], o);
+      const float M = sh_ml[j0][rj].x, l = sh_ml[j0][rj].y;
       if (all) {
         const int i = (int)((uint32_t)(x.row0 + rj) / (uint32_t)G), h = x.kvh * G + x.row0 + rj - i * G;
         const long long tok = x.start + i;
@@ -474,15 +538,17 @@ __global__ void __launch_bounds__(D) attend_join_kernel(Q8AttendArgs a, int nrt_
   const AttSlot x = reinterpret_cast<const AttSlot*>(a.slots)[b];
   const long long W = a.cum[a.b.n_seqs], at = a.cum[b];
   const int G = a.c.G;
-  if (rt >= x.nrt || rt * R + rj >= x.s.count * G) return;
+  if (rt >= x.nrt || rt * R + rj >= x.s.count * G || (a.lam && (rj & 1))) return;  // (a pair's first row answers both)
   const LineCut cut = line_cut(W, a.blocks, NW);
   const int T = x.T;
   const long long A = at + ((long long)kvh * x.nrt + rt) * T, B = A + T;
-  float M = -CUDART_INF_F, l = 0.0f, o = 0.0f;
-  if (T > 0) {
+  auto row_sum = [&](int rj, float& M, float& l, float& o) -> bool {  // false: answered already
+    M = -CUDART_INF_F;
+    l = o = 0.0f;
+    if (T == 0) return true;
     const long long w0 = cut.of(A), w1 = cut.of(B - 1);
     const bool tail = cut.begin(w1 + 1) > B;  // the last warp goes on: its piece lies apart
-    if (w0 == w1 || (!tail && w0 / NW == w1 / NW)) return;  // finished by that warp or block
+    if (w0 == w1 || (!tail && w0 / NW == w1 / NW)) return false;  // by that warp or block
     const long long c0 = w0 / NW, c1 = (tail ? w1 - 1 : w1) / NW;
     const int n = (int)(c1 - c0 + 1) + (tail ? 1 : 0);
     auto piece = [&](int i) -> size_t {
@@ -517,9 +583,30 @@ __global__ void __launch_bounds__(D) attend_join_kernel(Q8AttendArgs a, int nrt_
       }
       M = m;
     }
-  }
+    return true;
+  };
+  float M, l, o;
+  if (!row_sum(rj, M, l, o)) return;
   const int i = (int)((uint32_t)(rt * R + rj) / (uint32_t)G), h = kvh * G + rt * R + rj - i * G;
   const long long tok = x.s.start + i;
+  if (a.lam) {
+    float M1, l1, o1;
+    row_sum(rj + 1, M1, l1, o1);
+    float y = diff_of(o, att_inv(l), o1, att_inv(l1) * a.lam[tok * a.lam_ts + (h >> 1)]);
+    if (a.gain) {
+      __shared__ float sh2[D / 32];
+      const float part = warp_sum(y * y);
+      if ((threadIdx.x & 31) == 0) sh2[threadIdx.x >> 5] = part;
+      __syncthreads();
+      float sum2 = 0.0f;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) sum2 += sh2[k];
+      y *= diff_norm(a, sum2) * a.gain[threadIdx.x];
+    }
+    a.out.p[tok * a.out.ts + (long long)(h >> 1) * a.out.hs + threadIdx.x] = __float2bfloat16_rn(y);
+    if (a.tau && threadIdx.x < 2) a.tau[tok * a.c.Hkv * G + h + threadIdx.x] = threadIdx.x ? att_lse(M1, l1) : att_lse(M, l);
+    return;
+  }
   a.out.p[tok * a.out.ts + (long long)h * a.out.hs + threadIdx.x] = __float2bfloat16_rn(o * att_inv(l));
   if (a.tau && threadIdx.x == 0) a.tau[tok * a.c.Hkv * G + h] = att_lse(M, l);
 }

@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs g) {
         if (rho >= it.count * G) break;
         const int head = (int)(i % Hkv) * G + rho % G;
         const long long tok = it.start + rho / G;
-        for (int k = lane; k < D; k += 32) a.out.p[tok * a.out.ts + (long long)head * a.out.hs + k] = __float2bfloat16_rn(0.0f);
+        const int to = a.lam ? head >> 1 : head;  // (a pair's rows write the same zeros)
+        for (int k = lane; k < D; k += 32) a.out.p[tok * a.out.ts + (long long)to * a.out.hs + k] = __float2bfloat16_rn(0.0f);
         if (a.tau && lane == 0) a.tau[tok * Hkv * G + head] = CUDART_NAN_F;
       }
     }
@@ -107,13 +108,10 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs g) {
   const int c0 = (int)(((A + 1) * nb - 1) / W), n = (int)(((A + it.T) * nb - 1) / W) - c0 + 1;
   if (c0 != c - 1) return;  // joined at an earlier cut
   const int last0 = W * c0 / nb >= A - kChunkItem ? 0 : 1;  // the first block's piece: its first or its last
-#pragma unroll 2
-  for (int row = 32 * part + warp; row < 32 * part + 32; row += 8) {
-    const int rho = it.rt * kChunkRows + row;
-    if (rho >= it.count * G) break;
+  auto row_sum = [&](int row, float& M, float& l, float (&o)[V]) {
     auto piece = [&](int i) -> size_t { return (size_t)(2 * (c0 + i) + (i ? 0 : last0)) * kChunkRows + row; };
-    float M = -CUDART_INF_F, l = 0.0f;
-    float o[V];
+    M = -CUDART_INF_F;
+    l = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = 0.0f;
     for (int i0 = 0; i0 < n; i0 += 32) {  // 32 pieces' maxima and sums at once, one a lane
@@ -134,6 +132,40 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs g) {
         for (int k = 0; k < V; ++k) o[k] = fmaf(fi, p[32 * k], o[k]);
       }
     }
+  };
+  if (a.lam) {  // a warp a pair
+    for (int row = 32 * part + 2 * warp; row < 32 * part + 32; row += 16) {
+      const int rho = it.rt * kChunkRows + row;
+      if (rho >= it.count * G) break;
+      float M[2], l[2], o[V], o1[V], sum2 = 0.0f;
+      row_sum(row, M[0], l[0], o);
+      row_sum(row + 1, M[1], l[1], o1);
+      const int head = cut.y * G + rho % G;
+      const long long tok = it.start + rho / G;
+      const float i0 = att_inv(l[0]), i1 = att_inv(l[1]) * a.lam[tok * a.lam_ts + (head >> 1)];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        o[i] = diff_of(o[i], i0, o1[i], i1);
+        sum2 = fmaf(o[i], o[i], sum2);
+      }
+      if (a.gain) {
+        const float f = diff_norm(a, warp_sum(sum2));
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] *= f * a.gain[32 * i + lane];
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        a.out.p[tok * a.out.ts + (long long)(head >> 1) * a.out.hs + 32 * i + lane] = __float2bfloat16_rn(o[i]);
+      if (a.tau && lane < 2) a.tau[tok * Hkv * G + head + lane] = lane ? att_lse(M[1], l[1]) : att_lse(M[0], l[0]);
+    }
+    return;
+  }
+#pragma unroll 2
+  for (int row = 32 * part + warp; row < 32 * part + 32; row += 8) {
+    const int rho = it.rt * kChunkRows + row;
+    if (rho >= it.count * G) break;
+    float M, l, o[V];
+    row_sum(row, M, l, o);
     const int head = cut.y * G + rho % G;
     const long long tok = it.start + rho / G;
     const float inv = att_inv(l);

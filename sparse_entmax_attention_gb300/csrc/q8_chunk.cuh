@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
       float kc = 0.0f, slope = 0.0f;  // the raw sums' factor (times the page's K scale): log2 units, or of the cap
       int pos = -1, lo = 0;
       const long long q_at = (long long)(x.s.start + tok) * a.q.ts + (long long)head * a.q.hs;
-      const long long o_at = (long long)(x.s.start + tok) * a.out.ts + (long long)head * a.out.hs;
+      const long long o_at = (long long)(x.s.start + tok) * a.out.ts + (long long)(a.lam ? head >> 1 : head) * a.out.hs;
       const uint32_t rows_sm = q_sm + wg * TILE;  // this half's query tile, and its answers on their way out
       if (mine) {  // (asked for before the queries)
         pos = x.s.L - x.s.count + tok;
@@ -534,6 +534,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
       const bool whole = x.n == x.T;
       const int piece = 2 * blockIdx.x + (seg ? 1 : 0);
       const float inv = whole ? att_inv(l) : 1.0f;
+      // a pair's rows lie in neighbouring lanes: both form y = first + second, and each stores half of the chunks to
+      // the first one's row
+      const bool pairs = whole && a.lam;
+      float first = 0.0f, fn = 1.0f;
+      if (pairs) {
+        const float lam = mine ? a.lam[(long long)(x.s.start + tok) * a.lam_ts + (head >> 1)] : 0.0f;
+        first = lane & 1 ? -lam * inv : inv;
+        if (half && a.gain) {
+          float sum2 = 0.0f;
+#pragma unroll 1
+          for (int i = 0; i < D / 32; ++i) {
+            float o[32];
+            tm_ld32(o_tm + 32 * i, o);
+            tm_wait_ld();
+            tm_tie32(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float m = __fmul_rn(o[k], first), y = __fadd_rn(m, __shfl_xor_sync(0xffffffffu, m, 1));
+              sum2 = fmaf(y, y, sum2);
+            }
+          }
+          fn = diff_norm(a, sum2);
+        }
+      }
       if (half) {
         // rows leave through the query tile, so that a warp writes whole rows: bf16 rows at once, fp32 pieces in
         // column blocks of 256 bytes too
@@ -547,7 +571,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
           tm_ld32(o_tm + 32 * i, o);
           tm_wait_ld();
           tm_tie32(o);
-          if (whole) {
+          if (pairs) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float m = __fmul_rn(o[k], first);
+              o[k] = __fadd_rn(m, __shfl_xor_sync(0xffffffffu, m, 1));
+              if (a.gain) o[k] *= fn * a.gain[32 * i + k];
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+              if ((k / 8 & 1) == (lane & 1))
+                sts128(rows_sm + tile_off(row & ~1, 4 * i + k / 8),
+                       make_uint4(bf2_rn(o[k], o[k + 1]), bf2_rn(o[k + 2], o[k + 3]), bf2_rn(o[k + 4], o[k + 5]),
+                                  bf2_rn(o[k + 6], o[k + 7])));
+          } else if (whole) {
 #pragma unroll
             for (int k = 0; k < 32; k += 8)
               sts128(rows_sm + tile_off(row, 4 * i + k / 8),
@@ -574,7 +611,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
           for (int n = 0; n < LPR; ++n) {
             const int rl = n * (32 / LPR) + lane / LPR;
             const long long at = __shfl_sync(0xffffffffu, o_at, rl);
-            if (__shfl_sync(0xffffffffu, (int)mine, rl))
+            if (__shfl_sync(0xffffffffu, (int)mine, rl) && !(pairs && (rl & 1)))
               *reinterpret_cast<uint4*>(a.out.p + at + 8 * (lane % LPR)) = lds128(rows_sm + tile_off(wrow + rl, lane % LPR));
           }
         }
