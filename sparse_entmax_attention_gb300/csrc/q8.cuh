@@ -226,6 +226,10 @@ cudaError_t launch_attend_chunk(const Q8AttendArgs& a, bool i8, void* ws, int sm
 size_t attend_entmax_bytes(const entmaxkv_config& cfg, int n_seqs);
 cudaError_t launch_attend_entmax(const entmaxkv_config& cfg, Q8AttendArgs a, bool i8, float alpha, void* ws, int sms,
                                  cudaStream_t st);
+// Rows of a batch's largest slot up to which the streaming kernel weighs keys.
+constexpr int kWeighRows = 16;
+size_t weigh_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total);
+cudaError_t launch_weigh_chunk(const Q8WeighArgs& a, bool i8, void* ws, int sms, cudaStream_t st);
 cudaError_t launch_weigh_stream(const Q8WeighArgs& a, bool i8, int sms, cudaStream_t st);
 size_t evict_bytes(const entmaxkv_config& cfg, int n, int keep);
 cudaError_t launch_evict(const Q8Cache& c, const int32_t* seq_ids, int n, int keep, int above, int sinks, int recent,

@@ -224,10 +224,14 @@ int32_t entmaxkv_attend_diff_q8(const entmaxkv_config* cfg, const entmaxkv_q8_ca
                 stream);
 }
 
+static bool weigh_streams(const entmaxkv_config* c, int max_count) {
+  return (long long)max_count * c->group <= kWeighRows;
+}
+
 size_t entmaxkv_weigh_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, int32_t total, int32_t max_count,
                                    float alpha) {
   if (check_attend(cfg, n_seqs, total, max_count, alpha)) return 0;
-  return 256;
+  return weigh_streams(cfg, max_count) ? 256 : weigh_chunk_bytes(*cfg, n_seqs, total);
 }
 
 int32_t entmaxkv_weigh_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache, const entmaxkv_batch* batch,
@@ -251,7 +255,10 @@ int32_t entmaxkv_weigh_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* c
   const float a1 = (float)((double)alpha - 1.0);
   const Q8WeighArgs a{cache_of(cfg, cache), batch_of(batch), sc, rows_of(q), tau, coef, fresh, weights, decay, a1,
                       a1 > 0.0f ? (float)(1.0 / ((double)alpha - 1.0)) : 0.0f};
-  return code_of(launch_weigh_stream(a, cfg->kv_dtype == ENTMAXKV_I8, sms, (cudaStream_t)stream));
+  const bool i8 = cfg->kv_dtype == ENTMAXKV_I8;
+  const cudaStream_t s = (cudaStream_t)stream;
+  return code_of(weigh_streams(cfg, batch->max_count) ? launch_weigh_stream(a, i8, sms, s)
+                                                      : launch_weigh_chunk(a, i8, workspace, sms, s));
 }
 
 static int check_evict(const entmaxkv_config* cfg, int32_t n_seqs, int32_t keep) {

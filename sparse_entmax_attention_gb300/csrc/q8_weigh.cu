@@ -51,7 +51,7 @@ __device__ __forceinline__ WeighSlot weigh_slot(const Q8WeighArgs& a, int b, uin
 template <bool I8, int D, int P, int NT, bool ENT>
 __global__ void __launch_bounds__(kWeighWarps * 32, 1) weigh_kernel(Q8WeighArgs a, const __grid_constant__ CUtensorMap kmap) {
   pdl_enter();
-  constexpr int NW = kWeighWarps, ST = kWeighSlabs<D>, SLAB = kWeighKeys * D, R = 8 * NT, PP = kWeighKeys / P;
+  constexpr int NW = kWeighWarps, ST = kWeighSlabs<D>, SLAB = kWeighKeys * D, PP = kWeighKeys / P;
   extern __shared__ __align__(128) unsigned char dyn_sm[];
   __shared__ uint64_t bars[NW][ST];
   __shared__ LineSmem<NW> sh_line;
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 1) weigh_kernel(Q8WeighArgs 
     const long long off = w - cum;
     const int kvh = (int)div_line(off, x.T), t0 = (int)(off - (long long)kvh * x.T);
     const int n = (int)min((long long)(x.T - t0), at.end - w);
-    const int n_rows = x.s.count * G, n_rt = (n_rows + R - 1) / R, n_pages = x.pages();
+    const int n_rows = x.s.count * G, n_pages = x.pages();
     // 32 tiles' places and scales at once, a tile a lane
     int ph[PP];
     float ks_l[PP];
@@ -130,22 +130,19 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 1) weigh_kernel(Q8WeighArgs 
         ++filled;
       }
     };
-    // rows row0 .. row0 + R − 1 of the slot: queries, and what turns a score into a weight
+    // the slot's rows: queries, and what turns a score into a weight
     uint32_t bq[NT][D / 16][2];
     Q8Row row[NT][2];
     float add[NT][2], cf[NT][2];
-    int pos_min, lo_max;
-    auto rows_at = [&](int row0) {
-      const int rows = min(R, n_rows - row0);
+    int pos_min = 0x7fffffff, lo_max = 0;
+    {
       uint4 qw[NT][D / 32];
-      pos_min = 0x7fffffff;
-      lo_max = 0;
       float t[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint32_t rj = row0 + 8 * nt + 2 * c + j, i = rj / (uint32_t)G;
+          const uint32_t rj = 8 * nt + 2 * c + j, i = rj / (uint32_t)G;
           const int h = kvh * G + (int)(rj - i * G);
           Q8Row& q = row[nt][j];
           q.slope = 0.0f;
@@ -153,7 +150,7 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 1) weigh_kernel(Q8WeighArgs 
           q.lo = 0;
           t[nt][j] = CUDART_NAN_F;
           cf[nt][j] = 0.0f;
-          if (8 * nt + 2 * c + j < rows) {
+          if ((int)rj < n_rows) {
             const long long tok = x.s.start + (int)i;
             t[nt][j] = a.tau[tok * Hkv * G + h];
             cf[nt][j] = a.coef ? a.coef[tok * Hkv * G + h] : 1.0f;
@@ -167,8 +164,8 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 1) weigh_kernel(Q8WeighArgs 
         }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const uint32_t rho = row0 + 8 * nt + r, tok = rho / (uint32_t)G;
-        q_load<D>(8 * nt + r < rows ? a.q.p + (long long)(x.s.start + (int)tok) * a.q.ts +
+        const uint32_t rho = 8 * nt + r, tok = rho / (uint32_t)G;
+        q_load<D>((int)rho < n_rows ? a.q.p + (long long)(x.s.start + (int)tok) * a.q.ts +
                                           (long long)(kvh * G + (int)(rho - tok * G)) * a.q.hs
                                     : nullptr,
                   lane, qw[nt]);
@@ -188,8 +185,7 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 1) weigh_kernel(Q8WeighArgs 
       }
       pos_min = __reduce_min_sync(0xffffffffu, pos_min);
       lo_max = __reduce_max_sync(0xffffffffu, lo_max);
-    };
-    if (n_rt == 1) rows_at(0);
+    }
     look_up(0);
     refill(min(n, 32));
     for (int i = 0; i < n; ++i) {
@@ -224,40 +220,37 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 1) weigh_kernel(Q8WeighArgs 
           break;
         }
         const uint32_t slab = ring + (used % ST) * SLAB;
-        for (int rt = 0; rt < n_rt; ++rt) {
-          if (n_rt > 1) rows_at(rt * R);
-          bool all = whole;
+        bool all = whole;
 #pragma unroll
-          for (int q = 0; q < PP; ++q)
-            all = all && ((key0[q] + P - 1 <= pos_min && key0[q] >= lo_max) || key0[q] + P <= x.sp.pre);
+        for (int q = 0; q < PP; ++q)
+          all = all && ((key0[q] + P - 1 <= pos_min && key0[q] >= lo_max) || key0[q] + P <= x.sp.pre);
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            float s[NT][4];
-            k_dot<I8, D, NT>(slab, 16 * mt, lane, bq, s);
-            const int q = 16 * mt / P, j0 = key0[q] + (16 * mt) % P + r;
+        for (int mt = 0; mt < 2; ++mt) {
+          float s[NT][4];
+          k_dot<I8, D, NT>(slab, 16 * mt, lane, bq, s);
+          const int q = 16 * mt / P, j0 = key0[q] + (16 * mt) % P + r;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const float dot[2] = {s[nt][j], s[nt][2 + j]};
-                float v[2];
-                q8_scores(dot, v, row[nt][j], ks[q], j0, a.sc, unit, add[nt][j]);
-                const bool counts = cf[nt][j] > 0.0f;
+            for (int j = 0; j < 2; ++j) {
+              const float dot[2] = {s[nt][j], s[nt][2 + j]};
+              float v[2];
+              q8_scores(dot, v, row[nt][j], ks[q], j0, a.sc, unit, add[nt][j]);
+              const bool counts = cf[nt][j] > 0.0f;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float p;
-                  if constexpr (ENT) {
-                    p = fmaxf(v[e], 0.0f);
-                    if (a.beta == 2.0f) p *= p;
-                    else if (a.beta != 1.0f) p = p > 0.0f ? ex2f(a.beta * __log2f(p)) : 0.0f;
-                  } else {
-                    p = ex2f(v[e]);
-                  }
-                  if (!counts || !(all || q8_sees(row[nt][j], j0 + 8 * e, x.sp.pre))) p = 0.0f;
-                  sum[mt][e] = fmaf(p, cf[nt][j], sum[mt][e]);
+              for (int e = 0; e < 2; ++e) {
+                float p;
+                if constexpr (ENT) {
+                  p = fmaxf(v[e], 0.0f);
+                  if (a.beta == 2.0f) p *= p;
+                  else if (a.beta != 1.0f) p = p > 0.0f ? ex2f(a.beta * __log2f(p)) : 0.0f;
+                } else {
+                  p = ex2f(v[e]);
                 }
+                if (!counts || !(all || q8_sees(row[nt][j], j0 + 8 * e, x.sp.pre))) p = 0.0f;
+                sum[mt][e] = fmaf(p, cf[nt][j], sum[mt][e]);
               }
-          }
+            }
         }
         __syncwarp();  // every lane has read the slab
         ++used;

@@ -1,0 +1,561 @@
+// q8_weigh_chunk.cuh -- the weight that many rows a sequence give to the keys of
+// the 8-bit paged cache, on the fifth-generation tensor cores.
+//
+//   w_j ← decay·w_j + Σ over rows of 2^{t_j},  t_j = s_j·log2 e − tau·log2 e + log2 coef
+//
+// (s_j capped, biased, masked). A block holds 256 keys of a (slot, KV head) and
+// lets the rows pass, 128 (token, head of the group) at a time:
+//   S^T = K·Q^T   two products of 128 keys × 128 rows, codes and queries as bf16
+//                 (both exact), fp32 sums in tensor memory, keys along the lanes:
+//                 a thread has one key, and its sum over the rows needs no other;
+//   Σ 2^t         a key's scale is the thread's, what belongs to a row comes as a
+//                 broadcast from shared memory: an FMA, an exponential and an
+//                 addition a pair, the first and the last on two rows at once.
+//
+// A first pass lays the rows out as the products and the sums want them: tiles of
+// 128 queries in the operand's swizzled order, and what belongs to a row. (Copied
+// row by row from where they lie, a tile of rows took 1600 cycles to come in, more
+// than the products with it.)
+//
+// Warps: 4 + 4 of sums (a thread a key); 8 that bring the keys (the next 256 wait as
+// codes in registers until the products with the present ones are done); 2 that
+// issue the products, one for each 128 keys; 1 that asks for the rows, four tiles
+// ahead. Segments (key tile, share of the rows) go round the blocks in turns; rows
+// are shared out only where there are few key tiles, and the block that finishes a
+// tile last adds its shares in their order.
+#pragma once
+
+#include "q8_chunk.cuh"
+
+namespace ekv {
+
+constexpr int kWcThreads = 640;
+constexpr int kWcKeys = 256, kWcRows = 128;
+// Stages of the rows, and of their facts, which the sums read longer: the facts of unit u are asked for when the
+// products of u − kWcQ are done, so the sums of u − kWcQ − 2 are.
+constexpr int kWcQ = 4, kWcMeta = 6;
+constexpr int kWcMaxBlocks = 256;
+constexpr int kWcTurns = 6;  // segments a block should get at least
+
+struct __align__(16) WcSlot {
+  int seq, L, start, count;        // Q8Slot
+  int pre, npre, wfirst, npages;   // Q8Span
+  int lnpre, lwfirst, fresh, T;    // pages on the line, first fresh key, key tiles
+  int nrt, rt0, nsplit, pad;       // row tiles, the first of them in the list, shares of the rows
+};
+// What a row tile sees: smallest and largest position and first key.
+struct __align__(16) WcRows {
+  int pos_min, pos_max, lo_min, lo_max;
+};
+// What the sums know of a tile's rows.
+struct __align__(16) WcFacts {
+  float c[kWcRows];      // −tau·log2 e + log2 coef
+  float near[kWcRows];   // c − slope·ahead
+  float slope[kWcRows];  // −slope·log2 e
+  float ahead[kWcRows];  // position less the tile's first row's
+  int lo[kWcRows];       // first key of the row's document
+  uint32_t counts[kWcRows / 32];  // rows that are there and add something
+  int pos0, skip;        // position of the first row, and its head in the group
+  int whole, pad;        // all rows count
+};
+struct WcArgs {
+  Q8WeighArgs a;
+  WcSlot* slots;     // [n_seqs]
+  long long* cum;    // [n_seqs + 1] segments before each slot
+  WcRows* rows;      // [max_tiles]
+  uint4* packed;     // [Hkv][max_tiles] tiles of 128 queries
+  WcFacts* facts;    // [Hkv][max_tiles]
+  int* done;         // [2·kWcTurns·blocks][8] shares of a warp's keys that are there
+  float* part;       // [2·kWcTurns·blocks][256]
+  int max_tiles, blocks;
+};
+
+struct WcSeg {
+  WcSlot s;
+  long long id, first;  // of the segment, and of its key tile's first share
+  int kvh, kt, rt, rt_end;
+  int key_min, key_max;  // of the tile's keys
+  bool seen;             // some row may see some of them
+  __device__ __forceinline__ int pages() const { return s.lnpre + s.npages - s.lwfirst; }
+  __device__ __forceinline__ int page(int t) const { return t < s.lnpre ? t : t - s.lnpre + s.lwfirst; }
+};
+// The slots and their places, kept by a block where they are few.
+constexpr int kWcFew = 32;
+struct WcFew {
+  WcSlot slots[kWcFew];
+  long long cum[kWcFew + 1];
+};
+// Segment id; `slot` is the last one's slot (ids grow).
+template <int P>
+__device__ __forceinline__ WcSeg wc_seg(const WcArgs& g, const WcFew& sh, long long id, int& slot) {
+  const bool few = g.a.b.n_seqs <= kWcFew;
+  int lo = slot, hi = g.a.b.n_seqs - 1;
+  if (few) {
+    while (lo < hi && sh.cum[lo + 1] <= id) ++lo;
+  } else {
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (__ldcg(g.cum + m) <= id) lo = m;
+      else hi = m - 1;
+    }
+  }
+  slot = lo;
+  WcSeg x;
+  const int4* p = reinterpret_cast<const int4*>(few ? sh.slots + lo : g.slots + lo);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) reinterpret_cast<int4*>(&x.s)[i] = p[i];
+  const long long cum = few ? sh.cum[lo] : __ldcg(g.cum + lo), off = id - cum, rest = div_line(off, x.s.T);
+  x.kt = (int)(off - rest * x.s.T);
+  const int sp = (int)div_line(rest, g.a.c.Hkv);
+  x.kvh = (int)(rest - (long long)sp * g.a.c.Hkv);
+  x.id = id;
+  x.first = cum + (long long)x.kvh * x.s.T + x.kt;
+  x.rt = (int)div_line((long long)x.s.nrt * sp, x.s.nsplit);
+  x.rt_end = (int)div_line((long long)x.s.nrt * (sp + 1), x.s.nsplit);
+  constexpr int PT = kWcKeys / P;
+  const int p0 = x.page(x.kt * PT), p1 = x.page(min((x.kt + 1) * PT, x.pages()) - 1);
+  x.key_min = p0 * P;
+  x.key_max = min(p1 * P + P, x.s.L) - 1;
+  x.seen = p0 < x.s.npre || p1 >= x.s.wfirst;
+  return x;
+}
+// Of the 32 row tiles from rt on, those that may see the segment's keys, and those all of whose rows see them all.
+struct WcMask {
+  uint32_t some, all;
+};
+__device__ __forceinline__ WcMask wc_mask(const WcArgs& g, const WcSeg& x, int rt) {
+  bool some = false, all = false;
+  const int i = rt + (threadIdx.x & 31);
+  if (i < x.rt_end) {
+    const int4 r = __ldcg(reinterpret_cast<const int4*>(g.rows + x.s.rt0 + i));
+    some = (r.y >= x.key_min && r.z <= x.key_max) || x.key_min < x.s.pre;
+    all = r.x >= x.key_max && (r.w <= x.key_min || x.key_max < x.s.pre);
+  }
+  return WcMask{__ballot_sync(0xffffffffu, some), __ballot_sync(0xffffffffu, all)};
+}
+
+// Four codes as bf16 (exact): bytes 0 and 1 to x, 2 and 3 to y.
+template <bool I8>
+__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& x, uint32_t& y) {
+  if constexpr (I8) {  // 2^23 + 128 + v as a float for each byte
+    const uint32_t u = w ^ 0x80808080u;
+    const unsigned long long off = f2_splat(-8388736.0f);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float a, b;
+      f2_unpack(f2_add(f2_pack(__uint_as_float(__byte_perm(u, 0x4b000000u, j ? 0x7442 : 0x7440)),
+                               __uint_as_float(__byte_perm(u, 0x4b000000u, j ? 0x7443 : 0x7441))),
+                       off), a, b);
+      (j ? y : x) = bf2_rn(a, b);
+    }
+  } else {
+    uint32_t h[2];
+    e4m3x4_half(w, h[0], h[1]);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[0]));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[1]));
+    x = bf2_rn(a.x, a.y);
+    y = bf2_rn(b.x, b.y);
+  }
+}
+
+// D fp32, A and B bf16, both along K; M = 128.
+__device__ __forceinline__ uint32_t instr_desc_bf16(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+template <bool I8, int D, int P, bool capped, bool biased>
+__global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
+  pdl_enter();
+  constexpr int HALF = 128 * D * 2;      // bytes of 128 keys or rows
+  constexpr int PT = kWcKeys / P;        // pages a key tile
+  extern __shared__ __align__(128) unsigned char dyn_sm[];
+  __shared__ uint64_t q_full[kWcQ], q_empty[kWcQ], f_full[kWcMeta], k_full, k_empty, s_full[2][2], s_empty[2][2];
+  __shared__ uint32_t tm_base;
+  __shared__ WcFacts facts[kWcMeta];
+  __shared__ volatile int gave_up;
+  __shared__ WcFew few;
+  const Q8WeighArgs& a = g.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+  const uint32_t sm0 = (smem_u32(dyn_sm) + 1023u) & ~1023u;
+  const uint32_t k_sm = sm0, q_sm = sm0 + 2 * HALF;
+  if (tid == 0) {
+    for (int i = 0; i < kWcQ; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 2);
+    }
+    for (int i = 0; i < kWcMeta; ++i) mbar_init(&f_full[i], 1);
+    mbar_init(&k_full, 256);
+    mbar_init(&k_empty, 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i][0], 1);
+      mbar_init(&s_full[i][1], 1);
+      mbar_init(&s_empty[i][0], 128);
+      mbar_init(&s_empty[i][1], 128);
+    }
+    gave_up = 0;
+    mbar_fence_init();
+  }
+  if (warp == 16) tm_alloc(&tm_base);
+  if (a.b.n_seqs <= kWcFew) {
+    for (int i = tid; i < a.b.n_seqs * 4; i += kWcThreads)
+      reinterpret_cast<int4*>(few.slots)[i] = __ldcg(reinterpret_cast<const int4*>(g.slots) + i);
+    if (tid <= a.b.n_seqs) few.cum[tid] = __ldcg(g.cum + tid);
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  const uint32_t tm = tm_base;  // sums of stage s and half h at columns 256·s + 128·h
+  const long long n_segs = g.cum[a.b.n_seqs];
+  const int G = a.c.G, Hkv = a.c.Hkv;
+  auto wait = [&](uint64_t* bar, int phase) -> bool {  // a wait that runs out of its bound stops every role
+    if (mbar_wait_second(bar, (uint32_t)(phase & 1))) return true;
+    gave_up = 1;
+    return false;
+  };
+  auto wait_warp = [&](uint64_t* bar, int phase) -> bool { return __all_sync(0xffffffffu, wait(bar, phase)); };
+  int slot = 0, u = 0;  // units (row tiles against key tiles) so far, the same for every role
+  bool ok = true;
+
+  // Registers after the splits below: 256 x 128 + 256 x 80 + 128 x 56 = 60416; launched with 640 x 96 = 61440.
+  if (wg < 2) {  // ------------------------------------------------ sums: a thread a key
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;\n");
+    const int ks_ = 128 * wg + (tid & 127);
+    const uint32_t s_tm = tm + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * wg;
+    // the page of the thread's key, as the table has it (looked at a segment later: the load takes its time)
+    auto entry = [&](const WcSeg& x) -> int {
+      const int t = x.kt * PT + ks_ / P;
+      return t < x.pages() ? a.c.block_table[(size_t)x.s.seq * a.c.maxp + x.page(t)] : 0;
+    };
+    int next = 0;
+    if (blockIdx.x < n_segs) next = entry(wc_seg<P>(g, few, blockIdx.x, slot));
+    for (long long id = blockIdx.x; id < n_segs && ok; id += gridDim.x) {
+      const WcSeg x = wc_seg<P>(g, few, id, slot);
+      int ph = next;
+      if (id + gridDim.x < n_segs) {
+        int ahead = slot;
+        next = entry(wc_seg<P>(g, few, id + gridDim.x, ahead));
+      }
+      if (x.kt * PT + ks_ / P >= x.pages()) ph = -1;
+      else if (ph < 0 || ph >= a.c.nphys) {
+        raise_flag(a.c.status, ENTMAXKV_DEV_BAD_PAGE_TABLE);
+        ph = -1;
+      }
+      const int key = ph >= 0 ? x.page(x.kt * PT + ks_ / P) * P + ks_ % P : kNoKey;
+      const bool there = key < x.s.L;
+      const float ks = ph >= 0 ? a.c.k_scale[(size_t)ph * Hkv + x.kvh] : 0.0f;
+      float* wp = a.w + ((size_t)max(ph, 0) * Hkv + x.kvh) * P + ks_ % P;
+      float before = 0.0f;
+      if (there && key < x.s.fresh && a.decay != 0.0f && x.s.nsplit == 1) before = *wp;
+      const float k1 = ks * a.sc.scale * (capped ? a.sc.inv_cap : kLog2e), out = a.sc.cap * kLog2e;
+      const unsigned long long k2 = f2_splat(k1);
+      unsigned long long acc[4] = {0ull, 0ull, 0ull, 0ull};
+      for (int rt = x.rt; rt < x.rt_end && ok && x.seen; rt += 32) {
+        WcMask m = wc_mask(g, x, rt);
+        for (; m.some; m.some &= m.some - 1u, ++u) {
+          const int i = __ffs(m.some) - 1, st = u & 1, ms = u % kWcMeta;
+          const WcFacts& f = facts[ms];
+          const int n_rows = min(kWcRows, x.s.count * G - (rt + i) * kWcRows);
+          if (!wait_warp(&f_full[ms], u / kWcMeta) || !wait_warp(&s_full[st][wg], u >> 1)) {
+            ok = false;
+            break;
+          }
+          tm_fence_after();
+          const bool whole = (m.all >> i & 1u) && f.whole;
+          const float away = (float)(f.pos0 - key);  // (of the tile's first row; used where it is not negative)
+          // 32 rows: their raw sums to weights, added up; `bits` are the rows that see the key
+          auto weigh = [&](int c0, const float (&raw)[32], bool whole, uint32_t bits) {
+            unsigned long long t2[16];
+            if (capped) {  // y = raw·k, then cap·log2 e·y·T(y²), as in the chunk attention
+              unsigned long long z2[16];
+              float b4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+              for (int n = 0; n < 16; ++n) {
+                t2[n] = f2_mul(f2_pack(raw[2 * n], raw[2 * n + 1]), k2);
+                z2[n] = f2_mul(t2[n], t2[n]);
+                float y0, y1;
+                f2_unpack(z2[n], y0, y1);
+                b4[n & 3] = max3(b4[n & 3], y0, y1);
+              }
+              const float big = max3(max3(b4[0], b4[1], b4[2]), b4[3], 0.0f);
+              constexpr TanhPoly poly = tanh_poly();
+              if (__all_sync(0xffffffffu, big <= 0.25f)) {
+                const unsigned long long p0 = f2_splat(poly.near[0] * out), p1 = f2_splat(poly.near[1] * out),
+                                         p2 = f2_splat(poly.near[2] * out), p3 = f2_splat(poly.near[3] * out);
+#pragma unroll
+                for (int n = 0; n < 16; ++n)
+                  t2[n] = f2_mul(f2_fma(f2_fma(f2_fma(p3, z2[n], p2), z2[n], p1), z2[n], p0), t2[n]);
+              } else if (__all_sync(0xffffffffu, big <= 1.0f)) {
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                  unsigned long long r = f2_fma(z2[n], f2_splat(poly.far[6]), f2_splat(poly.far[5]));
+#pragma unroll
+                  for (int e = 4; e >= 0; --e) r = f2_fma(r, z2[n], f2_splat(poly.far[e]));
+                  t2[n] = f2_mul(f2_mul(r, f2_splat(out)), t2[n]);
+                }
+              } else {
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                  float y0, y1;
+                  f2_unpack(t2[n], y0, y1);
+                  t2[n] = f2_mul(f2_pack(soft_cap(y0, 1.0f, 1.0f), soft_cap(y1, 1.0f, 1.0f)), f2_splat(out));
+                }
+              }
+            }
+            // in steps, so that no row's chain waits for another's
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const bool near = biased && whole;
+              const float4 c = *reinterpret_cast<const float4*>((near ? f.near : f.c) + c0 + 4 * n);
+              unsigned long long a0 = f2_pack(c.x, c.y), a1 = f2_pack(c.z, c.w);
+              if (biased) {
+                const float4 sl = *reinterpret_cast<const float4*>(f.slope + c0 + 4 * n);
+                unsigned long long d0 = f2_splat(away), d1 = d0;
+                if (!whole) {  // (a prefix' keys may lie behind the row)
+                  const float4 ah = *reinterpret_cast<const float4*>(f.ahead + c0 + 4 * n);
+                  d0 = f2_pack(fabsf(ah.x + away), fabsf(ah.y + away));
+                  d1 = f2_pack(fabsf(ah.z + away), fabsf(ah.w + away));
+                }
+                a0 = f2_fma(f2_pack(sl.x, sl.y), d0, a0);
+                a1 = f2_fma(f2_pack(sl.z, sl.w), d1, a1);
+              }
+              t2[2 * n] = capped ? f2_add(t2[2 * n], a0) : f2_fma(f2_pack(raw[4 * n], raw[4 * n + 1]), k2, a0);
+              t2[2 * n + 1] = capped ? f2_add(t2[2 * n + 1], a1) : f2_fma(f2_pack(raw[4 * n + 2], raw[4 * n + 3]), k2, a1);
+            }
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+              float e0, e1;
+              f2_unpack(t2[n], e0, e1);
+              if (!whole) {
+                if (!(bits >> (2 * n) & 1u)) e0 = -CUDART_INF_F;
+                if (!(bits >> (2 * n + 1) & 1u)) e1 = -CUDART_INF_F;
+              }
+              t2[n] = f2_pack(ex2f(e0), ex2f(e1));
+            }
+#pragma unroll
+            for (int n = 0; n < 16; ++n) acc[n & 3] = f2_add(acc[n & 3], t2[n]);
+          };
+          const uint32_t from = s_tm + 256 * st;
+          if (whole) {  // (straight on, so that the sums stay where the loads put them)
+            float raw[kWcRows / 32][32];
+            tm_ld32(from, raw[0]);
+#pragma unroll
+            for (int c = 0; c < kWcRows / 32; ++c) {
+              tm_wait_ld();
+              tm_tie32(raw[c]);
+              if (c + 1 < kWcRows / 32) tm_ld32(from + 32 * (c + 1), raw[c + 1]);
+              weigh(32 * c, raw[c], true, 0xffffffffu);
+            }
+          } else {
+            // Rows lie in the order of their positions: those from the key's own on see it, up to the window's end.
+            int j0 = min(max(key - f.pos0, -1), kWcRows) * G - f.skip, j1 = kWcRows;
+            if (a.sc.window > 0)
+              j1 = (int)min(max((long long)key + a.sc.window - f.pos0, -1LL), (long long)kWcRows) * G - f.skip;
+            if (key < x.s.pre) {
+              j0 = 0;
+              j1 = kWcRows;
+            }
+            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+#pragma unroll 1
+            for (int c = 0; c < n_rows; c += 32) {
+              uint32_t bits = f.counts[c / 32] & below(j1 - c) & ~below(j0 - c);
+              if (a.sc.first_key && key >= x.s.pre) {
+#pragma unroll 8
+                for (int n = 0; n < 32; ++n)
+                  if (f.lo[c + n] > key) bits &= ~(1u << n);
+              }
+              if (!__any_sync(0xffffffffu, bits != 0u)) continue;
+              float raw[32];
+              tm_ld32(from + c, raw);
+              tm_wait_ld();
+              tm_tie32(raw);
+              weigh(c, raw, false, bits);
+            }
+          }
+          tm_fence_before();
+          mbar_arrive(&s_empty[st][wg]);
+        }
+      }
+      if (!ok) break;
+      float sum = f2_sum(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])));
+      if (x.s.nsplit > 1) {
+        // each warp for its own keys: the one that comes last adds the shares, in their order
+        g.part[x.id * kWcKeys + ks_] = sum;
+        __threadfence();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) last = atomicAdd(g.done + x.first * 8 + warp, 1) == x.s.nsplit - 1;
+        if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+        __threadfence();
+        sum = 0.0f;
+        for (int i = 0; i < x.s.nsplit; ++i) sum += __ldcg(g.part + (x.first + (long long)i * Hkv * x.s.T) * kWcKeys + ks_);
+        if (there && key < x.s.fresh && a.decay != 0.0f) before = *wp;
+      }
+      if (there) *wp = fmaf(before, a.decay, sum);
+    }
+  } else if (wg < 4) {  // ------------------------------------------------ keys
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
+    const int cw = warp - 8;                      // keys 32·cw .. 32·cw + 31 of a tile
+    constexpr int CPR = D / 16;                   // 16-code chunks of a key
+    constexpr int RPI = 32 / CPR, NI = 32 / RPI;  // keys a load, loads of a warp's keys
+    constexpr int PW = 32 / P;                    // pages of a warp's keys
+    // (as in the chunk attention: eight lanes store to eight banks' quads)
+    const int cch = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane % CPR;
+    const int crow = D == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane / CPR;
+    // the next segment with keys that somebody may see: its pages as the table has them, looked at when their codes
+    // are asked for
+    struct Ahead {
+      long long id;
+      int kvh, L, ph, key;
+    };
+    auto find = [&](long long id) -> Ahead {
+      for (; id < n_segs; id += gridDim.x) {
+        const WcSeg x = wc_seg<P>(g, few, id, slot);
+        if (!x.seen) continue;
+        Ahead n{id, x.kvh, x.s.L, -1, kNoKey};
+        const int t = x.kt * PT + cw * PW + lane;
+        if (lane < PW && t < x.pages()) {
+          n.key = x.page(t) * P;
+          n.ph = a.c.block_table[(size_t)x.s.seq * a.c.maxp + x.page(t)];
+        }
+        return n;
+      }
+      return Ahead{id, 0, 0, -1, kNoKey};
+    };
+    uint4 codes[NI];
+    auto load = [&](const Ahead& n) {
+      const int key = n.ph >= 0 && n.ph < a.c.nphys ? n.key : kNoKey;  // (the sums flag other pages)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int rr = i * RPI + crow, tk = rr % P;
+        const int fq = __shfl_sync(0xffffffffu, n.ph, rr / P), kq = __shfl_sync(0xffffffffu, key, rr / P);
+        codes[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (kq + tk < n.L)  // (false where there is no page)
+          codes[i] = __ldg(reinterpret_cast<const uint4*>(a.c.k_pool + (((size_t)fq * Hkv + n.kvh) * P + tk) * D + cch * 16));
+      }
+    };
+    int tiles = 0;  // key tiles so far
+    Ahead now = find(blockIdx.x);
+    Ahead next = find(now.id + gridDim.x);
+    if (now.id < n_segs) load(now);
+    while (now.id < n_segs && ok) {
+      if (tiles > 0 && !wait_warp(&k_empty, tiles - 1)) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int rr = 32 * (cw & 3) + i * RPI + crow;
+        const uint32_t dst = k_sm + (cw >> 2) * HALF;
+        uint4 h0, h1;
+        codes_bf16<I8>(codes[i].x, h0.x, h0.y);
+        codes_bf16<I8>(codes[i].y, h0.z, h0.w);
+        codes_bf16<I8>(codes[i].z, h1.x, h1.y);
+        codes_bf16<I8>(codes[i].w, h1.z, h1.w);
+        sts128(dst + tile_off(rr, 2 * cch), h0);
+        sts128(dst + tile_off(rr, 2 * cch + 1), h1);
+      }
+      asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+      mbar_arrive(&k_full);
+      now = next;
+      if (now.id < n_segs) {
+        load(now);
+        next = find(now.id + gridDim.x);
+      }
+      ++tiles;
+    }
+  } else {  // ------------------------------------------------ products, and the rows' copies
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+    if (warp < 18) {  // a warp a half of the keys, one elected thread of it
+      const int h = warp - 16;
+      const uint64_t k_desc = smem_desc(k_sm + h * HALF, 16, 1024), q_desc = smem_desc(q_sm, 16, 1024);
+      int tiles = 0;
+      for (long long id = blockIdx.x; id < n_segs && ok; id += gridDim.x) {
+        const WcSeg x = wc_seg<P>(g, few, id, slot);
+        if (!x.seen) continue;
+        ok = wait_warp(&k_full, tiles);
+        tm_fence_after();
+        for (int rt = x.rt; rt < x.rt_end && ok; rt += 32) {
+          WcMask m = wc_mask(g, x, rt);
+          for (; m.some; m.some &= m.some - 1u, ++u) {
+            const int i = __ffs(m.some) - 1, st = u & 1, qs = u % kWcQ;
+            const int n_rows = min(kWcRows, x.s.count * G - (rt + i) * kWcRows);
+            if (!wait_warp(&q_full[qs], u / kWcQ) || (u >= 2 && !wait_warp(&s_empty[st][h], (u >> 1) - 1))) {
+              ok = false;
+              break;
+            }
+            tm_fence_after();
+            if (elect_one()) {
+              const uint32_t id_s = instr_desc_bf16((n_rows + 15) / 16 * 16);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {  // (addresses advance in units of 16 bytes)
+                const uint32_t o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                mma_ss(tm + 256 * st + 128 * h, k_desc + o, q_desc + (uint32_t)(qs * (HALF >> 4)) + o, id_s, k > 0);
+              }
+              tm_commit(&s_full[st][h]);
+              tm_commit(&q_empty[qs]);
+            }
+            __syncwarp();
+          }
+        }
+        if (ok && elect_one()) tm_commit(&k_empty);
+        __syncwarp();
+        ++tiles;
+      }
+    } else if (warp == 18) {
+      for (long long id = blockIdx.x; id < n_segs && ok; id += gridDim.x) {
+        const WcSeg x = wc_seg<P>(g, few, id, slot);
+        for (int rt = x.rt; rt < x.rt_end && ok && x.seen; rt += 32) {
+          WcMask m = wc_mask(g, x, rt);
+          for (; m.some; m.some &= m.some - 1u, ++u) {
+            const int i = __ffs(m.some) - 1, st = u % kWcQ, ms = u % kWcMeta;
+            if (u >= kWcQ && !wait_warp(&q_empty[st], u / kWcQ - 1)) {
+              ok = false;
+              break;
+            }
+            if (elect_one()) {
+              const size_t at = (size_t)x.kvh * g.max_tiles + x.s.rt0 + rt + i;
+              mbar_expect_tx(&q_full[st], HALF);
+              bulk_g2s(dyn_sm + (q_sm - smem_u32(dyn_sm)) + st * HALF, g.packed + at * (HALF / 16), HALF, &q_full[st]);
+              mbar_expect_tx(&f_full[ms], sizeof(WcFacts));
+              bulk_g2s(&facts[ms], g.facts + at, sizeof(WcFacts), &f_full[ms]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      // what was asked for lands before the block ends, whatever gave up
+      if (!ok || gave_up) {
+        for (int k = max(0, u - kWcQ); k < u; ++k) mbar_wait_second(&q_full[k % kWcQ], (uint32_t)(k / kWcQ & 1));
+        for (int k = max(0, u - kWcMeta); k < u; ++k) mbar_wait_second(&f_full[k % kWcMeta], (uint32_t)(k / kWcMeta & 1));
+      }
+    }
+  }
+  tm_fence_before();
+  __syncthreads();
+  tm_fence_after();
+  if (warp == 16) tm_free(tm);
+  if (tid == 0 && gave_up) raise_flag(a.c.status, ENTMAXKV_DEV_TIMEOUT);
+}
+
+// The product kernel for one code type and head dimension (a translation unit each).
+template <bool I8, int D>
+cudaError_t weigh_chunk_run(const WcArgs& g, cudaStream_t st);
+
+template <bool I8, int D, int P, bool CAP, bool BIAS>
+cudaError_t weigh_chunk_start(const WcArgs& g, cudaStream_t st) {
+  const int smem = (2 + kWcQ) * 128 * D * 2 + 1024;
+  const cudaError_t e = ensure_smem((const void*)weigh_chunk_kernel<I8, D, P, CAP, BIAS>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_k(true, weigh_chunk_kernel<I8, D, P, CAP, BIAS>, dim3(g.blocks), dim3(kWcThreads), (size_t)smem, st, g);
+}
+template <bool I8, int D, int P>
+cudaError_t weigh_chunk_form(const WcArgs& g, cudaStream_t st) {
+  const bool cap = g.a.sc.cap > 0.0f, bias = g.a.sc.slopes != nullptr;
+  if (cap) return bias ? weigh_chunk_start<I8, D, P, true, true>(g, st) : weigh_chunk_start<I8, D, P, true, false>(g, st);
+  return bias ? weigh_chunk_start<I8, D, P, false, true>(g, st) : weigh_chunk_start<I8, D, P, false, false>(g, st);
+}
+template <bool I8, int D>
+cudaError_t weigh_chunk_pages(const WcArgs& g, cudaStream_t st) {
+  return g.a.c.P == 32 ? weigh_chunk_form<I8, D, 32>(g, st) : weigh_chunk_form<I8, D, 16>(g, st);
+}
+
+}  // namespace ekv
