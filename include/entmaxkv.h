@@ -660,9 +660,10 @@ int32_t entmaxkv_weigh_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* c
  * A slot with a bad row, named a second time or with a page outside the pool is
  * left as it was (ENTMAXKV_DEV_BAD_SEQ_ID, _BAD_BATCH, _BAD_PAGE_TABLE); a list that
  * would pass num_phys_pages raises ENTMAXKV_DEV_CAPACITY and takes no more.
- * Refused (ENTMAXKV_ERR_INVALID_ARG): above < keep, keep < 1 or more than a row of the table
- * holds, sinks + recent > keep.
- *   weights      as weigh_q8 writes them; NULL where sinks + recent = keep
+ * Refused: a pool of 2^32 tokens and more (ENTMAXKV_ERR_UNSUPPORTED); above < keep, keep < 1 or more than a row of the table
+ * holds, sinks + recent > keep (ENTMAXKV_ERR_INVALID_ARG).
+ *   weights      as weigh_q8 writes them, from a 16-byte boundary; NULL where
+ *                sinks + recent = keep
  *   weights_out  may be weights; otherwise only the evicted sequences' kept places are written
  *   lens_out     [max_seqs] evicted rows get `keep`, others are left; may be cache->seq_lens
  *   free_pages   [num_phys_pages] the stack; free_count_out may be free_count

@@ -264,6 +264,7 @@ int32_t entmaxkv_weigh_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* c
 static int check_evict(const entmaxkv_config* cfg, int32_t n_seqs, int32_t keep) {
   const int st = check_q8_config(cfg);
   if (st) return st;
+  if ((long long)cfg->num_phys_pages * cfg->page_size > 0xffffffffLL) return ENTMAXKV_ERR_UNSUPPORTED;  // (EvictArgs::src)
   return n_seqs < 0 || n_seqs > 65535 || keep < 1 || (long long)keep > (long long)cfg->max_pages_per_seq * cfg->page_size
              ? ENTMAXKV_ERR_INVALID_ARG : ENTMAXKV_OK;
 }
@@ -282,7 +283,7 @@ int32_t entmaxkv_evict_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* c
   if (above < keep || sinks < 0 || recent < 0 || (long long)sinks + recent > keep) return ENTMAXKV_ERR_INVALID_ARG;
   if (n_seqs == 0) return ENTMAXKV_OK;
   if (!seq_ids || !lens_out || !free_pages || !free_count || !free_count_out) return ENTMAXKV_ERR_INVALID_ARG;
-  if (weights ? !weights_out : sinks + recent < keep) return ENTMAXKV_ERR_INVALID_ARG;
+  if (weights ? !weights_out || ((uintptr_t)weights & 15u) : sinks + recent < keep) return ENTMAXKV_ERR_INVALID_ARG;
   if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < evict_bytes(*cfg, n_seqs, keep))
     return ENTMAXKV_ERR_WORKSPACE_TOO_SMALL;
   const int sms = device_sms();

@@ -9,27 +9,37 @@
 // of the exact product, as append rescales. Pages that are left over go back on
 // the free list.
 //
-// Two launches. The first (a cluster, a thread a slot) decides which slots are
-// evicted, and does the books: lengths, free list, the list of what to move. In
-// the second a cluster of 8 or 16 blocks has one (slot, KV head) at a time:
-//   select  the keep-th largest weight by three counts of 11, 11 and 10 bits of
-//           the weights' order-preserving codes, summed over the cluster through
-//           distributed shared memory; equal weights by index;
-//   move    in place and in one pass: a warp holds one page of the result, K and
-//           V, in registers; when all warps of the cluster have loaded theirs (a
-//           cluster barrier) they write. Source pages of later pages lie behind
-//           all pages written so far, as src(d) ≥ d and src grows.
+// plan    (a cluster, a thread a slot) decides which slots are evicted, and does
+//         the books: lengths, free list, the list of what to move.
+// select  (a block or a cluster for a (slot, KV head)) finds the keep-th largest
+//         weight by counts of a few bits at a time of the weights' order-preserving
+//         codes, summed over the cluster through distributed shared memory, and
+//         lists the kept keys; equal weights go by index.
+// move    (a block or a cluster for a (slot, KV head, side)) in place and in one
+//         pass: a warp holds one page of the result in registers; when all warps of
+//         the cluster have loaded theirs (a cluster barrier) they write. Source pages
+//         of later pages lie behind all pages written so far, as src(d) ≥ d and src
+//         grows.
+// One (slot, KV head) is a chain of latencies (loads, counts, barriers), so they run
+// side by side: a block each where they are many, clusters of 8 where they are few
+// and long. What counts is how many slots are evicted, which the plan finds out: both
+// forms are launched, and one returns at once.
 //
-// Bound: the bytes of the weights and the kept codes, and the latency of the
-// chain select - barrier - move where few sequences are evicted.
+// Bound: the bytes of the weights and the kept codes, and that chain.
 #include "q8_tiles.cuh"
 
 namespace ekv {
 
 constexpr int kEvictPlanThreads = 1024, kEvictPlanBlocks = 8;
-constexpr int kEvictWarps = 8, kEvictThreads = kEvictWarps * 32;
-constexpr int kEvictKeys = 16384;  // a block's weights that stay in shared memory; more are read again for each count
-constexpr int kBins = 2048;
+constexpr int kSelectWarps = 32, kSelectThreads = kSelectWarps * 32;
+constexpr int kEvictKeys = 40960;  // a block's weights that stay in shared memory; more are read again for each count
+// A block alone counts 11, 11 and 10 bits. A cluster's counts are read by each of its blocks, at about 9 bytes a clock:
+// 8 bits at a time (2048 counts of 8 blocks: 7000 clocks a pass; 256: 1000).
+constexpr int kBins = 2048, kClusterBins = 256;
+constexpr int kEvictCluster = 8;
+// Keys to keep from which few (slot, KV head) pairs get a cluster each: at most 4 waves of the 32 pages that a block's
+// warps hold are below.
+constexpr int kEvictLong = 4096;
 
 struct EvictItem {
   int seq, L;
@@ -49,7 +59,8 @@ struct EvictArgs {
   int* bad;          // [n] slots with a page outside the pool
   EvictItem* items;  // [n]
   int* n_items;
-  int32_t* src;      // [n][Hkv][keep] old key of each kept one
+  uint32_t* src;     // [n][Hkv][keep] where each kept key lies: physical page · page_size + offset
+  long long from, to;  // (slot, KV head) pairs to move for which this launch does: from < pairs <= to
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -71,6 +82,82 @@ __device__ __forceinline__ uint4 ld_cluster4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
+}
+
+// The same for at most 1024 slots, a thread each: what the general form leaves in
+// memory between its steps stays in registers and shared memory (one sequence of
+// 131k tokens: X us against 11).
+__global__ void __launch_bounds__(kEvictPlanThreads) evict_plan_few_kernel(EvictArgs a) {
+  pdl_enter();
+  __shared__ int sh_scan[32];
+  __shared__ int end_sh[kEvictPlanThreads], seq_sh[kEvictPlanThreads], bad_sh[kEvictPlanThreads];
+  const int tid = threadIdx.x, P = a.c.P;
+  const int all = gridDim.x * kEvictPlanThreads, me = blockIdx.x * kEvictPlanThreads + tid;
+  const bool head = blockIdx.x == 0;
+  uint32_t* status = head ? a.c.status : nullptr;
+  bad_sh[tid] = 0;
+  asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+  const int fc = min(max(*a.free_count, 0), a.c.nphys), kept = (a.keep + P - 1) / P;
+  int seq = -1, L = 0;
+  if (tid < a.n) seq = seq_row(a.seq_ids, tid, a.c.max_seqs, status);
+  seq_sh[tid] = seq;
+  if (seq >= 0) L = seq_len_clamped(a.c.seq_lens, seq, a.c.maxp, P, status);
+  __syncthreads();
+  if (seq >= 0) {
+    bool before = false;
+#pragma unroll 8
+    for (int j = 0; j < tid; ++j) before |= seq_sh[j] == seq;
+    if (before) {
+      raise_flag(status, ENTMAXKV_DEV_BAD_BATCH);
+      L = 0;
+    }
+  }
+  if (L <= a.above) L = 0;
+  const int have = (L + P - 1) / P;
+  int total, at = block_exclusive_scan(have, sh_scan, total);
+  end_sh[tid] = at + have;
+  __syncthreads();
+  auto find = [&](int j) {  // the slot that holds the j-th page
+    int lo = 0, hi = kEvictPlanThreads - 1;
+    while (lo < hi) {
+      const int m = (lo + hi) >> 1;
+      if (end_sh[m] > j) hi = m;
+      else lo = m + 1;
+    }
+    return lo;
+  };
+  asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+#pragma unroll 4
+  for (int j = me; j < total; j += all) {
+    const int i = find(j);
+    if (phys_page(a.c.block_table, seq_sh[i], j - (i ? end_sh[i - 1] : 0), a.c.maxp, a.c.nphys, a.c.status) < 0)
+      for (int r = 0; r < (int)gridDim.x; ++r)  // (every block is told)
+        asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(of_block(smem_u32(&bad_sh[i]), r)), "r"(1) : "memory");
+  }
+  cluster_sync();  // (and every read of the old lengths and of the list's height is done)
+  if (bad_sh[tid]) L = 0;
+  int items;
+  const int item = block_exclusive_scan(L > 0, sh_scan, items), gone = L > 0 ? have - kept : 0;
+  at = block_exclusive_scan(gone, sh_scan, total);
+  end_sh[tid] = at + gone;
+  bad_sh[tid] = have;
+  __syncthreads();
+#pragma unroll 4
+  for (int j = me; j < total; j += all) {
+    const int i = find(j), k = j - (i ? end_sh[i - 1] : 0);
+    const long long to = (long long)fc + j;
+    if (to < a.c.nphys) a.free_pages[to] = a.c.block_table[(size_t)seq_sh[i] * a.c.maxp + bad_sh[i] - 1 - k];
+    else raise_flag(a.c.status, ENTMAXKV_DEV_CAPACITY);
+  }
+  if (!head) return;
+  if (L > 0) {
+    a.items[item] = EvictItem{seq, L};
+    a.lens_out[seq] = a.keep;
+  }
+  if (tid == 0) {
+    *a.n_items = items;
+    *a.count_out = min(fc + total, a.c.nphys);
+  }
 }
 
 // Slots 1024 at a time in every block alike; pages are shared out over the
@@ -203,31 +290,57 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
   }
 }
 
-template <bool I8, int D, int P>
-__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(EvictArgs a) {
+// The launch's block or cluster count, and whether it is this form's turn.
+struct EvictTurn {
+  int C, rank, first, step;
+  long long n_work;
+  bool mine;
+};
+__device__ __forceinline__ EvictTurn evict_turn(const EvictArgs& a, int sides) {
+  uint32_t size;
+  asm("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(size));
+  EvictTurn t;
+  t.C = (int)size;
+  t.rank = (int)cluster_rank();
+  t.first = blockIdx.x / t.C;
+  t.step = gridDim.x / t.C;
+  const long long pairs = (long long)*a.n_items * a.c.Hkv;
+  t.n_work = pairs * sides;
+  t.mine = pairs > a.from && pairs <= a.to;
+  return t;
+}
+__device__ __forceinline__ void evict_sync(int C) {
+  if (C > 1) cluster_sync();
+  else __syncthreads();
+}
+
+template <int P>
+__global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(EvictArgs a) {
   pdl_enter();
   extern __shared__ __align__(16) uint32_t keys_sm[];  // [kEvictKeys]
-  __shared__ __align__(16) uint32_t hist[3][kBins];
+  __shared__ __align__(16) uint32_t hist[3 * kBins];
   __shared__ int sh_scan[32], sh_digit, sh_want;
-  __shared__ int warp_more[kEvictWarps], warp_same[kEvictWarps];
+  __shared__ int warp_more[kSelectWarps], warp_same[kSelectWarps];
   __shared__ __align__(16) int block_cnt[4];  // kept for certain, equal to the edge
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint32_t C;
-  asm("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(C));
-  const int rank = (int)cluster_rank(), Hkv = a.c.Hkv, keep = a.keep;
-  const int n_clusters = gridDim.x / C, take = keep - a.sinks - a.recent;
-  const long long n_work = (long long)*a.n_items * Hkv;
-  for (long long it = blockIdx.x / C; it < n_work; it += n_clusters) {
+  const int Hkv = a.c.Hkv, keep = a.keep, take = keep - a.sinks - a.recent;
+  const EvictTurn turn = evict_turn(a, 1);
+  if (!turn.mine) return;
+  const int C = turn.C, rank = turn.rank;
+  for (long long it = turn.first; it < turn.n_work; it += turn.step) {
     const int item = (int)(it / Hkv), h = (int)(it - (long long)item * Hkv);
     const EvictItem x = a.items[item];
     const int32_t* bt = a.c.block_table + (size_t)x.seq * a.c.maxp;
-    int32_t* src = a.src + (size_t)it * keep;
-    const int seg = ((x.L + (int)C - 1) / (int)C + 31) / 32 * 32;
+    uint32_t* src = a.src + (size_t)it * keep;
+    const int seg = ((x.L + C - 1) / C + 127) / 128 * 128;
     const int lo = min(x.L, rank * seg), hi = min(x.L, lo + seg);
-    const int c0 = a.sinks, c1 = x.L - a.recent;  // keys that are chosen among
-    auto code = [&](int i) -> uint32_t {  // larger weights have larger codes; NaN the largest, −0 is 0
-      const float w = a.w[((size_t)bt[i / P] * Hkv + h) * P + i % P];
+    const int c0 = max(lo, a.sinks), c1 = min(hi, x.L - a.recent);  // this block's keys that are chosen among
+    auto code_of = [](float w) -> uint32_t {  // larger weights have larger codes; NaN the largest, −0 is 0
       return w != w ? 0xffffffffu : ord_enc(w + 0.0f);
+    };
+    auto codes_at = [&](int i) -> uint4 {  // of four keys, the first a multiple of 4; any behind the sequence's end
+      const float4 w = *reinterpret_cast<const float4*>(a.w + ((size_t)bt[i / P] * Hkv + h) * P + i % P);
+      return make_uint4(code_of(w.x), code_of(w.y), code_of(w.z), code_of(w.w));
     };
     const bool held = seg <= kEvictKeys;
     uint32_t edge = 0u;
@@ -235,40 +348,47 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(EvictArgs a) {
     if (take > 0) {
       if (held) {
 #pragma unroll 8
-        for (int i = lo + tid; i < hi; i += kEvictThreads) keys_sm[i - lo] = code(i);
+        for (int i = lo + 4 * tid; i < hi; i += 4 * kSelectThreads)
+          *reinterpret_cast<uint4*>(keys_sm + i - lo) = codes_at(i);
       }
-      for (int i = tid; i < 3 * kBins; i += kEvictThreads) (&hist[0][0])[i] = 0u;
+      const int bits = C > 1 ? 8 : 11, bins = 1 << bits, passes = C > 1 ? 4 : 3;
+      for (int i = tid; i < passes * bins; i += kSelectThreads) hist[i] = 0u;
       __syncthreads();
+#pragma unroll 1
+      for (int p = 0; p < passes; ++p) {
+        const int shift = max(0, 32 - bits * (p + 1));
+        const uint32_t mask = C == 1 && p == 2 ? 1023u : (uint32_t)bins - 1u, above = p ? 0xffffffffu << (32 - bits * p) : 0u;
+        uint32_t* count = hist + p * bins;
+#pragma unroll 4
+        for (int i = lo + 4 * tid; i < hi; i += 4 * kSelectThreads) {
+          const uint4 k4 = held ? *reinterpret_cast<const uint4*>(keys_sm + i - lo) : codes_at(i);
+          const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        const int shift = p == 0 ? 21 : p == 1 ? 10 : 0;
-        const uint32_t mask = p == 2 ? 1023u : 2047u, above = p == 0 ? 0u : 0xffffffffu << (p == 1 ? 21 : 10);
-        for (int i = max(lo, c0) + tid; i < min(hi, c1); i += kEvictThreads) {
-          const uint32_t k = held ? keys_sm[i - lo] : code(i);
-          if (((k ^ edge) & above) == 0u) atomicAdd(&hist[p][k >> shift & mask], 1u);
+          for (int j = 0; j < 4; ++j)
+            if (i + j >= c0 && i + j < c1 && ((k[j] ^ edge) & above) == 0u) atomicAdd(count + (k[j] >> shift & mask), 1u);
         }
-        cluster_sync();
-        // eight bins a thread, the largest codes with the first thread
-        uint32_t n8[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-        const int bin0 = kBins - 8 - 8 * tid;
-        for (int r = 0; r < (int)C; ++r) {
-          const uint32_t at = of_block(smem_u32(&hist[p][bin0]), r);
-          const uint4 u = ld_cluster4(at), v = ld_cluster4(at + 16);
-          n8[0] += u.x, n8[1] += u.y, n8[2] += u.z, n8[3] += u.w;
-          n8[4] += v.x, n8[5] += v.y, n8[6] += v.z, n8[7] += v.w;
-        }
-        int sum = 0, total;
+        evict_sync(C);
+        // four bins a thread, the largest codes with the first thread
+        uint32_t n4[4] = {0u, 0u, 0u, 0u};
+        const int bin0 = bins - 4 - 4 * tid;
+        if (bin0 >= 0) {
+          uint4 u[kEvictCluster];  // (all blocks' counts in flight)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += (int)n8[j];
-        int before = block_exclusive_scan(sum, sh_scan, total);
+          for (int r = 0; r < kEvictCluster; ++r)
+            u[r] = r < C ? ld_cluster4(of_block(smem_u32(count + bin0), r)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int r = 0; r < kEvictCluster; ++r) n4[0] += u[r].x, n4[1] += u[r].y, n4[2] += u[r].z, n4[3] += u[r].w;
+        }
+        const int sum = (int)(n4[0] + n4[1] + n4[2] + n4[3]);
+        int total, before = block_exclusive_scan(sum, sh_scan, total);
         if (before < want && before + sum >= want) {
 #pragma unroll
-          for (int j = 7; j >= 0; --j) {
-            if (before < want && before + (int)n8[j] >= want) {
+          for (int j = 3; j >= 0; --j) {
+            if (before < want && before + (int)n4[j] >= want) {
               sh_digit = bin0 + j;
               sh_want = want - before;
             }
-            before += (int)n8[j];
+            before += (int)n4[j];
           }
         }
         __syncthreads();
@@ -277,125 +397,163 @@ __global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(EvictArgs a) {
         __syncthreads();
       }
     }
-    // Each warp has a part of the block's keys: how many are kept for certain and how many equal the edge, then the
-    // place of each kept key, the certain ones before it plus the equal ones, of which the first `want` are taken.
-    const int wseg = seg / 32 / kEvictWarps + 1, w0 = min(hi, lo + warp * wseg * 32), w1 = min(hi, w0 + wseg * 32);
-    auto look = [&](int i, bool& more, bool& same) {
-      more = i < w1 && (i < c0 || i >= c1);
-      same = false;
-      if (i < w1 && !more && take > 0) {
-        const uint32_t k = held ? keys_sm[i - lo] : code(i);
-        more = k > edge;
-        same = k == edge;
+    // Each warp has a part of the block's keys, four of them a lane at a time: how many are kept for certain and how
+    // many equal the edge (in the two halves of a word: a block has fewer than 2^16 keys a lane), then the place of
+    // each kept key, the certain ones before it plus the equal ones, of which the first `want` are taken.
+    const int wseg = (seg / 128 + kSelectWarps - 1) / kSelectWarps * 128;
+    const int w0 = min(hi, lo + warp * wseg), w1 = min(hi, w0 + wseg);
+    auto look = [&](int i, uint32_t& more, uint32_t& same) {  // a bit a key
+      more = same = 0u;
+      if (i >= w1) return;
+      uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
+      if (take > 0) k4 = held ? *reinterpret_cast<const uint4*>(keys_sm + i - lo) : codes_at(i);
+      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = i + j < w1, end = i + j < a.sinks || i + j >= x.L - a.recent, among = in && !end && take > 0;
+        if ((in && end) || (among && k[j] > edge)) more |= 1u << j;
+        if (among && k[j] == edge) same |= 1u << j;
       }
     };
     int n_more = 0, n_same = 0;
-    for (int i = w0; i < w1; i += 32) {
-      bool more, same;
-      look(i + lane, more, same);
-      n_more += __popc(__ballot_sync(0xffffffffu, more));
-      n_same += __popc(__ballot_sync(0xffffffffu, same));
+#pragma unroll 2
+    for (int i = w0 + 4 * lane; i - 4 * lane < w1; i += 128) {
+      uint32_t more, same;
+      look(i, more, same);
+      n_more += __popc(more);
+      n_same += __popc(same);
     }
+    n_more = __reduce_add_sync(0xffffffffu, n_more);
+    n_same = __reduce_add_sync(0xffffffffu, n_same);
     if (lane == 0) {
       warp_more[warp] = n_more;
       warp_same[warp] = n_same;
     }
     __syncthreads();
-    if (tid == 0) {
-      int m = 0, s = 0;
-      for (int i = 0; i < kEvictWarps; ++i) {
-        m += warp_more[i];
-        s += warp_same[i];
+    if (warp == 0) {
+      const int m = __reduce_add_sync(0xffffffffu, lane < kSelectWarps ? warp_more[lane] : 0);
+      const int n = __reduce_add_sync(0xffffffffu, lane < kSelectWarps ? warp_same[lane] : 0);
+      if (lane == 0) {
+        block_cnt[0] = m;
+        block_cnt[1] = n;
       }
-      block_cnt[0] = m;
-      block_cnt[1] = s;
     }
-    cluster_sync();
-    n_more = n_same = 0;
-    for (int r = 0; r < rank; ++r) {
-      const uint4 u = ld_cluster4(of_block(smem_u32(block_cnt), r));
-      n_more += (int)u.x;
-      n_same += (int)u.y;
+    evict_sync(C);
+    {  // those of the blocks and of the warps in front
+      uint4 u = make_uint4(0u, 0u, 0u, 0u);
+      if (lane < rank) u = ld_cluster4(of_block(smem_u32(block_cnt), lane));
+      n_more = __reduce_add_sync(0xffffffffu, (int)u.x + (lane < warp ? warp_more[lane] : 0));
+      n_same = __reduce_add_sync(0xffffffffu, (int)u.y + (lane < warp ? warp_same[lane] : 0));
     }
-    for (int i = 0; i < warp; ++i) {
-      n_more += warp_more[i];
-      n_same += warp_same[i];
-    }
-    for (int i = w0; i < w1; i += 32) {
-      bool more, same;
-      look(i + lane, more, same);
-      const uint32_t bm = __ballot_sync(0xffffffffu, more), bs = __ballot_sync(0xffffffffu, same);
-      const uint32_t below = (1u << lane) - 1u;
-      const int m = n_more + __popc(bm & below), s = n_same + __popc(bs & below);
-      if (more || (same && s < want)) {
-        const int to = m + min(s, want);
-        if (to < keep) src[to] = i + lane;
+    for (int i0 = w0; i0 < w1; i0 += 1024) {
+      int page[1024 / P / 32];  // of the next 1024 keys, as the table has them
+#pragma unroll
+      for (int q = 0; q < 1024 / P / 32; ++q) page[q] = i0 / P + 32 * q + lane <= (x.L - 1) / P ? bt[i0 / P + 32 * q + lane] : 0;
+      const int i1 = min(w1, i0 + 1024);
+      for (int i = i0 + 4 * lane; i - 4 * lane < i1; i += 128) {
+        uint32_t more, same;
+        look(i, more, same);
+        const int mine = __popc(more) | __popc(same) << 16;
+        int inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
+        }
+        const int all = __shfl_sync(0xffffffffu, inc, 31);
+        int m = n_more + ((inc - mine) & 0xffff), n = n_same + ((inc - mine) >> 16);
+        const int at = (i - i0) / P;
+        int ph = __shfl_sync(0xffffffffu, page[0], at & 31);
+        if (P == 16) {
+          const int ph1 = __shfl_sync(0xffffffffu, page[1024 / P / 32 - 1], at & 31);
+          if (at >= 32) ph = ph1;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool certain = more >> j & 1u, level = same >> j & 1u;
+          const int to = m + min(n, want);
+          if ((certain || (level && n < want)) && to < keep) src[to] = (uint32_t)ph * P + (i + j) % P;
+          m += certain;
+          n += level;
+        }
+        n_more += all & 0xffff;
+        n_same += all >> 16;
       }
-      n_more += __popc(bm);
-      n_same += __popc(bs);
     }
-    cluster_sync();  // the list is there, and every weight has been read
-    constexpr int LPR = D / 16, RPI = 32 / LPR, NI = P / RPI;  // lanes a row, rows a load, loads of a page
-    const int pages = (keep + P - 1) / P, wave = (int)C * kEvictWarps;
-    const int sub = lane / LPR, ch = lane % LPR;
-    for (int j0 = 0; j0 < pages; j0 += wave) {
-      const int j = j0 + warp * (int)C + rank, rows = min(P, keep - j * P);
-      const int d = j * P + min(lane, rows - 1);
+    evict_sync(C);  // counts and histograms are done with in every block
+  }
+}
+
+template <bool I8, int D, int P>
+__global__ void __launch_bounds__(1024, 1) evict_move_kernel(EvictArgs a) {
+  pdl_enter();
+  constexpr int LPR = D / 16, RPI = 32 / LPR, NI = P / RPI;  // lanes a row, rows a load, loads of a page
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, Hkv = a.c.Hkv, keep = a.keep;
+  const EvictTurn turn = evict_turn(a, 2);
+  if (!turn.mine) return;
+  const int pages = (keep + P - 1) / P, wave = turn.C * (blockDim.x >> 5);
+  const int sub = lane / LPR, ch = lane % LPR;
+  for (long long it = turn.first; it < turn.n_work; it += turn.step) {
+    const long long pair = it >> 1;
+    const int side = (int)(it & 1), item = (int)(pair / Hkv), h = (int)(pair - (long long)item * Hkv);
+    const int32_t* bt = a.c.block_table + (size_t)a.items[item].seq * a.c.maxp;
+    const uint32_t* src = a.src + (size_t)pair * keep;
+    uint8_t* pool = side ? a.c.v_pool : a.c.k_pool;
+    float* scales = side ? a.c.v_scale : a.c.k_scale;
+    const bool weighs = a.w && !side;
+    auto list = [&](int j) -> uint32_t {  // where the lane's key of page j lies
+      return j < pages ? src[j * P + min(lane, min(P, keep - j * P) - 1)] : 0u;
+    };
+    int j = warp * turn.C + turn.rank;
+    uint32_t next = list(j);
+    for (int j0 = 0; j0 < pages; j0 += wave, j += wave) {
+      const int rows = min(P, keep - j * P);
       const bool mine = j < pages;
-      int i = mine ? __ldcg(src + d) : 0;
-      const bool moves = mine && __shfl_sync(0xffffffffu, i, max(rows, 1) - 1) != j * P + rows - 1;
-      uint4 kc[NI], vc[NI];
-      float sk = 0.0f, sv = 0.0f, w = 0.0f;
+      const uint32_t t = next;
+      const size_t to = mine ? (size_t)bt[j] * Hkv + h : 0;
+      next = list(j + wave);
+      // (a key that lies where it should has all before it in their places)
+      const bool moves = mine && __shfl_sync(0xffffffffu, t, max(rows, 1) - 1) != (uint32_t)bt[mine ? j : 0] * P + rows - 1;
+      uint4 codes[NI];
+      float top = 0.0f, w = 0.0f;
       if (moves) {
-        const size_t at = (size_t)bt[i / P] * Hkv + h;  // page and head of the lane's key
-        const int off = i % P;
+        const size_t at = (size_t)(t / P) * Hkv + h;  // page and head of the lane's key
+        const size_t key = at * P + t % P;
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
-          const int rl = min(n * RPI + sub, rows - 1);
-          const size_t from = (__shfl_sync(0xffffffffu, (unsigned long long)at, rl) * P +
-                               __shfl_sync(0xffffffffu, off, rl)) * D + ch * 16;
-          kc[n] = __ldcg(reinterpret_cast<const uint4*>(a.c.k_pool + from));
-          vc[n] = __ldcg(reinterpret_cast<const uint4*>(a.c.v_pool + from));
+          const size_t from = __shfl_sync(0xffffffffu, (unsigned long long)key, min(n * RPI + sub, rows - 1)) * D + ch * 16;
+          codes[n] = __ldcg(reinterpret_cast<const uint4*>(pool + from));
         }
-        const float k1 = __ldcg(a.c.k_scale + at), v1 = __ldcg(a.c.v_scale + at);
-        if (a.w) w = __ldcg(a.w + at * P + off);
-        sk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(k1)));
-        sv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v1)));
-        const float rk = __fdiv_rn(k1, sk), rv = __fdiv_rn(v1, sv);
-        auto rescale = [&](uint4 (&c)[NI], float ratio) {
-          if (!__any_sync(0xffffffffu, ratio != 1.0f)) return;
+        const float own = __ldcg(scales + at);
+        if (weighs) w = __ldcg(a.w + key);
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(own)));
+        const float ratio = __fdiv_rn(own, top);
+        if (__any_sync(0xffffffffu, ratio != 1.0f)) {
 #pragma unroll
           for (int n = 0; n < NI; ++n) {
             const float r = __shfl_sync(0xffffffffu, ratio, min(n * RPI + sub, rows - 1));
-            c[n] = make_uint4(rescale4<I8>(c[n].x, r), rescale4<I8>(c[n].y, r), rescale4<I8>(c[n].z, r),
-                              rescale4<I8>(c[n].w, r));
+            codes[n] = make_uint4(rescale4<I8>(codes[n].x, r), rescale4<I8>(codes[n].y, r), rescale4<I8>(codes[n].z, r),
+                                  rescale4<I8>(codes[n].w, r));
           }
-        };
-        rescale(kc, rk);
-        rescale(vc, rv);
+        }
       }
-      cluster_sync();
+      if (j + wave < pages && lane < P) {  // the next wave's keys on their way, beside the barrier and the stores
+        const size_t key = ((size_t)(next / P) * Hkv + h) * P + next % P;
+        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(pool + key * D));
+      }
+      evict_sync(turn.C);
       if (moves) {
-        const size_t at = (size_t)bt[j] * Hkv + h;
 #pragma unroll
         for (int n = 0; n < NI; ++n) {
-          const int t = n * RPI + sub;
-          if (t < rows) {
-            *reinterpret_cast<uint4*>(a.c.k_pool + (at * P + t) * D + ch * 16) = kc[n];
-            *reinterpret_cast<uint4*>(a.c.v_pool + (at * P + t) * D + ch * 16) = vc[n];
-          }
+          const int row = n * RPI + sub;
+          if (row < rows) *reinterpret_cast<uint4*>(pool + (to * P + row) * D + ch * 16) = codes[n];
         }
-        if (lane == 0) {
-          a.c.k_scale[at] = sk;
-          a.c.v_scale[at] = sv;
-        }
-        if (a.w && lane < rows) a.w_out[at * P + lane] = w;
-      } else if (mine && a.w && a.w_out != a.w && lane < rows) {  // the page stays, its weights are wanted elsewhere
-        const size_t at = ((size_t)bt[j] * Hkv + h) * P + lane;
-        a.w_out[at] = a.w[at];
+        if (lane == 0) scales[to] = top;
+        if (weighs && lane < rows) a.w_out[to * P + lane] = w;
+      } else if (mine && weighs && a.w_out != a.w && lane < rows) {  // the page stays, its weights are wanted elsewhere
+        a.w_out[to * P + lane] = a.w[to * P + lane];
       }
     }
-    cluster_sync();  // counts and histograms are done with in every block
   }
 }
 
@@ -406,30 +564,46 @@ size_t evict_bytes(const entmaxkv_config& cfg, int n, int keep) {
          up256e((size_t)n * cfg.num_kv_heads * keep * 4);
 }
 
-template <bool I8, int D, int P>
-static cudaError_t evict_t(const EvictArgs& a, int sms, cudaStream_t st) {
-  const void* fn = (const void*)evict_kernel<I8, D, P>;
-  const int smem = kEvictKeys * 4;
-  cudaError_t e = ensure_smem(fn, smem);
-  if (e != cudaSuccess) return e;
-  const int C = 8;
-  // clusters that fit beside one another, two blocks a multiprocessor
-  const long long want = (long long)a.n * a.c.Hkv, fit = max(1, 2 * sms / C);
+static cudaError_t evict_launch(void (*kernel)(EvictArgs), const EvictArgs& a, long long clusters, int C, int threads,
+                                int smem, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(min(want, fit) * C));
-  cfg.blockDim = dim3(kEvictThreads);
+  cfg.gridDim = dim3((unsigned)(clusters * C));
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, evict_kernel<I8, D, P>, a);
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <bool I8, int D, int P>
+static cudaError_t evict_t(EvictArgs a, int sms, cudaStream_t st) {
+  const long long most = (long long)a.n * a.c.Hkv, few = sms / kEvictCluster;
+  const int smem = kEvictKeys * 4;
+  cudaError_t e = ensure_smem((const void*)evict_select_kernel<P>, smem);
+  const bool wide = most <= few || a.keep > kEvictLong, alone = most > few;
+  for (int step = 0; step < 2; ++step) {  // select, move
+    if (wide && e == cudaSuccess) {
+      a.from = 0;
+      a.to = few;
+      e = step ? evict_launch(evict_move_kernel<I8, D, P>, a, min(2 * most, 2 * few), kEvictCluster, 1024, 0, st)
+               : evict_launch(evict_select_kernel<P>, a, min(most, few), kEvictCluster, kSelectThreads, smem, st);
+    }
+    if (alone && e == cudaSuccess) {
+      a.from = wide ? few : 0;
+      a.to = most;
+      e = step ? evict_launch(evict_move_kernel<I8, D, P>, a, min(2 * most, 4LL * sms), 1, 512, 0, st)
+               : evict_launch(evict_select_kernel<P>, a, min(most, (long long)sms), 1, kSelectThreads, smem, st);
+    }
+  }
+  return e;
 }
 template <bool I8>
 static cudaError_t evict_d(const EvictArgs& a, int sms, cudaStream_t st) {
@@ -441,7 +615,7 @@ cudaError_t launch_evict(const Q8Cache& c, const int32_t* seq_ids, int n, int ke
                          const float* w, float* w_out, int32_t* lens_out, int32_t* free_pages,
                          const int32_t* free_count, int32_t* count_out, bool i8, void* ws, int sms, cudaStream_t st) {
   EvictArgs a{c, seq_ids, n, keep, above, sinks, recent, w, w_out, lens_out, free_pages, free_count, count_out,
-              nullptr, nullptr, nullptr, nullptr, nullptr};
+              nullptr, nullptr, nullptr, nullptr, nullptr, 0, 0};
   char* p = static_cast<char*>(ws);
   a.owner = reinterpret_cast<int*>(p);
   p += up256e((size_t)c.max_seqs * 4);
@@ -451,7 +625,7 @@ cudaError_t launch_evict(const Q8Cache& c, const int32_t* seq_ids, int n, int ke
   p += up256e((size_t)n * sizeof(EvictItem));
   a.n_items = reinterpret_cast<int*>(p);
   p += 256;
-  a.src = reinterpret_cast<int32_t*>(p);
+  a.src = reinterpret_cast<uint32_t*>(p);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kEvictPlanBlocks);
   cfg.blockDim = dim3(kEvictPlanThreads);
@@ -463,7 +637,7 @@ cudaError_t launch_evict(const Q8Cache& c, const int32_t* seq_ids, int n, int ke
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_plan_kernel, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, n <= kEvictPlanThreads ? evict_plan_few_kernel : evict_plan_kernel, a);
   if (e != cudaSuccess) return e;
   return i8 ? evict_d<true>(a, sms, st) : evict_d<false>(a, sms, st);
 }
