@@ -35,7 +35,10 @@ constexpr int kSelectWarps = 32, kSelectThreads = kSelectWarps * 32;
 constexpr int kEvictKeys = 40960;  // a block's weights that stay in shared memory; more are read again for each count
 // A block alone counts 11, 11 and 10 bits. A cluster's counts are read by each of its blocks, at about 9 bytes a clock:
 // 8 bits at a time (2048 counts of 8 blocks: 7000 clocks a pass; 256: 1000).
-constexpr int kBins = 2048, kClusterBins = 256;
+constexpr int kBins = 2048;
+// Codes of the weights, in their order: NaN above infinity, a key that stays whatever it weighs above all, and a place
+// behind the sequence's end below all (minus infinity is 0x007fffff). So the edge is the keep-th largest code.
+constexpr uint32_t kCodeStays = 0xffffffffu, kCodeNaN = 0xfffffffeu;
 constexpr int kEvictCluster = 8;
 // Keys to keep from which few (slot, KV head) pairs get a cluster each: at most 4 waves of the 32 pages that a block's
 // warps hold are below.
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(EvictAr
   __shared__ int warp_more[kSelectWarps], warp_same[kSelectWarps];
   __shared__ __align__(16) int block_cnt[4];  // kept for certain, equal to the edge
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int Hkv = a.c.Hkv, keep = a.keep, take = keep - a.sinks - a.recent;
+  const int Hkv = a.c.Hkv, keep = a.keep;
   const EvictTurn turn = evict_turn(a, 1);
   if (!turn.mine) return;
   const int C = turn.C, rank = turn.rank;
@@ -334,94 +337,82 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(EvictAr
     uint32_t* src = a.src + (size_t)it * keep;
     const int seg = ((x.L + C - 1) / C + 127) / 128 * 128;
     const int lo = min(x.L, rank * seg), hi = min(x.L, lo + seg);
-    const int c0 = max(lo, a.sinks), c1 = min(hi, x.L - a.recent);  // this block's keys that are chosen among
-    auto code_of = [](float w) -> uint32_t {  // larger weights have larger codes; NaN the largest, −0 is 0
-      return w != w ? 0xffffffffu : ord_enc(w + 0.0f);
-    };
-    auto codes_at = [&](int i) -> uint4 {  // of four keys, the first a multiple of 4; any behind the sequence's end
-      const float4 w = *reinterpret_cast<const float4*>(a.w + ((size_t)bt[i / P] * Hkv + h) * P + i % P);
-      return make_uint4(code_of(w.x), code_of(w.y), code_of(w.z), code_of(w.w));
-    };
-    const bool held = seg <= kEvictKeys;
-    uint32_t edge = 0u;
-    int want = take;
-    if (take > 0) {
-      if (held) {
-#pragma unroll 8
-        for (int i = lo + 4 * tid; i < hi; i += 4 * kSelectThreads)
-          *reinterpret_cast<uint4*>(keys_sm + i - lo) = codes_at(i);
-      }
-      const int bits = C > 1 ? 8 : 11, bins = 1 << bits, passes = C > 1 ? 4 : 3;
-      for (int i = tid; i < passes * bins; i += kSelectThreads) hist[i] = 0u;
-      __syncthreads();
-#pragma unroll 1
-      for (int p = 0; p < passes; ++p) {
-        const int shift = max(0, 32 - bits * (p + 1));
-        const uint32_t mask = C == 1 && p == 2 ? 1023u : (uint32_t)bins - 1u, above = p ? 0xffffffffu << (32 - bits * p) : 0u;
-        uint32_t* count = hist + p * bins;
-#pragma unroll 4
-        for (int i = lo + 4 * tid; i < hi; i += 4 * kSelectThreads) {
-          const uint4 k4 = held ? *reinterpret_cast<const uint4*>(keys_sm + i - lo) : codes_at(i);
-          const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (i + j >= c0 && i + j < c1 && ((k[j] ^ edge) & above) == 0u) atomicAdd(count + (k[j] >> shift & mask), 1u);
-        }
-        evict_sync(C);
-        // four bins a thread, the largest codes with the first thread
-        uint32_t n4[4] = {0u, 0u, 0u, 0u};
-        const int bin0 = bins - 4 - 4 * tid;
-        if (bin0 >= 0) {
-          uint4 u[kEvictCluster];  // (all blocks' counts in flight)
-#pragma unroll
-          for (int r = 0; r < kEvictCluster; ++r)
-            u[r] = r < C ? ld_cluster4(of_block(smem_u32(count + bin0), r)) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int r = 0; r < kEvictCluster; ++r) n4[0] += u[r].x, n4[1] += u[r].y, n4[2] += u[r].z, n4[3] += u[r].w;
-        }
-        const int sum = (int)(n4[0] + n4[1] + n4[2] + n4[3]);
-        int total, before = block_exclusive_scan(sum, sh_scan, total);
-        if (before < want && before + sum >= want) {
-#pragma unroll
-          for (int j = 3; j >= 0; --j) {
-            if (before < want && before + (int)n4[j] >= want) {
-              sh_digit = bin0 + j;
-              sh_want = want - before;
-            }
-            before += (int)n4[j];
-          }
-        }
-        __syncthreads();
-        edge |= (uint32_t)sh_digit << shift;
-        want = sh_want;
-        __syncthreads();
-      }
-    }
-    // Each warp has a part of the block's keys, four of them a lane at a time: how many are kept for certain and how
-    // many equal the edge (in the two halves of a word: a block has fewer than 2^16 keys a lane), then the place of
-    // each kept key, the certain ones before it plus the equal ones, of which the first `want` are taken.
-    const int wseg = (seg / 128 + kSelectWarps - 1) / kSelectWarps * 128;
-    const int w0 = min(hi, lo + warp * wseg), w1 = min(hi, w0 + wseg);
-    auto look = [&](int i, uint32_t& more, uint32_t& same) {  // a bit a key
-      more = same = 0u;
-      if (i >= w1) return;
-      uint4 k4 = make_uint4(0u, 0u, 0u, 0u);
-      if (take > 0) k4 = held ? *reinterpret_cast<const uint4*>(keys_sm + i - lo) : codes_at(i);
-      const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    auto codes_at = [&](int i) -> uint4 {  // of four keys, the first a multiple of 4
+      float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (a.w) w = *reinterpret_cast<const float4*>(a.w + ((size_t)bt[i / P] * Hkv + h) * P + i % P);
+      const float v[4] = {w.x, w.y, w.z, w.w};
+      uint32_t k[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bool in = i + j < w1, end = i + j < a.sinks || i + j >= x.L - a.recent, among = in && !end && take > 0;
-        if ((in && end) || (among && k[j] > edge)) more |= 1u << j;
-        if (among && k[j] == edge) same |= 1u << j;
+        k[j] = v[j] != v[j] ? kCodeNaN : ord_enc(v[j] + 0.0f);  // (−0 is 0)
+        if (i + j < a.sinks || i + j >= x.L - a.recent) k[j] = i + j < x.L ? kCodeStays : 0u;
       }
+      return make_uint4(k[0], k[1], k[2], k[3]);
     };
+    const bool held = seg <= kEvictKeys;
+    auto codes = [&](int i) -> uint4 { return held ? *reinterpret_cast<const uint4*>(keys_sm + i - lo) : codes_at(i); };
+    if (held) {
+#pragma unroll 8
+      for (int i = lo + 4 * tid; i < hi; i += 4 * kSelectThreads) *reinterpret_cast<uint4*>(keys_sm + i - lo) = codes_at(i);
+    }
+    uint32_t edge = 0u;
+    int want = keep;
+    const int bits = C > 1 ? 8 : 11, bins = 1 << bits, passes = C > 1 ? 4 : 3;
+    for (int i = tid; i < passes * bins; i += kSelectThreads) hist[i] = 0u;
+    __syncthreads();
+#pragma unroll 1
+    for (int p = 0; p < passes; ++p) {
+      const int shift = max(0, 32 - bits * (p + 1));
+      const uint32_t mask = C == 1 && p == 2 ? 1023u : (uint32_t)bins - 1u, above = p ? 0xffffffffu << (32 - bits * p) : 0u;
+      uint32_t* count = hist + p * bins;
+#pragma unroll 4
+      for (int i = lo + 4 * tid; i < hi; i += 4 * kSelectThreads) {
+        const uint4 k = codes(i);
+        if (((k.x ^ edge) & above) == 0u) atomicAdd(count + (k.x >> shift & mask), 1u);
+        if (((k.y ^ edge) & above) == 0u) atomicAdd(count + (k.y >> shift & mask), 1u);
+        if (((k.z ^ edge) & above) == 0u) atomicAdd(count + (k.z >> shift & mask), 1u);
+        if (((k.w ^ edge) & above) == 0u) atomicAdd(count + (k.w >> shift & mask), 1u);
+      }
+      evict_sync(C);
+      // four bins a thread, the largest codes with the first thread
+      uint32_t n4[4] = {0u, 0u, 0u, 0u};
+      const int bin0 = bins - 4 - 4 * tid;
+      if (bin0 >= 0) {
+        uint4 u[kEvictCluster];  // (all blocks' counts in flight)
+#pragma unroll
+        for (int r = 0; r < kEvictCluster; ++r)
+          u[r] = r < C ? ld_cluster4(of_block(smem_u32(count + bin0), r)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int r = 0; r < kEvictCluster; ++r) n4[0] += u[r].x, n4[1] += u[r].y, n4[2] += u[r].z, n4[3] += u[r].w;
+      }
+      const int sum = (int)(n4[0] + n4[1] + n4[2] + n4[3]);
+      int total, before = block_exclusive_scan(sum, sh_scan, total);
+      if (before < want && before + sum >= want) {
+#pragma unroll
+        for (int j = 3; j >= 0; --j) {
+          if (before < want && before + (int)n4[j] >= want) {
+            sh_digit = bin0 + j;
+            sh_want = want - before;
+          }
+          before += (int)n4[j];
+        }
+      }
+      __syncthreads();
+      edge |= (uint32_t)sh_digit << shift;
+      want = sh_want;
+      __syncthreads();
+    }
+    // Each warp has a part of the block's keys, four of them a lane at a time: how many lie above the edge and how many
+    // equal it, then the place of each kept key, those above before it plus the equal ones, of which the first `want`
+    // are taken.
+    const int wseg = (seg / 128 + kSelectWarps - 1) / kSelectWarps * 128;
+    const int w0 = min(hi, lo + warp * wseg), w1 = min(hi, w0 + wseg);
     int n_more = 0, n_same = 0;
 #pragma unroll 2
-    for (int i = w0 + 4 * lane; i - 4 * lane < w1; i += 128) {
-      uint32_t more, same;
-      look(i, more, same);
-      n_more += __popc(more);
-      n_same += __popc(same);
+    for (int i = w0 + 4 * lane; i < w1; i += 128) {
+      const uint4 k = codes(i);
+      n_more += (int)(k.x > edge) + (int)(k.y > edge) + (int)(k.z > edge) + (int)(k.w > edge);
+      n_same += (int)(k.x == edge) + (int)(k.y == edge) + (int)(k.z == edge) + (int)(k.w == edge);
     }
     n_more = __reduce_add_sync(0xffffffffu, n_more);
     n_same = __reduce_add_sync(0xffffffffu, n_same);
@@ -451,33 +442,33 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(EvictAr
       for (int q = 0; q < 1024 / P / 32; ++q) page[q] = i0 / P + 32 * q + lane <= (x.L - 1) / P ? bt[i0 / P + 32 * q + lane] : 0;
       const int i1 = min(w1, i0 + 1024);
       for (int i = i0 + 4 * lane; i - 4 * lane < i1; i += 128) {
-        uint32_t more, same;
-        look(i, more, same);
-        const int mine = __popc(more) | __popc(same) << 16;
-        int inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += v;
-        }
-        const int all = __shfl_sync(0xffffffffu, inc, 31);
-        int m = n_more + ((inc - mine) & 0xffff), n = n_same + ((inc - mine) >> 16);
+        const uint4 k4 = i < i1 ? codes(i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
         const int at = (i - i0) / P;
         int ph = __shfl_sync(0xffffffffu, page[0], at & 31);
         if (P == 16) {
           const int ph1 = __shfl_sync(0xffffffffu, page[1024 / P / 32 - 1], at & 31);
           if (at >= 32) ph = ph1;
         }
+        const uint32_t place = (uint32_t)ph * P + i % P, below = (1u << lane) - 1u;
+        uint32_t more[4], same[4];
+        int m = n_more, n = n_same;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bool certain = more >> j & 1u, level = same >> j & 1u;
-          const int to = m + min(n, want);
-          if ((certain || (level && n < want)) && to < keep) src[to] = (uint32_t)ph * P + (i + j) % P;
-          m += certain;
-          n += level;
+          more[j] = __ballot_sync(0xffffffffu, k[j] > edge);
+          same[j] = __ballot_sync(0xffffffffu, k[j] == edge);
+          m += __popc(more[j] & below);
+          n += __popc(same[j] & below);
+          n_more += __popc(more[j]);
+          n_same += __popc(same[j]);
         }
-        n_more += all & 0xffff;
-        n_same += all >> 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int to = m + min(n, want);
+          if ((k[j] > edge || (k[j] == edge && n < want)) && to < keep) src[to] = place + j;
+          m += k[j] > edge;
+          n += k[j] == edge;
+        }
       }
     }
     evict_sync(C);  // counts and histograms are done with in every block
@@ -593,7 +584,7 @@ static cudaError_t evict_t(EvictArgs a, int sms, cudaStream_t st) {
     if (wide && e == cudaSuccess) {
       a.from = 0;
       a.to = few;
-      e = step ? evict_launch(evict_move_kernel<I8, D, P>, a, min(2 * most, 2 * few), kEvictCluster, 1024, 0, st)
+      e = step ? evict_launch(evict_move_kernel<I8, D, P>, a, min(2 * most, 2 * few), kEvictCluster, 512, 0, st)
                : evict_launch(evict_select_kernel<P>, a, min(most, few), kEvictCluster, kSelectThreads, smem, st);
     }
     if (alone && e == cudaSuccess) {
