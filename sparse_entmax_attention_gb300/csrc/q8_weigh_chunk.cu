@@ -59,7 +59,10 @@ __global__ void __launch_bounds__(1024) weigh_plan_kernel(WcArgs g) {
         r.lo_max = w > 0 ? max(0, r.pos_max - w + 1) : 0;
       }
       atomicMin(&lo_sh[lo], r.lo_min);
-      if (tiles + j < g.max_tiles) g.rows[tiles + j] = r;
+      if (tiles + j < g.max_tiles) {
+        g.rows[tiles + j] = r;
+        g.slot_of[tiles + j] = b0 + lo;
+      }
     }
     __syncthreads();
     if (b < n) {
@@ -68,7 +71,6 @@ __global__ void __launch_bounds__(1024) weigh_plan_kernel(WcArgs g) {
         nrt = 0;
       }
       WcSlot x{};
-      x.rt0 = min(tiles + at, g.max_tiles);
       if (nrt > 0) {
         x = WcSlot{s.seq, s.L, s.start, s.count};
         x.pre = a.sc.prefix ? min(max(a.sc.prefix[b], 0), s.L) : 0;
@@ -117,7 +119,10 @@ __global__ void __launch_bounds__(1024) weigh_plan_kernel(WcArgs g) {
     if (b < n) g.cum[b] = at;
     __syncthreads();
   }
-  if (tid == 0) g.cum[n] = base;
+  if (tid == 0) {
+    g.cum[n] = base;
+    *g.n_tiles = min(tiles, g.max_tiles);
+  }
   if (shares > 1)
     for (long long i = tid; i < 8 * base; i += 1024) g.done[i] = 0;
 }
@@ -129,23 +134,13 @@ template <int D>
 __global__ void __launch_bounds__(128) weigh_pack_kernel(WcArgs g) {
   pdl_enter();
   const Q8WeighArgs& a = g.a;
-  const int kvh = blockIdx.y, tid = threadIdx.x, G = a.c.G, Hkv = a.c.Hkv, n = a.b.n_seqs;
+  const int kvh = blockIdx.y, tid = threadIdx.x, G = a.c.G, Hkv = a.c.Hkv;
   __shared__ long long at_sh[kWcRows];
-  __shared__ int slot_sh;
   for (int tile = blockIdx.x; tile < g.max_tiles; tile += gridDim.x) {
-    if (tid == 0) {  // its slot: the last one whose tiles begin at or before it
-      int lo = 0, hi = n - 1;
-      while (lo < hi) {
-        const int m = (lo + hi + 1) >> 1;
-        if (g.slots[m].rt0 <= tile) lo = m;
-        else hi = m - 1;
-      }
-      slot_sh = lo;
-    }
-    __syncthreads();
-    const WcSlot s = g.slots[slot_sh];
+    if (tile >= *g.n_tiles) return;
+    const WcSlot s = g.slots[g.slot_of[tile]];
     const int rt = tile - s.rt0;
-    if (rt >= s.nrt) return;  // past the last slot's tiles
+    if (rt >= s.nrt) return;  // (of a slot past the list)
     const int left = s.count * G - rt * kWcRows, rho = rt * kWcRows + tid;
     const bool mine = tid < left;
     const int tok = mine ? rho / G : 0, head = kvh * G + (mine ? rho - tok * G : 0);
@@ -197,7 +192,7 @@ static long long weigh_tiles(int n_seqs, int total, int G) { return (long long)t
 size_t weigh_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total) {
   const size_t segs = 2 * (size_t)kWcTurns * kWcMaxBlocks;
   return up256w((size_t)n_seqs * sizeof(WcSlot)) + up256w((size_t)(n_seqs + 1) * 8) +
-         up256w((size_t)weigh_tiles(n_seqs, total, cfg.group) * sizeof(WcRows)) + up256w(segs * 32) +
+         up256w((size_t)weigh_tiles(n_seqs, total, cfg.group) * (sizeof(WcRows) + 4)) + 256 + up256w(segs * 32) +
          (size_t)weigh_tiles(n_seqs, total, cfg.group) * cfg.num_kv_heads *
              (kWcRows * cfg.head_dim * 2 + sizeof(WcFacts)) +
          up256w(segs * kWcKeys * 4);
@@ -220,7 +215,10 @@ cudaError_t launch_weigh_chunk(const Q8WeighArgs& a, bool i8, void* ws, int sms,
   g.cum = reinterpret_cast<long long*>(p);
   p += up256w((size_t)(a.b.n_seqs + 1) * 8);
   g.rows = reinterpret_cast<WcRows*>(p);
-  p += up256w(tiles * sizeof(WcRows));
+  g.slot_of = reinterpret_cast<int*>(g.rows + tiles);
+  p += up256w(tiles * (sizeof(WcRows) + 4));
+  g.n_tiles = reinterpret_cast<int*>(p);
+  p += 256;
   g.done = reinterpret_cast<int*>(p);
   p += up256w(segs * 32);
   g.part = reinterpret_cast<float*>(p);

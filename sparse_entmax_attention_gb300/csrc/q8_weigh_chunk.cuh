@@ -17,10 +17,11 @@
 // row by row from where they lie, a tile of rows took 1600 cycles to come in, more
 // than the products with it.)
 //
-// Warps: 4 + 4 of sums (a thread a key); 8 that bring the keys (the next 256 wait as
+// Warps: 16 of sums (two threads a key, one for each 64 rows of a tile: four warps a
+// scheduler hide one another's waits); 8 that bring the keys (the next 256 wait as
 // codes in registers until the products with the present ones are done); 2 that
 // issue the products, one for each 128 keys; 1 that asks for the rows, four tiles
-// ahead. Segments (key tile, share of the rows) go round the blocks in turns; rows
+// ahead; 1 that looks up the segments ahead of them all. Segments (key tile, share of the rows) go round the blocks in turns; rows
 // are shared out only where there are few key tiles, and the block that finishes a
 // tile last adds its shares in their order.
 #pragma once
@@ -29,11 +30,11 @@
 
 namespace ekv {
 
-constexpr int kWcThreads = 640;
+constexpr int kWcThreads = 896;
 constexpr int kWcKeys = 256, kWcRows = 128;
 // Stages of the rows, and of their facts, which the sums read longer: the facts of unit u are asked for when the
 // products of u − kWcQ are done, so the sums of u − kWcQ − 2 are.
-constexpr int kWcQ = 4, kWcMeta = 6;
+constexpr int kWcQ = 4, kWcMeta = 6, kWcSegs = 3;
 constexpr int kWcMaxBlocks = 256;
 constexpr int kWcTurns = 6;  // segments a block should get at least
 
@@ -63,6 +64,8 @@ struct WcArgs {
   WcSlot* slots;     // [n_seqs]
   long long* cum;    // [n_seqs + 1] segments before each slot
   WcRows* rows;      // [max_tiles]
+  int* slot_of;      // [max_tiles]
+  int* n_tiles;
   uint4* packed;     // [Hkv][max_tiles] tiles of 128 queries
   WcFacts* facts;    // [Hkv][max_tiles]
   int* done;         // [2·kWcTurns·blocks][8] shares of a warp's keys that are there
@@ -134,6 +137,36 @@ __device__ __forceinline__ WcMask wc_mask(const WcArgs& g, const WcSeg& x, int r
   return WcMask{__ballot_sync(0xffffffffu, some), __ballot_sync(0xffffffffu, all)};
 }
 
+// A segment as the warps find it in shared memory: its pages, and the first 32 row tiles' bits.
+struct __align__(16) WcPage {
+  int at, key0;  // page · KV heads + KV head, first key; kNoKey: no page
+  float ks;
+  int pad;
+};
+struct __align__(16) WcInfo {
+  WcSeg x;
+  WcMask mask;
+  WcPage pages[kWcKeys / 16];
+};
+
+// 16 columns of the thread's lane, and the tie of their values behind a wait.
+__device__ __forceinline__ void tm_ask16(uint32_t addr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tm_tie16(float* v) {
+  asm volatile(""
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+}
+
 // Four codes as bf16 (exact): bytes 0 and 1 to x, 2 and 3 to y.
 template <bool I8>
 __device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& x, uint32_t& y) {
@@ -169,8 +202,11 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
   constexpr int PT = kWcKeys / P;        // pages a key tile
   extern __shared__ __align__(128) unsigned char dyn_sm[];
   __shared__ uint64_t q_full[kWcQ], q_empty[kWcQ], f_full[kWcMeta], k_full, k_empty, s_full[2][2], s_empty[2][2];
+  __shared__ uint64_t g_full[kWcSegs], g_empty[kWcSegs], x_full[2], x_empty[2];
   __shared__ uint32_t tm_base;
   __shared__ WcFacts facts[kWcMeta];
+  __shared__ WcInfo segs[kWcSegs];
+  __shared__ float x_sum[2][kWcKeys];  // the second rows' sums, of a segment and the next
   __shared__ volatile int gave_up;
   __shared__ WcFew few;
   const Q8WeighArgs& a = g.a;
@@ -183,18 +219,24 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
       mbar_init(&q_empty[i], 2);
     }
     for (int i = 0; i < kWcMeta; ++i) mbar_init(&f_full[i], 1);
+    for (int i = 0; i < kWcSegs; ++i) {
+      mbar_init(&g_full[i], 1);
+      mbar_init(&g_empty[i], 19);  // 16 warps of sums, 2 of products, 1 of rows
+    }
     mbar_init(&k_full, 256);
     mbar_init(&k_empty, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i][0], 1);
       mbar_init(&s_full[i][1], 1);
-      mbar_init(&s_empty[i][0], 128);
-      mbar_init(&s_empty[i][1], 128);
+      mbar_init(&s_empty[i][0], 256);
+      mbar_init(&s_empty[i][1], 256);
+      mbar_init(&x_full[i], 256);
+      mbar_init(&x_empty[i], 256);
     }
     gave_up = 0;
     mbar_fence_init();
   }
-  if (warp == 16) tm_alloc(&tm_base);
+  if (warp == 24) tm_alloc(&tm_base);
   if (a.b.n_seqs <= kWcFew) {
     for (int i = tid; i < a.b.n_seqs * 4; i += kWcThreads)
       reinterpret_cast<int4*>(few.slots)[i] = __ldcg(reinterpret_cast<const int4*>(g.slots) + i);
@@ -214,61 +256,58 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
   auto wait_warp = [&](uint64_t* bar, int phase) -> bool { return __all_sync(0xffffffffu, wait(bar, phase)); };
   int slot = 0, u = 0;  // units (row tiles against key tiles) so far, the same for every role
   bool ok = true;
+  // the k-th segment of the block, once it is there; given back with seg_done
+  auto seg_wait = [&](int k) -> bool { return wait_warp(&g_full[k % kWcSegs], k / kWcSegs); };
+  auto seg_done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&g_empty[k % kWcSegs]);
+  };
+  auto seg_mask = [&](const WcInfo& q, int rt) { return rt == q.x.rt ? q.mask : wc_mask(g, q.x, rt); };
+  const int n_mine = blockIdx.x < n_segs ? (int)((n_segs - 1 - blockIdx.x) / gridDim.x) + 1 : 0;
 
-  // Registers after the splits below: 256 x 128 + 256 x 80 + 128 x 56 = 60416; launched with 640 x 96 = 61440.
-  if (wg < 2) {  // ------------------------------------------------ sums: a thread a key
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;\n");
-    const int ks_ = 128 * wg + (tid & 127);
-    const uint32_t s_tm = tm + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * wg;
-    // the page of the thread's key, as the table has it (looked at a segment later: the load takes its time)
-    auto entry = [&](const WcSeg& x) -> int {
-      const int t = x.kt * PT + ks_ / P;
-      return t < x.pages() ? a.c.block_table[(size_t)x.s.seq * a.c.maxp + x.page(t)] : 0;
-    };
-    int next = 0;
-    if (blockIdx.x < n_segs) next = entry(wc_seg<P>(g, few, blockIdx.x, slot));
-    for (long long id = blockIdx.x; id < n_segs && ok; id += gridDim.x) {
-      const WcSeg x = wc_seg<P>(g, few, id, slot);
-      int ph = next;
-      if (id + gridDim.x < n_segs) {
-        int ahead = slot;
-        next = entry(wc_seg<P>(g, few, id + gridDim.x, ahead));
+  // Registers after the splits below: 512 x 80 + 256 x 64 + 128 x 48 = 63488; launched with 896 x 72 = 64512.
+  if (wg < 4) {  // ------------------------------------------------ sums: two threads a key
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 80;\n");
+    const int half = wg & 1, part = wg >> 1;  // of the keys, and of a tile's rows
+    const int ks_ = 128 * half + (tid & 127);
+    const uint32_t s_tm = tm + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * half;
+    for (int k = 0; k < n_mine && ok; ++k) {
+      if (!seg_wait(k)) {
+        ok = false;
+        break;
       }
-      if (x.kt * PT + ks_ / P >= x.pages()) ph = -1;
-      else if (ph < 0 || ph >= a.c.nphys) {
-        raise_flag(a.c.status, ENTMAXKV_DEV_BAD_PAGE_TABLE);
-        ph = -1;
-      }
-      const int key = ph >= 0 ? x.page(x.kt * PT + ks_ / P) * P + ks_ % P : kNoKey;
-      const bool there = key < x.s.L;
-      const float ks = ph >= 0 ? a.c.k_scale[(size_t)ph * Hkv + x.kvh] : 0.0f;
-      float* wp = a.w + ((size_t)max(ph, 0) * Hkv + x.kvh) * P + ks_ % P;
-      float before = 0.0f;
-      if (there && key < x.s.fresh && a.decay != 0.0f && x.s.nsplit == 1) before = *wp;
-      const float k1 = ks * a.sc.scale * (capped ? a.sc.inv_cap : kLog2e), out = a.sc.cap * kLog2e;
+      const WcInfo& q = segs[k % kWcSegs];
+      const WcPage page = q.pages[ks_ / P];
+      const int key = page.key0 + ks_ % P, pre = q.x.s.pre;
+      const bool there = key < q.x.s.L;
+      const float k1 = page.ks * a.sc.scale * (capped ? a.sc.inv_cap : kLog2e), out = a.sc.cap * kLog2e;
       const unsigned long long k2 = f2_splat(k1);
+      float* wp = a.w + (size_t)page.at * P + ks_ % P;
+      const bool reads = part == 0 && there && key < q.x.s.fresh && a.decay != 0.0f;
+      float before = 0.0f;
+      if (reads && q.x.s.nsplit == 1) before = *wp;
       unsigned long long acc[4] = {0ull, 0ull, 0ull, 0ull};
-      for (int rt = x.rt; rt < x.rt_end && ok && x.seen; rt += 32) {
-        WcMask m = wc_mask(g, x, rt);
+      for (int rt = q.x.rt; rt < q.x.rt_end && ok && q.x.seen; rt += 32) {
+        WcMask m = seg_mask(q, rt);
         for (; m.some; m.some &= m.some - 1u, ++u) {
           const int i = __ffs(m.some) - 1, st = u & 1, ms = u % kWcMeta;
           const WcFacts& f = facts[ms];
-          const int n_rows = min(kWcRows, x.s.count * G - (rt + i) * kWcRows);
-          if (!wait_warp(&f_full[ms], u / kWcMeta) || !wait_warp(&s_full[st][wg], u >> 1)) {
+          const int n_rows = min(kWcRows, q.x.s.count * G - (rt + i) * kWcRows);
+          if (!wait_warp(&f_full[ms], u / kWcMeta) || !wait_warp(&s_full[st][half], u >> 1)) {
             ok = false;
             break;
           }
           tm_fence_after();
           const bool whole = (m.all >> i & 1u) && f.whole;
           const float away = (float)(f.pos0 - key);  // (of the tile's first row; used where it is not negative)
-          // 32 rows: their raw sums to weights, added up; `bits` are the rows that see the key
-          auto weigh = [&](int c0, const float (&raw)[32], bool whole, uint32_t bits) {
-            unsigned long long t2[16];
+          // 16 rows: their raw sums to weights, added up; `bits` are the rows that see the key
+          auto weigh = [&](int c0, const float (&raw)[16], bool whole, uint32_t bits) {
+            unsigned long long t2[8];
             if (capped) {  // y = raw·k, then cap·log2 e·y·T(y²), as in the chunk attention
-              unsigned long long z2[16];
+              unsigned long long z2[8];
               float b4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-              for (int n = 0; n < 16; ++n) {
+              for (int n = 0; n < 8; ++n) {
                 t2[n] = f2_mul(f2_pack(raw[2 * n], raw[2 * n + 1]), k2);
                 z2[n] = f2_mul(t2[n], t2[n]);
                 float y0, y1;
@@ -281,11 +320,11 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
                 const unsigned long long p0 = f2_splat(poly.near[0] * out), p1 = f2_splat(poly.near[1] * out),
                                          p2 = f2_splat(poly.near[2] * out), p3 = f2_splat(poly.near[3] * out);
 #pragma unroll
-                for (int n = 0; n < 16; ++n)
+                for (int n = 0; n < 8; ++n)
                   t2[n] = f2_mul(f2_fma(f2_fma(f2_fma(p3, z2[n], p2), z2[n], p1), z2[n], p0), t2[n]);
               } else if (__all_sync(0xffffffffu, big <= 1.0f)) {
 #pragma unroll
-                for (int n = 0; n < 16; ++n) {
+                for (int n = 0; n < 8; ++n) {
                   unsigned long long r = f2_fma(z2[n], f2_splat(poly.far[6]), f2_splat(poly.far[5]));
 #pragma unroll
                   for (int e = 4; e >= 0; --e) r = f2_fma(r, z2[n], f2_splat(poly.far[e]));
@@ -293,7 +332,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
                 }
               } else {
 #pragma unroll
-                for (int n = 0; n < 16; ++n) {
+                for (int n = 0; n < 8; ++n) {
                   float y0, y1;
                   f2_unpack(t2[n], y0, y1);
                   t2[n] = f2_mul(f2_pack(soft_cap(y0, 1.0f, 1.0f), soft_cap(y1, 1.0f, 1.0f)), f2_splat(out));
@@ -302,7 +341,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
             }
             // in steps, so that no row's chain waits for another's
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
+            for (int n = 0; n < 4; ++n) {
               const bool near = biased && whole;
               const float4 c = *reinterpret_cast<const float4*>((near ? f.near : f.c) + c0 + 4 * n);
               unsigned long long a0 = f2_pack(c.x, c.y), a1 = f2_pack(c.z, c.w);
@@ -321,7 +360,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
               t2[2 * n + 1] = capped ? f2_add(t2[2 * n + 1], a1) : f2_fma(f2_pack(raw[4 * n + 2], raw[4 * n + 3]), k2, a1);
             }
 #pragma unroll
-            for (int n = 0; n < 16; ++n) {
+            for (int n = 0; n < 8; ++n) {
               float e0, e1;
               f2_unpack(t2[n], e0, e1);
               if (!whole) {
@@ -331,69 +370,90 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
               t2[n] = f2_pack(ex2f(e0), ex2f(e1));
             }
 #pragma unroll
-            for (int n = 0; n < 16; ++n) acc[n & 3] = f2_add(acc[n & 3], t2[n]);
+            for (int n = 0; n < 8; ++n) acc[n & 3] = f2_add(acc[n & 3], t2[n]);
           };
           const uint32_t from = s_tm + 256 * st;
+          const int c0 = 64 * part;
           if (whole) {  // (straight on, so that the sums stay where the loads put them)
-            float raw[kWcRows / 32][32];
-            tm_ld32(from, raw[0]);
+            float raw[4][16];
+            tm_ask16(from + c0, raw[0]);
 #pragma unroll
-            for (int c = 0; c < kWcRows / 32; ++c) {
+            for (int c = 0; c < 4; ++c) {
               tm_wait_ld();
-              tm_tie32(raw[c]);
-              if (c + 1 < kWcRows / 32) tm_ld32(from + 32 * (c + 1), raw[c + 1]);
-              weigh(32 * c, raw[c], true, 0xffffffffu);
+              tm_tie16(raw[c]);
+              if (c < 3) tm_ask16(from + c0 + 16 * (c + 1), raw[c + 1]);
+              weigh(c0 + 16 * c, raw[c], true, 0xffffffffu);
             }
           } else {
             // Rows lie in the order of their positions: those from the key's own on see it, up to the window's end.
             int j0 = min(max(key - f.pos0, -1), kWcRows) * G - f.skip, j1 = kWcRows;
             if (a.sc.window > 0)
               j1 = (int)min(max((long long)key + a.sc.window - f.pos0, -1LL), (long long)kWcRows) * G - f.skip;
-            if (key < x.s.pre) {
+            if (key < pre) {
               j0 = 0;
               j1 = kWcRows;
             }
-            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+            auto below = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1u; };
 #pragma unroll 1
-            for (int c = 0; c < n_rows; c += 32) {
-              uint32_t bits = f.counts[c / 32] & below(j1 - c) & ~below(j0 - c);
-              if (a.sc.first_key && key >= x.s.pre) {
-#pragma unroll 8
-                for (int n = 0; n < 32; ++n)
+            for (int c = c0; c < min(n_rows, c0 + 64); c += 16) {
+              uint32_t bits = f.counts[c / 32] >> (c & 16) & below(j1 - c) & ~below(j0 - c);
+              if (a.sc.first_key && key >= pre) {
+#pragma unroll 4
+                for (int n = 0; n < 16; ++n)
                   if (f.lo[c + n] > key) bits &= ~(1u << n);
               }
               if (!__any_sync(0xffffffffu, bits != 0u)) continue;
-              float raw[32];
-              tm_ld32(from + c, raw);
+              float raw[16];
+              tm_ask16(from + c, raw);
               tm_wait_ld();
-              tm_tie32(raw);
+              tm_tie16(raw);
               weigh(c, raw, false, bits);
             }
           }
           tm_fence_before();
-          mbar_arrive(&s_empty[st][wg]);
+          mbar_arrive(&s_empty[st][half]);
         }
       }
       if (!ok) break;
       float sum = f2_sum(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])));
-      if (x.s.nsplit > 1) {
+      const int b = k & 1;
+      if (part) {
+        if (k >= 2 && !wait_warp(&x_empty[b], (k >> 1) - 1)) {
+          ok = false;
+          break;
+        }
+        x_sum[b][ks_] = sum;
+        mbar_arrive(&x_full[b]);
+        seg_done(k);
+        continue;
+      }
+      if (!wait_warp(&x_full[b], k >> 1)) {
+        ok = false;
+        break;
+      }
+      sum += x_sum[b][ks_];
+      mbar_arrive(&x_empty[b]);
+      const int nsplit = q.x.s.nsplit;
+      const long long id = q.x.id, first = q.x.first, T = q.x.s.T;
+      seg_done(k);
+      if (nsplit > 1) {
         // each warp for its own keys: the one that comes last adds the shares, in their order
-        g.part[x.id * kWcKeys + ks_] = sum;
+        g.part[id * kWcKeys + ks_] = sum;
         __threadfence();
         __syncwarp();
         int last = 0;
-        if (lane == 0) last = atomicAdd(g.done + x.first * 8 + warp, 1) == x.s.nsplit - 1;
+        if (lane == 0) last = atomicAdd(g.done + first * 8 + warp, 1) == nsplit - 1;
         if (!__shfl_sync(0xffffffffu, last, 0)) continue;
         __threadfence();
         sum = 0.0f;
-        for (int i = 0; i < x.s.nsplit; ++i) sum += __ldcg(g.part + (x.first + (long long)i * Hkv * x.s.T) * kWcKeys + ks_);
-        if (there && key < x.s.fresh && a.decay != 0.0f) before = *wp;
+        for (int i = 0; i < nsplit; ++i) sum += __ldcg(g.part + (first + (long long)i * Hkv * T) * kWcKeys + ks_);
+        if (reads) before = *wp;
       }
       if (there) *wp = fmaf(before, a.decay, sum);
     }
-  } else if (wg < 4) {  // ------------------------------------------------ keys
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
-    const int cw = warp - 8;                      // keys 32·cw .. 32·cw + 31 of a tile
+  } else if (wg < 6) {  // ------------------------------------------------ keys
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    const int cw = warp - 16;                      // keys 32·cw .. 32·cw + 31 of a tile
     constexpr int CPR = D / 16;                   // 16-code chunks of a key
     constexpr int RPI = 32 / CPR, NI = 32 / RPI;  // keys a load, loads of a warp's keys
     constexpr int PW = 32 / P;                    // pages of a warp's keys
@@ -463,48 +523,58 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
       ++tiles;
     }
   } else {  // ------------------------------------------------ products, and the rows' copies
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
-    if (warp < 18) {  // a warp a half of the keys, one elected thread of it
-      const int h = warp - 16;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
+    if (warp < 26) {  // a warp a half of the keys, one elected thread of it
+      const int h = warp - 24;
       const uint64_t k_desc = smem_desc(k_sm + h * HALF, 16, 1024), q_desc = smem_desc(q_sm, 16, 1024);
       int tiles = 0;
-      for (long long id = blockIdx.x; id < n_segs && ok; id += gridDim.x) {
-        const WcSeg x = wc_seg<P>(g, few, id, slot);
-        if (!x.seen) continue;
-        ok = wait_warp(&k_full, tiles);
-        tm_fence_after();
-        for (int rt = x.rt; rt < x.rt_end && ok; rt += 32) {
-          WcMask m = wc_mask(g, x, rt);
-          for (; m.some; m.some &= m.some - 1u, ++u) {
-            const int i = __ffs(m.some) - 1, st = u & 1, qs = u % kWcQ;
-            const int n_rows = min(kWcRows, x.s.count * G - (rt + i) * kWcRows);
-            if (!wait_warp(&q_full[qs], u / kWcQ) || (u >= 2 && !wait_warp(&s_empty[st][h], (u >> 1) - 1))) {
-              ok = false;
-              break;
-            }
-            tm_fence_after();
-            if (elect_one()) {
-              const uint32_t id_s = instr_desc_bf16((n_rows + 15) / 16 * 16);
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k) {  // (addresses advance in units of 16 bytes)
-                const uint32_t o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                mma_ss(tm + 256 * st + 128 * h, k_desc + o, q_desc + (uint32_t)(qs * (HALF >> 4)) + o, id_s, k > 0);
-              }
-              tm_commit(&s_full[st][h]);
-              tm_commit(&q_empty[qs]);
-            }
-            __syncwarp();
-          }
+      for (int k = 0; k < n_mine && ok; ++k) {
+        if (!seg_wait(k)) {
+          ok = false;
+          break;
         }
-        if (ok && elect_one()) tm_commit(&k_empty);
-        __syncwarp();
-        ++tiles;
+        const WcInfo& q = segs[k % kWcSegs];
+        if (q.x.seen) {
+          ok = wait_warp(&k_full, tiles);
+          tm_fence_after();
+          for (int rt = q.x.rt; rt < q.x.rt_end && ok; rt += 32) {
+            WcMask m = seg_mask(q, rt);
+            for (; m.some; m.some &= m.some - 1u, ++u) {
+              const int i = __ffs(m.some) - 1, st = u & 1, qs = u % kWcQ;
+              const int n_rows = min(kWcRows, q.x.s.count * G - (rt + i) * kWcRows);
+              if (!wait_warp(&q_full[qs], u / kWcQ) || (u >= 2 && !wait_warp(&s_empty[st][h], (u >> 1) - 1))) {
+                ok = false;
+                break;
+              }
+              tm_fence_after();
+              if (elect_one()) {
+                const uint32_t id_s = instr_desc_bf16((n_rows + 15) / 16 * 16);
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n) {  // (addresses advance in units of 16 bytes)
+                  const uint32_t o = ((n >> 2) * 16384 + (n & 3) * 32) >> 4;
+                  mma_ss(tm + 256 * st + 128 * h, k_desc + o, q_desc + (uint32_t)(qs * (HALF >> 4)) + o, id_s, n > 0);
+                }
+                tm_commit(&s_full[st][h]);
+                tm_commit(&q_empty[qs]);
+              }
+              __syncwarp();
+            }
+          }
+          if (ok && elect_one()) tm_commit(&k_empty);
+          __syncwarp();
+          ++tiles;
+        }
+        seg_done(k);
       }
-    } else if (warp == 18) {
-      for (long long id = blockIdx.x; id < n_segs && ok; id += gridDim.x) {
-        const WcSeg x = wc_seg<P>(g, few, id, slot);
-        for (int rt = x.rt; rt < x.rt_end && ok && x.seen; rt += 32) {
-          WcMask m = wc_mask(g, x, rt);
+    } else if (warp == 26) {
+      for (int k = 0; k < n_mine && ok; ++k) {
+        if (!seg_wait(k)) {
+          ok = false;
+          break;
+        }
+        const WcInfo& q = segs[k % kWcSegs];
+        for (int rt = q.x.rt; rt < q.x.rt_end && ok && q.x.seen; rt += 32) {
+          WcMask m = seg_mask(q, rt);
           for (; m.some; m.some &= m.some - 1u, ++u) {
             const int i = __ffs(m.some) - 1, st = u % kWcQ, ms = u % kWcMeta;
             if (u >= kWcQ && !wait_warp(&q_empty[st], u / kWcQ - 1)) {
@@ -512,7 +582,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
               break;
             }
             if (elect_one()) {
-              const size_t at = (size_t)x.kvh * g.max_tiles + x.s.rt0 + rt + i;
+              const size_t at = (size_t)q.x.kvh * g.max_tiles + q.x.s.rt0 + rt + i;
               mbar_expect_tx(&q_full[st], HALF);
               bulk_g2s(dyn_sm + (q_sm - smem_u32(dyn_sm)) + st * HALF, g.packed + at * (HALF / 16), HALF, &q_full[st]);
               mbar_expect_tx(&f_full[ms], sizeof(WcFacts));
@@ -521,18 +591,46 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
             __syncwarp();
           }
         }
+        if (ok) seg_done(k);
       }
       // what was asked for lands before the block ends, whatever gave up
       if (!ok || gave_up) {
         for (int k = max(0, u - kWcQ); k < u; ++k) mbar_wait_second(&q_full[k % kWcQ], (uint32_t)(k / kWcQ & 1));
         for (int k = max(0, u - kWcMeta); k < u; ++k) mbar_wait_second(&f_full[k % kWcMeta], (uint32_t)(k / kWcMeta & 1));
       }
+    } else {  // segments, as far ahead as there is room
+      for (int k = 0; k < n_mine && ok; ++k) {
+        const WcSeg x = wc_seg<P>(g, few, blockIdx.x + (long long)k * gridDim.x, slot);
+        WcPage page{0, kNoKey, 0.0f, 0};
+        const int t = x.kt * PT + lane;
+        if (lane < PT && t < x.pages()) {
+          const int ph = phys_page(a.c.block_table, x.s.seq, x.page(t), a.c.maxp, a.c.nphys, a.c.status);
+          if (ph >= 0) {
+            page.at = ph * Hkv + x.kvh;
+            page.key0 = x.page(t) * P;
+            page.ks = a.c.k_scale[page.at];
+          }
+        }
+        const WcMask mask = wc_mask(g, x, x.rt);
+        if (k >= kWcSegs && !wait_warp(&g_empty[k % kWcSegs], k / kWcSegs - 1)) {
+          ok = false;
+          break;
+        }
+        WcInfo& q = segs[k % kWcSegs];
+        if (lane < PT) q.pages[lane] = page;
+        if (lane == 0) {
+          q.x = x;
+          q.mask = mask;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&g_full[k % kWcSegs]);
+      }
     }
   }
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
-  if (warp == 16) tm_free(tm);
+  if (warp == 24) tm_free(tm);
   if (tid == 0 && gave_up) raise_flag(a.c.status, ENTMAXKV_DEV_TIMEOUT);
 }
 
