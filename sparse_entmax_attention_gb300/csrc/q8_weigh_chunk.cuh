@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
     mbar_init(&k_full, 256);
     mbar_init(&k_empty, 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i][0], 1);
-      mbar_init(&s_full[i][1], 1);
+      mbar_init(&s_full[i][0], 2);  // the products, and the thread that issued them: it has waited for the rows' facts
+      mbar_init(&s_full[i][1], 2);
       mbar_init(&s_empty[i][0], 256);
       mbar_init(&s_empty[i][1], 256);
       mbar_init(&x_full[i], 256);
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
           const int i = __ffs(m.some) - 1, st = u & 1, ms = u % kWcMeta;
           const WcFacts& f = facts[ms];
           const int n_rows = min(kWcRows, q.x.s.count * G - (rt + i) * kWcRows);
-          if (!wait_warp(&f_full[ms], u / kWcMeta) || !wait_warp(&s_full[st][half], u >> 1)) {
+          if (!wait_warp(&s_full[st][half], u >> 1)) {
             ok = false;
             break;
           }
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
             for (; m.some; m.some &= m.some - 1u, ++u) {
               const int i = __ffs(m.some) - 1, st = u & 1, qs = u % kWcQ;
               const int n_rows = min(kWcRows, q.x.s.count * G - (rt + i) * kWcRows);
-              if (!wait_warp(&q_full[qs], u / kWcQ) || (u >= 2 && !wait_warp(&s_empty[st][h], (u >> 1) - 1))) {
+              if (!wait_warp(&f_full[u % kWcMeta], u / kWcMeta) || !wait_warp(&q_full[qs], u / kWcQ) || (u >= 2 && !wait_warp(&s_empty[st][h], (u >> 1) - 1))) {
                 ok = false;
                 break;
               }
@@ -555,6 +555,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
                   mma_ss(tm + 256 * st + 128 * h, k_desc + o, q_desc + (uint32_t)(qs * (HALF >> 4)) + o, id_s, n > 0);
                 }
                 tm_commit(&s_full[st][h]);
+                mbar_arrive(&s_full[st][h]);
                 tm_commit(&q_empty[qs]);
               }
               __syncwarp();
