@@ -34,7 +34,7 @@ constexpr int kWcThreads = 896;
 constexpr int kWcKeys = 256, kWcRows = 128;
 // Stages of the rows, and of their facts, which the sums read longer: the facts of unit u are asked for when the
 // products of u − kWcQ are done, so the sums of u − kWcQ − 2 are.
-constexpr int kWcQ = 4, kWcMeta = 6, kWcSegs = 3;
+constexpr int kWcQ = 2, kWcMeta = kWcQ + 2, kWcSegs = 3, kWcK = 2;
 constexpr int kWcMaxBlocks = 256;
 constexpr int kWcTurns = 6;  // segments a block should get at least
 
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
   constexpr int HALF = 128 * D * 2;      // bytes of 128 keys or rows
   constexpr int PT = kWcKeys / P;        // pages a key tile
   extern __shared__ __align__(128) unsigned char dyn_sm[];
-  __shared__ uint64_t q_full[kWcQ], q_empty[kWcQ], f_full[kWcMeta], k_full, k_empty, s_full[2][2], s_empty[2][2];
+  __shared__ uint64_t q_full[kWcQ], q_empty[kWcQ], f_full[kWcMeta], k_full[kWcK], k_empty[kWcK], s_full[2][2], s_empty[2][2];
   __shared__ uint64_t g_full[kWcSegs], g_empty[kWcSegs], x_full[2], x_empty[2];
   __shared__ uint32_t tm_base;
   __shared__ WcFacts facts[kWcMeta];
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
   const Q8WeighArgs& a = g.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
   const uint32_t sm0 = (smem_u32(dyn_sm) + 1023u) & ~1023u;
-  const uint32_t k_sm = sm0, q_sm = sm0 + 2 * HALF;
+  const uint32_t k_sm = sm0, q_sm = sm0 + kWcK * 2 * HALF;
   if (tid == 0) {
     for (int i = 0; i < kWcQ; ++i) {
       mbar_init(&q_full[i], 1);
@@ -223,8 +223,10 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
       mbar_init(&g_full[i], 1);
       mbar_init(&g_empty[i], 19);  // 16 warps of sums, 2 of products, 1 of rows
     }
-    mbar_init(&k_full, 256);
-    mbar_init(&k_empty, 2);
+    for (int i = 0; i < kWcK; ++i) {
+      mbar_init(&k_full[i], 256);
+      mbar_init(&k_empty[i], 2);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i][0], 2);  // the products, and the thread that issued them: it has waited for the rows' facts
       mbar_init(&s_full[i][1], 2);
@@ -497,14 +499,14 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
     Ahead next = find(now.id + gridDim.x);
     if (now.id < n_segs) load(now);
     while (now.id < n_segs && ok) {
-      if (tiles > 0 && !wait_warp(&k_empty, tiles - 1)) {
+      if (tiles >= kWcK && !wait_warp(&k_empty[tiles % kWcK], tiles / kWcK - 1)) {
         ok = false;
         break;
       }
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int rr = 32 * (cw & 3) + i * RPI + crow;
-        const uint32_t dst = k_sm + (cw >> 2) * HALF;
+        const uint32_t dst = k_sm + (tiles % kWcK * 2 + (cw >> 2)) * HALF;
         uint4 h0, h1;
         codes_bf16<I8>(codes[i].x, h0.x, h0.y);
         codes_bf16<I8>(codes[i].y, h0.z, h0.w);
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
         sts128(dst + tile_off(rr, 2 * cch + 1), h1);
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-      mbar_arrive(&k_full);
+      mbar_arrive(&k_full[tiles % kWcK]);
       now = next;
       if (now.id < n_segs) {
         load(now);
@@ -535,7 +537,8 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
         }
         const WcInfo& q = segs[k % kWcSegs];
         if (q.x.seen) {
-          ok = wait_warp(&k_full, tiles);
+          ok = wait_warp(&k_full[tiles % kWcK], tiles / kWcK);
+          const uint64_t k_tile = k_desc + (uint32_t)(tiles % kWcK * (2 * HALF >> 4));
           tm_fence_after();
           for (int rt = q.x.rt; rt < q.x.rt_end && ok; rt += 32) {
             WcMask m = seg_mask(q, rt);
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n) {  // (addresses advance in units of 16 bytes)
                   const uint32_t o = ((n >> 2) * 16384 + (n & 3) * 32) >> 4;
-                  mma_ss(tm + 256 * st + 128 * h, k_desc + o, q_desc + (uint32_t)(qs * (HALF >> 4)) + o, id_s, n > 0);
+                  mma_ss(tm + 256 * st + 128 * h, k_tile + o, q_desc + (uint32_t)(qs * (HALF >> 4)) + o, id_s, n > 0);
                 }
                 tm_commit(&s_full[st][h]);
                 mbar_arrive(&s_full[st][h]);
@@ -561,7 +564,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
               __syncwarp();
             }
           }
-          if (ok && elect_one()) tm_commit(&k_empty);
+          if (ok && elect_one()) tm_commit(&k_empty[tiles % kWcK]);
           __syncwarp();
           ++tiles;
         }
@@ -641,7 +644,7 @@ cudaError_t weigh_chunk_run(const WcArgs& g, cudaStream_t st);
 
 template <bool I8, int D, int P, bool CAP, bool BIAS>
 cudaError_t weigh_chunk_start(const WcArgs& g, cudaStream_t st) {
-  const int smem = (2 + kWcQ) * 128 * D * 2 + 1024;
+  const int smem = (2 * kWcK + kWcQ) * 128 * D * 2 + 1024;
   const cudaError_t e = ensure_smem((const void*)weigh_chunk_kernel<I8, D, P, CAP, BIAS>, smem);
   if (e != cudaSuccess) return e;
   return launch_k(true, weigh_chunk_kernel<I8, D, P, CAP, BIAS>, dim3(g.blocks), dim3(kWcThreads), (size_t)smem, st, g);
