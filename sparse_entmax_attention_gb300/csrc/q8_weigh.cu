@@ -188,11 +188,36 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 1) weigh_kernel(Q8WeighArgs 
     }
     look_up(0);
     refill(min(n, 32));
-    for (int i = 0; i < n; ++i) {
-      if ((i & 31) == 0 && i) {
-        look_up(i);
-        refill(min(n, i + 32));
+    // the lane's key of tile i (key 8c + r), and what it gathered; asked for a tile ahead, as the load takes longer than
+    // a tile's products
+    struct Place {
+      float* p;
+      float before;
+      bool there;
+    };
+    auto place = [&](int i) -> Place {
+      const bool second = PP == 2 && c >= 2;
+      int f = __shfl_sync(0xffffffffu, ph[0], i & 31);
+      if (PP == 2) {
+        const int g = __shfl_sync(0xffffffffu, ph[PP - 1], i & 31);
+        if (second) f = g;
       }
+      const int key = x.page((t0 + i) * PP + second) * P + 8 * c % P + r;
+      Place k{a.w + ((size_t)max(f, 0) * Hkv + kvh) * P + 8 * c % P + r, 0.0f, f >= 0 && key < x.s.L};
+      if (k.there && key < x.fresh && a.decay != 0.0f) k.before = *k.p;
+      return k;
+    };
+    Place next{};
+    for (int i = 0; i < n; ++i) {
+      if ((i & 31) == 0) {
+        if (i) {
+          look_up(i);
+          refill(min(n, i + 32));
+        }
+        next = place(i);
+      }
+      const Place mine = next;
+      if ((i & 31) < 31 && i + 1 < n) next = place(i + 1);
       const int end = min(n, (i | 31) + 1);
       int f[PP], key0[PP];
       float ks[PP];
@@ -206,13 +231,6 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 1) weigh_kernel(Q8WeighArgs 
         if (f[q] >= 0 && x.seen(page)) some = true;
         else whole = false;
       }
-      // the lane's key, and its weight so far
-      const bool second = PP == 2 && c >= 2;  // (key 8c + r of the tile)
-      const int mine = (second ? key0[PP - 1] : key0[0]) + 8 * c % P + r;
-      float* wp = a.w + ((size_t)max(second ? f[PP - 1] : f[0], 0) * Hkv + kvh) * P + 8 * c % P + r;
-      const bool there = mine < x.s.L;
-      float before = 0.0f;
-      if (there && mine < x.fresh && a.decay != 0.0f) before = *wp * a.decay;
       float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};  // keys r, r + 8, r + 16, r + 24
       if (some) {
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&bars[warp][used % ST], (used / ST) & 1))) {
@@ -264,7 +282,7 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 1) weigh_kernel(Q8WeighArgs 
           sum[mt][e] += __shfl_xor_sync(0xffffffffu, sum[mt][e], 2);
         }
       const float got = c & 2 ? (c & 1 ? sum[1][1] : sum[1][0]) : (c & 1 ? sum[0][1] : sum[0][0]);
-      if (there) *wp = before + got;
+      if (mine.there) *mine.p = fmaf(mine.before, a.decay, got);
     }
     w += n;
   }
