@@ -662,6 +662,8 @@ int32_t entmaxkv_weigh_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* c
  * would pass num_phys_pages raises ENTMAXKV_DEV_CAPACITY and takes no more.
  * Refused: a pool of 2^32 tokens and more (ENTMAXKV_ERR_UNSUPPORTED); above < keep, keep < 1 or more than a row of the table
  * holds, sinks + recent > keep (ENTMAXKV_ERR_INVALID_ARG).
+ *   seq_ids      (device) [n_seqs]. count: (device) [n_seqs], or NULL; a slot with 0
+ *                is idle and its seq_ids entry not looked at (a batch's count will do)
  *   weights      as weigh_q8 writes them, from a 16-byte boundary; NULL where
  *                sinks + recent = keep
  *   weights_out  may be weights; otherwise only the evicted sequences' kept places are written
@@ -671,10 +673,10 @@ int32_t entmaxkv_weigh_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* c
  */
 size_t entmaxkv_evict_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, int32_t keep);
 int32_t entmaxkv_evict_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache, const float* weights,
-                          const int32_t* seq_ids, int32_t n_seqs, int32_t keep, int32_t above, int32_t sinks,
-                          int32_t recent, float* weights_out, int32_t* lens_out, int32_t* free_pages,
-                          const int32_t* free_count, int32_t* free_count_out, void* workspace,
-                          size_t workspace_bytes, void* stream);
+                          const int32_t* seq_ids, const int32_t* count, int32_t n_seqs, int32_t keep,
+                          int32_t above, int32_t sinks, int32_t recent, float* weights_out, int32_t* lens_out,
+                          int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out,
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

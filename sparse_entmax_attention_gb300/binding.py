@@ -163,7 +163,7 @@ def lib() -> ctypes.CDLL:
     L.entmaxkv_evict_q8_workspace.restype = sz
     L.entmaxkv_evict_q8_workspace.argtypes = [cfg_p, i32, i32]
     L.entmaxkv_evict_q8.restype = i32
-    L.entmaxkv_evict_q8.argtypes = [cfg_p, q8_p, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.entmaxkv_evict_q8.argtypes = [cfg_p, q8_p, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
     _lib = L
     return L
 
@@ -890,11 +890,12 @@ def alloc_evict_workspace(cache: QuantCache, n_seqs, keep):
     return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
-def evict_q8(cache: QuantCache, pool: PagePool, weights, seq_ids, keep, above=0, sinks=0, recent=0, lens_out=None,
-             count_out=None, weights_out=None, workspace=None, stream=None):
+def evict_q8(cache: QuantCache, pool: PagePool, weights, seq_ids, keep, above=0, sinks=0, recent=0, count=None,
+             lens_out=None, count_out=None, weights_out=None, workspace=None, stream=None):
     """entmaxkv_evict_q8: each of the sequences seq_ids (int32) with more than `above` tokens (0: keep) is shortened to
     `keep`: in every KV head its first `sinks`, its last `recent` and the heaviest of the others by weights stay, in
     their order, and pages that are left over go back to the pool. weights may be None where sinks + recent = keep.
+    count: int32 beside seq_ids, slots with 0 are idle (a batch's count).
 
     Lengths, the free list's height and weights change in place, or go to lens_out, count_out and weights_out. A
     workspace that is not given is allocated on the call's stream.
@@ -906,7 +907,7 @@ def evict_q8(cache: QuantCache, pool: PagePool, weights, seq_ids, keep, above=0,
     _need(weights is not None or weights_out is None, "weights_out: without weights")
     lens = cache.seq_lens
     w_in = None if weights is None else _weights(cache, weights)
-    args = (w_in, _i32(seq_ids, (n,), dev, "seq_ids"), n, int(keep), int(above) or int(keep), int(sinks), int(recent),
+    args = (w_in, _i32(seq_ids, (n,), dev, "seq_ids"), None if count is None else _i32(count, (n,), dev, "count"), n, int(keep), int(above) or int(keep), int(sinks), int(recent),
             w_in if weights_out is None else _weights(cache, weights_out, "weights_out"),
             lens.data_ptr() if lens_out is None else _i32(lens_out, lens.shape, dev, "lens_out"), pool._pages, pool._count,
             pool._count if count_out is None else _i32(count_out, (1,), dev, "count_out"))
@@ -916,10 +917,23 @@ def evict_q8(cache: QuantCache, pool: PagePool, weights, seq_ids, keep, above=0,
     _q8_call(dev, stream, lib().entmaxkv_evict_q8, cache.cfg, cache.view, *args, workspace.data_ptr(), workspace.nbytes)
 
 
+class KeyBudget:
+    """How many keys a QuantStep leaves each of its sequences: behind the attention the step's rows weigh the keys
+    (weigh_q8 with decay and, for some, coef [n_seqs * max_count, Hq]), and sequences of more than `above` tokens
+    (0: keep) are shortened to `keep` (evict_q8). weights (alloc_weights) holds what the keys gathered; prompts that
+    were appended by other means are weighed by the caller."""
+
+    def __init__(self, keep, above=0, sinks=0, recent=0, decay=1.0, coef=None, weights=None):
+        self.keep, self.above, self.sinks, self.recent, self.decay = keep, above, sinks, recent, decay
+        self.coef, self.weights = coef, weights
+
+
 class QuantStep:
     """One serving step over an 8-bit cache for n_seqs slots of up to max_count new tokens each:
     plan pages, append, attend, captured once as a CUDA graph of the library's launches over fixed
-    buffers. Arguments as for attend_q8; prefix and first_key are fixed buffers too.
+    buffers. Arguments as for attend_q8; prefix and first_key are fixed buffers too. With lam the
+    attention is differential (attend_diff_q8 with lam, gain and eps, fixed buffers); a budget
+    (KeyBudget) weighs the keys and evicts behind it.
 
     run(n_new, seq_ids, q, k, v): n_new and seq_ids int32 [n_seqs] (a slot with n_new 0 is idle),
     q, k, v the new tokens' rows one slot behind the other, in the first sum(n_new) rows of at most
@@ -928,7 +942,9 @@ class QuantStep:
     stay as they were.
     Capturing launches nothing: the cache changes only on replay."""
 
-    def __init__(self, cache: QuantCache, pool: PagePool, n_seqs, max_count=1, alpha=1.0, **score):
+    def __init__(self, cache: QuantCache, pool: PagePool, n_seqs, max_count=1, alpha=1.0, lam=None, gain=None,
+                 eps=1e-5, budget: KeyBudget | None = None, **score):
+        _need(lam is None or alpha == 1.0, "lam: differential attention is of softmax maps (alpha = 1)")
         dev, c = cache.device, cache.cfg
         total, Hq = n_seqs * max_count, cache.num_q_heads
         bf = dict(dtype=torch.bfloat16, device=dev)
@@ -940,14 +956,29 @@ class QuantStep:
         self.v = torch.zeros_like(self.k)
         self.plan = alloc_plan(n_seqs, total, dev)
         self.batch = self.plan.batch(max_count, self.seq_ids)
-        self.outputs = alloc_attend_outputs(cache, self.batch)
+        self.outputs = alloc_attend_outputs(cache, self.batch) if lam is None else alloc_diff_outputs(cache, self.batch)
         self.workspace = alloc_attend_workspace(cache, self.batch, alpha)
-        self._score = dict(score, alpha=alpha)
+        self.budget = budget
+        self._fixed = (lam, gain, score)  # (the graph reads them where they are)
+        if budget is not None:
+            if budget.weights is None:
+                budget.weights = alloc_weights(cache)
+            self.weigh_workspace = alloc_weigh_workspace(cache, self.batch, alpha)
+            self.evict_workspace = alloc_evict_workspace(cache, n_seqs, budget.keep)
 
         def launches():
             plan_pages(cache, pool, self.n_new, self.plan, seq_ids=self.seq_ids, max_count=max_count)
             append_q8(cache, self.k, self.v, self.batch)
-            attend_q8(cache, self.q, self.batch, workspace=self.workspace, outputs=self.outputs, **self._score)
+            if lam is None:
+                attend_q8(cache, self.q, self.batch, alpha=alpha, workspace=self.workspace, outputs=self.outputs, **score)
+            else:
+                attend_diff_q8(cache, self.q, lam, self.batch, gain=gain, eps=eps, workspace=self.workspace,
+                               outputs=self.outputs, **score)
+            if budget is not None:
+                weigh_q8(cache, budget.weights, self.q, self.outputs.tau, self.batch, alpha=alpha, coef=budget.coef,
+                         decay=budget.decay, workspace=self.weigh_workspace, **score)
+                evict_q8(cache, pool, budget.weights, self.seq_ids, budget.keep, above=budget.above, sinks=budget.sinks,
+                         recent=budget.recent, count=self.plan.count, workspace=self.evict_workspace)
 
         with torch.cuda.device(dev):
             launches()  # every slot idle: first-launch set-up outside the capture

@@ -232,7 +232,7 @@ size_t weigh_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total);
 cudaError_t launch_weigh_chunk(const Q8WeighArgs& a, bool i8, void* ws, int sms, cudaStream_t st);
 cudaError_t launch_weigh_stream(const Q8WeighArgs& a, bool i8, int sms, cudaStream_t st);
 size_t evict_bytes(const entmaxkv_config& cfg, int n, int keep);
-cudaError_t launch_evict(const Q8Cache& c, const int32_t* seq_ids, int n, int keep, int above, int sinks, int recent,
+cudaError_t launch_evict(const Q8Cache& c, const int32_t* seq_ids, const int32_t* count, int n, int keep, int above, int sinks, int recent,
                          const float* w, float* w_out, int32_t* lens_out, int32_t* free_pages,
                          const int32_t* free_count, int32_t* count_out, bool i8, void* ws, int sms, cudaStream_t st);
 // A pool as (dim, KV head · token, page) of bytes, in boxes of one slab.

@@ -274,8 +274,8 @@ size_t entmaxkv_evict_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, i
 }
 
 int32_t entmaxkv_evict_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* cache, const float* weights,
-                          const int32_t* seq_ids, int32_t n_seqs, int32_t keep, int32_t above, int32_t sinks,
-                          int32_t recent, float* weights_out, int32_t* lens_out, int32_t* free_pages,
+                          const int32_t* seq_ids, const int32_t* count, int32_t n_seqs, int32_t keep, int32_t above,
+                          int32_t sinks, int32_t recent, float* weights_out, int32_t* lens_out, int32_t* free_pages,
                           const int32_t* free_count, int32_t* free_count_out, void* workspace, size_t workspace_bytes,
                           void* stream) {
   int st;
@@ -288,7 +288,7 @@ int32_t entmaxkv_evict_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* c
     return ENTMAXKV_ERR_WORKSPACE_TOO_SMALL;
   const int sms = device_sms();
   if (sms < 1) return ENTMAXKV_ERR_CUDA;
-  return code_of(launch_evict(cache_of(cfg, cache), seq_ids, n_seqs, keep, above, sinks, recent, weights, weights_out,
+  return code_of(launch_evict(cache_of(cfg, cache), seq_ids, count, n_seqs, keep, above, sinks, recent, weights, weights_out,
                               lens_out, free_pages, free_count, free_count_out, cfg->kv_dtype == ENTMAXKV_I8, workspace,
                               sms, (cudaStream_t)stream));
 }

@@ -50,6 +50,7 @@ struct EvictItem {
 struct EvictArgs {
   Q8Cache c;
   const int32_t* seq_ids;
+  const int32_t* count;  // [n] or null: slots with 0 are not looked at
   int n, keep, above, sinks, recent;
   const float* w;
   float* w_out;
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(kEvictPlanThreads) evict_plan_few_kernel(Evict
   asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
   const int fc = min(max(*a.free_count, 0), a.c.nphys), kept = (a.keep + P - 1) / P;
   int seq = -1, L = 0;
-  if (tid < a.n) seq = seq_row(a.seq_ids, tid, a.c.max_seqs, status);
+  if (tid < a.n && !(a.count && a.count[tid] == 0)) seq = seq_row(a.seq_ids, tid, a.c.max_seqs, status);
   seq_sh[tid] = seq;
   if (seq >= 0) L = seq_len_clamped(a.c.seq_lens, seq, a.c.maxp, P, status);
   __syncthreads();
@@ -175,20 +176,21 @@ __global__ void __launch_bounds__(kEvictPlanThreads) evict_plan_kernel(EvictArgs
   const bool head = blockIdx.x == 0;
   uint32_t* status = head ? a.c.status : nullptr;
   const int fc = min(max(*a.free_count, 0), a.c.nphys), kept = (a.keep + P - 1) / P;
+  auto idle = [&](int b) { return a.count && a.count[b] == 0; };
   for (int b = me; b < a.n; b += all) {
-    const int seq = a.seq_ids[b];
+    const int seq = idle(b) ? -1 : a.seq_ids[b];
     a.bad[b] = 0;
     if (seq >= 0 && seq < a.c.max_seqs) a.owner[seq] = 0x7fffffff;
   }
   cluster_sync();
   for (int b = me; b < a.n; b += all) {
-    const int seq = a.seq_ids[b];
+    const int seq = idle(b) ? -1 : a.seq_ids[b];
     if (seq >= 0 && seq < a.c.max_seqs) atomicMin(a.owner + seq, b);
   }
   cluster_sync();
   auto slot = [&](int b, uint32_t* st) -> EvictItem {  // L = 0: stays as it is
     EvictItem x{-1, 0};
-    if (b >= a.n) return x;
+    if (b >= a.n || idle(b)) return x;
     x.seq = seq_row(a.seq_ids, b, a.c.max_seqs, st);
     if (x.seq < 0) return x;
     if (__ldcg(a.owner + x.seq) != b) {  // named before
@@ -602,10 +604,10 @@ static cudaError_t evict_d(const EvictArgs& a, int sms, cudaStream_t st) {
   return a.c.P == 32 ? evict_t<I8, 64, 32>(a, sms, st) : evict_t<I8, 64, 16>(a, sms, st);
 }
 
-cudaError_t launch_evict(const Q8Cache& c, const int32_t* seq_ids, int n, int keep, int above, int sinks, int recent,
+cudaError_t launch_evict(const Q8Cache& c, const int32_t* seq_ids, const int32_t* count, int n, int keep, int above, int sinks, int recent,
                          const float* w, float* w_out, int32_t* lens_out, int32_t* free_pages,
                          const int32_t* free_count, int32_t* count_out, bool i8, void* ws, int sms, cudaStream_t st) {
-  EvictArgs a{c, seq_ids, n, keep, above, sinks, recent, w, w_out, lens_out, free_pages, free_count, count_out,
+  EvictArgs a{c, seq_ids, count, n, keep, above, sinks, recent, w, w_out, lens_out, free_pages, free_count, count_out,
               nullptr, nullptr, nullptr, nullptr, nullptr, 0, 0};
   char* p = static_cast<char*>(ws);
   a.owner = reinterpret_cast<int*>(p);

@@ -30,7 +30,7 @@ def weigh(lib, c=None, batch=BATCH, score=None, alpha=1.0, tau=P256, decay=1.0, 
 
 def evict(lib, c=None, view=VIEW, weights=P256, ids=P256, n=2, keep=100, above=100, sinks=4, recent=10, w_out=P256,
           lens=P256, free=P256, ws=P256, ws_bytes=1 << 50):
-    return lib.entmaxkv_evict_q8(c or cfg(), view, weights, ids, n, keep, above, sinks, recent, w_out, lens, free, P256,
+    return lib.entmaxkv_evict_q8(c or cfg(), view, weights, ids, None, n, keep, above, sinks, recent, w_out, lens, free, P256,
                                  P256, ws, ws_bytes, None)
 
 
@@ -77,7 +77,8 @@ def test_bad_evict_arguments(lib):  # noqa: F811
     assert evict(lib, sinks=-1) == 1 and evict(lib, recent=-1) == 1 and evict(lib, sinks=91, recent=10) == 1
     assert evict(lib, sinks=0x7fffffff, recent=0x7fffffff) == 1
     assert evict(lib, ids=None) == 1 and evict(lib, lens=None) == 1 and evict(lib, free=None) == 1
-    assert evict(lib, weights=None) == 1 and evict(lib, w_out=None) == 1
+    assert evict(lib, weights=None) == 1 and evict(lib, w_out=None) == 1 and evict(lib, weights=P256 + 8) == 1
+    assert evict(lib, cfg(num_phys_pages=(1 << 27) + 1)) == 2                   # places are counted in 32 bits
     assert evict(lib, ws=None) == 3 and evict(lib, ws=P256 + 4) == 3 and evict(lib, ws_bytes=4096) == 3
     assert evict(lib, view=B.Q8CacheView(P256, P256, None, *([P256] * 3), None)) == 1
     f = lib.entmaxkv_evict_q8_workspace
@@ -109,7 +110,7 @@ def test_binding_checks_its_tensors():
            lambda: B.weigh_q8(c, w, q, tau, batch, fresh=z(2)), lambda: B.weigh_q8(c, w, q[:1], tau, batch),
            lambda: B.evict_q8(c, pool, w.double(), z(1), 8), lambda: B.evict_q8(c, pool, w, z(1, dt=torch.int64), 8),
            lambda: B.evict_q8(c, B.PagePool(z(3), z(1)), w, z(1), 8),
-           lambda: B.evict_q8(c, pool, w, z(1), 8, lens_out=z(2)), lambda: B.evict_q8(c, pool, w, z(1), 8, count_out=z(2)),
+           lambda: B.evict_q8(c, pool, w, z(1), 8, count=z(2)), lambda: B.evict_q8(c, pool, w, z(1), 8, lens_out=z(2)), lambda: B.evict_q8(c, pool, w, z(1), 8, count_out=z(2)),
            lambda: B.evict_q8(c, pool, None, z(1), 8, sinks=8, weights_out=w),
            lambda: B.evict_q8(c, pool, w, z(1), 8, weights_out=w[:2])]
     for call in bad:
