@@ -25,7 +25,8 @@ SOURCES = ["api.cu", "append.cu", "score.cu", "select.cu", "decode.cu", "softmax
            "q8_chunk_i8_d128.cu", "q8_chunk_i8_d64.cu", "q8_chunk_e4m3_d128.cu", "q8_chunk_e4m3_d64.cu",
            "q8_entmax.cu", "q8_weigh.cu", "q8_evict.cu", "q8_weigh_chunk.cu",
            "q8_weigh_chunk_i8_d128.cu", "q8_weigh_chunk_i8_d64.cu", "q8_weigh_chunk_e4m3_d128.cu",
-           "q8_weigh_chunk_e4m3_d64.cu"]
+           "q8_weigh_chunk_e4m3_d64.cu", "q8_chunk_diff_i8_d128.cu", "q8_chunk_diff_i8_d64.cu",
+           "q8_chunk_diff_e4m3_d128.cu", "q8_chunk_diff_e4m3_d64.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

@@ -5,13 +5,21 @@
 namespace ekv {
 
 template <>
-cudaError_t chunk_run<true, 128>(const ChunkArgs& g, cudaStream_t st);
+cudaError_t chunk_run<true, 128, false>(const ChunkArgs& g, cudaStream_t st);
 template <>
-cudaError_t chunk_run<true, 64>(const ChunkArgs& g, cudaStream_t st);
+cudaError_t chunk_run<true, 128, true>(const ChunkArgs& g, cudaStream_t st);
 template <>
-cudaError_t chunk_run<false, 128>(const ChunkArgs& g, cudaStream_t st);
+cudaError_t chunk_run<true, 64, false>(const ChunkArgs& g, cudaStream_t st);
 template <>
-cudaError_t chunk_run<false, 64>(const ChunkArgs& g, cudaStream_t st);
+cudaError_t chunk_run<true, 64, true>(const ChunkArgs& g, cudaStream_t st);
+template <>
+cudaError_t chunk_run<false, 128, false>(const ChunkArgs& g, cudaStream_t st);
+template <>
+cudaError_t chunk_run<false, 128, true>(const ChunkArgs& g, cudaStream_t st);
+template <>
+cudaError_t chunk_run<false, 64, false>(const ChunkArgs& g, cudaStream_t st);
+template <>
+cudaError_t chunk_run<false, 64, true>(const ChunkArgs& g, cudaStream_t st);
 
 // One block lists the items and the line: slots 1024 at a time, then the
 // round's items, a thread each.
@@ -197,7 +205,8 @@ size_t attend_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total) {
 
 template <bool I8>
 static cudaError_t chunk_d(ChunkArgs& g, cudaStream_t st) {
-  return g.a.c.D == 128 ? chunk_run<I8, 128>(g, st) : chunk_run<I8, 64>(g, st);
+  if (g.a.lam) return g.a.c.D == 128 ? chunk_run<I8, 128, true>(g, st) : chunk_run<I8, 64, true>(g, st);
+  return g.a.c.D == 128 ? chunk_run<I8, 128, false>(g, st) : chunk_run<I8, 64, false>(g, st);
 }
 
 cudaError_t launch_attend_chunk(const Q8AttendArgs& a, bool i8, void* ws, int sms, cudaStream_t st) {

@@ -238,7 +238,7 @@ struct PageMeta {
   int key0;           // first key; beyond every key where there is no page
 };
 
-template <bool I8, int D, int P, bool capped, bool biased>
+template <bool I8, int D, int P, bool capped, bool biased, bool paired>
 __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
   pdl_enter();
   constexpr int KP = kChunkKeys / P;           // pages a tile
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
       float kc = 0.0f, slope = 0.0f;  // the raw sums' factor (times the page's K scale): log2 units, or of the cap
       int pos = -1, lo = 0;
       const long long q_at = (long long)(x.s.start + tok) * a.q.ts + (long long)head * a.q.hs;
-      const long long o_at = (long long)(x.s.start + tok) * a.out.ts + (long long)(a.lam ? head >> 1 : head) * a.out.hs;
+      const long long o_at = (long long)(x.s.start + tok) * a.out.ts + (long long)(paired ? head >> 1 : head) * a.out.hs;
       const uint32_t rows_sm = q_sm + wg * TILE;  // this half's query tile, and its answers on their way out
       if (mine) {  // (asked for before the queries)
         pos = x.s.L - x.s.count + tok;
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
       const float inv = whole ? att_inv(l) : 1.0f;
       // a pair's rows lie in neighbouring lanes: both form y = first + second, and each stores half of the chunks to
       // the first one's row
-      const bool pairs = whole && a.lam;
+      const bool pairs = paired && whole;
       float first = 0.0f, fn = 1.0f;
       if (pairs) {
         const float lam = mine ? a.lam[(long long)(x.s.start + tok) * a.lam_ts + (head >> 1)] : 0.0f;
@@ -806,27 +806,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
   if (tid == 0 && gave_up) raise_flag(a.c.status, ENTMAXKV_DEV_TIMEOUT);
 }
 
-// The product kernel for one code type and head dimension (a translation unit
-// each): the page size and the score forms choose among its variants.
-template <bool I8, int D>
+// The product kernel for one code type and head dimension, of heads or of pairs of
+// them (a translation unit each; one kernel for both cost the capped form 5%: 1179 ->
+// 1243 us): the page size and the score forms choose among its variants.
+template <bool I8, int D, bool PAIRED>
 cudaError_t chunk_run(const ChunkArgs& g, cudaStream_t st);
 
-template <bool I8, int D, int P, bool CAP, bool BIAS>
+template <bool I8, int D, int P, bool CAP, bool BIAS, bool PAIRED>
 cudaError_t chunk_start(const ChunkArgs& g, cudaStream_t st) {
   const int smem = 6 * kChunkKeys * D * 2 + 1024;
-  const cudaError_t e = ensure_smem((const void*)chunk_kernel<I8, D, P, CAP, BIAS>, smem);
+  const cudaError_t e = ensure_smem((const void*)chunk_kernel<I8, D, P, CAP, BIAS, PAIRED>, smem);
   if (e != cudaSuccess) return e;
-  return launch_k(true, chunk_kernel<I8, D, P, CAP, BIAS>, dim3(g.blocks), dim3(kChunkThreads), (size_t)smem, st, g);
+  return launch_k(true, chunk_kernel<I8, D, P, CAP, BIAS, PAIRED>, dim3(g.blocks), dim3(kChunkThreads), (size_t)smem, st, g);
 }
-template <bool I8, int D, int P>
+template <bool I8, int D, int P, bool PAIRED>
 cudaError_t chunk_form(const ChunkArgs& g, cudaStream_t st) {
   const bool cap = g.a.sc.cap > 0.0f, bias = g.a.sc.slopes != nullptr;
-  if (cap) return bias ? chunk_start<I8, D, P, true, true>(g, st) : chunk_start<I8, D, P, true, false>(g, st);
-  return bias ? chunk_start<I8, D, P, false, true>(g, st) : chunk_start<I8, D, P, false, false>(g, st);
+  if (cap) return bias ? chunk_start<I8, D, P, true, true, PAIRED>(g, st) : chunk_start<I8, D, P, true, false, PAIRED>(g, st);
+  return bias ? chunk_start<I8, D, P, false, true, PAIRED>(g, st) : chunk_start<I8, D, P, false, false, PAIRED>(g, st);
 }
-template <bool I8, int D>
+template <bool I8, int D, bool PAIRED>
 cudaError_t chunk_pages(const ChunkArgs& g, cudaStream_t st) {
-  return g.a.c.P == 32 ? chunk_form<I8, D, 32>(g, st) : chunk_form<I8, D, 16>(g, st);
+  return g.a.c.P == 32 ? chunk_form<I8, D, 32, PAIRED>(g, st) : chunk_form<I8, D, 16, PAIRED>(g, st);
 }
 
 }  // namespace ekv

@@ -4,8 +4,8 @@
 namespace ekv {
 
 template <>
-cudaError_t chunk_run<false, 128>(const ChunkArgs& g, cudaStream_t st) {
-  return chunk_pages<false, 128>(g, st);
+cudaError_t chunk_run<false, 128, false>(const ChunkArgs& g, cudaStream_t st) {
+  return chunk_pages<false, 128, false>(g, st);
 }
 
 }  // namespace ekv

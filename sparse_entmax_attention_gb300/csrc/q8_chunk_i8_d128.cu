@@ -4,8 +4,8 @@
 namespace ekv {
 
 template <>
-cudaError_t chunk_run<true, 128>(const ChunkArgs& g, cudaStream_t st) {
-  return chunk_pages<true, 128>(g, st);
+cudaError_t chunk_run<true, 128, false>(const ChunkArgs& g, cudaStream_t st) {
+  return chunk_pages<true, 128, false>(g, st);
 }
 
 }  // namespace ekv

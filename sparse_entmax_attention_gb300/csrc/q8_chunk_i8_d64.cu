@@ -4,8 +4,8 @@
 namespace ekv {
 
 template <>
-cudaError_t chunk_run<true, 64>(const ChunkArgs& g, cudaStream_t st) {
-  return chunk_pages<true, 64>(g, st);
+cudaError_t chunk_run<true, 64, false>(const ChunkArgs& g, cudaStream_t st) {
+  return chunk_pages<true, 64, false>(g, st);
 }
 
 }  // namespace ekv
