@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(EvictAr
     }
     n_more = __reduce_add_sync(0xffffffffu, n_more);
     n_same = __reduce_add_sync(0xffffffffu, n_same);
+    const bool ties = n_same > 0;  // among the warp's own keys
     if (lane == 0) {
       warp_more[warp] = n_more;
       warp_same[warp] = n_same;
@@ -453,23 +454,27 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(EvictAr
           if (at >= 32) ph = ph1;
         }
         const uint32_t place = (uint32_t)ph * P + i % P, below = (1u << lane) - 1u;
-        uint32_t more[4], same[4];
         int m = n_more, n = n_same;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          more[j] = __ballot_sync(0xffffffffu, k[j] > edge);
-          same[j] = __ballot_sync(0xffffffffu, k[j] == edge);
-          m += __popc(more[j] & below);
-          n += __popc(same[j] & below);
-          n_more += __popc(more[j]);
-          n_same += __popc(same[j]);
+          const uint32_t more = __ballot_sync(0xffffffffu, k[j] > edge);
+          m += __popc(more & below);
+          n_more += __popc(more);
+        }
+        if (ties) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t same = __ballot_sync(0xffffffffu, k[j] == edge);
+            n += __popc(same & below);
+            n_same += __popc(same);
+          }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int to = m + min(n, want);
-          if ((k[j] > edge || (k[j] == edge && n < want)) && to < keep) src[to] = place + j;
+          if ((k[j] > edge || (ties && k[j] == edge && n < want)) && to < keep) src[to] = place + j;
           m += k[j] > edge;
-          n += k[j] == edge;
+          if (ties) n += k[j] == edge;
         }
       }
     }
