@@ -34,7 +34,7 @@ constexpr int kWcThreads = 896;
 constexpr int kWcKeys = 256, kWcRows = 128;
 // Stages of the rows, and of their facts, which the sums read longer: the facts of unit u are asked for when the
 // products of u − kWcQ are done, so the sums of u − kWcQ − 2 are.
-constexpr int kWcQ = 2, kWcMeta = kWcQ + 2, kWcSegs = 3, kWcK = 2;
+constexpr int kWcQ = 2, kWcMeta = kWcQ + 2, kWcSegs = 5, kWcK = 2;
 constexpr int kWcMaxBlocks = 256;
 constexpr int kWcTurns = 6;  // segments a block should get at least
 
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
     for (int i = 0; i < kWcMeta; ++i) mbar_init(&f_full[i], 1);
     for (int i = 0; i < kWcSegs; ++i) {
       mbar_init(&g_full[i], 1);
-      mbar_init(&g_empty[i], 19);  // 16 warps of sums, 2 of products, 1 of rows
+      mbar_init(&g_empty[i], 27);  // 16 warps of sums, 8 of keys, 2 of products, 1 of rows
     }
     for (int i = 0; i < kWcK; ++i) {
       mbar_init(&k_full[i], 256);
@@ -458,47 +458,31 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
     const int cw = warp - 16;                      // keys 32·cw .. 32·cw + 31 of a tile
     constexpr int CPR = D / 16;                   // 16-code chunks of a key
     constexpr int RPI = 32 / CPR, NI = 32 / RPI;  // keys a load, loads of a warp's keys
-    constexpr int PW = 32 / P;                    // pages of a warp's keys
     // (as in the chunk attention: eight lanes store to eight banks' quads)
     const int cch = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane % CPR;
     const int crow = D == 128 ? (lane >> 2 & 1) | (lane >> 3 & 2) : lane / CPR;
-    // the next segment with keys that somebody may see: its pages as the table has them, looked at when their codes
-    // are asked for
-    struct Ahead {
-      long long id;
-      int kvh, L, ph, key;
-    };
-    auto find = [&](long long id) -> Ahead {
-      for (; id < n_segs; id += gridDim.x) {
-        const WcSeg x = wc_seg<P>(g, few, id, slot);
-        if (!x.seen) continue;
-        Ahead n{id, x.kvh, x.s.L, -1, kNoKey};
-        const int t = x.kt * PT + cw * PW + lane;
-        if (lane < PW && t < x.pages()) {
-          n.key = x.page(t) * P;
-          n.ph = a.c.block_table[(size_t)x.s.seq * a.c.maxp + x.page(t)];
-        }
-        return n;
-      }
-      return Ahead{id, 0, 0, -1, kNoKey};
-    };
     uint4 codes[NI];
-    auto load = [&](const Ahead& n) {
-      const int key = n.ph >= 0 && n.ph < a.c.nphys ? n.key : kNoKey;  // (the sums flag other pages)
+    auto load = [&](const WcInfo& q) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int rr = i * RPI + crow, tk = rr % P;
-        const int fq = __shfl_sync(0xffffffffu, n.ph, rr / P), kq = __shfl_sync(0xffffffffu, key, rr / P);
+        const WcPage page = q.pages[(32 * cw + rr) / P];
         codes[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (kq + tk < n.L)  // (false where there is no page)
-          codes[i] = __ldg(reinterpret_cast<const uint4*>(a.c.k_pool + (((size_t)fq * Hkv + n.kvh) * P + tk) * D + cch * 16));
+        if (page.key0 + tk < q.x.s.L)  // (false where there is no page)
+          codes[i] = __ldg(reinterpret_cast<const uint4*>(a.c.k_pool + ((size_t)page.at * P + tk) * D + cch * 16));
       }
     };
     int tiles = 0;  // key tiles so far
-    Ahead now = find(blockIdx.x);
-    Ahead next = find(now.id + gridDim.x);
-    if (now.id < n_segs) load(now);
-    while (now.id < n_segs && ok) {
+    for (int k = 0; k < n_mine && ok; ++k) {
+      if (!seg_wait(k)) {
+        ok = false;
+        break;
+      }
+      const WcInfo& q = segs[k % kWcSegs];
+      const bool seen = q.x.seen;
+      if (seen) load(q);
+      seg_done(k);
+      if (!seen) continue;
       if (tiles >= kWcK && !wait_warp(&k_empty[tiles % kWcK], tiles / kWcK - 1)) {
         ok = false;
         break;
@@ -517,11 +501,6 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
       }
       asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
       mbar_arrive(&k_full[tiles % kWcK]);
-      now = next;
-      if (now.id < n_segs) {
-        load(now);
-        next = find(now.id + gridDim.x);
-      }
       ++tiles;
     }
   } else {  // ------------------------------------------------ products, and the rows' copies
