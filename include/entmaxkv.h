@@ -371,7 +371,9 @@ int32_t entmaxkv_decode_softmax_noalloc(const entmaxkv_config* cfg, const entmax
 
 /* ------------------------------------------------------------------------
  * The 8-bit paged cache: page planning, a quantising append, its read-back
- * and attention over the cache. A serving step is plan, append, attend.
+ * and attention over the cache, differential attention too. A serving step is
+ * plan, append, attend; sequences are held to a budget of keys by two more
+ * calls, weigh (what the rows gave to each key) and evict.
  *
  * A stored value is code * scale with one float32 scale for the K and one for
  * the V rows of each (physical page, KV head). A page belongs to one sequence
@@ -635,7 +637,8 @@ int32_t entmaxkv_attend_diff_q8(const entmaxkv_config* cfg, const entmaxkv_q8_ca
  *            with decay = 1 keys that no row may see, are left as they were
  *   workspace  (device) at least entmaxkv_weigh_q8_workspace(...) bytes, 256-byte
  *            aligned, contents are scratch; not to be shared by calls that may run
- *            at the same time
+ *            at the same time. Past 32 rows a slot it holds the queries once more, in
+ *            tiles of 128 rows of a slot and KV head
  * Sums are float32 in an order that the arguments and the device fix.
  */
 size_t entmaxkv_weigh_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, int32_t total,

@@ -28,6 +28,10 @@
 // start, block join and join kernel, which is what a single sequence of 32k
 // tokens (67 MB) feels: 27.5 us (23.3 where L2 holds them). In a capture (789 MB, 131 us) the pipes wait
 // for nothing in particular: ALU 48% (codes to halves), IPC 2.2.
+//
+// Differential attention takes the difference of two rows' answers, and its norm, where they leave: a pair's rows lie
+// in one lane (whole units), one warp (block join) or one block (join kernel). One sequence of 32k tokens with the norm
+// 31 us, the ragged batch with a factor for every row 142 us.
 #include "q8_tiles.cuh"
 
 namespace ekv {

@@ -25,7 +25,13 @@
 // and long. What counts is how many slots are evicted, which the plan finds out: both
 // forms are launched, and one returns at once.
 //
-// Bound: the bytes of the weights and the kept codes, and that chain.
+// Bound: the bytes of the weights and the kept codes, and that chain. Measured (8 KV heads; a launch list, cold):
+// plan 7-9 us. One sequence of 131072 tokens to 16384, int8, d = 128 (4 MB of weights, 67 MB of codes in and out):
+// select 23 us, of which loads 4, the four counts 11 (half of it cluster barriers) and the listing 5; move 27 us, four
+// waves of a load (random rows of 128 bytes), a barrier and a store, 2.5 TB/s. 16 sequences of 1000-32000 to 1024,
+// e4m3, d = 64: select 27 us, as long as its longest sequence, move 14 us. 13 sequences of about 2400 to 2048: select 11,
+// move 17 us (109 MB: at the copy's rate). In one kernel, with K and V in one warp's registers and clusters of 16
+// (of which only a few run at a time), the first took 101 us and the second 160.
 #include "q8_tiles.cuh"
 
 namespace ekv {
@@ -40,9 +46,6 @@ constexpr int kBins = 2048;
 // behind the sequence's end below all (minus infinity is 0x007fffff). So the edge is the keep-th largest code.
 constexpr uint32_t kCodeStays = 0xffffffffu, kCodeNaN = 0xfffffffeu;
 constexpr int kEvictCluster = 8;
-// Keys to keep from which few (slot, KV head) pairs get a cluster each: at most 4 waves of the 32 pages that a block's
-// warps hold are below.
-constexpr int kEvictLong = 4096;
 
 struct EvictItem {
   int seq, L;
@@ -90,7 +93,7 @@ __device__ __forceinline__ uint4 ld_cluster4(uint32_t addr) {
 
 // The same for at most 1024 slots, a thread each: what the general form leaves in
 // memory between its steps stays in registers and shared memory (one sequence of
-// 131k tokens: X us against 11).
+// 131k tokens: 7.4 us against 11.3).
 __global__ void __launch_bounds__(kEvictPlanThreads) evict_plan_few_kernel(EvictArgs a) {
   pdl_enter();
   __shared__ int sh_scan[32];
@@ -583,19 +586,21 @@ static cudaError_t evict_launch(void (*kernel)(EvictArgs), const EvictArgs& a, l
 
 template <bool I8, int D, int P>
 static cudaError_t evict_t(EvictArgs a, int sms, cudaStream_t st) {
-  const long long most = (long long)a.n * a.c.Hkv, few = sms / kEvictCluster;
+  // Pairs up to which each has a cluster. Measured, clusters against blocks alone, 8 KV heads, int8, d = 128: one
+  // sequence of 17000 to 16000 (8 pairs) 43/116 us, two 55/166, four 99/125-175, 16 of 9000 to 8000 (128 pairs) 292/115;
+  // one of 3000 to 2000 25/29. Launching both costs 2 us.
+  const long long most = (long long)a.n * a.c.Hkv, few = sms / 4;
   const int smem = kEvictKeys * 4;
   cudaError_t e = ensure_smem((const void*)evict_select_kernel<P>, smem);
-  const bool wide = most <= few || a.keep > kEvictLong, alone = most > few;
   for (int step = 0; step < 2; ++step) {  // select, move
-    if (wide && e == cudaSuccess) {
+    if (e == cudaSuccess) {
       a.from = 0;
       a.to = few;
-      e = step ? evict_launch(evict_move_kernel<I8, D, P>, a, min(2 * most, 2 * few), kEvictCluster, 512, 0, st)
-               : evict_launch(evict_select_kernel<P>, a, min(most, few), kEvictCluster, kSelectThreads, smem, st);
+      e = step ? evict_launch(evict_move_kernel<I8, D, P>, a, min(2 * most, few), kEvictCluster, 512, 0, st)
+               : evict_launch(evict_select_kernel<P>, a, min(most, few / 2), kEvictCluster, kSelectThreads, smem, st);
     }
-    if (alone && e == cudaSuccess) {
-      a.from = wide ? few : 0;
+    if (most > few && e == cudaSuccess) {
+      a.from = few;
       a.to = most;
       e = step ? evict_launch(evict_move_kernel<I8, D, P>, a, min(2 * most, 4LL * sms), 1, 512, 0, st)
                : evict_launch(evict_select_kernel<P>, a, min(most, (long long)sms), 1, kSelectThreads, smem, st);

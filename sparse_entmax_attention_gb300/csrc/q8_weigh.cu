@@ -9,18 +9,26 @@
 // answered by whoever holds it: no pass is joined with another, and every sum has
 // one order.
 //
-// Bound: K's bytes. As in the streaming attention, the tiles (32 keys) of all
+// Up to 32 rows a sequence (max_count · group). Bound: K's bytes. As in the streaming attention, the tiles (32 keys) of all
 // (slot, KV head) units form one line cut into equal pieces for all warps of the
 // device, and a warp streams its K pages through a ring of tensor copies:
 //   S = K·q^T   m16n8k16 in halves, 16 keys × 8 rows a product, fp32 sums;
 //   p           in fp32, summed over a lane's rows and the four lanes of a key.
+//
+// Measured: 16 sequences of 1000-32000 tokens, 8 KV heads of 4 query heads, d = 128, e4m3, entmax (196 MB): 38-41 us,
+// 5.0 TB/s, 0.74 of the measured copy (45 with a key's weight asked for in its own tile); 16 of 24000, int8 (418 MB):
+// 75 us, 5.5 TB/s, codes to halves beside it (ALU 55%, IPC 2.4). One sequence of 32768 (36 MB): 13-15 us, of which the
+// bytes are 5.3: start, and three or four tiles a warp.
 #include "q8_tiles.cuh"
 
 namespace ekv {
 
-constexpr int kWeighWarps = 16, kWeighKeys = 32;
-template <int D>
-constexpr int kWeighSlabs = 192 * 1024 / (kWeighWarps * kWeighKeys * D);
+constexpr int kWeighKeys = 32;
+// Warps of a block: four tiles of 8 rows need twice the registers.
+template <int NT>
+constexpr int kWeighWarps = NT == 4 ? 8 : 16;
+template <int D, int NT>
+constexpr int kWeighSlabs = 192 * 1024 / (kWeighWarps<NT> * kWeighKeys * D);
 
 // A slot's pages: those of the span, and what changes beside it (faded or fresh
 // weights). T tiles on the line a KV head.
@@ -49,9 +57,9 @@ __device__ __forceinline__ WeighSlot weigh_slot(const Q8WeighArgs& a, int b, uin
 }
 
 template <bool I8, int D, int P, int NT, bool ENT>
-__global__ void __launch_bounds__(kWeighWarps * 32, 1) weigh_kernel(Q8WeighArgs a, const __grid_constant__ CUtensorMap kmap) {
+__global__ void __launch_bounds__(kWeighWarps<NT> * 32, 1) weigh_kernel(Q8WeighArgs a, const __grid_constant__ CUtensorMap kmap) {
   pdl_enter();
-  constexpr int NW = kWeighWarps, ST = kWeighSlabs<D>, SLAB = kWeighKeys * D, PP = kWeighKeys / P;
+  constexpr int NW = kWeighWarps<NT>, ST = kWeighSlabs<D, NT>, SLAB = kWeighKeys * D, PP = kWeighKeys / P;
   extern __shared__ __align__(128) unsigned char dyn_sm[];
   __shared__ uint64_t bars[NW][ST];
   __shared__ LineSmem<NW> sh_line;
@@ -297,18 +305,19 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 1) weigh_kernel(Q8WeighArgs 
 
 template <bool I8, int D, int P, int NT, bool ENT>
 static cudaError_t weigh_t(const Q8WeighArgs& a, int sms, cudaStream_t st) {
-  const int smem = kWeighWarps * kWeighSlabs<D> * kWeighKeys * D + 1024;
+  const int smem = kWeighWarps<NT> * kWeighSlabs<D, NT> * kWeighKeys * D + 1024;
   cudaError_t e = ensure_smem((const void*)weigh_kernel<I8, D, P, NT, ENT>, smem);
   if (e != cudaSuccess) return e;
   CUtensorMap km;
   if ((e = make_q8_map(&km, a.c.k_pool, a.c.nphys, a.c.Hkv, P, D)) != cudaSuccess) return e;
-  return launch_k(true, weigh_kernel<I8, D, P, NT, ENT>, dim3(sms), dim3(kWeighWarps * 32), (size_t)smem, st, a, km);
+  return launch_k(true, weigh_kernel<I8, D, P, NT, ENT>, dim3(sms), dim3(kWeighWarps<NT> * 32), (size_t)smem, st, a, km);
 }
 template <bool I8, int D, int P>
 static cudaError_t weigh_n(const Q8WeighArgs& a, int sms, cudaStream_t st) {
   if (a.a1 > 0.0f) return weigh_t<I8, D, P, 1, true>(a, sms, st);  // (one row a sequence: a group of at most 8)
-  return (long long)a.b.max_count * a.c.G <= 8 ? weigh_t<I8, D, P, 1, false>(a, sms, st)
-                                               : weigh_t<I8, D, P, 2, false>(a, sms, st);
+  const long long rows = (long long)a.b.max_count * a.c.G;
+  if (rows <= 8) return weigh_t<I8, D, P, 1, false>(a, sms, st);
+  return rows <= 16 ? weigh_t<I8, D, P, 2, false>(a, sms, st) : weigh_t<I8, D, P, 4, false>(a, sms, st);
 }
 template <bool I8>
 static cudaError_t weigh_d(const Q8WeighArgs& a, int sms, cudaStream_t st) {

@@ -20,10 +20,22 @@
 // Warps: 16 of sums (two threads a key, one for each 64 rows of a tile: four warps a
 // scheduler hide one another's waits); 8 that bring the keys (the next 256 wait as
 // codes in registers until the products with the present ones are done); 2 that
-// issue the products, one for each 128 keys; 1 that asks for the rows, four tiles
-// ahead; 1 that looks up the segments ahead of them all. Segments (key tile, share of the rows) go round the blocks in turns; rows
-// are shared out only where there are few key tiles, and the block that finishes a
-// tile last adds its shares in their order.
+// issue the products, one for each 128 keys; 1 that asks for the rows, two tiles
+// ahead; 1 that looks up the segments ahead of them all. Segments (key tile, share of
+// the rows) go round the blocks in turns; rows are shared out only where there are
+// few key tiles, and the block that finishes a tile last adds its shares in their
+// order. (Segments handed out as blocks are done with the last: no faster.)
+//
+// Bound: latency and issue of the sums. A tile of rows (256 keys × 128 rows) takes
+// them about 1700 cycles; its exponentials alone are 1024 (32 a clock and
+// multiprocessor), its products 1024, and the two meet in shared memory, where the
+// operands and the rows' facts are read. Measured, int8, 8 KV heads of 4 query heads,
+// d = 128: 2048 rows on 30001 keys before them (0.52 TFLOP) 407 us with listing and
+// packing (15 us), 1290 TFLOP/s, 0.66 of the measured bf16 burst; in a capture
+// (10240 keys) exponentials 53%, tensor pipe 51%, IPC 2.3. Kept aside, measured: two
+// warps of sums a scheduler 543 us; one key tile in shared memory (four stages of rows)
+// 463; keys in tensor memory and tiles of 96 rows 435-463, with the last rows of six
+// prompts at 77 us instead of 64; single fp32 operations in place of pairs 482.
 #pragma once
 
 #include "q8_chunk.cuh"
@@ -36,7 +48,7 @@ constexpr int kWcKeys = 256, kWcRows = 128;
 // products of u − kWcQ are done, so the sums of u − kWcQ − 2 are.
 constexpr int kWcQ = 2, kWcMeta = kWcQ + 2, kWcSegs = 5, kWcK = 2;
 constexpr int kWcMaxBlocks = 256;
-constexpr int kWcTurns = 6;  // segments a block should get at least
+constexpr int kWcTurns = 3;  // segments a block should get at least (12, 6, 3: 109, 97, 88 us for 1024 rows on 8001 keys)
 
 struct __align__(16) WcSlot {
   int seq, L, start, count;        // Q8Slot

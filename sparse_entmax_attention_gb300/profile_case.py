@@ -14,7 +14,9 @@ bench. Policies: gaussian, topk, softmax, softmax_topk, full, full_dense.
 repeats a call on the 8-bit cache instead (int8 codes, 32 query heads over 8 KV
 heads, d = 128, page 32, --seqs sequences of --tokens tokens of which the last
 --new are the step's): append, read, decode (softmax of one token each), chunk
-(softmax of --new tokens each, capped with --softcap) or entmax (one token each).
+(softmax of --new tokens each, capped with --softcap), entmax (one token each), diff
+(differences of pairs of heads, --new tokens each), weigh (what --new tokens give to
+the keys) or evict (to --keep tokens, with weights of many sizes).
 """
 
 from __future__ import annotations
@@ -47,9 +49,27 @@ def q8_case(args, flush) -> int:
     first = torch.full((args.seqs,), args.tokens - new, dtype=torch.int32, device="cuda")
     alpha = args.alpha if args.q8 == "entmax" else 1.0
     out, ws = B.alloc_attend_outputs(cache, last), B.alloc_attend_workspace(cache, last, alpha)
+    if args.q8 == "diff":
+        lam, pairs = torch.rand(16, device="cuda"), B.alloc_diff_outputs(cache, last)
+    if args.q8 == "weigh":
+        weights, weigh_ws = B.alloc_weights(cache), B.alloc_weigh_workspace(cache, last)
+        B.attend_q8(cache, q, last, softcap=args.softcap, workspace=ws, outputs=out)
+    if args.q8 == "evict":
+        weights = torch.exp(1.5 * torch.randn_like(B.alloc_weights(cache)))
+        keep = args.keep or args.tokens // 8
+        pool = B.PagePool(torch.zeros(pages, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"))
+        ids = torch.arange(args.seqs, dtype=torch.int32, device="cuda")
+        apart = dict(lens_out=torch.empty_like(cache.seq_lens), count_out=torch.empty_like(pool.free_count),
+                     weights_out=torch.empty_like(weights), workspace=B.alloc_evict_workspace(cache, args.seqs, keep))
     for _ in range(args.reps):
         flush.fill_(1)
-        if args.q8 == "append":
+        if args.q8 == "diff":
+            B.attend_diff_q8(cache, q, lam, last, softcap=args.softcap, workspace=ws, outputs=pairs)
+        elif args.q8 == "weigh":
+            B.weigh_q8(cache, weights, q, out.tau, last, softcap=args.softcap, decay=0.9, workspace=weigh_ws)
+        elif args.q8 == "evict":
+            B.evict_q8(cache, pool, weights, ids, keep, sinks=4, recent=keep // 8, **apart)
+        elif args.q8 == "append":
             B.append_q8(cache, k, v, last)
         elif args.q8 == "read":
             B.read_q8(cache, first, last, k, v)
@@ -69,10 +89,11 @@ def main(argv=None) -> int:
     ap.add_argument("--budget", type=int, default=2048, help="top-k budget in tokens")
     ap.add_argument("--alpha", type=float, default=1.5)
     ap.add_argument("--margin", type=float, default=0.5)
-    ap.add_argument("--q8", choices=["append", "read", "decode", "chunk", "entmax"], help="a call on the 8-bit cache")
+    ap.add_argument("--q8", choices=["append", "read", "decode", "chunk", "entmax", "diff", "weigh", "evict"], help="a call on the 8-bit cache")
     ap.add_argument("--seqs", type=int, default=1)
     ap.add_argument("--new", type=int, default=2048)
     ap.add_argument("--softcap", type=float, default=0.0)
+    ap.add_argument("--keep", type=int, default=0, help="tokens that an eviction leaves (an eighth)")
     args = ap.parse_args(argv)
     flush = torch.empty(128 << 20, dtype=torch.int32, device="cuda")
     if args.q8:

@@ -226,3 +226,17 @@ def test_a_call_on_slots_that_stay_changes_nothing():
     B.evict_q8(c, pool, w, torch.zeros(0, dtype=torch.int32, device="cuda"), 64)
     after = state(c, pool, w)
     assert all(torch.equal(before[k], after[k]) for k in before) and c.device_status() == 0
+
+
+@pytest.mark.parametrize("n_long,keep", [(1, 4100), (19, 4100), (20, 4100), (30, 900)])
+def test_few_and_many_long_ones_among_many_slots(n_long, keep):
+    """Clusters where few are evicted, blocks alone where many are: which of them is known on the device only."""
+    lens = [keep + 60 + 7 * i if i < n_long else 30 + i for i in range(32)]
+    c, pool = make("e4m3", lens, hkv=1, d=64, P=32, seed=3)
+    check(c, pool, spread_weights(c), "e4m3", list(range(32))[::-1], keep, sinks=2, recent=40)
+
+
+def test_idle_slots_are_not_looked_at():
+    c, pool = make("int8", [300, 300, 300], P=32)
+    B.evict_q8(c, pool, spread_weights(c), i32([0, 77, 0, 2]), 64, count=i32([1, 0, 0, 5]))
+    assert c.device_status() == 0 and c.seq_lens.tolist() == [64, 300, 64]

@@ -223,3 +223,23 @@ def test_more_slots_than_a_block_keeps_at_hand():
     run(c, q, [1] * n)
     c, q = filled("int8", [20 + i % 40 for i in range(n)], [9 + i % 9 for i in range(n)], hkv=1, g=4, d=64, P=16)
     run(c, q, [9 + i % 9 for i in range(n)], decay=0.5)
+
+
+def test_more_slots_than_a_round_of_the_planning():
+    n = 1100
+    counts = [5 + i % 7 if i % 5 else 0 for i in range(n)]
+    c, q = filled("int8", [12 + i % 30 for i in range(n)], counts, hkv=1, g=4, d=64, P=16)
+    run(c, q, counts)
+
+
+def test_slots_that_claim_the_same_rows_stop_at_the_lists_end():
+    """The third slot's row tiles do not fit the list that the rows have room for: it is flagged and left."""
+    c, q = filled("int8", [90, 80, 70], [60, 0, 0], hkv=1, g=8, d=64, P=16)
+    tau = B.attend_q8(c, q, batch_of([60])).tau
+    before = some_weights(c)
+    after = before.clone()
+    B.weigh_q8(c, after, q, tau, B.Batch(i32([0, 0, 0]), i32([60, 60, 60]), 60, 60))
+    assert c.device_status() == B.DEV_BAD_BATCH
+    check_weights(c, q, [60], tau, before, after)
+    others_untouched(c, before, after, [0, 1])
+    assert not torch.equal(before, after)
