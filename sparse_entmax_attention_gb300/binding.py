@@ -920,8 +920,9 @@ def evict_q8(cache: QuantCache, pool: PagePool, weights, seq_ids, keep, above=0,
 class KeyBudget:
     """How many keys a QuantStep leaves each of its sequences: behind the attention the step's rows weigh the keys
     (weigh_q8 with decay and, for some, coef [n_seqs * max_count, Hq]), and sequences of more than `above` tokens
-    (0: keep) are shortened to `keep` (evict_q8). weights (alloc_weights) holds what the keys gathered; prompts that
-    were appended by other means are weighed by the caller."""
+    (0: keep) are shortened to `keep` (evict_q8). weights holds what the keys gathered: the caller's (alloc_weights), or
+    None for some of the step's own (step.budget.weights); prompts that were appended by other means are weighed by
+    the caller."""
 
     def __init__(self, keep, above=0, sinks=0, recent=0, decay=1.0, coef=None, weights=None):
         self.keep, self.above, self.sinks, self.recent, self.decay = keep, above, sinks, recent, decay
@@ -958,7 +959,7 @@ class QuantStep:
         self.batch = self.plan.batch(max_count, self.seq_ids)
         self.outputs = alloc_attend_outputs(cache, self.batch) if lam is None else alloc_diff_outputs(cache, self.batch)
         self.workspace = alloc_attend_workspace(cache, self.batch, alpha)
-        self.budget = budget
+        self.budget = budget = copy.copy(budget)  # (steps over several caches may be given one budget)
         self._fixed = (lam, gain, score)  # (the graph reads them where they are)
         if budget is not None:
             if budget.weights is None:

@@ -67,7 +67,7 @@ def test_captured_step_matches_eager_calls_and_the_oracle(code, most, alpha, dif
         torch.cuda.synchronize()
         n = sum(counts)
         assert torch.equal(o.out, os_.out[:n]) and torch.equal(torch.nan_to_num(o.tau), torch.nan_to_num(os_.tau[:n]))
-        there = state(caches[1], pools[1], budget.weights)
+        there = state(caches[1], pools[1], step.budget.weights)
         assert all(torch.equal(got[name], there[name]) for name in got), i
     assert max(caches[0].seq_lens.tolist()) <= above
     assert caches[0].device_status() == 0 and caches[1].device_status() == 0
@@ -97,3 +97,14 @@ def test_a_prompt_by_its_last_rows_then_single_tokens():
         B.append_q8(c, k, v, plan.batch(1))
         check_attend(c, q, [1], B.attend_q8(c, q, plan.batch(1)))
     assert c.device_status() == 0 and c.seq_lens.tolist() == [503]
+
+
+def test_steps_given_one_budget_keep_weights_of_their_own():
+    hkv, g, d, P = 2, 4, 64, 16
+    budget = B.KeyBudget(20, 24, 2, 6)
+    q, k, v = rows(3, [1], hkv, g, d)
+    caches = [B.QuantCache(hkv, g, d, P, 1, 4, 4, torch.int8) for _ in range(2)]
+    steps = [B.QuantStep(c, B.PagePool.full(4), 1, budget=budget) for c in caches]
+    assert budget.weights is None
+    steps[0].run(i32([1]), i32([0]), q, k, v)
+    assert float(steps[0].budget.weights.sum()) > 0 and not steps[1].budget.weights.any()
