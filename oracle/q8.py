@@ -179,6 +179,6 @@ def evict_rows(codes, scales, kept, page, code):
         src = kept[p0:p0 + page]
         s = max(float(scales[j]) for j in src)
         now.append(s)
-        out += [nearest(np.asarray(codes[j], np.float64) * float(np.float32(np.float32(scales[j]) / np.float32(s))), code)
-                for j in src]
+        r = [1.0 if float(scales[j]) == s else float(np.float32(np.float32(scales[j]) / np.float32(s))) for j in src]
+        out += [nearest(np.asarray(codes[j], np.float64) * x, code) for j, x in zip(src, r)]
     return np.array(out), now

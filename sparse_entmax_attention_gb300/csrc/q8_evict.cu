@@ -29,8 +29,8 @@
 // plan 7-9 us. One sequence of 131072 tokens to 16384, int8, d = 128 (4 MB of weights, 67 MB of codes in and out):
 // select 23 us, of which loads 4, the four counts 11 (half of it cluster barriers) and the listing 5; move 27 us, four
 // waves of a load (random rows of 128 bytes), a barrier and a store, 2.5 TB/s. 16 sequences of 1000-32000 to 1024,
-// e4m3, d = 64: select 27 us, as long as its longest sequence, move 14 us. 13 sequences of about 2400 to 2048: select 11,
-// move 17 us (109 MB: at the copy's rate). In one kernel, with K and V in one warp's registers and clusters of 16
+// e4m3, d = 64: select 27 us, as long as its longest sequence, move 14 us. All three, int8, d = 128:
+// 55 us for 131072 to 16384, 25 for 3000 to 2000, 62 for 32768 to 28000. In one kernel, with K and V in one warp's registers and clusters of 16
 // (of which only a few run at a time), the first took 101 us and the second 160.
 #include "q8_tiles.cuh"
 
@@ -91,8 +91,8 @@ __device__ __forceinline__ uint4 ld_cluster4(uint32_t addr) {
   return v;
 }
 
-// The same for at most 1024 slots, a thread each: what the general form leaves in
-// memory between its steps stays in registers and shared memory (one sequence of
+// The plan for at most 1024 slots, a thread each: what the general form, below, leaves
+// in memory between its steps stays in registers and shared memory (one sequence of
 // 131k tokens: 7.4 us against 11.3).
 __global__ void __launch_bounds__(kEvictPlanThreads) evict_plan_few_kernel(EvictArgs a) {
   pdl_enter();
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(1024, 1) evict_move_kernel(EvictArgs a) {
         const float own = __ldcg(scales + at);
         if (weighs) w = __ldcg(a.w + key);
         top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(own)));
-        const float ratio = __fdiv_rn(own, top);
+        const float ratio = own == top ? 1.0f : __fdiv_rn(own, top);  // (0/0 of pages that hold nothing but zeros)
         if (__any_sync(0xffffffffu, ratio != 1.0f)) {
 #pragma unroll
           for (int n = 0; n < NI; ++n) {

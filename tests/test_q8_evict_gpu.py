@@ -132,6 +132,17 @@ def test_equal_and_odd_weights(ties):
     check(c, pool, w, "int8", [0, 1], 100, sinks=2, recent=5)
 
 
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+def test_pages_whose_scale_is_zero(code):
+    """All of a sequence's pages, every second one, and pages of the smallest scale that append writes."""
+    c, pool = make(code, [700, 650, 333], seed=4, P=16, d=64)
+    for s in (c.k_scale, c.v_scale):
+        s[c.block_table[0, :44].long()] = 0.0
+        s[c.block_table[1, :41:2].long()] = 0.0
+        s[c.block_table[2, :21].long()] = 2.0 ** -96
+    check(c, pool, spread_weights(c), code, [0, 1, 2], 100, sinks=2, recent=5)
+
+
 def test_above_leaves_sequences_until_they_pass_it():
     c, pool = make("e4m3", [100, 130, 131, 400], P=16)
     check(c, pool, spread_weights(c), "e4m3", [0, 1, 2, 3], 90, above=130)
