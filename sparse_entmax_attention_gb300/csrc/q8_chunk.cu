@@ -70,11 +70,10 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(ChunkArgs g) {
       if (j < total && items + j < g.max_items) g.cum[items + j] = tiles + before;
       tiles += all;
     }
-    items += total;
+    items = min(items + total, g.max_items);  // (rows claimed over and over: the sum may pass 31 bits)
     __syncthreads();
   }
   if (tid == 0) {
-    items = min(items, g.max_items);
     g.n_items[0] = items;
     g.n_items[1] = none_sh;
     g.cum[items] = tiles;

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(1024) weigh_plan_kernel(WcArgs g) {
       }
       g.slots[b] = x;
     }
-    tiles += total;
+    tiles = min(tiles + total, g.max_tiles);  // (rows claimed over and over: the sum may pass 31 bits)
     __syncthreads();
   }
   // rows are shared out where key tiles alone give a block less than kWcTurns segments
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(1024) weigh_plan_kernel(WcArgs g) {
   }
   if (tid == 0) {
     g.cum[n] = base;
-    *g.n_tiles = min(tiles, g.max_tiles);
+    *g.n_tiles = tiles;
   }
   if (shares > 1)
     for (long long i = tid; i < 8 * base; i += 1024) g.done[i] = 0;
