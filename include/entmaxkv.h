@@ -629,7 +629,8 @@ int32_t entmaxkv_attend_diff_q8(const entmaxkv_config* cfg, const entmaxkv_q8_ca
  *   coef     (device) [total][Hq] float32 factors, or NULL: 1. Those that are not
  *            above 0 count as 0. (1 and lam for the two maps of a pair weigh keys
  *            by a bound of the difference's.)
- *   decay    at least 0; with 0 what was gathered is not read
+ *   decay    at least 0; with 0 what was gathered is not read. Slots without rows are
+ *            left as they were
  *   fresh    (device) [n_seqs] int32: a sequence's last fresh[b] keys gathered
  *            nothing before, whatever lies in `weights`; NULL: its count[b] rows
  *   weights  (device, in/out) [num_phys_pages][num_kv_heads][page_size] float32: a key's

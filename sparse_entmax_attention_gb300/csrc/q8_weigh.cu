@@ -15,8 +15,8 @@
 //   S = K·q^T   m16n8k16 in halves, 16 keys × 8 rows a product, fp32 sums;
 //   p           in fp32, summed over a lane's rows and the four lanes of a key.
 //
-// Measured: 16 sequences of 1000-32000 tokens, 8 KV heads of 4 query heads, d = 128, e4m3, entmax (196 MB): 38-41 us,
-// 5.0 TB/s, 0.74 of the measured copy (45 with a key's weight asked for in its own tile); 16 of 24000, int8 (418 MB):
+// Measured: 16 sequences of 1000-32000 tokens, 8 KV heads of 4 query heads, d = 128, e4m3, entmax (165 MB): 38 us,
+// 4.3 TB/s, 0.64 of the measured copy (45 with a key's weight asked for in its own tile); 16 of 24000, int8 (418 MB):
 // 75 us, 5.5 TB/s, codes to halves beside it (ALU 55%, IPC 2.4). One sequence of 32768 (36 MB): 13-15 us, of which the
 // bytes are 5.3: start, and three or four tiles a warp.
 #include "q8_tiles.cuh"
