@@ -21,8 +21,8 @@
 //         of later pages lie behind all pages written so far, as src(d) ≥ d and src
 //         grows.
 // One (slot, KV head) is a chain of latencies (loads, counts, barriers), so they run
-// side by side: a block each where they are many, clusters of 8 where they are few
-// and long. What counts is how many slots are evicted, which the plan finds out: both
+// side by side: a block each where they are many or short, clusters of 8 where they
+// are few and long. What counts is how many slots are evicted, which the plan finds out: both
 // forms are launched, and one returns at once.
 //
 // Bound: the bytes of the weights and the kept codes, and that chain. Measured (8 KV heads; a launch list, cold):
@@ -586,18 +586,19 @@ static cudaError_t evict_launch(void (*kernel)(EvictArgs), const EvictArgs& a, l
 
 template <bool I8, int D, int P>
 static cudaError_t evict_t(EvictArgs a, int sms, cudaStream_t st) {
-  // Pairs up to which each has a cluster. Measured, clusters against blocks alone, 8 KV heads, int8, d = 128: one
-  // sequence of 17000 to 16000 (8 pairs) 43/116 us, two 55/166, four 99/125-175, 16 of 9000 to 8000 (128 pairs) 292/115;
-  // one of 3000 to 2000 25/29. Launching both costs 2 us.
-  const long long most = (long long)a.n * a.c.Hkv, few = sms / 4;
+  // Pairs up to which each has a cluster. A block alone takes as long as its pages do, whatever runs beside it; clusters
+  // run about 16 at a time. Measured, clusters/blocks alone, int8, d = 128, 8, 16, 24 and 32 pairs: 2400 to 2048 tokens
+  // 27/31, 37/31, 39/31, 51/31 us; 4700 to 4096 29/44, 41/45, 43/45, 56/45; 9000 to 8000 35/68, 45/70, 55/70, 69/72; 17000
+  // to 16000 43/111, 57/117, 85/121, 101/125; 32000 to 1024 27/39, 39/39, 43/39, 53/39. Launching both costs 2 us.
+  const long long most = (long long)a.n * a.c.Hkv, few = min(sms / 4, max(8, a.keep / 160));
   const int smem = kEvictKeys * 4;
   cudaError_t e = ensure_smem((const void*)evict_select_kernel<P>, smem);
   for (int step = 0; step < 2; ++step) {  // select, move
     if (e == cudaSuccess) {
       a.from = 0;
       a.to = few;
-      e = step ? evict_launch(evict_move_kernel<I8, D, P>, a, min(2 * most, few), kEvictCluster, 512, 0, st)
-               : evict_launch(evict_select_kernel<P>, a, min(most, few / 2), kEvictCluster, kSelectThreads, smem, st);
+      e = step ? evict_launch(evict_move_kernel<I8, D, P>, a, min(2 * min(most, few), sms / 4LL), kEvictCluster, 512, 0, st)
+               : evict_launch(evict_select_kernel<P>, a, min(min(most, few), sms / 8LL), kEvictCluster, kSelectThreads, smem, st);
     }
     if (most > few && e == cudaSuccess) {
       a.from = few;
