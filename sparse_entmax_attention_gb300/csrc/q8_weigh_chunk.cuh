@@ -138,14 +138,17 @@ __device__ __forceinline__ WcSeg wc_seg(const WcArgs& g, const WcFew& sh, long l
 struct WcMask {
   uint32_t some, all;
 };
-__device__ __forceinline__ WcMask wc_mask(const WcArgs& g, const WcSeg& x, int rt) {
-  bool some = false, all = false;
-  const int i = rt + (threadIdx.x & 31);
-  if (i < x.rt_end) {
-    const int4 r = __ldcg(reinterpret_cast<const int4*>(g.rows + x.s.rt0 + i));
+__device__ __forceinline__ void wc_sees(const WcArgs& g, const WcSeg& x, int rt, bool& some, bool& all) {
+  some = all = false;
+  if (rt < x.rt_end) {
+    const int4 r = __ldcg(reinterpret_cast<const int4*>(g.rows + x.s.rt0 + rt));
     some = (r.y >= x.key_min && r.z <= x.key_max) || x.key_min < x.s.pre;
     all = r.x >= x.key_max && (r.w <= x.key_min || x.key_max < x.s.pre);
   }
+}
+__device__ __forceinline__ WcMask wc_mask(const WcArgs& g, const WcSeg& x, int rt) {
+  bool some, all;
+  wc_sees(g, x, rt + (threadIdx.x & 31), some, all);
   return WcMask{__ballot_sync(0xffffffffu, some), __ballot_sync(0xffffffffu, all)};
 }
 
@@ -593,12 +596,19 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
         for (int k = max(0, u - kWcQ); k < u; ++k) mbar_wait_second(&q_full[k % kWcQ], (uint32_t)(k / kWcQ & 1));
         for (int k = max(0, u - kWcMeta); k < u; ++k) mbar_wait_second(&f_full[k % kWcMeta], (uint32_t)(k / kWcMeta & 1));
       }
-    } else {  // segments, as far ahead as there is room
-      for (int k = 0; k < n_mine && ok; ++k) {
-        const WcSeg x = wc_seg<P>(g, few, blockIdx.x + (long long)k * gridDim.x, slot);
+    } else {
+      // Segments, as far ahead as there is room, two at a time: a look-up is a chain of divisions and loads, longer than
+      // the work with a segment of few row tiles. A half of the warp has one each.
+      const int side = lane >> 4, l16 = lane & 15;
+      auto halves = [&](bool b0, bool b1) {  // a half's 16 bits of each
+        const uint32_t v0 = __ballot_sync(0xffffffffu, b0), v1 = __ballot_sync(0xffffffffu, b1);
+        return (v0 >> (16 * side) & 0xffffu) | (v1 >> (16 * side)) << 16;
+      };
+      for (int k = 0; k < n_mine && ok; k += 2) {
+        const WcSeg x = wc_seg<P>(g, few, blockIdx.x + (long long)min(k + side, n_mine - 1) * gridDim.x, slot);
         WcPage page{0, kNoKey, 0.0f, 0};
-        const int t = x.kt * PT + lane;
-        if (lane < PT && t < x.pages()) {
+        const int t = x.kt * PT + l16;
+        if (l16 < PT && t < x.pages()) {
           const int ph = phys_page(a.c.block_table, x.s.seq, x.page(t), a.c.maxp, a.c.nphys, a.c.status);
           if (ph >= 0) {
             page.at = ph * Hkv + x.kvh;
@@ -606,19 +616,26 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
             page.ks = a.c.k_scale[page.at];
           }
         }
-        const WcMask mask = wc_mask(g, x, x.rt);
-        if (k >= kWcSegs && !wait_warp(&g_empty[k % kWcSegs], k / kWcSegs - 1)) {
-          ok = false;
-          break;
+        bool some[2], all[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) wc_sees(g, x, x.rt + 16 * i + l16, some[i], all[i]);
+        const WcMask mask{halves(some[0], some[1]), halves(all[0], all[1])};
+        for (int j = 0; j < 2 && k + j < n_mine; ++j) {
+          if (k + j >= kWcSegs && !wait_warp(&g_empty[(k + j) % kWcSegs], (k + j) / kWcSegs - 1)) {
+            ok = false;
+            break;
+          }
+          WcInfo& q = segs[(k + j) % kWcSegs];
+          if (side == j) {
+            if (l16 < PT) q.pages[l16] = page;
+            if (l16 == 0) {
+              q.x = x;
+              q.mask = mask;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&g_full[(k + j) % kWcSegs]);
         }
-        WcInfo& q = segs[k % kWcSegs];
-        if (lane < PT) q.pages[lane] = page;
-        if (lane == 0) {
-          q.x = x;
-          q.mask = mask;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&g_full[k % kWcSegs]);
       }
     }
   }
