@@ -127,15 +127,26 @@ __global__ void __launch_bounds__(1024) weigh_plan_kernel(WcArgs g) {
     for (long long i = tid; i < 8 * base; i += 1024) g.done[i] = 0;
 }
 
+// Eight bf16 values times a power of two as halves.
+__device__ __forceinline__ uint4 halves_of(const uint4& v, float scale) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * scale, __uint_as_float(w[i] & 0xffff0000u) * scale);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 // The rows of a (row tile, KV head) as the products want them, and what the sums
 // know of them: a block of 128 threads, a row each for the facts, D/8 threads a
-// row for the copy.
+// row for the copy. Rows that add nothing are laid out as zeros.
 template <int D>
 __global__ void __launch_bounds__(128) weigh_pack_kernel(WcArgs g) {
   pdl_enter();
   const Q8WeighArgs& a = g.a;
   const int kvh = blockIdx.y, tid = threadIdx.x, G = a.c.G, Hkv = a.c.Hkv;
   __shared__ long long at_sh[kWcRows];
+  __shared__ uint32_t top_sh[4];
   for (int tile = blockIdx.x; tile < g.max_tiles; tile += gridDim.x) {
     if (tile >= *g.n_tiles) return;
     const WcSlot s = g.slots[g.slot_of[tile]];
@@ -145,7 +156,6 @@ __global__ void __launch_bounds__(128) weigh_pack_kernel(WcArgs g) {
     const bool mine = tid < left;
     const int tok = mine ? rho / G : 0, head = kvh * G + (mine ? rho - tok * G : 0);
     const long long row = s.start + tok;
-    at_sh[tid] = mine ? row * a.q.ts + (long long)head * a.q.hs : -1;
     const size_t to = (size_t)kvh * g.max_tiles + tile;
     WcFacts& f = g.facts[to];
     const int first = rt * kWcRows / G, pos = s.L - s.count + tok, pos0 = s.L - s.count + first;
@@ -159,6 +169,7 @@ __global__ void __launch_bounds__(128) weigh_pack_kernel(WcArgs g) {
       if (a.sc.first_key) lo = a.sc.first_key[row];
       if (counts) c = a.coef ? fmaf(-tau, kLog2e, __log2f(coef)) : -tau * kLog2e;
     }
+    at_sh[tid] = counts ? row * a.q.ts + (long long)head * a.q.hs : -1;
     const float ahead = (float)(pos - pos0);
     f.c[tid] = c;
     f.near[tid] = fmaf(slope, ahead, c);
@@ -173,15 +184,35 @@ __global__ void __launch_bounds__(128) weigh_pack_kernel(WcArgs g) {
       f.skip = rt * kWcRows - first * G;
       f.whole = whole;
     }
-    constexpr int CPR = D / 8;
-    uint4* dst = g.packed + to * (kWcRows * CPR);
-#pragma unroll 8
-    for (int i = tid; i < kWcRows * CPR; i += 128) {
-      const int rl = i / CPR, ch = i % CPR;
+    constexpr int CPR = D / 8, N = kWcRows * CPR / 128;
+    uint4 v[N];
+    uint32_t top = 0u;  // of the finite magnitudes, two at a time
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int rl = (i * 128 + tid) / CPR, ch = (i * 128 + tid) % CPR;
       const long long at = at_sh[rl];
-      const uint4 v = at >= 0 ? *reinterpret_cast<const uint4*>(a.q.p + at + ch * 8) : make_uint4(0u, 0u, 0u, 0u);
-      dst[tile_off(rl, ch) >> 4] = v;
+      v[i] = at >= 0 ? *reinterpret_cast<const uint4*>(a.q.p + at + ch * 8) : make_uint4(0u, 0u, 0u, 0u);
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t m = w[j] & 0x7fff7fffu;
+        top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
+    if ((tid & 31) == 0) top_sh[tid >> 5] = top;
+    __syncthreads();
+    top = max(max(top_sh[0], top_sh[1]), max(top_sh[2], top_sh[3])) >> 7;  // the largest's exponent
+    const uint32_t up = top ? min(268u - top, 253u) : 127u;                // to 2^14 and more, as a float's exponent
+    const float scale = __uint_as_float(up << 23);
+    if (tid == 0) f.unit = __uint_as_float((254u - up) << 23);
+    uint4* dst = g.packed + to * (kWcRows * CPR);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      dst[tile_off((i * 128 + tid) / CPR, (i * 128 + tid) % CPR) >> 4] = halves_of(v[i], scale);
     __syncthreads();
   }
 }

@@ -5,12 +5,18 @@
 //
 // (s_j capped, biased, masked). A block holds 256 keys of a (slot, KV head) and
 // lets the rows pass, 128 (token, head of the group) at a time:
-//   S^T = K·Q^T   two products of 128 keys × 128 rows, codes and queries as bf16
-//                 (both exact), fp32 sums in tensor memory, keys along the lanes:
-//                 a thread has one key, and its sum over the rows needs no other;
+//   S^T = K·Q^T   two products of 128 keys × 128 rows, codes and queries as halves,
+//                 fp32 sums in tensor memory, keys along the lanes: a thread has
+//                 one key, and its sum over the rows needs no other;
 //   Σ 2^t         a key's scale is the thread's, what belongs to a row comes as a
 //                 broadcast from shared memory: an FMA, an exponential and an
 //                 addition a pair, the first and the last on two rows at once.
+//
+// Codes are exact in halves, at a quarter to a half of the instructions of bf16 (a tile of
+// keys took as much of the issue as a tile of rows does). Queries are brought by a power of
+// two to just below 2^15 at their tile's largest: a value down to 2^-29 of that stays exact,
+// and what smaller ones lose is 2^-40 of it, in the score, of which a weight is the
+// exponential, far less than the fp32 sum's own rounding of the largest row.
 //
 // A first pass lays the rows out as the products and the sums want them: tiles of
 // 128 queries in the operand's swizzled order, and what belongs to a row. (Copied
@@ -69,7 +75,8 @@ struct __align__(16) WcFacts {
   int lo[kWcRows];       // first key of the row's document
   uint32_t counts[kWcRows / 32];  // rows that are there and add something
   int pos0, skip;        // position of the first row, and its head in the group
-  int whole, pad;        // all rows count
+  int whole;             // all rows count
+  float unit;            // what a value 1 of the packed queries stands for, a power of two
 };
 struct WcArgs {
   Q8WeighArgs a;
@@ -182,33 +189,9 @@ __device__ __forceinline__ void tm_tie16(float* v) {
                  "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
 }
 
-// Four codes as bf16 (exact): bytes 0 and 1 to x, 2 and 3 to y.
-template <bool I8>
-__device__ __forceinline__ void codes_bf16(uint32_t w, uint32_t& x, uint32_t& y) {
-  if constexpr (I8) {  // 2^23 + 128 + v as a float for each byte
-    const uint32_t u = w ^ 0x80808080u;
-    const unsigned long long off = f2_splat(-8388736.0f);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float a, b;
-      f2_unpack(f2_add(f2_pack(__uint_as_float(__byte_perm(u, 0x4b000000u, j ? 0x7442 : 0x7440)),
-                               __uint_as_float(__byte_perm(u, 0x4b000000u, j ? 0x7443 : 0x7441))),
-                       off), a, b);
-      (j ? y : x) = bf2_rn(a, b);
-    }
-  } else {
-    uint32_t h[2];
-    e4m3x4_half(w, h[0], h[1]);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[0]));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[1]));
-    x = bf2_rn(a.x, a.y);
-    y = bf2_rn(b.x, b.y);
-  }
-}
-
-// D fp32, A and B bf16, both along K; M = 128.
-__device__ __forceinline__ uint32_t instr_desc_bf16(int n) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+// D fp32, A and B halves, both along K; M = 128.
+__device__ __forceinline__ uint32_t instr_desc_half(int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 template <bool I8, int D, int P, bool capped, bool biased>
 __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
@@ -298,7 +281,6 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
       const int key = page.key0 + ks_ % P, pre = q.x.s.pre;
       const bool there = key < q.x.s.L;
       const float k1 = page.ks * a.sc.scale * (capped ? a.sc.inv_cap : kLog2e), out = a.sc.cap * kLog2e;
-      const unsigned long long k2 = f2_splat(k1);
       float* wp = a.w + (size_t)page.at * P + ks_ % P;
       const bool reads = part == 0 && there && key < q.x.s.fresh && a.decay != 0.0f;
       float before = 0.0f;
@@ -316,6 +298,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
           }
           tm_fence_after();
           const bool whole = (m.all >> i & 1u) && f.whole;
+          const unsigned long long k2 = f2_splat(k1 * f.unit);
           const float away = (float)(f.pos0 - key);  // (of the tile's first row; used where it is not negative)
           // 16 rows: their raw sums to weights, added up; `bits` are the rows that see the key
           auto weigh = [&](int c0, const float (&raw)[16], bool whole, uint32_t bits) {
@@ -507,10 +490,10 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
         const int rr = 32 * (cw & 3) + i * RPI + crow;
         const uint32_t dst = k_sm + (tiles % kWcK * 2 + (cw >> 2)) * HALF;
         uint4 h0, h1;
-        codes_bf16<I8>(codes[i].x, h0.x, h0.y);
-        codes_bf16<I8>(codes[i].y, h0.z, h0.w);
-        codes_bf16<I8>(codes[i].z, h1.x, h1.y);
-        codes_bf16<I8>(codes[i].w, h1.z, h1.w);
+        codes_half<I8, false>(codes[i].x, h0.x, h0.y);
+        codes_half<I8, false>(codes[i].y, h0.z, h0.w);
+        codes_half<I8, false>(codes[i].z, h1.x, h1.y);
+        codes_half<I8, false>(codes[i].w, h1.z, h1.w);
         sts128(dst + tile_off(rr, 2 * cch), h0);
         sts128(dst + tile_off(rr, 2 * cch + 1), h1);
       }
@@ -545,7 +528,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
               }
               tm_fence_after();
               if (elect_one()) {
-                const uint32_t id_s = instr_desc_bf16((n_rows + 15) / 16 * 16);
+                const uint32_t id_s = instr_desc_half((n_rows + 15) / 16 * 16);
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n) {  // (addresses advance in units of 16 bytes)
                   const uint32_t o = ((n >> 2) * 16384 + (n & 3) * 32) >> 4;
