@@ -634,13 +634,15 @@ cudaError_t launch_evict(const Q8Cache& c, const int32_t* seq_ids, const int32_t
   cfg.gridDim = dim3(kEvictPlanBlocks);
   cfg.blockDim = dim3(kEvictPlanThreads);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kEvictPlanBlocks;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, n <= kEvictPlanThreads ? evict_plan_few_kernel : evict_plan_kernel, a);
   if (e != cudaSuccess) return e;
   return i8 ? evict_d<true>(a, sms, st) : evict_d<false>(a, sms, st);

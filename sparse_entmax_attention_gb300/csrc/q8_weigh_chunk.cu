@@ -257,7 +257,7 @@ cudaError_t launch_weigh_chunk(const Q8WeighArgs& a, bool i8, void* ws, int sms,
   g.packed = reinterpret_cast<uint4*>(p);
   p += tiles * a.c.Hkv * kWcRows * a.c.D * 2;
   g.facts = reinterpret_cast<WcFacts*>(p);
-  cudaError_t e = launch_k(false, weigh_plan_kernel, dim3(1), dim3(1024), 0, st, g);
+  cudaError_t e = launch_k(true, weigh_plan_kernel, dim3(1), dim3(1024), 0, st, g);
   const dim3 grid((unsigned)min(tiles, (size_t)65535), (unsigned)a.c.Hkv);
   if (e == cudaSuccess)
     e = a.c.D == 128 ? launch_k(true, weigh_pack_kernel<128>, grid, dim3(128), 0, st, g)
