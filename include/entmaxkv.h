@@ -640,7 +640,8 @@ int32_t entmaxkv_attend_diff_q8(const entmaxkv_config* cfg, const entmaxkv_q8_ca
  *            aligned, contents are scratch; not to be shared by calls that may run
  *            at the same time. Past 32 rows a slot it holds the queries once more, in
  *            tiles of 128 rows of a slot and KV head
- * Sums are float32 in an order that the arguments and the device fix.
+ * Sums are float32 in an order that the arguments and the device fix. Past 32 rows a
+ * slot, a query value less than 2^-40 of the largest in the same 128 rows counts as 0.
  */
 size_t entmaxkv_weigh_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, int32_t total,
                                    int32_t max_count, float alpha);

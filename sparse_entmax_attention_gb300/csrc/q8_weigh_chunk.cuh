@@ -36,9 +36,10 @@
 // them about 1700 cycles; its exponentials alone are 1024 (32 a clock and
 // multiprocessor), its products 1024, and the two meet in shared memory, where the
 // operands and the rows' facts are read. Measured, int8, 8 KV heads of 4 query heads,
-// d = 128: 2048 rows on 30001 keys before them (0.52 TFLOP) 407 us with listing and
-// packing (15 us), 1290 TFLOP/s, 0.66 of the measured bf16 burst; in a capture
-// (10240 keys) exponentials 53%, tensor pipe 51%, IPC 2.3. Kept aside, measured: two
+// d = 128: 2048 rows on 30001 keys before them (0.52 TFLOP) 408 us with listing and
+// packing (15 us), 1275 TFLOP/s, 0.65 of the measured bf16 burst; in a capture
+// (10240 keys) exponentials 55%, tensor pipe 54%, IPC 2.3; the last 64 rows of six prompts of 500-32000, e4m3, 63 us.
+// Kept aside, measured: two
 // warps of sums a scheduler 543 us; one key tile in shared memory (four stages of rows)
 // 463; keys in tensor memory and tiles of 96 rows 435-463, with the last rows of six
 // prompts at 77 us instead of 64; single fp32 operations in place of pairs 482.

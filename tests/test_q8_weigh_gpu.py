@@ -243,3 +243,30 @@ def test_slots_that_claim_the_same_rows_stop_at_the_lists_end():
     check_weights(c, q, [60], tau, before, after)
     others_untouched(c, before, after, [0, 1])
     assert not torch.equal(before, after)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_rows_of_unlike_loudness_share_a_tile(code, softcap):
+    """Queries over 24 factors of two in one tile, tiles of nothing but tiny or zero queries, and rows that add nothing
+    with infinities, NaN and huge values in them."""
+    counts = [100, 64, 40]
+    c, q = filled(code, [900, 300, 500], counts, hkv=2, g=4, d=128, P=32, seed=8)
+    q = q.clone()
+    for t in range(100):
+        q[t] *= 2.0 ** (4 - t % 25)
+    q[100:132] *= 2.0 ** -100
+    q[132:164] = 0.0
+    tau = B.attend_q8(c, q, batch_of(counts), softcap=softcap).tau.clone()
+    loud = q.clone()
+    for t, bad in ((3, 1e38), (50, float("inf")), (99, float("nan")), (170, -1e30)):
+        loud[t, ::3] = bad
+        q[t, ::3] = 0.0
+        tau[t, ::3] = float("nan")
+    before = some_weights(c)
+    after = before.clone()
+    B.weigh_q8(c, after, loud, tau, batch_of(counts), softcap=softcap, decay=0.5)
+    check_weights(c, q, counts, tau, before, after, decay=0.5, softcap=softcap)
+    plain = before.clone()
+    B.weigh_q8(c, plain, q, tau, batch_of(counts), softcap=softcap, decay=0.5)
+    assert torch.equal(plain, after) and c.device_status() == 0
