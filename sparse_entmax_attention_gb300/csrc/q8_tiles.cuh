@@ -153,9 +153,20 @@ __device__ __forceinline__ float q8_row_scale(float q_inv, const Q8Score& sc, fl
   return q_inv * sc.scale * (sc.cap > 0.0f ? sc.inv_cap : unit);
 }
 
+// tanh(y) to 3e-7 of itself, for weights that leave in fp32: the polynomial up to 1, past it 1 − 2/(1 + e^{2|y|}), whose
+// second part is then at most 0.24.
+__device__ __forceinline__ float tanh_fine(float y) {
+  constexpr TanhPoly poly = tanh_poly();
+  const float z = y * y;
+  float t = poly.far[6];
+#pragma unroll
+  for (int n = 5; n >= 0; --n) t = fmaf(t, z, poly.far[n]);
+  return z <= 1.0f ? t * y : copysignf(soft_cap(fabsf(y), 1.0f, 1.0f), y);
+}
+
 // Scores of N keys for one row: dot[i] is of key j0 + 8·i; add is added to
-// each. NaN-free for finite codes.
-template <int N>
+// each. NaN-free for finite codes. FINE: caps to fp32's precision rather than bf16 outputs'.
+template <bool FINE = false, int N>
 __device__ __forceinline__ void q8_scores(const float (&dot)[N], float (&out)[N], const Q8Row& r, float ks, int j0,
                                           const Q8Score& sc, float unit, float add) {
   const float k = r.cs * ks;
@@ -168,7 +179,10 @@ __device__ __forceinline__ void q8_scores(const float (&dot)[N], float (&out)[N]
     }
     constexpr TanhPoly poly = tanh_poly();
     const float c = sc.cap * unit;
-    if (__all_sync(0xffffffffu, big <= 0.5f)) {
+    if constexpr (FINE) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) out[i] = fmaf(tanh_fine(out[i]), c, add);
+    } else if (__all_sync(0xffffffffu, big <= 0.5f)) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float z = out[i] * out[i];

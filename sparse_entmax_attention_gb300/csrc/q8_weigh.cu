@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kWeighWarps<NT> * 32, 1) weigh_kernel(Q8WeighA
             for (int j = 0; j < 2; ++j) {
               const float dot[2] = {s[nt][j], s[nt][2 + j]};
               float v[2];
-              q8_scores(dot, v, row[nt][j], ks[q], j0, a.sc, unit, add[nt][j]);
+              q8_scores<true>(dot, v, row[nt][j], ks[q], j0, a.sc, unit, add[nt][j]);
               const bool counts = cf[nt][j] > 0.0f;
 #pragma unroll
               for (int e = 0; e < 2; ++e) {

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
           // 16 rows: their raw sums to weights, added up; `bits` are the rows that see the key
           auto weigh = [&](int c0, const float (&raw)[16], bool whole, uint32_t bits) {
             unsigned long long t2[8];
-            if (capped) {  // y = raw·k, then cap·log2 e·y·T(y²), as in the chunk attention
+            if (capped) {  // y = raw·k, then cap·log2 e·y·T(y²)
               unsigned long long z2[8];
               float b4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -317,13 +317,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
               }
               const float big = max3(max3(b4[0], b4[1], b4[2]), b4[3], 0.0f);
               constexpr TanhPoly poly = tanh_poly();
-              if (__all_sync(0xffffffffu, big <= 0.25f)) {
-                const unsigned long long p0 = f2_splat(poly.near[0] * out), p1 = f2_splat(poly.near[1] * out),
-                                         p2 = f2_splat(poly.near[2] * out), p3 = f2_splat(poly.near[3] * out);
-#pragma unroll
-                for (int n = 0; n < 8; ++n)
-                  t2[n] = f2_mul(f2_fma(f2_fma(f2_fma(p3, z2[n], p2), z2[n], p1), z2[n], p0), t2[n]);
-              } else if (__all_sync(0xffffffffu, big <= 1.0f)) {
+              if (__all_sync(0xffffffffu, big <= 1.0f)) {
 #pragma unroll
                 for (int n = 0; n < 8; ++n) {
                   unsigned long long r = f2_fma(z2[n], f2_splat(poly.far[6]), f2_splat(poly.far[5]));
@@ -336,7 +330,7 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
                 for (int n = 0; n < 8; ++n) {
                   float y0, y1;
                   f2_unpack(t2[n], y0, y1);
-                  t2[n] = f2_mul(f2_pack(soft_cap(y0, 1.0f, 1.0f), soft_cap(y1, 1.0f, 1.0f)), f2_splat(out));
+                  t2[n] = f2_mul(f2_pack(tanh_fine(y0), tanh_fine(y1)), f2_splat(out));
                 }
               }
             }
