@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kEvictPlanThreads) evict_plan_kernel(EvictArgs
       return x;
     }
     x.L = seq_len_clamped(a.c.seq_lens, x.seq, a.c.maxp, P, st);
-    if (x.L <= a.above || __ldcg(a.bad + b)) x.L = 0;
+    if (x.L <= a.above) x.L = 0;
     return x;
   };
   auto find = [&](int j) {  // the round's slot that holds its j-th page
@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(kEvictPlanThreads) evict_plan_kernel(EvictArgs
     }
     return lo;
   };
-  // pages outside the pool: their slots stay as they are
+  // Pages outside the pool: their slots stay as they are. Each block numbers a round's pages for itself and looks at its
+  // share, so the marks are read behind the barrier only: a block that saw another's would number fewer.
   for (int b0 = 0; b0 < a.n; b0 += kEvictPlanThreads) {
     const EvictItem x = slot(b0 + tid, status);
     const int pages = (x.L + P - 1) / P;
@@ -233,7 +234,8 @@ __global__ void __launch_bounds__(kEvictPlanThreads) evict_plan_kernel(EvictArgs
   int items = 0;
   long long freed = 0;
   for (int b0 = 0; b0 < a.n; b0 += kEvictPlanThreads) {
-    const EvictItem x = slot(b0 + tid, nullptr);
+    EvictItem x = slot(b0 + tid, nullptr);
+    if (x.L > 0 && __ldcg(a.bad + b0 + tid)) x.L = 0;
     int some, total;
     const int at_item = block_exclusive_scan(x.L > 0, sh_scan, some);
     if (head && x.L > 0) a.items[items + at_item] = x;
