@@ -679,11 +679,22 @@ class QuantCache:
         self.status = status if status is not None else torch.zeros(1, dtype=torch.int32, device=self.device)
         self.cfg = Config(shape[1], group, shape[3], shape[2], max_seqs, max_pages, shape[0], _CODES[k_pool.dtype])
         self.num_q_heads = shape[1] * group
+        self._key_weights = None
         self.view = Q8CacheView(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                 block_table.data_ptr(), seq_lens.data_ptr(), self.status.data_ptr())
 
     def device_status(self) -> int:
         return int(self.status.item()) & 0xffffffff
+
+    def key_weights(self):
+        """What the cache's keys gathered (alloc_weights), kept beside their codes: made at the first call, the same
+        tensor from then on. An eviction moves keys and their weights, so all that weighs or evicts keys of one
+        cache has to use one tensor."""
+        if self._key_weights is None:
+            _need(not self.k_pool.is_cuda or not torch.cuda.is_current_stream_capturing(),
+                  "key_weights: the first call makes the tensor and is wanted before a capture")
+            self._key_weights = alloc_weights(self)
+        return self._key_weights
 
 
 def _on_cache(cache, batch):
@@ -920,9 +931,10 @@ def evict_q8(cache: QuantCache, pool: PagePool, weights, seq_ids, keep, above=0,
 class KeyBudget:
     """How many keys a QuantStep leaves each of its sequences: behind the attention the step's rows weigh the keys
     (weigh_q8 with decay and, for some, coef [n_seqs * max_count, Hq]), and sequences of more than `above` tokens
-    (0: keep) are shortened to `keep` (evict_q8). weights holds what the keys gathered: the caller's (alloc_weights), or
-    None for some of the step's own (step.budget.weights); prompts that were appended by other means are weighed by
-    the caller."""
+    (0: keep) are shortened to `keep` (evict_q8). weights holds what the keys gathered: None for the cache's own
+    (cache.key_weights()), which all steps over a cache then share, or a tensor of the caller's (alloc_weights) that is
+    given to every step over that cache. Prompts that were appended by other means are weighed by the caller, with the
+    same tensor: a key that no call weighed has what its place held before."""
 
     def __init__(self, keep, above=0, sinks=0, recent=0, decay=1.0, coef=None, weights=None):
         self.keep, self.above, self.sinks, self.recent, self.decay = keep, above, sinks, recent, decay
@@ -963,7 +975,7 @@ class QuantStep:
         self._fixed = (lam, gain, score)  # (the graph reads them where they are)
         if budget is not None:
             if budget.weights is None:
-                budget.weights = alloc_weights(cache)
+                budget.weights = cache.key_weights()
             self.weigh_workspace = alloc_weigh_workspace(cache, self.batch, alpha)
             self.evict_workspace = alloc_evict_workspace(cache, n_seqs, budget.keep)
 
