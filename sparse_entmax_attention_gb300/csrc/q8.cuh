@@ -180,9 +180,12 @@ struct Q8AttendArgs {
 __device__ __forceinline__ float diff_of(float o0, float i0, float o1, float i1) {
   return __fsub_rn(__fmul_rn(o0, i0), __fmul_rn(o1, i1));
 }
-// What a pair's difference y is multiplied by, dim by dim gain's: 1/√(mean y² + ε), from Σ y².
-__device__ __forceinline__ float diff_norm(const Q8AttendArgs& a, float sum2) {
-  return rsqrtf(fmaf(sum2, 1.0f / (float)a.c.D, a.eps));
+// What a pair's difference y is multiplied by, dim by dim gain's: 1/√(mean y² + ε), from Σ (y·down)². down is 1, or
+// where that sum passes fp32 (values of 2^60 and more) 2^-70: then it lies between 2^-12 and 2^123.
+constexpr float kDiffDown = 0x1p-70f;
+__device__ __forceinline__ bool diff_past(float sum2) { return sum2 > 0x1.fffffep127f; }
+__device__ __forceinline__ float diff_norm(const Q8AttendArgs& a, float sum2, float down = 1.0f) {
+  return down * rsqrtf(fmaf(sum2, 1.0f / (float)a.c.D, a.eps * down * down));
 }
 
 struct Q8WeighArgs {

@@ -380,10 +380,25 @@ __global__ void __launch_bounds__(kAttWarps<D, NT> * 32, 1)
             sum2 = fmaf(acc[mt][nt][e], acc[mt][nt][e], sum2);
           }
         if (a.gain) {
-          sum2 += __shfl_xor_sync(0xffffffffu, sum2, 4);
-          sum2 += __shfl_xor_sync(0xffffffffu, sum2, 8);
-          sum2 += __shfl_xor_sync(0xffffffffu, sum2, 16);
-          const float f = diff_norm(a, sum2);
+          auto all_dims = [](float v) {
+            v += __shfl_xor_sync(0xffffffffu, v, 4);
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            return v + __shfl_xor_sync(0xffffffffu, v, 16);
+          };
+          sum2 = all_dims(sum2);
+          float f = diff_norm(a, sum2);
+          if (__any_sync(0xffffffffu, diff_past(sum2))) {
+            float s = 0.0f;
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                const float y = acc[mt][nt][e] * kDiffDown;
+                s = fmaf(y, y, s);
+              }
+            s = all_dims(s);
+            if (diff_past(sum2)) f = diff_norm(a, s, kDiffDown);
+          }
 #pragma unroll
           for (int mt = 0; mt < D / 16; ++mt) {
             acc[mt][nt][0] *= f * a.gain[16 * mt + 2 * r];
@@ -498,7 +513,7 @@ __global__ void __launch_bounds__(kAttWarps<D, NT> * 32, 1)
           sum2 = fmaf(y[k], y[k], sum2);
         }
         if (a.gain) {
-          const float f = diff_norm(a, warp_sum(sum2));
+          const float f = diff_norm_warp(a, y, sum2);
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) y[k] *= f * a.gain[32 * k + lane];
         }
@@ -598,14 +613,20 @@ __global__ void __launch_bounds__(D) attend_join_kernel(Q8AttendArgs a, int nrt_
     row_sum(rj + 1, M1, l1, o1);
     float y = diff_of(o, att_inv(l), o1, att_inv(l1) * a.lam[tok * a.lam_ts + (h >> 1)]);
     if (a.gain) {
-      __shared__ float sh2[D / 32];
-      const float part = warp_sum(y * y);
-      if ((threadIdx.x & 31) == 0) sh2[threadIdx.x >> 5] = part;
-      __syncthreads();
-      float sum2 = 0.0f;
+      __shared__ float sh2[2][D / 32];
+      auto all_dims = [&](float v, float(&sh)[D / 32]) {
+        v = warp_sum(v);
+        if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+        __syncthreads();
+        float s = 0.0f;
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) sum2 += sh2[k];
-      y *= diff_norm(a, sum2) * a.gain[threadIdx.x];
+        for (int k = 0; k < D / 32; ++k) s += sh[k];
+        return s;
+      };
+      const float sum2 = all_dims(y * y, sh2[0]);
+      float f = diff_norm(a, sum2);
+      if (diff_past(sum2)) f = diff_norm(a, all_dims(y * kDiffDown * (y * kDiffDown), sh2[1]), kDiffDown);  // (all threads alike)
+      y *= f * a.gain[threadIdx.x];
     }
     a.out.p[tok * a.out.ts + (long long)(h >> 1) * a.out.hs + threadIdx.x] = __float2bfloat16_rn(y);
     if (a.tau && threadIdx.x < 2) a.tau[tok * a.c.Hkv * G + h + threadIdx.x] = threadIdx.x ? att_lse(M1, l1) : att_lse(M, l);

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(ChunkArgs g) {
         sum2 = fmaf(o[i], o[i], sum2);
       }
       if (a.gain) {
-        const float f = diff_norm(a, warp_sum(sum2));
+        const float f = diff_norm_warp(a, o, sum2);
 #pragma unroll
         for (int i = 0; i < V; ++i) o[i] *= f * a.gain[32 * i + lane];
       }

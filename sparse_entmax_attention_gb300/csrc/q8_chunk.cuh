@@ -542,20 +542,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs g) {
         const float lam = mine ? a.lam[(long long)(x.s.start + tok) * a.lam_ts + (head >> 1)] : 0.0f;
         first = lane & 1 ? -lam * inv : inv;
         if (half && a.gain) {
-          float sum2 = 0.0f;
+          float down = 1.0f, sum2;
 #pragma unroll 1
-          for (int i = 0; i < D / 32; ++i) {
-            float o[32];
-            tm_ld32(o_tm + 32 * i, o);
-            tm_wait_ld();
-            tm_tie32(o);
+          for (bool again = false;; again = true) {  // (once more where a row's squares pass fp32)
+            sum2 = 0.0f;
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              float o[32];
+              tm_ld32(o_tm + 32 * i, o);
+              tm_wait_ld();
+              tm_tie32(o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float m = __fmul_rn(o[k], first), y = __fadd_rn(m, __shfl_xor_sync(0xffffffffu, m, 1));
-              sum2 = fmaf(y, y, sum2);
+              for (int k = 0; k < 32; ++k) {
+                const float m = __fmul_rn(o[k], first), y = __fadd_rn(m, __shfl_xor_sync(0xffffffffu, m, 1)) * down;
+                sum2 = fmaf(y, y, sum2);
+              }
             }
+            if (again || !__any_sync(0xffffffffu, diff_past(sum2))) break;
+            if (diff_past(sum2)) down = kDiffDown;
           }
-          fn = diff_norm(a, sum2);
+          fn = diff_norm(a, sum2, down);
         }
       }
       if (half) {

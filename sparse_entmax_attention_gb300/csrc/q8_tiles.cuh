@@ -223,6 +223,17 @@ __device__ __forceinline__ float att_lse(float m, float l) {
   return l != 0.0f ? (m + log2f(l)) * 0.6931471805599453f : CUDART_NAN_F;
 }
 
+// diff_norm of a warp's pair: y's dims lie N a lane, sum2 is of the lane's.
+template <int N>
+__device__ __forceinline__ float diff_norm_warp(const Q8AttendArgs& a, const float (&y)[N], float sum2) {
+  sum2 = warp_sum(sum2);
+  if (!diff_past(sum2)) return diff_norm(a, sum2);
+  float s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) s = fmaf(y[k] * kDiffDown, y[k] * kDiffDown, s);
+  return diff_norm(a, warp_sum(s), kDiffDown);
+}
+
 // n / d for n ≥ 0, d > 0: in 32 bits where both fit (the 64-bit division is a
 // long subroutine, and code that runs once costs its instructions' fetch).
 __device__ __forceinline__ long long div_line(long long n, long long d) {

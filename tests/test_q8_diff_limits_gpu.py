@@ -1,0 +1,31 @@
+"""Differences of pairs whose values are far from 1."""
+
+import pytest
+import torch
+
+from sparse_entmax_attention_gb300 import binding as B
+
+from q8_cases import batch_of, filled
+from test_q8_diff_gpu import check_diff, factors, gains
+
+pytestmark = pytest.mark.gpu
+
+# single tokens (whole units, pieces joined in a block, and over blocks), drafted tokens, chunks (whole and joined)
+SHAPES = [([700, 40], [1, 1]), ([70000, 5], [1, 1]), ([70000, 900], [2, 1]), ([600, 300], [40, 9]), ([40000, 50], [60, 7])]
+
+
+@pytest.mark.parametrize("lens,counts", SHAPES)
+@pytest.mark.parametrize("code,d,power", [("int8", 64, 80), ("e4m3", 128, 100), ("int8", 128, 63), ("e4m3", 64, -80)])
+def test_a_norm_of_values_whose_squares_pass_fp32(code, lens, counts, d, power):
+    """One sequence's V rows are 2^power times as large as the others': its normalised rows are those of the cache
+    as it was but for ε, and the other sequences' are untouched."""
+    c, q = filled(code, lens, counts, hkv=2, g=4, d=d, P=32, seed=11)
+    lam, gain = factors(sum(counts), 4, True), gains(d)
+    batch = batch_of(counts)
+    plain = B.attend_diff_q8(c, q, lam, batch, gain=gain).out.clone()
+    pages = c.block_table[0, :-(-lens[0] // 32)].long()
+    c.v_scale[pages] *= 2.0 ** power
+    o = B.attend_diff_q8(c, q, lam, batch, gain=gain)
+    check_diff(c, q, counts, o, lam, gain)
+    assert torch.equal(o.out[counts[0]:], plain[counts[0]:])
+    assert bool(o.out[:counts[0]].isfinite().all()) and c.device_status() == 0
