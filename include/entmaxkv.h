@@ -601,7 +601,11 @@ int32_t entmaxkv_attend_q8(const entmaxkv_config* cfg, const entmaxkv_q8_cache* 
  *   y = softmax(s_2i) V - lam * softmax(s_2i+1) V,
  * and with a gain y / sqrt(mean(y^2) + eps) * gain over its head_dim values. Sums,
  * difference and norm are float32, rounded once, to bfloat16; the rest is as for
- * attend_q8 with alpha = 1, workspace included.
+ * attend_q8 with alpha = 1, workspace included, also that each map's weights meet V's
+ * codes with 11 bits: before the norm y is off by up to 2^-11 of sum_j p_j |v_j| of
+ * each map (the second's times lam), which where the maps nearly cancel is more
+ * beside y than its own rounding is, and a norm scales it up with y. Maps of equal
+ * queries and a factor of 1 cancel to 0.
  *   lam   (device) float32, pair i of row t takes lam[t * lam_stride + i]; a
  *         stride of 0 gives all rows the same Hq/2 factors. Finite
  *   gain  (device) [head_dim] float32, or NULL for no norm. eps: at least 2^-100

@@ -1,4 +1,4 @@
-"""Differences of pairs whose values are far from 1."""
+"""Differences of pairs whose values are far from 1, and of maps that are nearly alike."""
 
 import pytest
 import torch
@@ -29,3 +29,20 @@ def test_a_norm_of_values_whose_squares_pass_fp32(code, lens, counts, d, power):
     check_diff(c, q, counts, o, lam, gain)
     assert torch.equal(o.out[counts[0]:], plain[counts[0]:])
     assert bool(o.out[:counts[0]].isfinite().all()) and c.device_status() == 0
+
+
+@pytest.mark.parametrize("lens,counts", SHAPES)
+@pytest.mark.parametrize("code,d,norm", [("int8", 128, False), ("e4m3", 64, True)])
+@pytest.mark.parametrize("apart", [2.0 ** -3, 2.0 ** -8])
+def test_maps_that_are_nearly_alike(code, lens, counts, d, norm, apart):
+    """Second queries are the first ones but for a part, and factors next to 1: the difference is small beside both
+    maps, and its error stays that of their weights' 11 bits (which is what check_diff allows, before the norm)."""
+    c, q = filled(code, lens, counts, hkv=2, g=4, d=d, P=32, seed=12)
+    q = q.clone()
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q[:, 1::2] = q[:, 0::2] * (1.0 + apart * torch.randn(q[:, 0::2].shape, generator=gen, device="cuda"))
+    lam = 1.0 - 2.0 ** -6 * factors(sum(counts), 4, True)
+    gain = gains(d) if norm else None
+    o = B.attend_diff_q8(c, q, lam, batch_of(counts), gain=gain)
+    check_diff(c, q, counts, o, lam, gain)
+    assert c.device_status() == 0
