@@ -895,6 +895,7 @@ def weigh_q8(cache: QuantCache, weights, q, tau, batch: Batch, alpha=1.0, scale=
 
 
 def alloc_evict_workspace(cache: QuantCache, n_seqs, keep):
+    _need(int(keep) < 2 ** 31, "keep: a number of 32 bits is wanted")
     n = int(lib().entmaxkv_evict_q8_workspace(cache.cfg, int(n_seqs), int(keep)))
     if n == 0:
         raise EntmaxKVError("invalid arguments for workspace sizing")
@@ -916,9 +917,13 @@ def evict_q8(cache: QuantCache, pool: PagePool, weights, seq_ids, keep, above=0,
         raise EntmaxKVError("cache, pool and workspace: on one device are wanted")
     _need(pool._n >= cache.cfg.num_phys_pages, "pool: a free list of num_phys_pages entries is wanted")
     _need(weights is not None or weights_out is None, "weights_out: without weights")
+    keep, above, sinks, recent = int(keep), int(above) or int(keep), int(sinks), int(recent)
+    _need(all(-2 ** 31 <= x < 2 ** 31 for x in (keep, above, sinks, recent)),
+          "keep, above, sinks, recent: numbers of 32 bits are wanted")  # (the call would take the low bits)
     lens = cache.seq_lens
     w_in = None if weights is None else _weights(cache, weights)
-    args = (w_in, _i32(seq_ids, (n,), dev, "seq_ids"), None if count is None else _i32(count, (n,), dev, "count"), n, int(keep), int(above) or int(keep), int(sinks), int(recent),
+    args = (w_in, _i32(seq_ids, (n,), dev, "seq_ids"), None if count is None else _i32(count, (n,), dev, "count"), n,
+            keep, above, sinks, recent,
             w_in if weights_out is None else _weights(cache, weights_out, "weights_out"),
             lens.data_ptr() if lens_out is None else _i32(lens_out, lens.shape, dev, "lens_out"), pool._pages, pool._count,
             pool._count if count_out is None else _i32(count_out, (1,), dev, "count_out"))
