@@ -963,6 +963,7 @@ class QuantStep:
     def __init__(self, cache: QuantCache, pool: PagePool, n_seqs, max_count=1, alpha=1.0, lam=None, gain=None,
                  eps=1e-5, budget: KeyBudget | None = None, **score):
         _need(lam is None or alpha == 1.0, "lam: differential attention is of softmax maps (alpha = 1)")
+        _need(gain is None or lam is not None, "gain: without lam")
         dev, c = cache.device, cache.cfg
         total, Hq = n_seqs * max_count, cache.num_q_heads
         bf = dict(dtype=torch.bfloat16, device=dev)

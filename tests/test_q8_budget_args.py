@@ -28,3 +28,10 @@ def test_numbers_past_32_bits_are_refused(monkeypatch, name, value):
     if name == "keep" and value > 0:
         with pytest.raises(B.EntmaxKVError, match="32 bits"):
             B.alloc_evict_workspace(c, 1, value)
+
+
+def test_a_step_takes_a_gain_with_factors_only():
+    """(Attention of heads has no norm: the gain was left aside without a word.)"""
+    c, _ = small()
+    with pytest.raises(B.EntmaxKVError, match="gain"):
+        B.QuantStep(c, B.PagePool(z(4), z(1)), 1, gain=torch.ones(64))
