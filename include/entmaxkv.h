@@ -631,7 +631,7 @@ int32_t entmaxkv_attend_diff_q8(const entmaxkv_config* cfg, const entmaxkv_q8_ca
  *   tau      (device) [total][Hq] float32, as attend_q8 or attend_diff_q8 wrote it;
  *            a row and head whose tau is not finite (it saw no key) adds nothing
  *   coef     (device) [total][Hq] float32 factors, or NULL: 1. Those that are not
- *            above 0 count as 0. (1 and lam for the two maps of a pair weigh keys
+ *            above 0 count as 0; the others are finite. (1 and lam for the two maps of a pair weigh keys
  *            by a bound of the difference's.)
  *   decay    at least 0; with 0 what was gathered is not read. Slots without rows are
  *            left as they were
@@ -645,7 +645,9 @@ int32_t entmaxkv_attend_diff_q8(const entmaxkv_config* cfg, const entmaxkv_q8_ca
  *            at the same time. Past 32 rows a slot it holds the queries once more, in
  *            tiles of 128 rows of a slot and KV head
  * Sums are float32 in an order that the arguments and the device fix. Past 32 rows a
- * slot, a query value less than 2^-40 of the largest in the same 128 rows counts as 0.
+ * slot, queries are halves under one power of two for 128 rows: a value down to 2^-29 of
+ * the largest of them is exact, a smaller one is held to 2^-39 of that largest (below
+ * 2^-40 it counts as 0).
  */
 size_t entmaxkv_weigh_q8_workspace(const entmaxkv_config* cfg, int32_t n_seqs, int32_t total,
                                    int32_t max_count, float alpha);

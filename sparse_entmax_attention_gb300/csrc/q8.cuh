@@ -230,10 +230,11 @@ size_t attend_entmax_bytes(const entmaxkv_config& cfg, int n_seqs);
 cudaError_t launch_attend_entmax(const entmaxkv_config& cfg, Q8AttendArgs a, bool i8, float alpha, void* ws, int sms,
                                  cudaStream_t st);
 // Rows of a batch's largest slot up to which the streaming kernel weighs keys; with
-// more, 128-row product tiles do. Measured, streaming against products, batches of
-// equal slots, int8, 8 KV heads: 24 sequences of 6000 tokens at d = 128 43/90 us at 16
-// rows, 70/92 at 32; 4 of 30000 37/75, 61/78; one of 32768 17/31, 23/33; 24 of 6000 at
-// d = 64 31/74, 55/80.
+// more, 128-row product tiles do. 32 is what the streaming kernel's largest variant
+// holds (four tiles of 8 rows in registers), not where the two cross: it is still ahead
+// there. Measured, streaming against products, batches of equal slots, int8, 8 KV heads:
+// 24 sequences of 6000 tokens at d = 128 43/90 us at 16 rows, 70/92 at 32; 4 of 30000
+// 37/75, 61/78; one of 32768 17/31, 23/33; 24 of 6000 at d = 64 31/74, 55/80.
 constexpr int kWeighRows = 32;
 size_t weigh_chunk_bytes(const entmaxkv_config& cfg, int n_seqs, int total);
 cudaError_t launch_weigh_chunk(const Q8WeighArgs& a, bool i8, void* ws, int sms, cudaStream_t st);

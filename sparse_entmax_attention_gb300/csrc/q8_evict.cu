@@ -30,8 +30,8 @@
 // select 23 us, of which loads 4, the four counts 11 (half of it cluster barriers) and the listing 5; move 27 us, four
 // waves of a load (random rows of 128 bytes), a barrier and a store, 2.5 TB/s. 16 sequences of 1000-32000 to 1024,
 // e4m3, d = 64: select 27 us, as long as its longest sequence, move 14 us. All three, int8, d = 128:
-// 55 us for 131072 to 16384, 25 for 3000 to 2000, 62 for 32768 to 28000. In one kernel, with K and V in one warp's registers and clusters of 16
-// (of which only a few run at a time), the first took 101 us and the second 160.
+// 55 us for 131072 to 16384, 25 for 3000 to 2000, 62 for 32768 to 28000. In one kernel, with K and V in one warp's
+// registers and clusters of 16 (of which only a few run at a time), the first took 101 us and the second 160.
 #include "q8_tiles.cuh"
 
 namespace ekv {
@@ -592,6 +592,8 @@ static cudaError_t evict_t(EvictArgs a, int sms, cudaStream_t st) {
   // run about 16 at a time. Measured, clusters/blocks alone, int8, d = 128, 8, 16, 24 and 32 pairs: 2400 to 2048 tokens
   // 27/31, 37/31, 39/31, 51/31 us; 4700 to 4096 29/44, 41/45, 43/45, 56/45; 9000 to 8000 35/68, 45/70, 55/70, 69/72; 17000
   // to 16000 43/111, 57/117, 85/121, 101/125; 32000 to 1024 27/39, 39/39, 43/39, 53/39. Launching both costs 2 us.
+  // The rule knows what the move depends on, pairs and keys that stay. The selection goes by the old length, which only
+  // the device knows: 16 pairs of 131072 to 1024 are blocks alone, whose weights do not fit (158 us, 8 pairs 44).
   const long long most = (long long)a.n * a.c.Hkv, few = min(sms / 4, max(8, a.keep / 160));
   const int smem = kEvictKeys * 4;
   cudaError_t e = ensure_smem((const void*)evict_select_kernel<P>, smem);

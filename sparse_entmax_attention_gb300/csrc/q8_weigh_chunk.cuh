@@ -14,8 +14,8 @@
 //
 // Codes are exact in halves, at a quarter to a half of the instructions of bf16 (a tile of
 // keys took as much of the issue as a tile of rows does). Queries are brought by a power of
-// two to just below 2^15 at their tile's largest: a value down to 2^-29 of that stays exact,
-// and what smaller ones lose is 2^-40 of it, in the score, of which a weight is the
+// two to [2^14, 2^15) at their tile's largest: a value down to 2^-29 of that stays exact,
+// and what smaller ones lose is at most 2^-39 of it, in the score, of which a weight is the
 // exponential, far less than the fp32 sum's own rounding of the largest row.
 //
 // A first pass lays the rows out as the products and the sums want them: tiles of
@@ -517,7 +517,8 @@ __global__ void __launch_bounds__(kWcThreads, 1) weigh_chunk_kernel(WcArgs g) {
             for (; m.some; m.some &= m.some - 1u, ++u) {
               const int i = __ffs(m.some) - 1, st = u & 1, qs = u % kWcQ;
               const int n_rows = min(kWcRows, q.x.s.count * G - (rt + i) * kWcRows);
-              if (!wait_warp(&f_full[u % kWcMeta], u / kWcMeta) || !wait_warp(&q_full[qs], u / kWcQ) || (u >= 2 && !wait_warp(&s_empty[st][h], (u >> 1) - 1))) {
+              if (!wait_warp(&f_full[u % kWcMeta], u / kWcMeta) || !wait_warp(&q_full[qs], u / kWcQ) ||
+                  (u >= 2 && !wait_warp(&s_empty[st][h], (u >> 1) - 1))) {
                 ok = false;
                 break;
               }

@@ -46,3 +46,15 @@ def test_maps_that_are_nearly_alike(code, lens, counts, d, norm, apart):
     o = B.attend_diff_q8(c, q, lam, batch_of(counts), gain=gain)
     check_diff(c, q, counts, o, lam, gain)
     assert c.device_status() == 0
+
+
+@pytest.mark.parametrize("lens,counts", SHAPES)
+def test_equal_calls_give_equal_bits(lens, counts):
+    c, q = filled("e4m3", lens, counts, hkv=2, g=4, d=128, P=16, seed=13)
+    lam, gain, batch = factors(sum(counts), 4, True), gains(128), batch_of(counts)
+    want = B.attend_diff_q8(c, q, lam, batch, gain=gain)
+    busy = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    for i in range(10):
+        busy.fill_(i)
+        o = B.attend_diff_q8(c, q, lam, batch, gain=gain)
+        assert torch.equal(o.out, want.out) and torch.equal(o.tau, want.tau)
